@@ -50,9 +50,17 @@ typedef enum {
     GEMMRELU_ERR_LAUNCH = 4,             /* CUDA reported an error configuring or launching a kernel */
     GEMMRELU_ERR_TIMEOUT = 5,            /* a bounded device-side wait expired (from gemm_relu_status) */
     GEMMRELU_ERR_CUDA = 6,               /* another CUDA runtime error (e.g. while reading the status) */
-    GEMMRELU_ERR_SCRATCH_LIMIT = 7       /* gemm_relu_f16_splitk_noalloc: problem needs more scratch
+    GEMMRELU_ERR_SCRATCH_LIMIT = 7,      /* gemm_relu_f16_splitk_noalloc: problem needs more scratch
                                             than GEMMRELU_NOALLOC_SCRATCH_BYTES */
+    GEMMRELU_ERR_PAGE = 8                /* a page number, length or count out of range (kv_cache.h;
+                                            from gemm_relu_status) */
 } gemmrelu_status;
+
+/* Types of 16-bit tensors, for the entry points that take both. */
+typedef enum {
+    GEMMRELU_F16 = 0,
+    GEMMRELU_BF16 = 1
+} gemmrelu_dtype;
 
 /*
  * gemm_relu_f16 -- C = fp16(max(A . B, 0)).

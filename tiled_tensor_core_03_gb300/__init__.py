@@ -23,7 +23,9 @@ ERR_LAUNCH = 4
 ERR_TIMEOUT = 5
 ERR_CUDA = 6
 ERR_SCRATCH_LIMIT = 7
+ERR_PAGE = 8
 NOALLOC_SCRATCH_BYTES = 8 << 20
+F16, BF16 = 0, 1   # types of 16-bit tensors
 
 PATH_NONE, PATH_TMA, PATH_LSU = 0, 1, 2
 (KERNEL_PAIR, KERNEL_ONE_CTA_256, KERNEL_ONE_CTA_128, KERNEL_PREDICATED, KERNEL_GEMV,
@@ -83,6 +85,11 @@ def lib():
         L.gemm_relu_debug_force_split.restype = i32
         L.flash_attention_f16.argtypes = [vp, vp, vp, vp, i64, i64, i64, i64, i32, vp]
         L.flash_attention_f16.restype = i32
+        L.kv_cache_append_x16.argtypes = [vp, vp, vp, i32, i64, i64, vp, vp, vp, i64, vp, vp, vp]
+        L.kv_cache_append_x16.restype = i32
+        L.kv_cache_evict_e4m3.argtypes = [vp, vp, i64, vp, i64, vp, i64, i64, i64, i64, vp, vp,
+                                          i64, vp, vp, vp, vp]
+        L.kv_cache_evict_e4m3.restype = i32
         L.gemm_relu_debug_streamk.argtypes = [i32]
         L.gemm_relu_debug_streamk.restype = i32
         L.gemm_relu_debug_streamk_pieces.argtypes = [i32]
@@ -323,3 +330,11 @@ def flash_attention(q, k, v, causal=False, out=None, stream=None):
     if rc != OK:
         raise GemmReluError(rc, "flash_attention_f16")
     return out
+
+
+def __getattr__(name):
+    # the cache's front end needs torch at import; the rest of this module does not
+    if name in ("KVCache", "kv_cache_append", "kv_cache_attention", "kv_cache_evict"):
+        from . import kv_cache
+        return globals().setdefault(name, getattr(kv_cache, name))
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1201,6 +1201,7 @@ const char *gemm_relu_strerror(int code) {
     case GEMMRELU_ERR_CUDA: return "CUDA runtime error";
     case GEMMRELU_ERR_SCRATCH_LIMIT:
         return "split-K scratch needed exceeds the built-in GEMMRELU_NOALLOC_SCRATCH_BYTES buffer";
+    case GEMMRELU_ERR_PAGE: return "a page number, length or count out of range on the device";
     default: return "unknown status";
     }
 }
@@ -1287,3 +1288,5 @@ int gemm_relu_debug_set(int drop_arrive, int64_t wait_limit_ns_arg) {
 }
 
 }  // extern "C"
+
+#include "kv_cache_api.cuh"

@@ -1,0 +1,201 @@
+"""A paged K/V cache held in 8 bits: torch front end of include/kv_cache.h.
+
+The cache is a tuple (k, v, k_scale, v_scale): e4m3 values
+[num_pages, kv_heads, page, head_dim] and fp32 scales [num_pages, kv_heads].
+The functions check and marshal tensors; all arithmetic runs in the library's
+kernels.  Calls are asynchronous on `stream` (default: torch's current stream)
+and allocate their outputs and workspaces on it.
+"""
+import ctypes
+from typing import NamedTuple
+
+import torch
+
+from . import OK, F16, BF16, GemmReluError, lib
+
+_DTYPES = {torch.float16: F16, torch.bfloat16: BF16}
+_VALUES = (torch.float8_e4m3fn, torch.uint8)
+_HEAD_DIMS = (64, 128)
+_PAGES = (16, 32, 64, 128)
+
+
+class KVCache(NamedTuple):
+    """The pool: value of a token's element = k (or v) * its page's and head's scale."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+    @classmethod
+    def empty(cls, num_pages, kv_heads, head_dim, page=64, device="cuda"):
+        """A pool of pages of `page` (16, 32, 64 or 128) tokens; nothing needs initialising."""
+        if head_dim not in _HEAD_DIMS or page not in _PAGES:
+            raise ValueError(f"head_dim must be one of {_HEAD_DIMS}, page one of {_PAGES}")
+        values = [torch.empty((num_pages, kv_heads, page, head_dim), dtype=torch.float8_e4m3fn,
+                              device=device) for _ in range(2)]
+        scales = [torch.ones((num_pages, kv_heads), dtype=torch.float32, device=device)
+                  for _ in range(2)]
+        return cls(*values, *scales)
+
+
+class Pool(ctypes.Structure):
+    """kv_cache_pool of the C ABI."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
+                ("kv_heads", ctypes.c_int64), ("page", ctypes.c_int64),
+                ("head_dim", ctypes.c_int64)]
+
+
+Strides = ctypes.c_int64 * 3
+
+
+# The checks below run before every launch of a few microseconds, so each asks a
+# tensor as few questions as it can.
+
+def _device(t):
+    """The current device's number, which t (and every other tensor) must be on."""
+    d = t.get_device()
+    if d < 0 or d != torch.cuda.current_device():
+        raise ValueError("tensors must be on the current CUDA device")
+    return d
+
+
+def _pool(cache, d):
+    """(Pool, shape) of a cache on device d."""
+    k, v, ks, vs = cache
+    shape = k.shape
+    if len(shape) != 4 or v.shape != shape or k.dtype not in _VALUES or v.dtype != k.dtype \
+            or not k.is_contiguous() or not v.is_contiguous():
+        raise ValueError("cache k and v must be contiguous e4m3 tensors of one shape "
+                         "[num_pages, kv_heads, page, head_dim]")
+    pages, heads, page, dim = shape
+    if dim not in _HEAD_DIMS or page not in _PAGES:
+        raise ValueError(f"head_dim must be one of {_HEAD_DIMS}, page one of {_PAGES}: "
+                         f"got {tuple(shape)}")
+    if ks.shape != (pages, heads) or vs.shape != (pages, heads) or ks.dtype != torch.float32 \
+            or vs.dtype != torch.float32 or not ks.is_contiguous() or not vs.is_contiguous():
+        raise ValueError("cache scales must be contiguous float32 [num_pages, kv_heads]")
+    if k.get_device() != d or v.get_device() != d or ks.get_device() != d \
+            or vs.get_device() != d:
+        raise ValueError(f"the cache must be on cuda:{d}")
+    return Pool(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages, heads, page,
+                dim), shape
+
+
+def _ints(t, shape, name, d):
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous() or t.get_device() != d:
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)} "
+                         f"on cuda:{d}")
+    return t.data_ptr()
+
+
+def _table(pages, batch, name, d):
+    """(pointer, max_pages) of a page table."""
+    if pages.dim() != 2:
+        raise ValueError(f"{name} must be int32 [batch, max_pages]")
+    width = pages.shape[1]
+    return _ints(pages, (batch, width), name, d), width
+
+
+def _strides(t, name):
+    """(pointer, {batch, token, head} strides) of a 16-bit [batch, tokens, heads, head_dim]
+    tensor whose heads start on 16-byte boundaries."""
+    p = t.data_ptr()
+    a, b, c, e = t.stride()
+    if e != 1 or (a | b | c | p >> 1) & 7:
+        # an axis of one element is never stepped over
+        a, b, c = (0 if n == 1 else x for n, x in zip(t.shape, (a, b, c)))
+        if e != 1 or (a | b | c | p >> 1) & 7:
+            raise ValueError(f"{name}: heads must be contiguous and start on 16-byte boundaries "
+                             f"(strides {t.stride()}, address {p:#x})")
+    return p, Strides(a, b, c)
+
+
+def _current(d):
+    return torch._C._cuda_getCurrentRawStream(d)   # current_stream().cuda_stream, directly
+
+
+def _on(stream, f, *args):
+    """f(raw stream, *args); what f allocates belongs to the stream."""
+    if stream is None:
+        return f(_current(torch.cuda.current_device()), *args)
+    with torch.cuda.stream(stream):
+        return f(stream.cuda_stream, *args)
+
+
+def kv_cache_append(cache, k, v, pages, lengths, counts=None, stream=None):
+    """Write new tokens' k and v (fp16 or bf16 [batch, tokens, kv_heads, head_dim], any
+    strides between heads) into their sequences' pages.
+
+    pages int32 [batch, max_pages]; lengths int32 [batch] INCLUDES the new tokens;
+    counts int32 [batch] says how many of the `tokens` rows are new ones (default: all):
+    row i becomes token lengths - counts + i."""
+    d = _device(k)
+    dtype = _DTYPES.get(k.dtype)
+    if dtype is None or v.dtype != k.dtype:
+        raise TypeError("k and v must both be float16 or both bfloat16")
+    shape = k.shape
+    if len(shape) != 4 or v.shape != shape or v.get_device() != d:
+        raise ValueError("k and v must have the same shape [batch, tokens, kv_heads, head_dim]")
+    pool, held = _pool(cache, d)
+    batch, tokens, heads, dim = shape
+    if heads != held[1] or dim != held[3]:
+        raise ValueError(f"k has {heads} heads of {dim}, the cache {held[1]} of {held[3]}")
+    table, width = _table(pages, batch, "pages", d)
+    lens = _ints(lengths, (batch,), "lengths", d)
+    new = None if counts is None else _ints(counts, (batch,), "counts", d)
+    if batch == 0 or tokens == 0:
+        return
+    kp, ks = _strides(k, "k")
+    vp, vs = _strides(v, "v")
+    rc = lib().kv_cache_append_x16(ctypes.byref(pool), kp, vp, dtype, batch, tokens, ks, vs, table,
+                                   width, lens, new,
+                                   _current(d) if stream is None else stream.cuda_stream)
+    if rc != OK:
+        raise GemmReluError(rc, "kv_cache_append_x16")
+
+
+def kv_cache_evict(cache, weights, pages, lengths, budget, sinks, recent, to, to_pages,
+                   stream=None):
+    """Keep `budget` tokens of every sequence and head: the first `sinks`, the last
+    `recent` and the heaviest others by `weights` (fp32 [batch, kv_heads, at least
+    max_pages * page]; ties go to the earlier token), moved in order into the pages
+    to_pages (int32 [batch, to_max_pages]) of the pool `to` (may be `cache`; pages that
+    no sequence uses).
+
+    Returns (lengths int32 [batch], weights fp32 [batch, kv_heads, to_max_pages * page],
+    kept int32 [batch, kv_heads, budget]: former positions, -1 past the length)."""
+    d = _device(weights)
+    pool, held = _pool(cache, d)
+    dest, to_held = _pool(to, d)
+    if held[1:] != to_held[1:]:
+        raise ValueError("both pools must have the same kv_heads, page and head_dim")
+    if weights.dim() != 3 or weights.dtype != torch.float32 or not weights.is_contiguous() \
+            or weights.shape[1] != held[1]:
+        raise ValueError("weights must be contiguous float32 [batch, kv_heads, tokens]")
+    batch, heads, width = weights.shape
+    page = held[2]
+    table, max_pages = _table(pages, batch, "pages", d)
+    to_table, to_max = _table(to_pages, batch, "to_pages", d)
+    lens = _ints(lengths, (batch,), "lengths", d)
+    if width < max_pages * page:
+        raise ValueError(f"weights has room for {width} tokens, the page table for "
+                         f"{max_pages * page}")
+    if budget < 1 or sinks < 0 or recent < 0 or sinks + recent > budget:
+        raise ValueError("need budget >= 1, sinks and recent >= 0, sinks + recent <= budget")
+    if to_max * page < budget:
+        raise ValueError(f"to_pages has room for {to_max * page} tokens, the budget is {budget}")
+
+    def call(s):
+        new_lengths = torch.empty(batch, dtype=torch.int32, device=weights.device)
+        new_weights = torch.empty((batch, heads, to_max * page), dtype=torch.float32,
+                                  device=weights.device)
+        kept = torch.empty((batch, heads, budget), dtype=torch.int32, device=weights.device)
+        rc = lib().kv_cache_evict_e4m3(
+            ctypes.byref(pool), weights.data_ptr(), width, table, max_pages, lens, batch, budget,
+            sinks, recent, ctypes.byref(dest), to_table, to_max, new_lengths.data_ptr(),
+            new_weights.data_ptr(), kept.data_ptr(), s)
+        if rc != OK:
+            raise GemmReluError(rc, "kv_cache_evict_e4m3")
+        return new_lengths, new_weights, kept
+    return _on(stream, call)
