@@ -74,6 +74,48 @@ int kv_cache_append_x16(const kv_cache_pool *cache, const void *k, const void *v
                         const int32_t *lengths, const int32_t *counts, void *stream);
 
 /*
+ * kv_cache_attention_x16_workspace_bytes -- bytes of device workspace that
+ * kv_cache_attention_x16 needs for these sizes on the current device (its SM
+ * count decides the partials); weights_width 0 when no weights are collected.
+ * 0 for invalid arguments, or when no CUDA device is available.
+ */
+size_t kv_cache_attention_x16_workspace_bytes(int64_t batch, int64_t tokens, int64_t q_heads,
+                                              int64_t kv_heads, int64_t head_dim,
+                                              int64_t weights_width);
+
+/*
+ * kv_cache_attention_x16 -- attention of the last `tokens` tokens of every
+ * sequence over the cache: O = softmax(q K^T / sqrt(head_dim)) V over the
+ * tokens that each one sees.
+ *
+ * q        : [batch][tokens][q_heads][head_dim] of `dtype`, q_strides its
+ *            {sequence, token, head}; q_heads a multiple of kv_heads: query head h
+ *            reads K/V head h / (q_heads / kv_heads).
+ * out      : [batch][tokens][q_heads][head_dim] of `dtype`, contiguous, 16-byte
+ *            aligned.
+ * lengths  : int32 [batch], each sequence's length including these tokens: query
+ *            token i has position p = length - tokens + i.  It sees the tokens
+ *            t <= p; with a window > 0 only those with t > p - window or
+ *            t < sinks.  A token at a negative position (a sequence shorter
+ *            than `tokens`) sees nothing: its output is 0.
+ * weights  : fp32 [batch][kv_heads][weights_width] or NULL.  weights[t] grows by the
+ *            sum, over the query tokens and the head's group of query heads,
+ *            of the softmax weight of token t; weights_width >= max_pages * page.
+ * workspace: at least kv_cache_attention_x16_workspace_bytes(...), 16-byte
+ *            aligned, no initialisation; calls that may overlap on the GPU need
+ *            different ones.
+ *
+ * Scores, softmax statistics and sums are fp32, the softmax weights are rounded
+ * to fp16 for the product with V.  The order of all sums is fixed: the same call
+ * gives the same bits.
+ */
+int kv_cache_attention_x16(const kv_cache_pool *cache, const void *q, int dtype, int64_t batch,
+                           int64_t tokens, int64_t q_heads, const int64_t *q_strides, void *out,
+                           const int32_t *pages, int64_t max_pages, const int32_t *lengths,
+                           int64_t window, int64_t sinks, float *weights, int64_t weights_width,
+                           void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * kv_cache_evict_e4m3 -- keep `budget` tokens of every sequence and head, by
  * accumulated attention weight, in new pages.
  *

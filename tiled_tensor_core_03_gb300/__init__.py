@@ -87,6 +87,11 @@ def lib():
         L.flash_attention_f16.restype = i32
         L.kv_cache_append_x16.argtypes = [vp, vp, vp, i32, i64, i64, vp, vp, vp, i64, vp, vp, vp]
         L.kv_cache_append_x16.restype = i32
+        L.kv_cache_attention_x16_workspace_bytes.argtypes = [i64] * 6
+        L.kv_cache_attention_x16_workspace_bytes.restype = sz
+        L.kv_cache_attention_x16.argtypes = [vp, vp, i32, i64, i64, i64, vp, vp, vp, i64, vp, i64,
+                                             i64, vp, i64, vp, sz, vp]
+        L.kv_cache_attention_x16.restype = i32
         L.kv_cache_evict_e4m3.argtypes = [vp, vp, i64, vp, i64, vp, i64, i64, i64, i64, vp, vp,
                                           i64, vp, vp, vp, vp]
         L.kv_cache_evict_e4m3.restype = i32
@@ -334,7 +339,8 @@ def flash_attention(q, k, v, causal=False, out=None, stream=None):
 
 def __getattr__(name):
     # the cache's front end needs torch at import; the rest of this module does not
-    if name in ("KVCache", "kv_cache_append", "kv_cache_attention", "kv_cache_evict"):
+    if name in ("KVCache", "kv_cache_append", "kv_cache_attention",
+                "kv_cache_attention_workspace", "kv_cache_evict"):
         from . import kv_cache
         return globals().setdefault(name, getattr(kv_cache, name))
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

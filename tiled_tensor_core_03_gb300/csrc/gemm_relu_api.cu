@@ -106,6 +106,7 @@ struct DeviceState {
     bool attr_pair_pred = false;
     bool attr_gemv[4] = {false, false, false, false};
     bool attr_attn[2] = {false, false};
+    bool attr_kv[8] = {};   // kv_cache_attention: head_dim 64, 128 x weights or not x type
 };
 constexpr int kMaxDevices = 64;
 DeviceState g_dev[kMaxDevices];

@@ -4,6 +4,7 @@
 
 #include "kv_cache.h"
 #include "kv_cache.cuh"
+#include "kv_attention.cuh"
 
 namespace {
 
@@ -75,6 +76,84 @@ int launch_move(const KC::EvictParams &p, int64_t grid, cudaStream_t s) {
     if (p.from.page * D / 16 > KC::kMoveThreads)
         return launch_kv(KC::kv_evict_move_kernel<D, 2>, grid, KC::kMoveThreads, s, p);
     return launch_kv(KC::kv_evict_move_kernel<D, 1>, grid, KC::kMoveThreads, s, p);
+}
+
+// K or V of a pool as a 4-D tensor of bytes {head_dim, page, kv_heads, num_pages}; boxes
+// of one head's `box_tokens` tokens, swizzled by the row's width.
+bool make_pool_map(CUtensorMap *map, const void *ptr, const kv_cache_pool *c, uint32_t box_tokens) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc)
+        return false;
+    const cuuint64_t d = (cuuint64_t)c->head_dim, row = d * (cuuint64_t)c->page;
+    cuuint64_t dims[4] = {d, (cuuint64_t)c->page, (cuuint64_t)c->kv_heads, (cuuint64_t)c->num_pages};
+    cuuint64_t strides[3] = {d, row, row * (cuuint64_t)c->kv_heads};
+    cuuint32_t box[4] = {(cuuint32_t)d, box_tokens, 1, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(ptr), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Workspace of kv_cache_attention_x16: partials, unit counts, and with weights every
+// row's log-sum-exp and scores.
+struct AttnSpace {
+    size_t before, lse, scores, total;   // byte offsets; partials at 0
+};
+
+AttnSpace attention_space(int64_t batch, int64_t rows, int64_t kv_heads, int64_t head_dim,
+                          int64_t weights_width, int sms) {
+    AttnSpace a{};
+    size_t at = (size_t)sms * KC::kAttnBlocksPerSm * 2 * KC::kRows * (head_dim + 2) * 4;
+    a.before = at = round256(at);
+    at += (size_t)(batch + 1) * 8;
+    a.lse = at = round256(at);
+    if (weights_width > 0) {
+        at += (size_t)batch * kv_heads * rows * 4;
+        a.scores = at = round256(at);
+        at += (size_t)batch * kv_heads * weights_width * rows * 4;
+    }
+    a.total = round256(at);
+    return a;
+}
+
+// batch, tokens and heads of an attention call; their products stay far from 2^63.
+bool attention_sizes_ok(int64_t batch, int64_t tokens, int64_t q_heads, int64_t kv_heads,
+                        int64_t head_dim, int64_t weights_width) {
+    return batch >= 0 && batch <= 65535 && tokens >= 0 && tokens <= 65535 && kv_heads > 0 &&
+           kv_heads <= 65535 && q_heads > 0 && q_heads <= 65535 && q_heads % kv_heads == 0 &&
+           (head_dim == 64 || head_dim == 128) && weights_width >= 0 && weights_width <= kMaxTokens &&
+           batch * kv_heads <= kMaxGrid && tokens * q_heads <= (int64_t)1 << 24 &&
+           batch * kv_heads * (tokens * (q_heads / kv_heads)) <= kMaxGrid;
+}
+
+template <int D, bool kBf16, bool kScores>
+int launch_kv_attention(const CUtensorMap &mK, const CUtensorMap &mV, const KC::AttnParams &p,
+                        cudaStream_t s, bool &attr_done) {
+    using G = KC::AttnCfg<D>;
+    auto kern = KC::kv_attention_kernel<D, kBf16, kScores>;
+    if (!ensure_smem_attr(attr_done, kern, G::kSmem))
+        return GEMMRELU_ERR_LAUNCH;
+    int rc = launch_kernel(kern, (unsigned)p.grid, KC::kAttnThreads, G::kSmem, s, false, 1u, mK, mV, p);
+    if (rc != GEMMRELU_OK)
+        return rc;
+    rc = launch_kv(KC::kv_attention_join_kernel<D, kBf16, kScores>,
+                   (int64_t)p.batch * p.pool.kv_heads * p.rows, KC::kJoinThreads, s, p);
+    if (rc != GEMMRELU_OK || !kScores)
+        return rc;
+    const int64_t blocks = (p.width + KC::kWeightThreads - 1) / KC::kWeightThreads;
+    return launch_kv(KC::kv_attention_weights_kernel, (int64_t)p.batch * p.pool.kv_heads * blocks,
+                     KC::kWeightThreads, s, p);
+}
+
+template <int D>
+int launch_kv_attention_as(bool bf16, bool scores, const CUtensorMap &mK, const CUtensorMap &mV,
+                           const KC::AttnParams &p, cudaStream_t s, bool *attr) {
+    if (scores)
+        return bf16 ? launch_kv_attention<D, true, true>(mK, mV, p, s, attr[0])
+                    : launch_kv_attention<D, false, true>(mK, mV, p, s, attr[1]);
+    return bf16 ? launch_kv_attention<D, true, false>(mK, mV, p, s, attr[2])
+                : launch_kv_attention<D, false, false>(mK, mV, p, s, attr[3]);
 }
 
 }  // namespace
@@ -175,6 +254,86 @@ int kv_cache_evict_e4m3(const kv_cache_pool *cache, const float *weights, int64_
     if (rc != GEMMRELU_OK)
         return rc;
     return cache->head_dim == 64 ? launch_move<64>(p, moves, s) : launch_move<128>(p, moves, s);
+}
+
+size_t kv_cache_attention_x16_workspace_bytes(int64_t batch, int64_t tokens, int64_t q_heads,
+                                              int64_t kv_heads, int64_t head_dim,
+                                              int64_t weights_width) {
+    if (!attention_sizes_ok(batch, tokens, q_heads, kv_heads, head_dim, weights_width))
+        return 0;
+    DeviceState *ds = nullptr;
+    if (current_device_state(&ds) != GEMMRELU_OK)
+        return 0;
+    return attention_space(batch, tokens * (q_heads / kv_heads), kv_heads, head_dim, weights_width,
+                           ds->sms).total;
+}
+
+int kv_cache_attention_x16(const kv_cache_pool *cache, const void *q, int dtype, int64_t batch,
+                           int64_t tokens, int64_t q_heads, const int64_t *q_strides, void *out,
+                           const int32_t *pages, int64_t max_pages, const int32_t *lengths,
+                           int64_t window, int64_t sinks, float *weights, int64_t weights_width,
+                           void *workspace, size_t workspace_bytes, void *stream) {
+    if (!pool_ok(cache) || (dtype != GEMMRELU_F16 && dtype != GEMMRELU_BF16) || window < 0 ||
+        sinks < 0 ||
+        !attention_sizes_ok(batch, tokens, q_heads, cache->kv_heads, cache->head_dim,
+                            weights ? weights_width : 0))
+        return GEMMRELU_ERR_INVALID_ARG;
+    if (batch == 0 || tokens == 0)
+        return GEMMRELU_OK;
+    if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || !strides_ok(q_strides) ||
+        !table_ok(pages, batch, max_pages, cache->page) || !lengths || !aligned(lengths, 4) ||
+        !aligned(weights, 4) || (weights && weights_width < max_pages * cache->page) ||
+        (weights && batch * cache->kv_heads * ((weights_width + KC::kWeightThreads - 1) /
+                                               KC::kWeightThreads) > kMaxGrid))
+        return GEMMRELU_ERR_INVALID_ARG;
+    DeviceState *ds = nullptr;
+    const int rc = current_device_state(&ds);
+    if (rc != GEMMRELU_OK)
+        return rc;
+    const int64_t rows = tokens * (q_heads / cache->kv_heads);
+    const AttnSpace sp = attention_space(batch, rows, cache->kv_heads, cache->head_dim,
+                                         weights ? weights_width : 0, ds->sms);
+    if (!workspace || workspace_bytes < sp.total || !aligned(workspace, 16))
+        return GEMMRELU_ERR_WORKSPACE;
+    const uint32_t box = (uint32_t)std::min<int64_t>(cache->page, KC::kUnit);
+    CUtensorMap mK, mV;
+    if (!make_pool_map(&mK, cache->k, cache, box) || !make_pool_map(&mV, cache->v, cache, box))
+        return GEMMRELU_ERR_LAUNCH;
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
+    KC::AttnParams p{};
+    p.pool = device_pool(cache);
+    p.q = static_cast<const uint16_t *>(q);
+    for (int i = 0; i < 3; ++i)
+        p.q_stride[i] = q_strides[i];
+    p.out = static_cast<uint16_t *>(out);
+    p.pages = pages;
+    p.lengths = lengths;
+    p.max_pages = max_pages;
+    p.batch = (int)batch;
+    p.tokens = (int)tokens;
+    p.q_heads = (int)q_heads;
+    p.group = (int)(q_heads / cache->kv_heads);
+    p.rows = (int)rows;
+    p.row_tiles = (int)((rows + KC::kRows - 1) / KC::kRows);
+    p.window = (int)std::min<int64_t>(window, kMaxTokens);
+    p.sinks = (int)std::min<int64_t>(sinks, kMaxTokens);
+    p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)cache->head_dim));
+    p.grid = ds->sms * KC::kAttnBlocksPerSm;
+    p.partial = reinterpret_cast<float *>(ws);
+    p.before = reinterpret_cast<int64_t *>(ws + sp.before);
+    if (weights) {
+        p.lse = reinterpret_cast<float *>(ws + sp.lse);
+        p.scores = reinterpret_cast<float *>(ws + sp.scores);
+        p.weights = weights;
+        p.width = weights_width;
+    }
+    p.drop_arrive = g_drop_arrive.load();
+    p.wait_limit_ns = wait_limit_ns();
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool bf16 = dtype == GEMMRELU_BF16;
+    return cache->head_dim == 64
+               ? launch_kv_attention_as<64>(bf16, weights != nullptr, mK, mV, p, s, ds->attr_kv)
+               : launch_kv_attention_as<128>(bf16, weights != nullptr, mK, mV, p, s, ds->attr_kv + 4);
 }
 
 }  // extern "C"

@@ -155,6 +155,66 @@ def kv_cache_append(cache, k, v, pages, lengths, counts=None, stream=None):
         raise GemmReluError(rc, "kv_cache_append_x16")
 
 
+def kv_cache_attention_workspace(q, cache, weights=None):
+    """A device workspace sized for kv_cache_attention (uint8 tensor)."""
+    batch, tokens, heads, dim = q.shape
+    n = lib().kv_cache_attention_x16_workspace_bytes(
+        batch, tokens, heads, cache[0].shape[1], dim, 0 if weights is None else weights.shape[2])
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
+
+
+def kv_cache_attention(q, cache, pages, lengths, window=0, sinks=0, weights=None, out=None,
+                       workspace=None, stream=None):
+    """softmax(q K^T / sqrt(head_dim)) V of the last tokens of every sequence over the cache:
+    q fp16 or bf16 [batch, tokens, q_heads, head_dim] (any strides between heads), query
+    head h reading K/V head h // (q_heads // kv_heads).
+
+    lengths int32 [batch] includes these tokens; token i sees the tokens t <= p = length -
+    tokens + i, with a window > 0 only those with t > p - window or t < sinks.  With
+    `weights` (fp32 [batch, kv_heads, at least max_pages * page]) each token's softmax
+    weights, summed over the query tokens and heads of its group, are added to it."""
+    d = _device(q)
+    dtype = _DTYPES.get(q.dtype)
+    if dtype is None:
+        raise TypeError("q must be float16 or bfloat16")
+    shape = q.shape
+    if len(shape) != 4:
+        raise ValueError("q must be [batch, tokens, q_heads, head_dim]")
+    pool, held = _pool(cache, d)
+    batch, tokens, heads, dim = shape
+    if dim != held[3] or heads % held[1] or heads == 0:
+        raise ValueError(f"q has {heads} heads of {dim}, the cache {held[1]} of {held[3]}")
+    if window < 0 or sinks < 0:
+        raise ValueError("window and sinks must not be negative")
+    table, max_pages = _table(pages, batch, "pages", d)
+    lens = _ints(lengths, (batch,), "lengths", d)
+    width, wp = 0, None
+    if weights is not None:
+        if weights.dtype != torch.float32 or weights.dim() != 3 or not weights.is_contiguous() \
+                or weights.shape[:2] != (batch, held[1]) or weights.get_device() != d \
+                or weights.shape[2] < max_pages * held[2]:
+            raise ValueError("weights must be contiguous float32 [batch, kv_heads, at least "
+                             f"{max_pages * held[2]}] on cuda:{d}")
+        width, wp = weights.shape[2], weights.data_ptr()
+    if out is not None and (out.shape != shape or out.dtype != q.dtype or out.get_device() != d
+                            or not out.is_contiguous()):
+        raise ValueError("out must be a contiguous tensor like q")
+    if batch == 0 or tokens == 0:
+        return torch.empty_like(q) if out is None else out
+    qp, qs = _strides(q, "q")
+
+    def call(s):
+        o = torch.empty(shape, dtype=q.dtype, device=q.device) if out is None else out
+        w = kv_cache_attention_workspace(q, cache, weights) if workspace is None else workspace
+        rc = lib().kv_cache_attention_x16(
+            ctypes.byref(pool), qp, dtype, batch, tokens, heads, qs, o.data_ptr(), table,
+            max_pages, lens, window, sinks, wp, width, w.data_ptr(), w.nbytes, s)
+        if rc != OK:
+            raise GemmReluError(rc, "kv_cache_attention_x16")
+        return o
+    return _on(stream, call)
+
+
 def kv_cache_evict(cache, weights, pages, lengths, budget, sinks, recent, to, to_pages,
                    stream=None):
     """Keep `budget` tokens of every sequence and head: the first `sinks`, the last
