@@ -44,6 +44,35 @@ int flash_attention_f16(const void *Q, const void *K, const void *V, void *O,
                         int64_t batch, int64_t seq, int64_t heads, int64_t head_dim,
                         int causal, void *stream);
 
+/*
+ * flash_attention_window_x16 -- attention forward of a prompt with a sliding
+ * window and first tokens that stay visible: query i stands at position
+ * p = i + kv_seq - q_seq and sees the keys j <= p; with window > 0 only those
+ * with j > p - window or j < sinks (window 0: causal attention).  A query that
+ * sees nothing (p < 0) gets 0.
+ *
+ * Q, O       : [batch][q_seq][q_heads][head_dim], K, V
+ *              [batch][kv_seq][kv_heads][head_dim], DEVICE pointers, all of
+ *              `dtype` (GEMMRELU_F16 or GEMMRELU_BF16), 16-byte aligned.  O is
+ *              contiguous and must not overlap the inputs (not checked).
+ * q_heads    : a multiple of kv_heads; query head h reads K/V head
+ *              h / (q_heads / kv_heads).  head_dim: 64 or 128.
+ * *_strides  : {sequence, token, head} strides of Q, K and V in elements,
+ *              positive multiples of 8 (any value for an axis of one
+ *              element); head_dim elements are contiguous.
+ * sizes      : batch and heads at most 65535, sequences at most 2^30.
+ *
+ * Softmax statistics and sums are fp32; the softmax weights are rounded to
+ * `dtype` for the product with V, the result once.  NaN and infinities
+ * reach exactly the queries that see them.  The summation order is fixed: the
+ * same call gives the same bits.  Asynchronous on `stream`, allocates nothing.
+ */
+int flash_attention_window_x16(const void *Q, const void *K, const void *V, void *O, int dtype,
+                               int64_t batch, int64_t q_seq, int64_t kv_seq, int64_t q_heads,
+                               int64_t kv_heads, int64_t head_dim, const int64_t *q_strides,
+                               const int64_t *k_strides, const int64_t *v_strides, int64_t window,
+                               int64_t sinks, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

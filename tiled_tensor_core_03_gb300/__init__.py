@@ -85,6 +85,9 @@ def lib():
         L.gemm_relu_debug_force_split.restype = i32
         L.flash_attention_f16.argtypes = [vp, vp, vp, vp, i64, i64, i64, i64, i32, vp]
         L.flash_attention_f16.restype = i32
+        L.flash_attention_window_x16.argtypes = [vp, vp, vp, vp, i32] + [i64] * 6 + [vp] * 3 + \
+            [i64, i64, vp]
+        L.flash_attention_window_x16.restype = i32
         L.kv_cache_append_x16.argtypes = [vp, vp, vp, i32, i64, i64, vp, vp, vp, i64, vp, vp, vp]
         L.kv_cache_append_x16.restype = i32
         L.kv_cache_attention_x16_workspace_bytes.argtypes = [i64] * 6
@@ -338,9 +341,9 @@ def flash_attention(q, k, v, causal=False, out=None, stream=None):
 
 
 def __getattr__(name):
-    # the cache's front end needs torch at import; the rest of this module does not
-    if name in ("KVCache", "kv_cache_append", "kv_cache_attention",
+    # the serving operators' front end needs torch at import; the rest of this module does not
+    if name in ("flash_attention_window", "KVCache", "kv_cache_append", "kv_cache_attention",
                 "kv_cache_attention_workspace", "kv_cache_evict"):
-        from . import kv_cache
-        return globals().setdefault(name, getattr(kv_cache, name))
+        from . import serving
+        return globals().setdefault(name, getattr(serving, name))
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

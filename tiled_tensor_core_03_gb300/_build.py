@@ -9,6 +9,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 SOURCES = [os.path.join(CSRC, "gemm_relu_api.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("gemm_relu_kernels.cuh", "gemm_relu_splitk.cuh", "gemm_relu_2sm.cuh", "gemm_relu_gemv.cuh", "flash_attention.cuh", "sm103.cuh", "gemm_relu_stage.cuh",
+                                                 "flash_attention_window.cuh", "flash_attention_window_api.cuh",
                                                  "kv_cache.cuh", "kv_attention.cuh", "kv_cache_api.cuh")] + [
     os.path.join(INCLUDE, f) for f in ("gemm_relu.h", "flash_attention.h", "kv_cache.h")]
 LIB = os.path.join(PKG, "libgemmrelu.so")

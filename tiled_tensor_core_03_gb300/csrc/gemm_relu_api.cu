@@ -106,6 +106,7 @@ struct DeviceState {
     bool attr_pair_pred = false;
     bool attr_gemv[4] = {false, false, false, false};
     bool attr_attn[2] = {false, false};
+    bool attr_window[4] = {};
     bool attr_kv[8] = {};   // kv_cache_attention: head_dim 64, 128 x weights or not x type
 };
 constexpr int kMaxDevices = 64;
@@ -1290,4 +1291,5 @@ int gemm_relu_debug_set(int drop_arrive, int64_t wait_limit_ns_arg) {
 
 }  // extern "C"
 
+#include "flash_attention_window_api.cuh"
 #include "kv_cache_api.cuh"

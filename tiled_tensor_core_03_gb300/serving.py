@@ -1,4 +1,5 @@
-"""A paged K/V cache held in 8 bits: torch front end of include/kv_cache.h.
+"""Operators of a serving loop: torch front end of include/kv_cache.h (a paged K/V cache
+held in 8 bits) and of flash_attention_window in include/flash_attention.h.
 
 The cache is a tuple (k, v, k_scale, v_scale): e4m3 values
 [num_pages, kv_heads, page, head_dim] and fp32 scales [num_pages, kv_heads].
@@ -121,6 +122,48 @@ def _on(stream, f, *args):
         return f(_current(torch.cuda.current_device()), *args)
     with torch.cuda.stream(stream):
         return f(stream.cuda_stream, *args)
+
+
+def flash_attention_window(q, k, v, window, sinks=0, out=None, stream=None):
+    """softmax(q k^T / sqrt(d)) v of a prompt with a sliding window: q [batch, q_seq, q_heads, d],
+    k and v [batch, kv_seq, kv_heads, d], fp16 or bf16, any strides between heads, d = 64 or
+    128; query head h reads K/V head h // (q_heads // kv_heads).
+
+    Query i stands at p = i + kv_seq - q_seq and sees the keys j <= p; with a window > 0
+    only those with j > p - window or j < sinks.  A query that sees nothing gets 0."""
+    d = _device(q)
+    dtype = _DTYPES.get(q.dtype)
+    if dtype is None or k.dtype != q.dtype or v.dtype != q.dtype:
+        raise TypeError("q, k and v must all be float16 or all bfloat16")
+    shape, kv_shape = q.shape, k.shape
+    if len(shape) != 4 or len(kv_shape) != 4 or v.shape != kv_shape or k.get_device() != d \
+            or v.get_device() != d:
+        raise ValueError("q must be [batch, q_seq, q_heads, d], k and v [batch, kv_seq, "
+                         "kv_heads, d], all on one device")
+    batch, q_seq, q_heads, dim = shape
+    _, kv_seq, kv_heads, _ = kv_shape
+    if kv_shape[0] != batch or kv_shape[3] != dim or dim not in _HEAD_DIMS or kv_heads == 0 \
+            or q_heads % kv_heads:
+        raise ValueError(f"shapes {tuple(shape)} and {tuple(kv_shape)} do not go together")
+    if window < 0 or sinks < 0:
+        raise ValueError("window and sinks must not be negative")
+    if out is not None and (out.shape != shape or out.dtype != q.dtype or out.get_device() != d
+                            or not out.is_contiguous()):
+        raise ValueError("out must be a contiguous tensor like q")
+    if q.numel() == 0:
+        return torch.empty_like(q) if out is None else out
+    qp, qs = _strides(q, "q")
+    kp, ks = _strides(k, "k")
+    vp, vs = _strides(v, "v")
+
+    def call(s):
+        o = torch.empty(shape, dtype=q.dtype, device=q.device) if out is None else out
+        rc = lib().flash_attention_window_x16(qp, kp, vp, o.data_ptr(), dtype, batch, q_seq, kv_seq,
+                                              q_heads, kv_heads, dim, qs, ks, vs, window, sinks, s)
+        if rc != OK:
+            raise GemmReluError(rc, "flash_attention_window_x16")
+        return o
+    return _on(stream, call)
 
 
 def kv_cache_append(cache, k, v, pages, lengths, counts=None, stream=None):
