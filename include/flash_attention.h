@@ -73,6 +73,13 @@ int flash_attention_window_x16(const void *Q, const void *K, const void *V, void
                                const int64_t *k_strides, const int64_t *v_strides, int64_t window,
                                int64_t sinks, void *stream);
 
+/*
+ * Host-only test hook: the blocks of 128 keys that flash_attention_window_x16 visits
+ * for rows at positions first .. last: [0, out[0]) and [out[1], out[2]).
+ */
+int flash_attention_window_debug_blocks(int64_t first, int64_t last, int64_t window, int64_t sinks,
+                                        int *out);
+
 #ifdef __cplusplus
 }
 #endif

@@ -145,6 +145,16 @@ int kv_cache_evict_e4m3(const kv_cache_pool *cache, const float *weights, int64_
                         const kv_cache_pool *to, const int32_t *to_pages, int64_t to_max_pages,
                         int32_t *to_lengths, float *to_weights, int32_t *kept, void *stream);
 
+/*
+ * Host-only test hooks.  kv_cache_debug_span: out[0] units of 64 tokens from the
+ * first on, then those from out[1], out[2] in all -- what kv_cache_attention_x16
+ * reads of a sequence.  kv_cache_debug_range: first of `total` units that block
+ * x of `grid` takes, or (owner != 0) the block that takes unit x; -1 for
+ * invalid arguments.
+ */
+int kv_cache_debug_span(int64_t length, int64_t tokens, int64_t window, int64_t sinks, int *out);
+int64_t kv_cache_debug_range(int64_t x, int64_t total, int grid, int owner);
+
 #ifdef __cplusplus
 }
 #endif

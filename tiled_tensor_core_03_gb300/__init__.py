@@ -88,6 +88,12 @@ def lib():
         L.flash_attention_window_x16.argtypes = [vp, vp, vp, vp, i32] + [i64] * 6 + [vp] * 3 + \
             [i64, i64, vp]
         L.flash_attention_window_x16.restype = i32
+        L.flash_attention_window_debug_blocks.argtypes = [i64] * 4 + [vp]
+        L.flash_attention_window_debug_blocks.restype = i32
+        L.kv_cache_debug_span.argtypes = [i64] * 4 + [vp]
+        L.kv_cache_debug_span.restype = i32
+        L.kv_cache_debug_range.argtypes = [i64, i64, i32, i32]
+        L.kv_cache_debug_range.restype = i64
         L.kv_cache_append_x16.argtypes = [vp, vp, vp, i32, i64, i64, vp, vp, vp, i64, vp, vp, vp]
         L.kv_cache_append_x16.restype = i32
         L.kv_cache_attention_x16_workspace_bytes.argtypes = [i64] * 6

@@ -125,3 +125,16 @@ extern "C" int flash_attention_window_x16(const void *Q, const void *K, const vo
                ? launch_window<128, true>(mQ, mK, mV, p, kv_heads, batch, s, ds->attr_window[2])
                : launch_window<128, false>(mQ, mK, mV, p, kv_heads, batch, s, ds->attr_window[3]);
 }
+
+extern "C" int flash_attention_window_debug_blocks(int64_t first, int64_t last, int64_t window,
+                                                   int64_t sinks, int *out) {
+    const int64_t most = (int64_t)1 << 30;
+    if (first < -most || last < first || last >= most || window < 0 || window > most || sinks < 0 ||
+        sinks > most || !out)
+        return GEMMRELU_ERR_INVALID_ARG;
+    const FA::Blocks b = FA::blocks_seen((int)first, (int)last, (int)window, (int)sinks);
+    out[0] = b.sinks;
+    out[1] = b.low;
+    out[2] = b.high;
+    return GEMMRELU_OK;
+}

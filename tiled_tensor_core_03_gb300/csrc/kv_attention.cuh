@@ -97,19 +97,21 @@ __device__ __forceinline__ float exp2_fast(float x) {
 // sinks left of the first row's window, then all from that window on.
 struct Span {
     int sink_units, low_unit, units;
-    __device__ __forceinline__ int chunk(int u) const {
+    __host__ __device__ __forceinline__ int chunk(int u) const {
         return u < sink_units ? u : low_unit + (u - sink_units);
     }
 };
 
-__device__ __forceinline__ Span span_of(int n, int tokens, int window, int sinks) {
+__host__ __device__ __forceinline__ Span span_of(int n, int tokens, int window, int sinks) {
     Span s{0, 0, (n + kUnit - 1) / kUnit};
     const int first = n > tokens ? n - tokens : 0;   // position of the first row
     if (window > 0 && first >= window) {
         const int low = first - window + 1;
         const int head = sinks < low ? sinks : low;
         s.low_unit = low / kUnit;
-        s.sink_units = min((head + kUnit - 1) / kUnit, s.low_unit);
+        s.sink_units = (head + kUnit - 1) / kUnit;
+        if (s.sink_units > s.low_unit)
+            s.sink_units = s.low_unit;
         s.units = s.units - s.low_unit + s.sink_units;
     }
     return s;
@@ -125,10 +127,10 @@ __device__ __forceinline__ int length_of(const AttnParams &p, int b) {
 }
 
 // First unit of block c of `grid`, of `total`: equal ranges, and the block that owns unit x.
-__device__ __forceinline__ int64_t range_start(int64_t c, int64_t total, int grid) {
+__host__ __device__ __forceinline__ int64_t range_start(int64_t c, int64_t total, int grid) {
     return c * total / grid;
 }
-__device__ __forceinline__ int range_owner(int64_t x, int64_t total, int grid) {
+__host__ __device__ __forceinline__ int range_owner(int64_t x, int64_t total, int grid) {
     return (int)(((x + 1) * grid - 1) / total);
 }
 

@@ -336,4 +336,21 @@ int kv_cache_attention_x16(const kv_cache_pool *cache, const void *q, int dtype,
                : launch_kv_attention_as<128>(bf16, weights != nullptr, mK, mV, p, s, ds->attr_kv + 4);
 }
 
+int kv_cache_debug_span(int64_t length, int64_t tokens, int64_t window, int64_t sinks, int *out) {
+    if (length < 0 || length > kMaxTokens || tokens < 1 || tokens > kMaxTokens || window < 0 ||
+        window > kMaxTokens || sinks < 0 || sinks > kMaxTokens || !out)
+        return GEMMRELU_ERR_INVALID_ARG;
+    const KC::Span s = KC::span_of((int)length, (int)tokens, (int)window, (int)sinks);
+    out[0] = s.sink_units;
+    out[1] = s.low_unit;
+    out[2] = s.units;
+    return GEMMRELU_OK;
+}
+
+int64_t kv_cache_debug_range(int64_t x, int64_t total, int grid, int owner) {
+    if (x < 0 || total < 1 || grid < 1)
+        return -1;
+    return owner ? KC::range_owner(x, total, grid) : KC::range_start(x, total, grid);
+}
+
 }  // extern "C"
