@@ -107,7 +107,7 @@ struct DeviceState {
     bool attr_gemv[4] = {false, false, false, false};
     bool attr_attn[2] = {false, false};
     bool attr_window[4] = {};
-    bool attr_kv[8] = {};   // kv_cache_attention: head_dim 64, 128 x weights or not x type
+    bool attr_kv[16] = {};   // kv_cache_attention: head_dim x row groups x type x weights or not
 };
 constexpr int kMaxDevices = 64;
 DeviceState g_dev[kMaxDevices];

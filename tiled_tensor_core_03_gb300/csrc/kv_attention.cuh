@@ -6,25 +6,29 @@
 // or t < sinks), p_r the row's position.  The rows of one K/V head are
 // its group's query heads of every new token, 16 rows a tile.
 //
-// What bounds it: every visible token's 2 D bytes are read once per 16 rows and
+// What bounds it: every visible token's 2 D bytes are read once per row tile and
 // used for 4 D flops a row, so up to some tens of rows it is a stream from HBM.  The
 // kernel is built around that stream:
 //
 //  - Work is cut into units of 64 tokens of one (sequence, head, row tile); the
 //    units of all of them, in order, are dealt to the blocks in equal contiguous
-//    ranges whatever the lengths are, two blocks an SM.  A block finishes what lies
+//    ranges whatever the lengths are.  A block finishes what lies
 //    inside its range; a (sequence, head, row tile) that is cut leaves one fp32
 //    partial (O, m, l) per block in the workspace, and a second kernel joins them in
 //    order.  Nothing depends on the order in which blocks run: the same call gives
 //    the same bits.
 //  - One warp feeds a ring of 64-token stages by TMA (a page or a part of one per
 //    copy), reading page numbers and scales 32 pieces ahead.
-//  - Four warps take 16 tokens of a stage each.  The products run on
-//    mma.sync.m16n8k16 with fp16 operands: 16 rows are all there is, far below the
-//    128 of a tcgen05.mma, and e4m3 has to become fp16 (exact) on the way, which
-//    happens in registers here.  The operand layouts are chosen so that the bytes a
-//    lane loads from shared memory are the ones its fragment needs, with no
-//    shuffle (see key_of / chunk_of below).
+//  - Four warps take 16 tokens of a stage each.  The products run on mma.sync.m16n8k16
+//    with fp16 operands, tokens in the M of 16 and query rows in the N of 8:
+//    S^T = K Q^T and O^T += V^T P^T.  Eight rows are all that a decode step with up to
+//    8 heads a group has, far below the 128 of a tcgen05.mma, and e4m3 has to become
+//    fp16 (exact) on the way, which happens in registers here.  The operand layouts are
+//    chosen so that the bytes a lane loads from shared memory are the ones its fragment
+//    needs (see key_of / piece_of below); P^T is turned with movmatrix.
+//    Rows in M instead (S = Q K^T, 16 rows) took twice the products, accumulators and
+//    exponentials and 168 registers: 729 us at 64 sequences of up to 32768 tokens (8 K/V
+//    heads of 128), 4.25 TB/s, at 1.3 instructions a cycle from 10 warps an SM.
 //  - Softmax in one pass, base 2, a running reference m per row that moves only when
 //    a score exceeds it by 2^8; fp32 statistics and accumulators.  P is
 //    rounded to fp16 for the second product (relative 2^-11, like the output's own
@@ -39,23 +43,24 @@ namespace gemmrelu {
 namespace kvc {
 
 constexpr int kUnit = 64;            // tokens of a stage
-constexpr int kRows = 16;            // query rows of a tile
 constexpr int kWarps = 4;            // computing warps
 constexpr int kFeedWarp = 4;
 constexpr int kAttnThreads = 160;
-constexpr int kAttnBlocksPerSm = 2;
 constexpr float kMoveLog2 = 8.0f;    // the reference moves when a score exceeds it by more
 constexpr float kPShift = 128.0f;    // 2^7, see above
 
-template <int D>
+// kN groups of 8 query rows a tile: 1 (up to 8 rows: three blocks an SM) or 2 (two).
+template <int D, int kN>
 struct AttnCfg {
+    static constexpr int kRows = 8 * kN;
+    static constexpr int kBlocksPerSm = kN == 1 ? 3 : 2;
     static constexpr uint32_t kTile = kUnit * D;                 // bytes of K (or V) in a stage
-    static constexpr int kStages = D == 128 ? 4 : 8;
+    static constexpr int kStages = (kN == 1 ? 3 : 4) * (128 / D);
     static constexpr uint32_t kOffK = 0;
     static constexpr uint32_t kOffV = kOffK + kStages * kTile;
     static constexpr int kPitch = D + 4;                         // floats a row of the join buffer
-    static constexpr uint32_t kOffJoin = kOffV + kStages * kTile;   // [4 warps][16][kPitch]
-    static constexpr uint32_t kOffStat = kOffJoin + kWarps * kRows * kPitch * 4;   // m, l [4][16], vref [4]
+    static constexpr uint32_t kOffJoin = kOffV + kStages * kTile;   // [4 warps][kRows][kPitch]
+    static constexpr uint32_t kOffStat = kOffJoin + kWarps * kRows * kPitch * 4;   // m, l [4][kRows], vref [4]
     static constexpr uint32_t kOffMeta = kOffStat + (2 * kWarps * kRows + kWarps) * 4;
     static constexpr uint32_t kOffScan = kOffMeta + kStages * 4 * 8;   // (ks, vs) per 16 tokens
     static constexpr uint32_t kOffBar = kOffScan + (kAttnThreads + 8) * 8;
@@ -71,10 +76,10 @@ struct AttnParams {
     const int32_t *pages, *lengths;
     int64_t max_pages;
     int batch, tokens, q_heads, group;
-    int rows, row_tiles;               // tokens * group, in tiles of 16
+    int rows, row_tiles;               // tokens * group, in tiles of 8 or 16
     int window, sinks;
     float scale_log2;                  // log2(e) / sqrt(D)
-    float *partial;                    // [2 * grid][16][D], then [2 * grid][16][2] (m, l)
+    float *partial;                    // [2 * grid][kRows][D], then [2 * grid][kRows][2] (m, l)
     int grid;
     int64_t *before;                   // [batch + 1] units of the sequences before
     float *scores;                     // with weights: [batch][kv_heads][width][rows], base 2
@@ -146,17 +151,17 @@ __device__ __forceinline__ uint32_t at_chunk(int row, int chunk) {
         return (uint32_t)(row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
 }
 
-// In fragments of mma.m16n8k16 lane = 4 g + c.  S = Q K^T: column g of an 8-token group is
-// token key_of(g), so that the score fragment's columns 2c, 2c+1 are tokens c, c + 4 and
-// eight lanes that load together touch eight different chunks.
-__device__ __forceinline__ int key_of(int g) { return (g >> 1) | ((g & 1) << 2); }
+// In fragments of mma.m16n8k16 lane = 4 g + c.  S^T = K Q^T: token row i of 16 is token
+// key_of(i), so that eight lanes that load together touch eight different chunks, here and
+// in V, where lane c takes the rows 2c, 2c + 1, 2c + 8, 2c + 9: tokens c, c + 4, c + 8, c + 12.
+__device__ __forceinline__ int key_of(int i) { return (i & 8) | (i >> 1 & 3) | ((i & 1) << 2); }
 
-// The k index of S = Q K^T runs over the D elements in an order of its own: lane c's
+// The k index of S^T = K Q^T runs over the D elements in an order of its own: lane c's
 // k-steps are the consecutive fours of its chunk(s) c (and c + 4), so a K fragment is 4
 // consecutive bytes.  Q's fragment uses the same order.
 //
-// O += P V: lane g's columns of the D / 8 column groups are D / 8 consecutive elements,
-// those of piece piece_of(g) (16 bytes for D = 128, 8 for D = 64).
+// O^T += V^T P^T: lane g's rows of the D / 16 row groups are D / 8 consecutive elements,
+// those of piece piece_of(g) (16 bytes for D = 128, 8 for D = 64), two per group.
 template <int D>
 __device__ __forceinline__ int piece_of(int g) {
     if constexpr (D == 128)
@@ -165,13 +170,20 @@ __device__ __forceinline__ int piece_of(int g) {
         return ((g >> 1) & 1) << 2 | (g >> 2) << 1 | (g & 1);
 }
 
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                        uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Transpose an 8 x 8 matrix of 16-bit elements held two a lane (row g, columns 2c, 2c + 1).
+__device__ __forceinline__ uint32_t turned(uint32_t x) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
 }
 
 __device__ __forceinline__ uint32_t half2_of(float a, float b) {
@@ -248,11 +260,12 @@ __device__ __forceinline__ int64_t out_row(const AttnParams &p, int b, int h, in
 
 // ---------------------------------------------------------------- the stream
 
-template <int D, bool kBf16, bool kScores>
-__global__ void __launch_bounds__(kAttnThreads, kAttnBlocksPerSm)
+template <int D, int kN, bool kBf16, bool kScores>
+__global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
     kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const AttnParams p) {
-    using G = AttnCfg<D>;
+    using G = AttnCfg<D, kN>;
+    constexpr int kRows = G::kRows;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -436,33 +449,46 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnBlocksPerSm)
             const int64_t end = seg1 < stop ? seg1 : stop;
             const int row0 = tile * kRows;
 
-            // this lane's rows g and g + 8: position (-1: sees nothing) and query
-            int pos[2];
-            uint32_t q[2][D / 8];
-            float row_scale[2];
+            // the query rows as fragments (lane g's row of each group of 8), and what the lane
+            // knows of the rows of its scores, 2c and 2c + 1: position (-1: sees nothing), scale
+            uint32_t q[kN][D / 8];
+            int pos[kN][2];
+            float row_scale[kN][2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = row0 + g + 8 * i, token = r / p.group;
-                const bool there = r < p.rows;
-                pos[i] = there ? n - p.tokens + token : -1;
+            for (int t = 0; t < kN; ++t) {
+                const int r = row0 + 8 * t + g, token = r / p.group;
                 const uint16_t *src = p.q + b * p.q_stride[0] + token * p.q_stride[1] +
                                       (h * p.group + r % p.group) * p.q_stride[2];
                 float back;
-                load_row<D, kBf16>(there ? src : nullptr, c, q[i], back);
-                row_scale[i] = back * p.scale_log2;
+                load_row<D, kBf16>(r < p.rows ? src : nullptr, c, q[t], back);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int row = row0 + 8 * t + 2 * c + e;
+                    pos[t][e] = row < p.rows ? n - p.tokens + row / p.group : -1;
+                    row_scale[t][e] = p.scale_log2;
+                    if constexpr (kBf16)
+                        row_scale[t][e] *= __shfl_sync(0xffffffffu, back, 4 * (2 * c + e));
+                }
             }
             const int pos_min = n - p.tokens + row0 / p.group;
             const int pos_max = n - p.tokens + (min(row0 + kRows, p.rows) - 1) / p.group;
 
-            float o[D / 8][4];
+            // o[t][j]: elements 2j (0, 1) and 2j + 1 (2, 3) of the lane's piece, rows 2c, 2c + 1
+            float o[kN][D / 16][4];
+            float m[kN][2], l[kN][2];
 #pragma unroll
-            for (int j = 0; j < D / 8; ++j)
-                o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
-            float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+            for (int t = 0; t < kN; ++t) {
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j)
+                    o[t][j][0] = o[t][j][1] = o[t][j][2] = o[t][j][3] = 0.0f;
+                m[t][0] = m[t][1] = -INFINITY;
+                l[t][0] = l[t][1] = 0.0f;
+            }
             float vref = 0.0f, vinv = 0.0f;
 
-            for (; unit < end; ++unit) {
-                const int t0 = s.chunk((int)(unit - seg0)) * kUnit + 16 * warp;
+            const int units_here = (int)(end - unit), u0 = (int)(unit - seg0);
+            for (int u = 0; u < units_here; ++u) {
+                const int t0 = s.chunk(u0 + u) * kUnit + 16 * warp;
                 if (alive)
                     alive = wait_bounded_eager(full(stage), phase, p.wait_limit_ns, abort_flag,
                                                kSiteMmaFull);
@@ -478,110 +504,133 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnBlocksPerSm)
                     (p.window == 0 || t0 + 15 > pos_min - p.window || t0 < p.sinks)) {
                     const uint32_t k_at = base + G::kOffK + stage * G::kTile + 16 * warp * D;
                     const uint32_t v_at = base + G::kOffV + stage * G::kTile + 16 * warp * D;
-                    // ---- S = Q K^T, two groups of 8 tokens
-                    float acc[2][4];
+                    // ---- S^T = K Q^T; acc[t][2 i + e]: token row g + 8 i, query row 2c + e
+                    float acc[kN][4];
+                    {
+                        float part[kN][2][4];   // two chains of products
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
-                        const int row = 8 * j + key_of(g);
+                        for (int t = 0; t < kN; ++t)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x)
+                                part[t][x][0] = part[t][x][1] = part[t][x][2] = part[t][x][3] = 0.0f;
 #pragma unroll
                         for (int half = 0; half < D / 64; ++half) {
-                            const uint4 k4 = ld_shared_v4(k_at + at_chunk<D>(row, c + 4 * half));
-                            const uint32_t kw[4] = {k4.x, k4.y, k4.z, k4.w};
+                            const uint4 lo = ld_shared_v4(k_at + at_chunk<D>(key_of(g), c + 4 * half));
+                            const uint4 hi = ld_shared_v4(k_at + at_chunk<D>(8 + key_of(g), c + 4 * half));
+                            const uint32_t k0[4] = {lo.x, lo.y, lo.z, lo.w};
+                            const uint32_t k1[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
                             for (int st = 0; st < 4; ++st) {
-                                const int x = 8 * half + 2 * st;
-                                const uint32_t a[4] = {q[0][x], q[1][x], q[0][x + 1], q[1][x + 1]};
-                                mma_f16(acc[j], a, e4m3x2_to_half2(kw[st] & 0xffffu),
-                                        e4m3x2_to_half2(kw[st] >> 16));
+                                const uint32_t a0 = e4m3x2_to_half2(k0[st] & 0xffffu);
+                                const uint32_t a1 = e4m3x2_to_half2(k1[st] & 0xffffu);
+                                const uint32_t a2 = e4m3x2_to_half2(k0[st] >> 16);
+                                const uint32_t a3 = e4m3x2_to_half2(k1[st] >> 16);
+#pragma unroll
+                                for (int t = 0; t < kN; ++t)
+                                    mma_f16(part[t][st & 1], a0, a1, a2, a3, q[t][8 * half + 2 * st],
+                                            q[t][8 * half + 2 * st + 1]);
                             }
                         }
+#pragma unroll
+                        for (int t = 0; t < kN; ++t)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                acc[t][x] = part[t][0][x] + part[t][1][x];
                     }
-                    // ---- scores in base 2, masked; acc[j][2 i + e]: row i, token 8 j + c + 4 e
+                    // ---- scores in base 2 relative to the rows' references, masked
                     const bool masked = !(t0 + 15 <= pos_min &&
                                           (p.window == 0 || t0 > pos_max - p.window || t0 + 15 < p.sinks));
-                    const float f0 = sc.x * row_scale[0], f1 = sc.x * row_scale[1];
+                    const int ta = t0 + key_of(g), tb = ta + 8;   // the lane's tokens
+                    float x[kN][4];
                     bool high = false;
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
+                    for (int t = 0; t < kN; ++t) {
+                        if constexpr (kScores) {
+                            float *dst = p.scores + (((int64_t)b * p.pool.kv_heads + h) * p.width + ta) * p.rows +
+                                         row0 + 8 * t + 2 * c;
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
+                            for (int i = 0; i < 4; ++i)
+                                if (pos[t][i & 1] >= 0 && (i < 2 ? ta : tb) < n)
+                                    dst[(i >> 1) * 8 * p.rows + (i & 1)] =
+                                        acc[t][i] * (sc.x * row_scale[t][i & 1]);
+                        }
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                float &x = acc[j][2 * i + e];
-                                x *= i ? f1 : f0;
-                                if (masked && !sees(t0 + 8 * j + c + 4 * e, pos[i], p.window, p.sinks))
-                                    x = -INFINITY;
-                                high |= x > m[i] + kMoveLog2;
-                            }
-                    if constexpr (kScores) {
-                        float *dst = p.scores + (((int64_t)b * p.pool.kv_heads + h) * p.width + t0) * p.rows + row0;
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-#pragma unroll
-                            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                                for (int e = 0; e < 2; ++e)
-                                    if (pos[i] >= 0 && t0 + 8 * j + c + 4 * e < n)
-                                        dst[(int64_t)(8 * j + c + 4 * e) * p.rows + g + 8 * i] = acc[j][2 * i + e];
+                        for (int i = 0; i < 4; ++i) {
+                            const int e = i & 1;
+                            x[t][i] = fmaf(acc[t][i], sc.x * row_scale[t][e], -m[t][e]);
+                            if (masked && !sees(i < 2 ? ta : tb, pos[t][e], p.window, p.sinks))
+                                x[t][i] = acc[t][i] = -INFINITY;
+                        }
+                        high |= fmaxf(fmaxf(x[t][0], x[t][1]), fmaxf(x[t][2], x[t][3])) > kMoveLog2;
                     }
                     if (__any_sync(0xffffffffu, high)) {
                         // move the rows' references to their largest score so far
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            float x = fmaxf(fmaxf(acc[0][2 * i], acc[0][2 * i + 1]),
-                                            fmaxf(acc[1][2 * i], acc[1][2 * i + 1]));
-                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                            const float to = fmaxf(m[i], x);
-                            const float f = to > m[i] ? exp2_fast(m[i] - to) : 1.0f;   // 0 at first
-                            l[i] *= f;
+                        for (int t = 0; t < kN; ++t)
 #pragma unroll
-                            for (int j = 0; j < D / 8; ++j) {
-                                o[j][2 * i] *= f;
-                                o[j][2 * i + 1] *= f;
+                            for (int e = 0; e < 2; ++e) {
+                                const float f = sc.x * row_scale[t][e];
+                                float top = fmaxf(acc[t][e] * f, acc[t][2 + e] * f);
+                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                                const float to = fmaxf(m[t][e], top);
+                                const float a = to > m[t][e] ? exp2_fast(m[t][e] - to) : 1.0f;   // 0 at first
+                                l[t][e] *= a;
+#pragma unroll
+                                for (int j = 0; j < D / 16; ++j) {
+                                    o[t][j][e] *= a;
+                                    o[t][j][2 + e] *= a;
+                                }
+                                m[t][e] = to;
+                                const float ref = to == -INFINITY ? 0.0f : to;
+#pragma unroll
+                                for (int i = 0; i < 2; ++i)
+                                    x[t][2 * i + e] = acc[t][2 * i + e] == -INFINITY
+                                                          ? -INFINITY
+                                                          : fmaf(acc[t][2 * i + e], f, -ref);
                             }
-                            m[i] = to;
-                        }
                     }
                     const float vs = fmaxf(sc.y, kMinScale);
                     if (vs > vref) {   // uniform in the warp
                         const float f = vref / vs;
 #pragma unroll
-                        for (int j = 0; j < D / 8; ++j) {
-                            o[j][0] *= f;
-                            o[j][1] *= f;
-                            o[j][2] *= f;
-                            o[j][3] *= f;
-                        }
+                        for (int t = 0; t < kN; ++t)
+#pragma unroll
+                            for (int j = 0; j < D / 16; ++j) {
+                                o[t][j][0] *= f;
+                                o[t][j][1] *= f;
+                                o[t][j][2] *= f;
+                                o[t][j][3] *= f;
+                            }
                         vref = vs;
                         vinv = kPShift / vs;
                     }
-                    // ---- P
-                    const float m0 = m[0] == -INFINITY ? 0.0f : m[0], m1 = m[1] == -INFINITY ? 0.0f : m[1];
+                    // ---- P^T as the second product's B operand: {rows 2c, 2c + 1} of a token to
+                    // {tokens 2c, 2c + 1} of a row
                     const float pf = vs * vinv;
-                    uint32_t a[4];
+                    uint32_t pt[kN][2];
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float e0 = exp2_fast(acc[j][0] - m0), e1 = exp2_fast(acc[j][1] - m0);
-                        const float e2 = exp2_fast(acc[j][2] - m1), e3 = exp2_fast(acc[j][3] - m1);
-                        l[0] += e0 + e1;
-                        l[1] += e2 + e3;
-                        a[2 * j] = half2_of(e0 * pf, e1 * pf);
-                        a[2 * j + 1] = half2_of(e2 * pf, e3 * pf);
+                    for (int t = 0; t < kN; ++t) {
+                        const float e0 = exp2_fast(x[t][0]), e1 = exp2_fast(x[t][1]);
+                        const float e2 = exp2_fast(x[t][2]), e3 = exp2_fast(x[t][3]);
+                        l[t][0] += e0 + e2;
+                        l[t][1] += e1 + e3;
+                        pt[t][0] = turned(half2_of(e0 * pf, e1 * pf));
+                        pt[t][1] = turned(half2_of(e2 * pf, e3 * pf));
                     }
-                    // ---- O += P V: the lane's four tokens c, c + 4, c + 8, c + 12
+                    // ---- O^T += V^T P^T: the lane's four tokens c, c + 4, c + 8, c + 12
                     constexpr int kW = D / 32;   // words of a lane's piece
                     uint32_t v[4][kW];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int row = c + 4 * k, piece = piece_of<D>(g);
                         if constexpr (D == 128) {
-                            const uint4 x = ld_shared_v4(v_at + at_chunk<D>(row, piece));
-                            v[k][0] = x.x, v[k][1] = x.y, v[k][2] = x.z, v[k][3] = x.w;
+                            const uint4 w = ld_shared_v4(v_at + at_chunk<D>(row, piece));
+                            v[k][0] = w.x, v[k][1] = w.y, v[k][2] = w.z, v[k][3] = w.w;
                         } else {
-                            const uint2 x = ld_shared_v2(v_at + at_chunk<D>(row, piece >> 1) + 8 * (piece & 1));
-                            v[k][0] = x.x, v[k][1] = x.y;
+                            const uint2 w = ld_shared_v2(v_at + at_chunk<D>(row, piece >> 1) + 8 * (piece & 1));
+                            v[k][0] = w.x, v[k][1] = w.y;
                         }
                     }
                     if (masked) {
@@ -589,8 +638,8 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnBlocksPerSm)
                         uint32_t bad = 0;
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const int t = t0 + c + 4 * k;
-                            const bool any = t <= pos_max && (p.window == 0 || t > pos_min - p.window || t < p.sinks);
+                            const int at = t0 + c + 4 * k;
+                            const bool any = at <= pos_max && (p.window == 0 || at > pos_min - p.window || at < p.sinks);
 #pragma unroll
                             for (int w = 0; w < kW; ++w) {
                                 v[k][w] = any ? v[k][w] : 0u;
@@ -601,50 +650,53 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnBlocksPerSm)
                             // a NaN that some rows see and others do not: count it for
                             // the rows that see it, then take it out
                             const uint32_t one = 0x3c00u;
-                            uint32_t seen[4];
 #pragma unroll
-                            for (int j = 0; j < 2; ++j)
+                            for (int t = 0; t < kN; ++t) {
+                                const int row = row0 + 8 * t + g;
+                                const int at = row < p.rows ? n - p.tokens + row / p.group : -1;
+                                uint32_t seen[2];
 #pragma unroll
-                                for (int i = 0; i < 2; ++i) {
-                                    const int t = t0 + 8 * j + c;
-                                    seen[2 * j + i] = (sees(t, pos[i], p.window, p.sinks) ? one : 0u) |
-                                                      (sees(t + 4, pos[i], p.window, p.sinks) ? one << 16 : 0u);
+                                for (int i = 0; i < 2; ++i)
+                                    seen[i] = (sees(t0 + c + 8 * i, at, p.window, p.sinks) ? one : 0u) |
+                                              (sees(t0 + c + 8 * i + 4, at, p.window, p.sinks) ? one << 16 : 0u);
+#pragma unroll
+                                for (int j = 0; j < D / 16; ++j) {
+                                    uint32_t a[4];   // elements 2j, 2j + 1 (i & 1), tokens k, k + 1 (k = i & 2)
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        const int sh = 8 * ((2 * j + (i & 1)) & 3) + 7;
+                                        const int k = i & 2;
+                                        a[i] = (nan_bytes(v[k][j >> 1]) >> sh & 1u ? one : 0u) |
+                                               (nan_bytes(v[k + 1][j >> 1]) >> sh & 1u ? one << 16 : 0u);
+                                    }
+                                    float count[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                                    mma_f16(count, a[0], a[1], a[2], a[3], seen[0], seen[1]);
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i)
+                                        if (count[i] > 0.0f)
+                                            o[t][j][i] = __uint_as_float(0x7fffffffu);
                                 }
-#pragma unroll
-                            for (int j = 0; j < D / 8; ++j) {
-                                const int sh = 8 * (j & 3) + 7;
-                                uint32_t n4[4];
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    n4[k] = (nan_bytes(v[k][j >> 2]) >> sh) & 1u ? one : 0u;
-                                float count[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                                mma_f16(count, seen, n4[0] | n4[1] << 16, n4[2] | n4[3] << 16);
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    if (count[e] > 0.0f)
-                                        o[j][e] = __uint_as_float(0x7fffffffu);
                             }
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
 #pragma unroll
-                                for (int w = 0; w < kW; ++w) {
-                                    const uint32_t z = nan_bytes(v[k][w]);
-                                    v[k][w] &= ~((z >> 7) * 0xffu);
-                                }
+                                for (int w = 0; w < kW; ++w)
+                                    v[k][w] &= ~((nan_bytes(v[k][w]) >> 7) * 0xffu);
                         }
                     }
 #pragma unroll
                     for (int w = 0; w < kW; ++w)
 #pragma unroll
                         for (int pair = 0; pair < 2; ++pair) {
-                            // bytes 2 pair, 2 pair + 1 of two tokens each: {t0, t1} of both columns
+                            // bytes 2 pair, 2 pair + 1 of two tokens each: {token, token} of both elements
                             const uint32_t sel = pair ? 0x7362u : 0x5140u;
-                            const uint32_t x = __byte_perm(v[0][w], v[1][w], sel);
-                            const uint32_t y = __byte_perm(v[2][w], v[3][w], sel);
-                            mma_f16(o[4 * w + 2 * pair], a, e4m3x2_to_half2(x & 0xffffu),
-                                    e4m3x2_to_half2(y & 0xffffu));
-                            mma_f16(o[4 * w + 2 * pair + 1], a, e4m3x2_to_half2(x >> 16),
-                                    e4m3x2_to_half2(y >> 16));
+                            const uint32_t y = __byte_perm(v[0][w], v[1][w], sel);
+                            const uint32_t z = __byte_perm(v[2][w], v[3][w], sel);
+                            const uint32_t a0 = e4m3x2_to_half2(y & 0xffffu), a1 = e4m3x2_to_half2(y >> 16);
+                            const uint32_t a2 = e4m3x2_to_half2(z & 0xffffu), a3 = e4m3x2_to_half2(z >> 16);
+#pragma unroll
+                            for (int t = 0; t < kN; ++t)
+                                mma_f16(o[t][2 * w + pair], a0, a1, a2, a3, pt[t][0], pt[t][1]);
                         }
                 }
                 __syncwarp();
@@ -655,40 +707,42 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnBlocksPerSm)
                     phase ^= 1u;
                 }
             }
+            unit = end;
 
-            // ---- join the four warps: each leaves (O, m, l), then eight threads take a row
+            // ---- join the four warps: each leaves (O, m, l), then 16 / kN threads take a row
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-                l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-                float *row = join + (warp * kRows + g + 8 * i) * G::kPitch;
-                // columns 2c and 2c + 1 of the groups: D / 8 consecutive elements each
+            for (int t = 0; t < kN; ++t)
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
+                for (int e = 0; e < 2; ++e) {
+                    l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 4);
+                    l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 8);
+                    l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 16);
+                    const int row = warp * kRows + 8 * t + 2 * c + e;
+                    float *dst = join + row * G::kPitch + piece_of<D>(g) * (D / 8);
 #pragma unroll
-                    for (int j = 0; j < D / 8; j += 4)
-                        *reinterpret_cast<float4 *>(row + piece_of<D>(2 * c + e) * (D / 8) + j) =
-                            make_float4(o[j][2 * i + e], o[j + 1][2 * i + e], o[j + 2][2 * i + e],
-                                        o[j + 3][2 * i + e]);
-                if (c == 0) {
-                    stat_m[warp * kRows + g + 8 * i] = m[i];
-                    stat_l[warp * kRows + g + 8 * i] = l[i];
+                    for (int j = 0; j < D / 16; j += 2)
+                        *reinterpret_cast<float4 *>(dst + 2 * j) =
+                            make_float4(o[t][j][e], o[t][j][2 + e], o[t][j + 1][e], o[t][j + 1][2 + e]);
+                    if (g == 0) {
+                        stat_m[row] = m[t][e];
+                        stat_l[row] = l[t][e];
+                    }
                 }
-            }
             if (lane == 0)
                 stat_v[warp] = vref / kPShift;
             named_bar_sync(1, 32 * kWarps);
             {
-                const int r = tid >> 3, d0 = (tid & 7) * (D / 8);
+                constexpr int kF = D * kN / 16;   // elements a thread
+                const int r = tid * kN / 16, d0 = tid % (16 / kN) * kF;
                 float top = -INFINITY, sum = 0.0f;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w)
                     top = fmaxf(top, stat_m[w * kRows + r]);
                 const float ref = top == -INFINITY ? 0.0f : top;
-                float x[D / 8];
+                float y[kF];
 #pragma unroll
-                for (int j = 0; j < D / 8; ++j)
-                    x[j] = 0.0f;
+                for (int j = 0; j < kF; ++j)
+                    y[j] = 0.0f;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
                     const float f = exp2_fast(stat_m[w * kRows + r] - ref);
@@ -697,12 +751,12 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnBlocksPerSm)
                     const float4 *src = reinterpret_cast<const float4 *>(
                         join + (w * kRows + r) * G::kPitch + d0);
 #pragma unroll
-                    for (int j = 0; j < D / 32; ++j) {
-                        const float4 y = src[j];
-                        x[4 * j] += fv * y.x;
-                        x[4 * j + 1] += fv * y.y;
-                        x[4 * j + 2] += fv * y.z;
-                        x[4 * j + 3] += fv * y.w;
+                    for (int j = 0; j < kF / 4; ++j) {
+                        const float4 z = src[j];
+                        y[4 * j] += fv * z.x;
+                        y[4 * j + 1] += fv * z.y;
+                        y[4 * j + 2] += fv * z.z;
+                        y[4 * j + 3] += fv * z.w;
                     }
                 }
                 if (alive && seg0 >= start && seg1 <= stop) {
@@ -712,12 +766,10 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnBlocksPerSm)
                         const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
                         uint16_t *dst = p.out + out_row(p, b, h, row) * D + d0;
 #pragma unroll
-                        for (int j = 0; j < D / 8; j += 8)
-                            *reinterpret_cast<uint4 *>(dst + j) = make_uint4(
-                                pack_out<kBf16>(x[j] * inv, x[j + 1] * inv),
-                                pack_out<kBf16>(x[j + 2] * inv, x[j + 3] * inv),
-                                pack_out<kBf16>(x[j + 4] * inv, x[j + 5] * inv),
-                                pack_out<kBf16>(x[j + 6] * inv, x[j + 7] * inv));
+                        for (int j = 0; j < kF; j += 4)
+                            *reinterpret_cast<uint2 *>(dst + j) =
+                                make_uint2(pack_out<kBf16>(y[j] * inv, y[j + 1] * inv),
+                                           pack_out<kBf16>(y[j + 2] * inv, y[j + 3] * inv));
                         if (kScores && d0 == 0)
                             p.lse[((int64_t)b * p.pool.kv_heads + h) * p.rows + row] =
                                 sum == 0.0f ? INFINITY : ref + log2f(sum);
@@ -727,8 +779,8 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnBlocksPerSm)
                     const int64_t at = ((int64_t)blockIdx.x * 2 + (seg0 > start ? 1 : 0)) * kRows + r;
                     float *dst = p.partial + at * D + d0;
 #pragma unroll
-                    for (int j = 0; j < D / 8; j += 4)
-                        *reinterpret_cast<float4 *>(dst + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+                    for (int j = 0; j < kF; j += 4)
+                        *reinterpret_cast<float4 *>(dst + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
                     if (d0 == 0)
                         *reinterpret_cast<float2 *>(p.partial + (int64_t)p.grid * 2 * kRows * D + at * 2) =
                             make_float2(top, sum);
@@ -746,8 +798,9 @@ constexpr int kJoinThreads = 128;
 // One block per (sequence, head, row): joins the partials of the blocks that the row's
 // (sequence, head, row tile) was cut between, in their order; 0 for a row of a sequence
 // without tokens.
-template <int D, bool kBf16, bool kScores>
+template <int D, int kN, bool kBf16, bool kScores>
 __global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const AttnParams p) {
+    constexpr int kRows = 8 * kN;
     __shared__ float wide[kJoinThreads / 32][2];
     __shared__ float acc[kJoinThreads / 32][D];
     pdl_launch_dependents();

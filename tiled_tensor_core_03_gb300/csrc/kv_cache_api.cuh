@@ -104,7 +104,9 @@ struct AttnSpace {
 AttnSpace attention_space(int64_t batch, int64_t rows, int64_t kv_heads, int64_t head_dim,
                           int64_t weights_width, int sms) {
     AttnSpace a{};
-    size_t at = (size_t)sms * KC::kAttnBlocksPerSm * 2 * KC::kRows * (head_dim + 2) * 4;
+    const size_t slots = 2 * (size_t)sms * std::max(KC::AttnCfg<128, 1>::kBlocksPerSm * 8,
+                                                    KC::AttnCfg<128, 2>::kBlocksPerSm * 16);
+    size_t at = slots * (head_dim + 2) * 4;
     a.before = at = round256(at);
     at += (size_t)(batch + 1) * 8;
     a.lse = at = round256(at);
@@ -127,17 +129,20 @@ bool attention_sizes_ok(int64_t batch, int64_t tokens, int64_t q_heads, int64_t 
            batch * kv_heads * (tokens * (q_heads / kv_heads)) <= kMaxGrid;
 }
 
-template <int D, bool kBf16, bool kScores>
-int launch_kv_attention(const CUtensorMap &mK, const CUtensorMap &mV, const KC::AttnParams &p,
-                        cudaStream_t s, bool &attr_done) {
-    using G = KC::AttnCfg<D>;
-    auto kern = KC::kv_attention_kernel<D, kBf16, kScores>;
+template <int D, int kN, bool kBf16, bool kScores>
+int launch_kv_attention(const CUtensorMap &mK, const CUtensorMap &mV, KC::AttnParams &p,
+                        cudaStream_t s, int sms, bool *attr) {
+    using G = KC::AttnCfg<D, kN>;
+    auto kern = KC::kv_attention_kernel<D, kN, kBf16, kScores>;
+    bool &attr_done = attr[(D == 128 ? 8 : 0) + (kN == 2 ? 4 : 0) + (kBf16 ? 2 : 0) + (kScores ? 1 : 0)];
     if (!ensure_smem_attr(attr_done, kern, G::kSmem))
         return GEMMRELU_ERR_LAUNCH;
+    p.row_tiles = (p.rows + G::kRows - 1) / G::kRows;
+    p.grid = sms * G::kBlocksPerSm;
     int rc = launch_kernel(kern, (unsigned)p.grid, KC::kAttnThreads, G::kSmem, s, false, 1u, mK, mV, p);
     if (rc != GEMMRELU_OK)
         return rc;
-    rc = launch_kv(KC::kv_attention_join_kernel<D, kBf16, kScores>,
+    rc = launch_kv(KC::kv_attention_join_kernel<D, kN, kBf16, kScores>,
                    (int64_t)p.batch * p.pool.kv_heads * p.rows, KC::kJoinThreads, s, p);
     if (rc != GEMMRELU_OK || !kScores)
         return rc;
@@ -146,14 +151,14 @@ int launch_kv_attention(const CUtensorMap &mK, const CUtensorMap &mV, const KC::
                      KC::kWeightThreads, s, p);
 }
 
-template <int D>
-int launch_kv_attention_as(bool bf16, bool scores, const CUtensorMap &mK, const CUtensorMap &mV,
-                           const KC::AttnParams &p, cudaStream_t s, bool *attr) {
-    if (scores)
-        return bf16 ? launch_kv_attention<D, true, true>(mK, mV, p, s, attr[0])
-                    : launch_kv_attention<D, false, true>(mK, mV, p, s, attr[1]);
-    return bf16 ? launch_kv_attention<D, true, false>(mK, mV, p, s, attr[2])
-                : launch_kv_attention<D, false, false>(mK, mV, p, s, attr[3]);
+template <int D, int kN>
+int launch_kv_attention_as(bool bf16, const CUtensorMap &mK, const CUtensorMap &mV, KC::AttnParams &p,
+                           cudaStream_t s, int sms, bool *attr) {
+    if (p.weights)
+        return bf16 ? launch_kv_attention<D, kN, true, true>(mK, mV, p, s, sms, attr)
+                    : launch_kv_attention<D, kN, false, true>(mK, mV, p, s, sms, attr);
+    return bf16 ? launch_kv_attention<D, kN, true, false>(mK, mV, p, s, sms, attr)
+                : launch_kv_attention<D, kN, false, false>(mK, mV, p, s, sms, attr);
 }
 
 }  // namespace
@@ -314,11 +319,9 @@ int kv_cache_attention_x16(const kv_cache_pool *cache, const void *q, int dtype,
     p.q_heads = (int)q_heads;
     p.group = (int)(q_heads / cache->kv_heads);
     p.rows = (int)rows;
-    p.row_tiles = (int)((rows + KC::kRows - 1) / KC::kRows);
     p.window = (int)std::min<int64_t>(window, kMaxTokens);
     p.sinks = (int)std::min<int64_t>(sinks, kMaxTokens);
     p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)cache->head_dim));
-    p.grid = ds->sms * KC::kAttnBlocksPerSm;
     p.partial = reinterpret_cast<float *>(ws);
     p.before = reinterpret_cast<int64_t *>(ws + sp.before);
     if (weights) {
@@ -331,9 +334,12 @@ int kv_cache_attention_x16(const kv_cache_pool *cache, const void *q, int dtype,
     p.wait_limit_ns = wait_limit_ns();
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool bf16 = dtype == GEMMRELU_BF16;
-    return cache->head_dim == 64
-               ? launch_kv_attention_as<64>(bf16, weights != nullptr, mK, mV, p, s, ds->attr_kv)
-               : launch_kv_attention_as<128>(bf16, weights != nullptr, mK, mV, p, s, ds->attr_kv + 4);
+    // up to 8 rows fit one group of 8; two groups share the conversion of K and V
+    if (cache->head_dim == 64)
+        return rows <= 8 ? launch_kv_attention_as<64, 1>(bf16, mK, mV, p, s, ds->sms, ds->attr_kv)
+                         : launch_kv_attention_as<64, 2>(bf16, mK, mV, p, s, ds->sms, ds->attr_kv);
+    return rows <= 8 ? launch_kv_attention_as<128, 1>(bf16, mK, mV, p, s, ds->sms, ds->attr_kv)
+                     : launch_kv_attention_as<128, 2>(bf16, mK, mV, p, s, ds->sms, ds->attr_kv);
 }
 
 int kv_cache_debug_span(int64_t length, int64_t tokens, int64_t window, int64_t sinks, int *out) {
