@@ -14,9 +14,9 @@
 //    units of all of them, in order, are dealt to the blocks in equal contiguous
 //    ranges whatever the lengths are.  A block finishes what lies
 //    inside its range; a (sequence, head, row tile) that is cut leaves one fp32
-//    partial (O, m, l) per block in the workspace, and a second kernel joins them in
-//    order.  Nothing depends on the order in which blocks run: the same call gives
-//    the same bits.
+//    partial (O, m, l) per block in the workspace, and the block that comes last joins
+//    them, in the order of the ranges.  No block waits for another and nothing depends on
+//    the order in which they come: the same call gives the same bits.
 //  - One warp feeds a ring of 64-token stages by TMA (a page or a part of one per
 //    copy), reading page numbers and scales 32 pieces ahead.
 //  - Four warps take 16 tokens of a stage each.  The products run on mma.sync.m16n8k16
@@ -81,7 +81,8 @@ struct AttnParams {
     float scale_log2;                  // log2(e) / sqrt(D)
     float *partial;                    // [2 * grid][kRows][D], then [2 * grid][kRows][2] (m, l)
     int grid;
-    int64_t *before;                   // [batch + 1] units of the sequences before
+    unsigned long long *arrived;       // [batch][kv_heads][row_tiles] parts that are there, tagged
+    unsigned long long epoch;          // this call's tag: a multiple of 1024, never 0
     float *scores;                     // with weights: [batch][kv_heads][width][rows], base 2
     float *lse;                        //               [batch][kv_heads][rows], base 2
     float *weights;                    // [batch][kv_heads][width]
@@ -131,12 +132,26 @@ __device__ __forceinline__ int length_of(const AttnParams &p, int b) {
     return checked_length(p.lengths, b, p.max_pages * p.pool.page);
 }
 
-// First unit of block c of `grid`, of `total`: equal ranges, and the block that owns unit x.
+// First unit of block c of `grid`, of `total`: equal ranges (the first ones one unit
+// longer), and the block that owns unit x.
 __host__ __device__ __forceinline__ int64_t range_start(int64_t c, int64_t total, int grid) {
-    return c * total / grid;
+    const int64_t q = total / grid, r = total % grid;
+    return c * q + (c < r ? c : r);
 }
 __host__ __device__ __forceinline__ int range_owner(int64_t x, int64_t total, int grid) {
-    return (int)(((x + 1) * grid - 1) / total);
+    const int64_t q = total / grid, r = total % grid, longer = r * (q + 1);
+    return (int)(x < longer ? x / (q + 1) : r + (x - longer) / q);
+}
+
+// How many of the launched blocks work: each takes a unit at least, and a (sequence, head,
+// row tile) is cut into about sqrt(8 units) parts at most.  A part costs its block's start
+// and, in the join, a read of its O by one block; a unit in sequence costs its copy.
+__device__ __forceinline__ int blocks_used(int64_t total, int64_t segments, int grid) {
+    const float most = sqrtf(8.0f * (float)total * (float)segments);
+    int64_t n = total < grid ? total : grid;
+    if (most < (float)n)
+        n = (int64_t)most;
+    return (int)(n > 1 ? n : 1);
 }
 
 // ---------------------------------------------------------------- layouts
@@ -280,7 +295,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (uint32_t s = 0; s < (uint32_t)G::kStages; ++s) {
-            mbar_init(full(s), 1u);
+            mbar_init(full(s), 2u);   // the copies, and the scales
             mbar_init(empty(s), kWarps);
         }
         *abort_flag = 0u;
@@ -326,24 +341,32 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
     }
     __syncthreads();
     const int64_t total = scan[kAttnThreads] * per_seq;
-    const int64_t start = range_start(blockIdx.x, total, p.grid);
-    const int64_t stop = range_start(blockIdx.x + 1, total, p.grid);
+    const int blocks = blocks_used(total, (int64_t)p.batch * per_seq, p.grid);
+    const int64_t start = (int)blockIdx.x < blocks ? range_start(blockIdx.x, total, blocks) : total;
+    const int64_t stop = (int)blockIdx.x < blocks ? range_start(blockIdx.x + 1, total, blocks) : total;
     {
-        int64_t at = scan[tid];
+        int64_t at = scan[tid] * per_seq;
         for (int b = b0; b < b1; ++b) {
-            const int64_t u = span_of(length_of(p, b), p.tokens, p.window, p.sinks).units;
-            if (blockIdx.x == 0)
-                p.before[b] = at;
-            if (start < stop && start >= at * per_seq && start < (at + u) * per_seq) {
+            const int64_t u = (int64_t)span_of(length_of(p, b), p.tokens, p.window, p.sinks).units * per_seq;
+            if (start < stop && start >= at && start < at + u) {
                 scan[kAttnThreads + 1] = b;
-                scan[kAttnThreads + 2] = at * per_seq;
+                scan[kAttnThreads + 2] = at;
             }
             at += u;
         }
-        if (blockIdx.x == 0 && tid == 0)
-            p.before[p.batch] = scan[kAttnThreads];
     }
     __syncthreads();
+    // sequences without tokens
+    for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
+        if (length_of(p, b) > 0)
+            continue;
+        uint4 *dst = reinterpret_cast<uint4 *>(p.out + (int64_t)b * p.tokens * p.q_heads * D);
+        for (int i = tid; i < p.tokens * p.q_heads * (D / 8); i += kAttnThreads)
+            dst[i] = make_uint4(0, 0, 0, 0);
+        if (kScores)
+            for (int i = tid; i < p.rows * p.pool.kv_heads; i += kAttnThreads)
+                p.lse[(int64_t)b * p.pool.kv_heads * p.rows + i] = INFINITY;   // no token has a weight
+    }
     int b = (int)scan[kAttnThreads + 1];
     int64_t seq_at = scan[kAttnThreads + 2];   // first unit of sequence b
 
@@ -400,9 +423,6 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
                     break;
                 }
                 const bool in = lane / pieces == i;
-                if (in)
-                    for (int s = 0; s < piece_tokens / 16; ++s)
-                        meta[stage * 4 + (lane % pieces) * (piece_tokens / 16) + s] = make_float2(ks, vs);
                 const uint32_t copies = __popc(__ballot_sync(0xffffffffu, in && id >= 0));
                 if (lane == 0)
                     mbar_arrive_expect_tx(full(stage), copies * 2u * piece_tokens * D);
@@ -412,6 +432,12 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
                     tma_load_4d(&tmK, base + G::kOffK + off, full(stage), 0, slot, h, id);
                     tma_load_4d(&tmV, base + G::kOffV + off, full(stage), 0, slot, h, id);
                 }
+                if (in)
+                    for (int s = 0; s < piece_tokens / 16; ++s)
+                        meta[stage * 4 + (lane % pieces) * (piece_tokens / 16) + s] = make_float2(ks, vs);
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(full(stage));
                 issued |= 1u << stage;
                 parity = (parity & ~(1u << stage)) | (phase << stage);
                 if (++stage == (uint32_t)G::kStages) {
@@ -759,120 +785,89 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
                         y[4 * j + 3] += fv * z.w;
                     }
                 }
-                if (alive && seg0 >= start && seg1 <= stop) {
-                    // the whole of it: the result
-                    const int row = row0 + r;
-                    if (row < p.rows) {
-                        const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-                        uint16_t *dst = p.out + out_row(p, b, h, row) * D + d0;
-#pragma unroll
-                        for (int j = 0; j < kF; j += 4)
-                            *reinterpret_cast<uint2 *>(dst + j) =
-                                make_uint2(pack_out<kBf16>(y[j] * inv, y[j + 1] * inv),
-                                           pack_out<kBf16>(y[j + 2] * inv, y[j + 3] * inv));
-                        if (kScores && d0 == 0)
-                            p.lse[((int64_t)b * p.pool.kv_heads + h) * p.rows + row] =
-                                sum == 0.0f ? INFINITY : ref + log2f(sum);
-                    }
-                } else if (alive) {
+                const int row = row0 + r;
+                bool finish = seg0 >= start && seg1 <= stop;   // the whole of it
+                if (!finish) {
                     // a part: slot 0 where it starts this block's range, else slot 1
+                    const int64_t stats = (int64_t)p.grid * 2 * kRows * D;
                     const int64_t at = ((int64_t)blockIdx.x * 2 + (seg0 > start ? 1 : 0)) * kRows + r;
                     float *dst = p.partial + at * D + d0;
 #pragma unroll
                     for (int j = 0; j < kF; j += 4)
                         *reinterpret_cast<float4 *>(dst + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
                     if (d0 == 0)
-                        *reinterpret_cast<float2 *>(p.partial + (int64_t)p.grid * 2 * kRows * D + at * 2) =
-                            make_float2(top, sum);
+                        *reinterpret_cast<float2 *>(p.partial + stats + at * 2) = make_float2(top, sum);
+                    __threadfence();
+                    named_bar_sync(1, 32 * kWarps);
+                    const int c0 = range_owner(seg0, total, blocks), c1 = range_owner(seg1 - 1, total, blocks);
+                    if (tid == 0) {
+                        // count this part; the word returns to 0 with the last one.  Words of
+                        // another call or of memory never used carry another tag.
+                        unsigned long long *word = p.arrived + ((int64_t)b * p.pool.kv_heads + h) * p.row_tiles + tile;
+                        unsigned long long cur = atomicAdd(word, 0ull), was;
+                        bool last;
+                        do {
+                            was = cur;
+                            const unsigned long long before = (was & ~1023ull) == p.epoch ? (was & 1023ull) : 0ull;
+                            last = before + 1 == (unsigned long long)(c1 - c0 + 1);
+                            cur = atomicCAS(word, was, last ? 0ull : p.epoch + before + 1);
+                        } while (cur != was);
+                        __threadfence();
+                        stat_v[0] = last ? 1.0f : 0.0f;
+                    }
+                    named_bar_sync(1, 32 * kWarps);
+                    finish = stat_v[0] != 0.0f;
+                    if (finish) {
+                        // all parts, in the order of their blocks
+                        auto slot_of = [&](int c) {
+                            return ((int64_t)c * 2 + (seg0 > range_start(c, total, blocks) ? 1 : 0)) * kRows + r;
+                        };
+                        // only the first part can start inside its block's range
+                        const int64_t first = slot_of(c0);
+                        auto slot = [&](int c) { return c == c0 ? first : (int64_t)c * 2 * kRows + r; };
+                        float high = -INFINITY;
+#pragma unroll 4
+                        for (int c = c0; c <= c1; ++c)
+                            high = fmaxf(high, __ldcg(p.partial + stats + slot(c) * 2));
+                        const float base2 = high == -INFINITY ? 0.0f : high;
+                        sum = 0.0f;
+#pragma unroll
+                        for (int j = 0; j < kF; ++j)
+                            y[j] = 0.0f;
+#pragma unroll 4
+                        for (int c = c0; c <= c1; ++c) {
+                            const int64_t k = slot(c);
+                            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.partial + stats + k * 2));
+                            const float f = exp2_fast(ml.x - base2);
+                            sum += f * ml.y;
+#pragma unroll
+                            for (int j = 0; j < kF; j += 4) {
+                                const float4 z = __ldcg(reinterpret_cast<const float4 *>(p.partial + k * D + d0 + j));
+                                y[j] += f * z.x;
+                                y[j + 1] += f * z.y;
+                                y[j + 2] += f * z.z;
+                                y[j + 3] += f * z.w;
+                            }
+                        }
+                        top = base2;
+                    }
+                }
+                if (alive && finish && row < p.rows) {
+                    const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+                    uint16_t *dst = p.out + out_row(p, b, h, row) * D + d0;
+#pragma unroll
+                    for (int j = 0; j < kF; j += 4)
+                        *reinterpret_cast<uint2 *>(dst + j) =
+                            make_uint2(pack_out<kBf16>(y[j] * inv, y[j + 1] * inv),
+                                       pack_out<kBf16>(y[j + 2] * inv, y[j + 3] * inv));
+                    if (kScores && d0 == 0)
+                        p.lse[((int64_t)b * p.pool.kv_heads + h) * p.rows + row] =
+                            sum == 0.0f ? INFINITY : (top == -INFINITY ? 0.0f : top) + log2f(sum);
                 }
             }
             named_bar_sync(1, 32 * kWarps);
         }
     }
-}
-
-// ---------------------------------------------------------------- joining the parts
-
-constexpr int kJoinThreads = 128;
-
-// One block per (sequence, head, row): joins the partials of the blocks that the row's
-// (sequence, head, row tile) was cut between, in their order; 0 for a row of a sequence
-// without tokens.
-template <int D, int kN, bool kBf16, bool kScores>
-__global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const AttnParams p) {
-    constexpr int kRows = 8 * kN;
-    __shared__ float wide[kJoinThreads / 32][2];
-    __shared__ float acc[kJoinThreads / 32][D];
-    pdl_launch_dependents();
-    pdl_wait_primary();
-    int64_t i = blockIdx.x;
-    const int row = (int)(i % p.rows);
-    i /= p.rows;
-    const int h = (int)(i % p.pool.kv_heads), b = (int)(i / p.pool.kv_heads);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int64_t at = p.before[b], units = p.before[b + 1] - at;
-    const int per_seq = p.pool.kv_heads * p.row_tiles;
-    const int64_t total = p.before[p.batch] * per_seq;
-    const int64_t seg0 = at * per_seq + (h * p.row_tiles + row / kRows) * units, seg1 = seg0 + units;
-    uint16_t *dst = p.out + out_row(p, b, h, row) * D;
-    float *lse = kScores ? p.lse + ((int64_t)b * p.pool.kv_heads + h) * p.rows + row : nullptr;
-    if (units == 0) {
-        for (int d = tid; d < D; d += kJoinThreads)
-            dst[d] = 0;
-        if (kScores && tid == 0)
-            *lse = INFINITY;   // no token has a weight
-        return;
-    }
-    const int c0 = range_owner(seg0, total, p.grid), c1 = range_owner(seg1 - 1, total, p.grid);
-    if (c0 == c1)
-        return;   // one block had all of it
-    const float *stats = p.partial + (int64_t)p.grid * 2 * kRows * D;
-    auto slot_of = [&](int c) -> int64_t {   // -1: a block without units
-        const int64_t lo = range_start(c, total, p.grid), hi = range_start(c + 1, total, p.grid);
-        return lo == hi ? -1 : ((int64_t)c * 2 + (seg0 > lo ? 1 : 0)) * kRows + row % kRows;
-    };
-    float top = -INFINITY;
-    for (int c = c0 + tid; c <= c1; c += kJoinThreads) {
-        const int64_t s = slot_of(c);
-        if (s >= 0)
-            top = fmaxf(top, stats[s * 2]);
-    }
-    for (int o = 16; o; o >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0)
-        wide[warp][0] = top;
-    __syncthreads();
-    top = fmaxf(fmaxf(wide[0][0], wide[1][0]), fmaxf(wide[2][0], wide[3][0]));
-    const float ref = top == -INFINITY ? 0.0f : top;
-    // warp w takes the parts c0 + w, c0 + w + 4, ...; then the four sums in order
-    float x[D / 32], sum = 0.0f;
-#pragma unroll
-    for (int j = 0; j < D / 32; ++j)
-        x[j] = 0.0f;
-    for (int c = c0 + warp; c <= c1; c += kJoinThreads / 32) {
-        const int64_t s = slot_of(c);
-        if (s < 0)
-            continue;
-        const float f = exp2_fast(stats[s * 2] - ref);
-        sum += f * stats[s * 2 + 1];
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j)
-            x[j] += f * p.partial[s * D + 32 * j + lane];
-    }
-#pragma unroll
-    for (int j = 0; j < D / 32; ++j)
-        acc[warp][32 * j + lane] = x[j];
-    if (lane == 0)
-        wide[warp][1] = sum;
-    __syncthreads();
-    sum = (wide[0][1] + wide[1][1]) + (wide[2][1] + wide[3][1]);
-    const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-    for (int d = tid; d < D; d += kJoinThreads) {
-        const float y = ((acc[0][d] + acc[1][d]) + (acc[2][d] + acc[3][d])) * inv;
-        dst[d] = (uint16_t)(pack_out<kBf16>(y, 0.0f) & 0xffffu);
-    }
-    if (kScores && tid == 0)
-        *lse = sum == 0.0f ? INFINITY : ref + log2f(sum);
 }
 
 // weights[t] += sum over the rows that see t of softmax_t, from the scores and each row's

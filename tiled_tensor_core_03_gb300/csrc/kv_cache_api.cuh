@@ -95,11 +95,23 @@ bool make_pool_map(CUtensorMap *map, const void *ptr, const kv_cache_pool *c, ui
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Workspace of kv_cache_attention_x16: partials, unit counts, and with weights every
-// row's log-sum-exp and scores.
+// Workspace of kv_cache_attention_x16: partials, a word per (sequence, head, row tile), and with
+// weights every row's log-sum-exp and scores.
 struct AttnSpace {
-    size_t before, lse, scores, total;   // byte offsets; partials at 0
+    size_t arrived, lse, scores, total;   // byte offsets; partials at 0
 };
+
+// Tags of kv_cache_attention_x16 calls: 54 bits that start at random and count up, never 0, so
+// that no word left in reused memory carries the tag of a later call.
+std::atomic<uint64_t> g_kv_epoch{(uint64_t)std::random_device{}() << 20};
+
+unsigned long long next_kv_epoch() {
+    for (;;) {
+        const uint64_t e = (++g_kv_epoch) << 10;
+        if (e)
+            return e;
+    }
+}
 
 AttnSpace attention_space(int64_t batch, int64_t rows, int64_t kv_heads, int64_t head_dim,
                           int64_t weights_width, int sms) {
@@ -107,8 +119,8 @@ AttnSpace attention_space(int64_t batch, int64_t rows, int64_t kv_heads, int64_t
     const size_t slots = 2 * (size_t)sms * std::max(KC::AttnCfg<128, 1>::kBlocksPerSm * 8,
                                                     KC::AttnCfg<128, 2>::kBlocksPerSm * 16);
     size_t at = slots * (head_dim + 2) * 4;
-    a.before = at = round256(at);
-    at += (size_t)(batch + 1) * 8;
+    a.arrived = at = round256(at);
+    at += (size_t)batch * kv_heads * ((rows + 7) / 8) * 8;
     a.lse = at = round256(at);
     if (weights_width > 0) {
         at += (size_t)batch * kv_heads * rows * 4;
@@ -139,11 +151,7 @@ int launch_kv_attention(const CUtensorMap &mK, const CUtensorMap &mV, KC::AttnPa
         return GEMMRELU_ERR_LAUNCH;
     p.row_tiles = (p.rows + G::kRows - 1) / G::kRows;
     p.grid = sms * G::kBlocksPerSm;
-    int rc = launch_kernel(kern, (unsigned)p.grid, KC::kAttnThreads, G::kSmem, s, false, 1u, mK, mV, p);
-    if (rc != GEMMRELU_OK)
-        return rc;
-    rc = launch_kv(KC::kv_attention_join_kernel<D, kN, kBf16, kScores>,
-                   (int64_t)p.batch * p.pool.kv_heads * p.rows, KC::kJoinThreads, s, p);
+    const int rc = launch_kernel(kern, (unsigned)p.grid, KC::kAttnThreads, G::kSmem, s, false, 1u, mK, mV, p);
     if (rc != GEMMRELU_OK || !kScores)
         return rc;
     const int64_t blocks = (p.width + KC::kWeightThreads - 1) / KC::kWeightThreads;
@@ -323,7 +331,8 @@ int kv_cache_attention_x16(const kv_cache_pool *cache, const void *q, int dtype,
     p.sinks = (int)std::min<int64_t>(sinks, kMaxTokens);
     p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)cache->head_dim));
     p.partial = reinterpret_cast<float *>(ws);
-    p.before = reinterpret_cast<int64_t *>(ws + sp.before);
+    p.arrived = reinterpret_cast<unsigned long long *>(ws + sp.arrived);
+    p.epoch = next_kv_epoch();
     if (weights) {
         p.lse = reinterpret_cast<float *>(ws + sp.lse);
         p.scores = reinterpret_cast<float *>(ws + sp.scores);
