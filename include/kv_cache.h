@@ -46,6 +46,8 @@
 extern "C" {
 #endif
 
+#define GEMMRELU_KV_COUNTER_BYTES 4096   /* of kv_cache_attention_x16's workspace */
+
 typedef struct {
     void *k, *v;               /* e4m3 [num_pages][kv_heads][page][head_dim], 16-byte aligned */
     float *k_scale, *v_scale;  /* [num_pages][kv_heads] */
@@ -102,8 +104,12 @@ size_t kv_cache_attention_x16_workspace_bytes(int64_t batch, int64_t tokens, int
  *            sum, over the query tokens and the head's group of query heads,
  *            of the softmax weight of token t; weights_width >= max_pages * page.
  * workspace: at least kv_cache_attention_x16_workspace_bytes(...), 16-byte
- *            aligned, no initialisation; calls that may overlap on the GPU need
- *            different ones.
+ *            aligned.  Its first GEMMRELU_KV_COUNTER_BYTES must be 0 before its
+ *            first call; every call leaves them 0, whatever its sizes.  Calls
+ *            that may overlap on the GPU need different workspaces.
+ *
+ * Sizes whose 64-token units, batch * kv_heads * ceil(tokens * group / 8) *
+ * ceil(max_pages * page / 64), reach 2^31 are refused.
  *
  * Scores, softmax statistics and sums are fp32, the softmax weights are rounded
  * to fp16 for the product with V.  The order of all sums is fixed: the same call
@@ -153,7 +159,7 @@ int kv_cache_evict_e4m3(const kv_cache_pool *cache, const float *weights, int64_
  * invalid arguments.
  */
 int kv_cache_debug_span(int64_t length, int64_t tokens, int64_t window, int64_t sinks, int *out);
-int64_t kv_cache_debug_range(int64_t x, int64_t total, int grid, int owner);
+int kv_cache_debug_range(int x, int total, int grid, int owner);
 
 #ifdef __cplusplus
 }

@@ -445,10 +445,12 @@ def test_cache_attention_workspace_and_errors():
     pages, lengths = _i32([[0, 1], [2, 3]]), _i32([20, 31])
     ws = gr.kv_cache_attention_workspace(q, cache)
     guard = torch.full((ws.numel() + 512,), 0x5a, dtype=torch.uint8, device="cuda")
+    guard[256:256 + gr.KV_COUNTER_BYTES] = 0
     out = torch.full_like(q, 7.0)
     got = gr.kv_cache_attention(q, cache, pages, lengths, out=out, workspace=guard[256:-256])
     assert got is out
     assert (guard[:256] == 0x5a).all() and (guard[-256:] == 0x5a).all()
+    assert (guard[256:256 + gr.KV_COUNTER_BYTES] == 0).all()       # left as they were found
     assert torch.equal(out, gr.kv_cache_attention(q, cache, pages, lengths))
     with pytest.raises(gr.GemmReluError) as e:
         gr.kv_cache_attention(q, cache, pages, lengths, workspace=ws[:-256])

@@ -26,6 +26,7 @@ ERR_SCRATCH_LIMIT = 7
 ERR_PAGE = 8
 NOALLOC_SCRATCH_BYTES = 8 << 20
 F16, BF16 = 0, 1   # types of 16-bit tensors
+KV_COUNTER_BYTES = 4096   # zeroed once in kv_cache_attention's workspaces
 
 PATH_NONE, PATH_TMA, PATH_LSU = 0, 1, 2
 (KERNEL_PAIR, KERNEL_ONE_CTA_256, KERNEL_ONE_CTA_128, KERNEL_PREDICATED, KERNEL_GEMV,
@@ -92,8 +93,8 @@ def lib():
         L.flash_attention_window_debug_blocks.restype = i32
         L.kv_cache_debug_span.argtypes = [i64] * 4 + [vp]
         L.kv_cache_debug_span.restype = i32
-        L.kv_cache_debug_range.argtypes = [i64, i64, i32, i32]
-        L.kv_cache_debug_range.restype = i64
+        L.kv_cache_debug_range.argtypes = [i32, i32, i32, i32]
+        L.kv_cache_debug_range.restype = i32
         L.kv_cache_append_x16.argtypes = [vp, vp, vp, i32, i64, i64, vp, vp, vp, i64, vp, vp, vp]
         L.kv_cache_append_x16.restype = i32
         L.kv_cache_attention_x16_workspace_bytes.argtypes = [i64] * 6

@@ -16,7 +16,9 @@
 //    inside its range; a (sequence, head, row tile) that is cut leaves one fp32
 //    partial (O, m, l) per block in the workspace, and the block that comes last joins
 //    them, in the order of the ranges.  No block waits for another and nothing depends on
-//    the order in which they come: the same call gives the same bits.
+//    the order in which they come: the same call gives the same bits.  Parts are counted and
+//    joined after a block's last unit: done where they arise, between two segments, a
+//    block's copies stood still for up to 10 us.
 //  - One warp feeds a ring of 64-token stages by TMA (a page or a part of one per
 //    copy), reading page numbers and scales 32 pieces ahead.
 //  - Four warps take 16 tokens of a stage each.  The products run on mma.sync.m16n8k16
@@ -63,7 +65,7 @@ struct AttnCfg {
     static constexpr uint32_t kOffStat = kOffJoin + kWarps * kRows * kPitch * 4;   // m, l [4][kRows], vref [4]
     static constexpr uint32_t kOffMeta = kOffStat + (2 * kWarps * kRows + kWarps) * 4;
     static constexpr uint32_t kOffScan = kOffMeta + kStages * 4 * 8;   // (ks, vs) per 16 tokens
-    static constexpr uint32_t kOffBar = kOffScan + (kAttnThreads + 8) * 8;
+    static constexpr uint32_t kOffBar = kOffScan + 16 * 4;
     static constexpr uint32_t kOffMisc = kOffBar + 2 * kStages * 8;
     static constexpr uint32_t kSmem = kOffMisc + 16 + 1024;
 };
@@ -81,8 +83,8 @@ struct AttnParams {
     float scale_log2;                  // log2(e) / sqrt(D)
     float *partial;                    // [2 * grid][kRows][D], then [2 * grid][kRows][2] (m, l)
     int grid;
-    unsigned long long *arrived;       // [batch][kv_heads][row_tiles] parts that are there, tagged
-    unsigned long long epoch;          // this call's tag: a multiple of 1024, never 0
+    unsigned *arrived;                 // [grid] parts that are there of the segment that leaves
+                                       // block i; all 0 between calls
     float *scores;                     // with weights: [batch][kv_heads][width][rows], base 2
     float *lse;                        //               [batch][kv_heads][rows], base 2
     float *weights;                    // [batch][kv_heads][width]
@@ -133,25 +135,25 @@ __device__ __forceinline__ int length_of(const AttnParams &p, int b) {
 }
 
 // First unit of block c of `grid`, of `total`: equal ranges (the first ones one unit
-// longer), and the block that owns unit x.
-__host__ __device__ __forceinline__ int64_t range_start(int64_t c, int64_t total, int grid) {
-    const int64_t q = total / grid, r = total % grid;
+// longer), and the block that owns unit x.  (The host keeps the units of a call below 2^31.)
+__host__ __device__ __forceinline__ int range_start(int c, int total, int grid) {
+    const int q = total / grid, r = total % grid;
     return c * q + (c < r ? c : r);
 }
-__host__ __device__ __forceinline__ int range_owner(int64_t x, int64_t total, int grid) {
-    const int64_t q = total / grid, r = total % grid, longer = r * (q + 1);
-    return (int)(x < longer ? x / (q + 1) : r + (x - longer) / q);
+__host__ __device__ __forceinline__ int range_owner(int x, int total, int grid) {
+    const int q = total / grid, r = total % grid, longer = r * (q + 1);
+    return x < longer ? x / (q + 1) : r + (x - longer) / q;
 }
 
 // How many of the launched blocks work: each takes a unit at least, and a (sequence, head,
 // row tile) is cut into about sqrt(8 units) parts at most.  A part costs its block's start
 // and, in the join, a read of its O by one block; a unit in sequence costs its copy.
-__device__ __forceinline__ int blocks_used(int64_t total, int64_t segments, int grid) {
+__device__ __forceinline__ int blocks_used(int total, int segments, int grid) {
     const float most = sqrtf(8.0f * (float)total * (float)segments);
-    int64_t n = total < grid ? total : grid;
+    int n = total < grid ? total : grid;
     if (most < (float)n)
-        n = (int64_t)most;
-    return (int)(n > 1 ? n : 1);
+        n = (int)most;
+    return n > 1 ? n : 1;
 }
 
 // ---------------------------------------------------------------- layouts
@@ -273,6 +275,32 @@ __device__ __forceinline__ int64_t out_row(const AttnParams &p, int b, int h, in
     return ((int64_t)b * p.tokens + row / p.group) * p.q_heads + h * p.group + row % p.group;
 }
 
+// kF elements of a row of the result from their sum y and the row's sum of weights, relative
+// to the reference ref; with scores also the row's log-sum-exp.
+template <int D, int kF, bool kBf16, bool kScores>
+__device__ __forceinline__ void write_row(const AttnParams &p, int b, int h, int row, int d0,
+                                          const float (&y)[kF], float ref, float sum) {
+    const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;   // 0: the row sees nothing
+    uint16_t *dst = p.out + out_row(p, b, h, row) * D + d0;
+#pragma unroll
+    for (int j = 0; j < kF; j += 4)
+        *reinterpret_cast<uint2 *>(dst + j) =
+            make_uint2(pack_out<kBf16>(y[j] * inv, y[j + 1] * inv), pack_out<kBf16>(y[j + 2] * inv, y[j + 3] * inv));
+    if (kScores && d0 == 0)
+        p.lse[((int64_t)b * p.pool.kv_heads + h) * p.rows + row] = sum == 0.0f ? INFINITY : ref + log2f(sum);
+}
+
+// Count a part of a segment of n + 1: the number counted before; wraps to 0 with the last.
+// Releases this block's part (whose writers a barrier precedes), acquires the others'.
+__device__ __forceinline__ unsigned count_part(unsigned *word, unsigned n) {
+    unsigned old;
+    asm volatile("fence.acq_rel.gpu;\n\tatom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;\n\tfence.acq_rel.gpu;"
+                 : "=r"(old)
+                 : "l"(word), "r"(n)
+                 : "memory");
+    return old;
+}
+
 // ---------------------------------------------------------------- the stream
 
 template <int D, int kN, bool kBf16, bool kScores>
@@ -289,7 +317,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
     auto full = [&](uint32_t s) { return bar0 + 8u * s; };
     auto empty = [&](uint32_t s) { return bar0 + 8u * (G::kStages + s); };
     volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(gbase + G::kOffMisc);
-    int64_t *scan = reinterpret_cast<int64_t *>(gbase + G::kOffScan);
+    int *scan = reinterpret_cast<int *>(gbase + G::kOffScan);   // 5 warps' units, then what was found
     float2 *meta = reinterpret_cast<float2 *>(gbase + G::kOffMeta);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -306,69 +334,59 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
         tma_prefetch_map(&tmK);
         tma_prefetch_map(&tmV);
     }
+    // Warm L2 with what the start depends on, one load after the other: the lengths and the page
+    // table (L2 is where all writes meet, so fetching early returns nothing stale).
+    {
+        const int64_t i = ((int64_t)blockIdx.x * kAttnThreads + tid) * 32;
+        if (i < p.batch * p.max_pages)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.pages + i));
+        if (i < p.batch)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.lengths + i));
+    }
     pdl_wait_primary();
 
-    // this block's range of units, and the sequence that it starts in
+    // this block's range of units, and the sequence that it starts in: every thread counts a
+    // slice of the sequences
     const int per_seq = p.pool.kv_heads * p.row_tiles;   // (head, row tile) pairs
     const int slice = (p.batch + kAttnThreads - 1) / kAttnThreads;
     const int b0 = min(tid * slice, p.batch), b1 = min(b0 + slice, p.batch);
-    int64_t mine = 0;
-    for (int b = b0; b < b1; ++b)
-        mine += span_of(length_of(p, b), p.tokens, p.window, p.sinks).units;
-    scan[tid] = mine;
+    int mine = 0;
+    for (int i = b0; i < b1; ++i)
+        mine += span_of(length_of(p, i), p.tokens, p.window, p.sinks).units;
+    int run = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, run, o);
+        run += lane >= o ? x : 0;
+    }
+    if (lane == 31)
+        scan[warp] = run;
     __syncthreads();
-    if (warp == 0) {   // exclusive sums of the 160 slices
-        int64_t v[5], sum = 0;
+    int total = 0, seq_at = run - mine;
 #pragma unroll
-        for (int i = 0; i < 5; ++i) {
-            v[i] = scan[lane * 5 + i];
-            sum += v[i];
+    for (int w = 0; w < kAttnThreads / 32; ++w) {
+        seq_at += w < warp ? scan[w] : 0;
+        total += scan[w];
+    }
+    total *= per_seq;
+    seq_at *= per_seq;
+    const int blocks = blocks_used(total, p.batch * per_seq, p.grid);
+    const int start = (int)blockIdx.x < blocks ? range_start(blockIdx.x, total, blocks) : total;
+    const int stop = (int)blockIdx.x < blocks ? range_start(blockIdx.x + 1, total, blocks) : total;
+    if (start < stop && start >= seq_at && start < seq_at + mine * per_seq) {
+        int i = b0;
+        for (; slice > 1; ++i) {
+            const int u = span_of(length_of(p, i), p.tokens, p.window, p.sinks).units * per_seq;
+            if (start < seq_at + u)
+                break;
+            seq_at += u;
         }
-        int64_t run = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, run, o);
-            run += lane >= o ? x : 0;
-        }
-        int64_t at = run - sum;
-#pragma unroll
-        for (int i = 0; i < 5; ++i) {
-            scan[lane * 5 + i] = at;
-            at += v[i];
-        }
-        if (lane == 31)
-            scan[kAttnThreads] = run;
+        scan[8] = i;
+        scan[9] = seq_at;
     }
     __syncthreads();
-    const int64_t total = scan[kAttnThreads] * per_seq;
-    const int blocks = blocks_used(total, (int64_t)p.batch * per_seq, p.grid);
-    const int64_t start = (int)blockIdx.x < blocks ? range_start(blockIdx.x, total, blocks) : total;
-    const int64_t stop = (int)blockIdx.x < blocks ? range_start(blockIdx.x + 1, total, blocks) : total;
-    {
-        int64_t at = scan[tid] * per_seq;
-        for (int b = b0; b < b1; ++b) {
-            const int64_t u = (int64_t)span_of(length_of(p, b), p.tokens, p.window, p.sinks).units * per_seq;
-            if (start < stop && start >= at && start < at + u) {
-                scan[kAttnThreads + 1] = b;
-                scan[kAttnThreads + 2] = at;
-            }
-            at += u;
-        }
-    }
-    __syncthreads();
-    // sequences without tokens
-    for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
-        if (length_of(p, b) > 0)
-            continue;
-        uint4 *dst = reinterpret_cast<uint4 *>(p.out + (int64_t)b * p.tokens * p.q_heads * D);
-        for (int i = tid; i < p.tokens * p.q_heads * (D / 8); i += kAttnThreads)
-            dst[i] = make_uint4(0, 0, 0, 0);
-        if (kScores)
-            for (int i = tid; i < p.rows * p.pool.kv_heads; i += kAttnThreads)
-                p.lse[(int64_t)b * p.pool.kv_heads * p.rows + i] = INFINITY;   // no token has a weight
-    }
-    int b = (int)scan[kAttnThreads + 1];
-    int64_t seq_at = scan[kAttnThreads + 2];   // first unit of sequence b
+    int b = scan[8];
+    seq_at = scan[9];   // first unit of sequence b
 
     if (start < stop && warp == kFeedWarp) {
         // ============================================================ the feed
@@ -378,25 +396,24 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
         const int pieces = kUnit / piece_tokens, per_batch = 32 / pieces;
         uint32_t issued = 0, parity = 0;
         bool ok = !(p.drop_arrive && blockIdx.x == 0);
-        int64_t u0 = start;
+        int u0 = start;
         uint32_t stage = 0, phase = 0;
         while (ok && u0 < stop) {
-            const int64_t unit = u0 + lane / pieces;
+            const int unit = u0 + lane / pieces;
             float ks = -1.0f, vs = -1.0f;   // < 0: no such page
             int id = -1, slot = 0, h = 0;
             if (unit < stop) {
                 int n = length_of(p, b);
                 Span s = span_of(n, p.tokens, p.window, p.sinks);
-                int lb = b;
-                int64_t lat = seq_at;
-                while (unit >= lat + (int64_t)s.units * per_seq) {
-                    lat += (int64_t)s.units * per_seq;
+                int lb = b, lat = seq_at;
+                while (unit >= lat + s.units * per_seq) {
+                    lat += s.units * per_seq;
                     n = length_of(p, ++lb);
                     s = span_of(n, p.tokens, p.window, p.sinks);
                 }
-                const int local = (int)((unit - lat) / s.units);
+                const int local = (unit - lat) / s.units;
                 h = local / p.row_tiles;
-                const int token = s.chunk((int)((unit - lat) % s.units)) * kUnit +
+                const int token = s.chunk((unit - lat) % s.units) * kUnit +
                                   (lane % pieces) * piece_tokens;
                 slot = token & (p.pool.page - 1);
                 if (token < n) {
@@ -413,7 +430,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
                 seq_at = lat;
             }
             // the next batch starts in the sequence of this one's last unit
-            const int last = (int)min((int64_t)per_batch, stop - u0) * pieces - 1;
+            const int last = min(per_batch, stop - u0) * pieces - 1;
             b = __shfl_sync(0xffffffffu, b, last);
             seq_at = __shfl_sync(0xffffffffu, seq_at, last);
             for (int i = 0; i < per_batch && u0 + i < stop; ++i) {
@@ -457,22 +474,26 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
         float *join = reinterpret_cast<float *>(gbase + G::kOffJoin);
         float *stat = reinterpret_cast<float *>(gbase + G::kOffStat);
         float *stat_m = stat, *stat_l = stat + kWarps * kRows, *stat_v = stat + 2 * kWarps * kRows;
+        float *stats = p.partial + (int64_t)p.grid * 2 * kRows * D;   // the parts' (m, l)
         bool alive = true;
         uint32_t stage = 0, phase = 0;
-        int64_t unit = start;
+        int unit = start;
+        // the segments that this block has a part of, at most two: the one that it starts in
+        // and the one that it ends in
+        int cut_b[2], cut_local[2], cut_seg0[2], cut_seg1[2], cuts = 0;
         while (unit < stop) {
             // the (sequence, head, row tile) of this unit, and its units in this block
             int n = length_of(p, b);
             Span s = span_of(n, p.tokens, p.window, p.sinks);
-            while (unit >= seq_at + (int64_t)s.units * per_seq) {
-                seq_at += (int64_t)s.units * per_seq;
+            while (unit >= seq_at + s.units * per_seq) {
+                seq_at += s.units * per_seq;
                 n = length_of(p, ++b);
                 s = span_of(n, p.tokens, p.window, p.sinks);
             }
-            const int local = (int)((unit - seq_at) / s.units);
+            const int local = (unit - seq_at) / s.units;
             const int h = local / p.row_tiles, tile = local % p.row_tiles;
-            const int64_t seg0 = seq_at + (int64_t)local * s.units, seg1 = seg0 + s.units;
-            const int64_t end = seg1 < stop ? seg1 : stop;
+            const int seg0 = seq_at + local * s.units, seg1 = seg0 + s.units;
+            const int end = seg1 < stop ? seg1 : stop;
             const int row0 = tile * kRows;
 
             // the query rows as fragments (lane g's row of each group of 8), and what the lane
@@ -512,7 +533,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
             }
             float vref = 0.0f, vinv = 0.0f;
 
-            const int units_here = (int)(end - unit), u0 = (int)(unit - seg0);
+            const int units_here = end - unit, u0 = unit - seg0;
             for (int u = 0; u < units_here; ++u) {
                 const int t0 = s.chunk(u0 + u) * kUnit + 16 * warp;
                 if (alive)
@@ -785,88 +806,110 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
                         y[4 * j + 3] += fv * z.w;
                     }
                 }
-                const int row = row0 + r;
-                bool finish = seg0 >= start && seg1 <= stop;   // the whole of it
-                if (!finish) {
+                if (seg0 >= start && seg1 <= stop) {   // the whole of it
+                    if (alive && row0 + r < p.rows)
+                        write_row<D, kF, kBf16, kScores>(p, b, h, row0 + r, d0, y, ref, sum);
+                } else {
                     // a part: slot 0 where it starts this block's range, else slot 1
-                    const int64_t stats = (int64_t)p.grid * 2 * kRows * D;
                     const int64_t at = ((int64_t)blockIdx.x * 2 + (seg0 > start ? 1 : 0)) * kRows + r;
                     float *dst = p.partial + at * D + d0;
 #pragma unroll
                     for (int j = 0; j < kF; j += 4)
                         *reinterpret_cast<float4 *>(dst + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
                     if (d0 == 0)
-                        *reinterpret_cast<float2 *>(p.partial + stats + at * 2) = make_float2(top, sum);
-                    __threadfence();
-                    named_bar_sync(1, 32 * kWarps);
-                    const int c0 = range_owner(seg0, total, blocks), c1 = range_owner(seg1 - 1, total, blocks);
-                    if (tid == 0) {
-                        // count this part; the word returns to 0 with the last one.  Words of
-                        // another call or of memory never used carry another tag.
-                        unsigned long long *word = p.arrived + ((int64_t)b * p.pool.kv_heads + h) * p.row_tiles + tile;
-                        unsigned long long cur = atomicAdd(word, 0ull), was;
-                        bool last;
-                        do {
-                            was = cur;
-                            const unsigned long long before = (was & ~1023ull) == p.epoch ? (was & 1023ull) : 0ull;
-                            last = before + 1 == (unsigned long long)(c1 - c0 + 1);
-                            cur = atomicCAS(word, was, last ? 0ull : p.epoch + before + 1);
-                        } while (cur != was);
-                        __threadfence();
-                        stat_v[0] = last ? 1.0f : 0.0f;
-                    }
-                    named_bar_sync(1, 32 * kWarps);
-                    finish = stat_v[0] != 0.0f;
-                    if (finish) {
-                        // all parts, in the order of their blocks
-                        auto slot_of = [&](int c) {
-                            return ((int64_t)c * 2 + (seg0 > range_start(c, total, blocks) ? 1 : 0)) * kRows + r;
-                        };
-                        // only the first part can start inside its block's range
-                        const int64_t first = slot_of(c0);
-                        auto slot = [&](int c) { return c == c0 ? first : (int64_t)c * 2 * kRows + r; };
-                        float high = -INFINITY;
-#pragma unroll 4
-                        for (int c = c0; c <= c1; ++c)
-                            high = fmaxf(high, __ldcg(p.partial + stats + slot(c) * 2));
-                        const float base2 = high == -INFINITY ? 0.0f : high;
-                        sum = 0.0f;
-#pragma unroll
-                        for (int j = 0; j < kF; ++j)
-                            y[j] = 0.0f;
-#pragma unroll 4
-                        for (int c = c0; c <= c1; ++c) {
-                            const int64_t k = slot(c);
-                            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.partial + stats + k * 2));
-                            const float f = exp2_fast(ml.x - base2);
-                            sum += f * ml.y;
-#pragma unroll
-                            for (int j = 0; j < kF; j += 4) {
-                                const float4 z = __ldcg(reinterpret_cast<const float4 *>(p.partial + k * D + d0 + j));
-                                y[j] += f * z.x;
-                                y[j + 1] += f * z.y;
-                                y[j + 2] += f * z.z;
-                                y[j + 3] += f * z.w;
-                            }
-                        }
-                        top = base2;
-                    }
-                }
-                if (alive && finish && row < p.rows) {
-                    const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-                    uint16_t *dst = p.out + out_row(p, b, h, row) * D + d0;
-#pragma unroll
-                    for (int j = 0; j < kF; j += 4)
-                        *reinterpret_cast<uint2 *>(dst + j) =
-                            make_uint2(pack_out<kBf16>(y[j] * inv, y[j + 1] * inv),
-                                       pack_out<kBf16>(y[j + 2] * inv, y[j + 3] * inv));
-                    if (kScores && d0 == 0)
-                        p.lse[((int64_t)b * p.pool.kv_heads + h) * p.rows + row] =
-                            sum == 0.0f ? INFINITY : (top == -INFINITY ? 0.0f : top) + log2f(sum);
+                        *reinterpret_cast<float2 *>(stats + at * 2) = make_float2(top, sum);
+                    cut_b[cuts & 1] = b;
+                    cut_local[cuts & 1] = local;
+                    cut_seg0[cuts & 1] = seg0;
+                    cut_seg1[cuts & 1] = seg1;
+                    ++cuts;
                 }
             }
             named_bar_sync(1, 32 * kWarps);
         }
+
+        // ---- count the parts; who counts the last one of a segment joins it
+        if (cuts > 0) {
+            int *last = reinterpret_cast<int *>(stat_v);
+            named_bar_sync(1, 32 * kWarps);
+            if (lane == 0 && warp < cuts) {
+                const int i = warp;
+                const int c0 = range_owner(i ? cut_seg0[1] : cut_seg0[0], total, blocks);
+                const int c1 = range_owner((i ? cut_seg1[1] : cut_seg1[0]) - 1, total, blocks);
+                last[i] = count_part(p.arrived + c0, (unsigned)(c1 - c0)) == (unsigned)(c1 - c0);
+            }
+            named_bar_sync(1, 32 * kWarps);
+#pragma unroll 1
+            for (int i = 0; i < cuts; ++i) {
+                if (!last[i])
+                    continue;
+                const int seg0 = i ? cut_seg0[1] : cut_seg0[0], seg1 = i ? cut_seg1[1] : cut_seg1[0];
+                const int local = i ? cut_local[1] : cut_local[0], bb = i ? cut_b[1] : cut_b[0];
+                const int c0 = range_owner(seg0, total, blocks), c1 = range_owner(seg1 - 1, total, blocks);
+                constexpr int kF = D * kN / 16;
+                const int r = tid * kN / 16, d0 = tid % (16 / kN) * kF;
+                // a part's row: only the first part can start inside its block's range
+                const int first = (c0 * 2 + (seg0 > range_start(c0, total, blocks) ? 1 : 0)) * kRows + r;
+                auto slot = [&](int c) { return (int64_t)(c == c0 ? first : c * 2 * kRows + r); };
+                float ref = -INFINITY, sum = 0.0f, y[kF];
+#pragma unroll
+                for (int j = 0; j < kF; ++j)
+                    y[j] = 0.0f;
+                // four parts are read at a time
+                for (int c = c0; c <= c1; c += 4) {
+                    float2 ml[4];
+                    float4 z[4][kF / 4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        ml[k] = make_float2(-INFINITY, 0.0f);
+                        if (c + k <= c1) {
+                            const int64_t at = slot(c + k);
+                            ml[k] = __ldcg(reinterpret_cast<const float2 *>(stats + at * 2));
+#pragma unroll
+                            for (int j = 0; j < kF / 4; ++j)
+                                z[k][j] = __ldcg(reinterpret_cast<const float4 *>(p.partial + at * D + d0) + j);
+                        }
+                    }
+                    const float top = fmaxf(fmaxf(ref, fmaxf(ml[0].x, ml[1].x)), fmaxf(ml[2].x, ml[3].x));
+                    if (top > ref) {
+                        const float f = exp2_fast(ref - top);   // 0 at first
+                        sum *= f;
+#pragma unroll
+                        for (int j = 0; j < kF; ++j)
+                            y[j] *= f;
+                        ref = top;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (c + k > c1)
+                            break;
+                        const float f = exp2_fast(ml[k].x - (ref == -INFINITY ? 0.0f : ref));
+                        sum += f * ml[k].y;
+#pragma unroll
+                        for (int j = 0; j < kF / 4; ++j) {
+                            y[4 * j] += f * z[k][j].x;
+                            y[4 * j + 1] += f * z[k][j].y;
+                            y[4 * j + 2] += f * z[k][j].z;
+                            y[4 * j + 3] += f * z[k][j].w;
+                        }
+                    }
+                }
+                if (ref == -INFINITY)
+                    ref = 0.0f;
+                const int row = local % p.row_tiles * kRows + r;
+                if (alive && row < p.rows)
+                    write_row<D, kF, kBf16, kScores>(p, bb, local / p.row_tiles, row, d0, y, ref, sum);
+            }
+        }
+    }
+
+    // sequences without tokens
+    for (int i = blockIdx.x; i < p.batch; i += gridDim.x) {
+        if (length_of(p, i) > 0)
+            continue;
+        uint4 *dst = reinterpret_cast<uint4 *>(p.out + (int64_t)i * p.tokens * p.q_heads * D);
+        for (int j = tid; j < p.tokens * p.q_heads * (D / 8); j += kAttnThreads)
+            dst[j] = make_uint4(0, 0, 0, 0);
     }
 }
 

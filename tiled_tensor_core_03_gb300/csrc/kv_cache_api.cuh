@@ -95,32 +95,19 @@ bool make_pool_map(CUtensorMap *map, const void *ptr, const kv_cache_pool *c, ui
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Workspace of kv_cache_attention_x16: partials, a word per (sequence, head, row tile), and with
-// weights every row's log-sum-exp and scores.
+// Workspace of kv_cache_attention_x16: the counters of cut segments, one per block at most, at a
+// place that no call's sizes move; partials; with weights every row's log-sum-exp and scores.
 struct AttnSpace {
-    size_t arrived, lse, scores, total;   // byte offsets; partials at 0
+    size_t partial, lse, scores, total;   // byte offsets; counters at 0
 };
-
-// Tags of kv_cache_attention_x16 calls: 54 bits that start at random and count up, never 0, so
-// that no word left in reused memory carries the tag of a later call.
-std::atomic<uint64_t> g_kv_epoch{(uint64_t)std::random_device{}() << 20};
-
-unsigned long long next_kv_epoch() {
-    for (;;) {
-        const uint64_t e = (++g_kv_epoch) << 10;
-        if (e)
-            return e;
-    }
-}
 
 AttnSpace attention_space(int64_t batch, int64_t rows, int64_t kv_heads, int64_t head_dim,
                           int64_t weights_width, int sms) {
     AttnSpace a{};
     const size_t slots = 2 * (size_t)sms * std::max(KC::AttnCfg<128, 1>::kBlocksPerSm * 8,
                                                     KC::AttnCfg<128, 2>::kBlocksPerSm * 16);
-    size_t at = slots * (head_dim + 2) * 4;
-    a.arrived = at = round256(at);
-    at += (size_t)batch * kv_heads * ((rows + 7) / 8) * 8;
+    size_t at = a.partial = GEMMRELU_KV_COUNTER_BYTES;
+    at += slots * (head_dim + 2) * 4;
     a.lse = at = round256(at);
     if (weights_width > 0) {
         at += (size_t)batch * kv_heads * rows * 4;
@@ -150,7 +137,7 @@ int launch_kv_attention(const CUtensorMap &mK, const CUtensorMap &mV, KC::AttnPa
     if (!ensure_smem_attr(attr_done, kern, G::kSmem))
         return GEMMRELU_ERR_LAUNCH;
     p.row_tiles = (p.rows + G::kRows - 1) / G::kRows;
-    p.grid = sms * G::kBlocksPerSm;
+    p.grid = std::min(sms * G::kBlocksPerSm, (int)(GEMMRELU_KV_COUNTER_BYTES / sizeof(unsigned)));
     const int rc = launch_kernel(kern, (unsigned)p.grid, KC::kAttnThreads, G::kSmem, s, false, 1u, mK, mV, p);
     if (rc != GEMMRELU_OK || !kScores)
         return rc;
@@ -304,6 +291,9 @@ int kv_cache_attention_x16(const kv_cache_pool *cache, const void *q, int dtype,
     if (rc != GEMMRELU_OK)
         return rc;
     const int64_t rows = tokens * (q_heads / cache->kv_heads);
+    // units of 64 tokens, counted in 32 bits
+    if (batch * cache->kv_heads * ((rows + 7) / 8) > kMaxGrid / ((max_pages * cache->page + 63) / 64))
+        return GEMMRELU_ERR_INVALID_ARG;
     const AttnSpace sp = attention_space(batch, rows, cache->kv_heads, cache->head_dim,
                                          weights ? weights_width : 0, ds->sms);
     if (!workspace || workspace_bytes < sp.total || !aligned(workspace, 16))
@@ -330,9 +320,8 @@ int kv_cache_attention_x16(const kv_cache_pool *cache, const void *q, int dtype,
     p.window = (int)std::min<int64_t>(window, kMaxTokens);
     p.sinks = (int)std::min<int64_t>(sinks, kMaxTokens);
     p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)cache->head_dim));
-    p.partial = reinterpret_cast<float *>(ws);
-    p.arrived = reinterpret_cast<unsigned long long *>(ws + sp.arrived);
-    p.epoch = next_kv_epoch();
+    p.partial = reinterpret_cast<float *>(ws + sp.partial);
+    p.arrived = reinterpret_cast<unsigned *>(ws);
     if (weights) {
         p.lse = reinterpret_cast<float *>(ws + sp.lse);
         p.scores = reinterpret_cast<float *>(ws + sp.scores);
@@ -362,7 +351,7 @@ int kv_cache_debug_span(int64_t length, int64_t tokens, int64_t window, int64_t 
     return GEMMRELU_OK;
 }
 
-int64_t kv_cache_debug_range(int64_t x, int64_t total, int grid, int owner) {
+int kv_cache_debug_range(int x, int total, int grid, int owner) {
     if (x < 0 || total < 1 || grid < 1)
         return -1;
     return owner ? KC::range_owner(x, total, grid) : KC::range_start(x, total, grid);

@@ -12,7 +12,7 @@ from typing import NamedTuple
 
 import torch
 
-from . import OK, F16, BF16, GemmReluError, lib
+from . import OK, F16, BF16, KV_COUNTER_BYTES, GemmReluError, lib
 
 _DTYPES = {torch.float16: F16, torch.bfloat16: BF16}
 _VALUES = (torch.float8_e4m3fn, torch.uint8)
@@ -199,11 +199,30 @@ def kv_cache_append(cache, k, v, pages, lengths, counts=None, stream=None):
 
 
 def kv_cache_attention_workspace(q, cache, weights=None):
-    """A device workspace sized for kv_cache_attention (uint8 tensor)."""
+    """A device workspace for kv_cache_attention calls of these sizes (uint8 tensor, its
+    counters zeroed on the current stream); for calls that follow one another."""
     batch, tokens, heads, dim = q.shape
     n = lib().kv_cache_attention_x16_workspace_bytes(
         batch, tokens, heads, cache[0].shape[1], dim, 0 if weights is None else weights.shape[2])
-    return torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
+    w = torch.empty(max(n, KV_COUNTER_BYTES), dtype=torch.uint8, device=q.device)
+    w[:KV_COUNTER_BYTES].zero_()
+    return w
+
+
+# Workspaces of calls that bring none and collect no weights (a few MB whose size depends
+# on head_dim alone), one per device, stream and head_dim: calls on a stream follow one
+# another.  Calls being captured get their own, since their graph may run anywhere.
+_workspaces = {}
+
+
+def _workspace(q, cache, weights, s):
+    if weights is not None or torch.cuda.is_current_stream_capturing():
+        return kv_cache_attention_workspace(q, cache, weights)
+    key = (q.get_device(), s, q.shape[3])
+    w = _workspaces.get(key)
+    if w is None:
+        w = _workspaces[key] = kv_cache_attention_workspace(q, cache)
+    return w
 
 
 def kv_cache_attention(q, cache, pages, lengths, window=0, sinks=0, weights=None, out=None,
@@ -248,7 +267,7 @@ def kv_cache_attention(q, cache, pages, lengths, window=0, sinks=0, weights=None
 
     def call(s):
         o = torch.empty(shape, dtype=q.dtype, device=q.device) if out is None else out
-        w = kv_cache_attention_workspace(q, cache, weights) if workspace is None else workspace
+        w = _workspace(q, cache, weights, s) if workspace is None else workspace
         rc = lib().kv_cache_attention_x16(
             ctypes.byref(pool), qp, dtype, batch, tokens, heads, qs, o.data_ptr(), table,
             max_pages, lens, window, sinks, wp, width, w.data_ptr(), w.nbytes, s)
