@@ -542,6 +542,15 @@ def test_evict(page, d, hkv, lengths, budget, sinks, recent):
     _evict(np.random.default_rng(page + d + budget), page, d, hkv, lengths, budget, sinks, recent)
 
 
+@pytest.mark.parametrize("n,budget", [(5000, 700), (20000, 12345), (70000, 1000), (140000, 100000)])
+def test_evict_long(n, budget):
+    """Clusters of 1 to 8 blocks a head, and more tokens than their registers hold; ties at
+    the border."""
+    rng = np.random.default_rng(n)
+    w = np.round(np.exp(rng.standard_normal((2, 1, n + 128))) * 50) / 50
+    _evict(rng, 128, 64, 1, [n, n // 3], budget, 4, budget // 4, weights=w)
+
+
 def test_evict_within_one_pool():
     _evict(np.random.default_rng(21), 32, 64, 2, [200, 90], 64, 2, 10, same_pool=True)
 

@@ -216,6 +216,8 @@ struct EvictParams {
     const int32_t *pages, *lengths, *to_pages;
     int64_t max_pages, to_max_pages;
     int batch, budget, sinks, recent;
+    int cluster;                       // blocks per (sequence, head) of the selection
+    int items;                         // (sequence, new page, head) items of the move
     int32_t *to_lengths;
     float *to_weights;
     int32_t *kept;
@@ -240,189 +242,331 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 }
 
 constexpr int kSelectThreads = 1024;
+constexpr int kSelectWarps = kSelectThreads / 32;
+constexpr int kMaxSelectCluster = 8;
 
-// One block per (sequence, head): which tokens stay.  Between the sinks and the
-// recent tokens the k heaviest are those above the k-th largest key and the
-// first few equal to it; the k-th largest key is found 8 bits at a time
-// from the top with a histogram of the keys that share the bits found so far.
-__global__ void __launch_bounds__(kSelectThreads) kv_evict_select_kernel(const EvictParams p) {
-    __shared__ uint32_t hist[256];
-    __shared__ uint32_t found[2];
-    __shared__ uint32_t above[32], equal[32];
+// Which tokens stay, a cluster of 1 to 8 blocks per (sequence, head), each with a stretch of
+// the tokens.  Between the sinks and the recent tokens the k heaviest are those above the
+// k-th largest key and the first few equal to it.  The keys are read once into registers
+// (kKeys a thread; what does not fit is read again from L2), and the k-th largest is built
+// two bits at a time from the top: of three candidates the largest that k keys reach.
+// Counting takes 16 rounds of compares whatever the weights are; a histogram of
+// digits had its atomics collide, since weights share exponents: 23 us at 2000 tokens and
+// 51 us at 16384, against 4 and 9 us for this.
+template <int kKeys>
+__global__ void __launch_bounds__(kSelectThreads, 1) kv_evict_select_kernel(const EvictParams p) {
+    __shared__ int warp_count[2][3][kSelectWarps];
+    __shared__ int block_count[2][kMaxSelectCluster][3];
+    __shared__ int slot_sure[kKeys * kSelectWarps], slot_tie[kKeys * kSelectWarps];
     pdl_launch_dependents();
     pdl_wait_primary();
-    const int h = blockIdx.x % p.from.kv_heads, b = blockIdx.x / p.from.kv_heads;
+    const int cluster = p.cluster, rank = cluster > 1 ? (int)cluster_ctarank() : 0;
+    const int64_t bh = blockIdx.x / cluster;
+    const int h = (int)(bh % p.from.kv_heads), b = (int)(bh / p.from.kv_heads);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int n = checked_length(p.lengths, b, p.max_pages * p.from.page);
     const int m = n < p.budget ? n : p.budget;
-    const float *w = p.weights + (int64_t)blockIdx.x * p.width;
-    int32_t *kept = p.kept + (int64_t)blockIdx.x * p.budget;
-    if (h == 0 && tid == 0)
+    const float *w = p.weights + bh * p.width;
+    int32_t *kept = p.kept + bh * p.budget;
+    if (h == 0 && rank == 0 && tid == 0)
         p.to_lengths[b] = m;
-    for (int i = m + tid; i < p.budget; i += kSelectThreads)
+    for (int i = m + rank * kSelectThreads + tid; i < p.budget; i += cluster * kSelectThreads)
         kept[i] = -1;
     if (n <= p.budget) {
-        for (int i = tid; i < n; i += kSelectThreads)
+        for (int i = rank * kSelectThreads + tid; i < n; i += cluster * kSelectThreads)
             kept[i] = i;
-        return;
+        return;   // all blocks of the cluster
     }
-    const int lo = p.sinks, hi = n - p.recent;
-    uint32_t need = (uint32_t)(p.budget - p.sinks - p.recent);   // of the keys that still match
-    uint32_t prefix = 0, mask = 0;
-    if (need > 0) {
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int i = tid; i < 256; i += kSelectThreads)
-                hist[i] = 0;
-            __syncthreads();
-            for (int i = lo + tid; i < hi; i += kSelectThreads) {
-                const uint32_t key = weight_key(w[i]);
-                if ((key & mask) == prefix)
-                    atomicAdd(&hist[(key >> shift) & 255u], 1u);
-            }
-            __syncthreads();
-            if (tid == 0) {
-                uint32_t left = need;
-                int bin = 255;
-                while (hist[bin] < left)
-                    left -= hist[bin--];
-                found[0] = (uint32_t)bin;
-                found[1] = left;
-            }
-            __syncthreads();
-            prefix |= found[0] << shift;
-            mask |= 255u << shift;
-            need = found[1];
+    const int lo = p.sinks, hi = n - p.recent;   // the tokens that compete
+    const int stretch = (n + cluster - 1) / cluster;
+    const int t0 = min(rank * stretch, n), t1 = min(t0 + stretch, n);
+    constexpr int kGroup = kKeys * kSelectThreads;
+    // token t0 + s * threads + tid is slot s of this thread; 0, below every key, for the others
+    auto key_at = [&](int i) { return i >= lo && i < hi && i < t1 ? weight_key(w[i]) : 0u; };
+    uint32_t key[kKeys];
+#pragma unroll
+    for (int s = 0; s < kKeys; ++s)
+        key[s] = key_at(t0 + s * kSelectThreads + tid);
+
+    int turn = 0;
+    // how many of all keys reach three thresholds
+    auto count = [&](uint32_t c1, uint32_t c2, uint32_t c3, int (&got)[3]) {
+        int x[3] = {0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < kKeys; ++s) {
+            x[0] += key[s] >= c1;
+            x[1] += key[s] >= c2;
+            x[2] += key[s] >= c3;
         }
-    } else {
-        prefix = 0xffffffffu;   // no weight has this key
-    }
-    // write the survivors in order; `need` = how many of the keys equal to prefix stay
-    uint32_t out = 0, ties = 0;   // survivors and equal keys before this stretch of tokens
-    for (int base = 0; base < n; base += kSelectThreads) {
-        const int i = base + tid;
-        bool sure = false, tie = false;
-        if (i < n) {
-            sure = i < lo || i >= hi;
-            if (!sure) {
-                const uint32_t key = weight_key(w[i]);
-                sure = key > prefix;
-                tie = key == prefix;
-            }
+        for (int i = t0 + kGroup + tid; i < t1; i += kSelectThreads) {
+            const uint32_t k = key_at(i);
+            x[0] += k >= c1;
+            x[1] += k >= c2;
+            x[2] += k >= c3;
         }
-        const uint32_t below = (1u << lane) - 1;
-        const uint32_t bs = __ballot_sync(0xffffffffu, sure), bt = __ballot_sync(0xffffffffu, tie);
-        if (lane == 0) {
-            above[warp] = __popc(bs);
-            equal[warp] = __popc(bt);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            x[i] = __reduce_add_sync(0xffffffffu, x[i]);
+            if (lane == 0)
+                warp_count[turn][i][warp] = x[i];
         }
         __syncthreads();
-        uint32_t s = 0, t = 0, all_s = 0, all_t = 0;
-        for (int k = 0; k < kSelectThreads / 32; ++k) {
-            s += k < warp ? above[k] : 0u;
-            t += k < warp ? equal[k] : 0u;
-            all_s += above[k];
-            all_t += equal[k];
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+            got[i] = __reduce_add_sync(0xffffffffu, warp_count[turn][i][lane]);
+        if (cluster > 1) {
+            if (warp == 0 && lane < cluster) {
+                const uint32_t at = mapa_shared(smem_addr(&block_count[turn][rank][0]), (uint32_t)lane);
+#pragma unroll
+                for (int i = 0; i < 3; ++i)
+                    st_cluster_f32(at + 4 * i, __int_as_float(got[i]));
+            }
+            cluster_sync();
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                got[i] = 0;
+                for (int c = 0; c < cluster; ++c)
+                    got[i] += block_count[turn][c][i];
+            }
         }
-        const uint32_t kept_ties = ties < need ? ties : need;
-        const uint32_t tie_rank = ties + t + __popc(bt & below);
-        const uint32_t at = out + s + __popc(bs & below) + (tie_rank < need ? tie_rank : need) - kept_ties;
-        if (sure || (tie && tie_rank < need))
-            kept[at] = i;
-        ties += all_t;
-        out += all_s + (ties < need ? ties : need) - kept_ties;
+        turn ^= 1;
+    };
+
+    const int need = p.budget - p.sinks - p.recent;
+    uint32_t kth = 0xffffffffu;   // no weight has this key
+    int ties_kept = 0;
+    if (need > 0) {
+        kth = 0;
+        for (int shift = 30; shift >= 0; shift -= 2) {
+            int got[3];
+            count(kth | 1u << shift, kth | 2u << shift, kth | 3u << shift, got);
+            kth |= (uint32_t)(got[2] >= need ? 3 : got[1] >= need ? 2 : got[0] >= need ? 1 : 0) << shift;
+        }
+        int got[3];   // kth < 0xffffffff, which no weight has
+        count(kth + 1, kth + 1, kth + 1, got);
+        ties_kept = need - got[0];
+    }
+
+    // survivors and equal keys of the blocks before
+    int out = 0, ties = 0;
+    if (cluster > 1) {
+        int sure = 0, tie = 0;
+        auto look = [&](int i, uint32_t k) {
+            sure += i < t1 && (i < lo || i >= hi || k > kth);
+            tie += i < t1 && k == kth && i >= lo && i < hi;
+        };
+#pragma unroll
+        for (int s = 0; s < kKeys; ++s)
+            look(t0 + s * kSelectThreads + tid, key[s]);
+        for (int i = t0 + kGroup + tid; i < t1; i += kSelectThreads)
+            look(i, key_at(i));
+        sure = __reduce_add_sync(0xffffffffu, sure);
+        tie = __reduce_add_sync(0xffffffffu, tie);
+        if (lane == 0) {
+            warp_count[turn][0][warp] = sure;
+            warp_count[turn][1][warp] = tie;
+        }
+        __syncthreads();
+        sure = __reduce_add_sync(0xffffffffu, warp_count[turn][0][lane]);
+        tie = __reduce_add_sync(0xffffffffu, warp_count[turn][1][lane]);
+        if (warp == 0 && lane < cluster) {
+            const uint32_t at = mapa_shared(smem_addr(&block_count[turn][rank][0]), (uint32_t)lane);
+            st_cluster_f32(at, __int_as_float(sure));
+            st_cluster_f32(at + 4, __int_as_float(tie));
+        }
+        cluster_sync();   // the last access to another block's memory
+        for (int c = 0; c < rank; ++c) {
+            out += block_count[turn][c][0];
+            ties += block_count[turn][c][1];
+        }
+        out += min(ties, ties_kept);
+    }
+    // write this block's survivors in order, kGroup tokens at a time
+    for (int g0 = t0; g0 < t1; g0 += kGroup) {
+        uint32_t sure[kKeys], tie[kKeys];
+#pragma unroll
+        for (int s = 0; s < kKeys; ++s) {
+            const int i = g0 + s * kSelectThreads + tid;
+            const uint32_t k = g0 == t0 ? key[s] : key_at(i);
+            const bool in = i < t1, compete = i >= lo && i < hi;
+            sure[s] = __ballot_sync(0xffffffffu, in && (!compete || k > kth));
+            tie[s] = __ballot_sync(0xffffffffu, in && compete && k == kth);
+            if (lane == 0) {
+                slot_sure[s * kSelectWarps + warp] = __popc(sure[s]);
+                slot_tie[s * kSelectWarps + warp] = __popc(tie[s]);
+            }
+        }
+        __syncthreads();
+        if (warp == 0) {   // exclusive sums in token order, kKeys entries a lane
+            int a[kKeys], c[kKeys], sum_a = 0, sum_c = 0;
+#pragma unroll
+            for (int s = 0; s < kKeys; ++s) {
+                a[s] = slot_sure[lane * kKeys + s];
+                c[s] = slot_tie[lane * kKeys + s];
+                sum_a += a[s];
+                sum_c += c[s];
+            }
+            int run_a = sum_a, run_c = sum_c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, run_a, o), y = __shfl_up_sync(0xffffffffu, run_c, o);
+                run_a += lane >= o ? x : 0;
+                run_c += lane >= o ? y : 0;
+            }
+            int at_a = run_a - sum_a, at_c = run_c - sum_c;
+#pragma unroll
+            for (int s = 0; s < kKeys; ++s) {
+                slot_sure[lane * kKeys + s] = at_a;
+                slot_tie[lane * kKeys + s] = at_c;
+                at_a += a[s];
+                at_c += c[s];
+            }
+            if (lane == 31) {
+                warp_count[0][0][0] = run_a;
+                warp_count[0][0][1] = run_c;
+            }
+        }
+        __syncthreads();
+        const uint32_t below = (1u << lane) - 1;
+        const int kept_before = min(ties, ties_kept);
+#pragma unroll
+        for (int s = 0; s < kKeys; ++s) {
+            const int rank_tie = ties + slot_tie[s * kSelectWarps + warp] + __popc(tie[s] & below);
+            const int at = out + slot_sure[s * kSelectWarps + warp] + __popc(sure[s] & below) +
+                           min(rank_tie, ties_kept) - kept_before;
+            const bool stays = (sure[s] >> lane & 1u) || ((tie[s] >> lane & 1u) && rank_tie < ties_kept);
+            if (stays)
+                kept[at] = g0 + s * kSelectThreads + tid;
+        }
+        const int more_sure = warp_count[0][0][0], more_ties = warp_count[0][0][1];
+        ties += more_ties;
+        out += more_sure + min(ties, ties_kept) - kept_before;
         __syncthreads();
     }
 }
 
 constexpr int kMoveThreads = 256;
 
-// One block per (sequence, new page, head): gathers the page's kept tokens, K
-// then V, 16 elements a thread and vector, and stores them under a
-// scale of their own.  The bytes stay in registers between the maximum and the
-// rounding.
+// Gathers the kept tokens of (sequence, new page, head) items, 16 elements a thread and
+// vector of K and of V, and stores them under scales of their own.  The bytes stay
+// in registers between the maximum and the rounding.  A token's bytes are three dependent reads
+// away (its position, its page, itself), so a block walks over items and reads the next
+// item's positions and pages while this one's bytes are under way.
 template <int D, int kVec>
 __global__ void __launch_bounds__(kMoveThreads) kv_evict_move_kernel(const EvictParams p) {
-    __shared__ uint32_t slots[2][kMoveThreads / 32];
+    __shared__ uint32_t slots[2][2][kMoveThreads / 32];
     pdl_launch_dependents();
     pdl_wait_primary();
-    int64_t i = blockIdx.x;
-    const int h = (int)(i % p.from.kv_heads);
-    i /= p.from.kv_heads;
-    const int at = (int)(i % p.to_max_pages);
-    const int b = (int)(i / p.to_max_pages);
-    const int page = p.from.page;
-    const int64_t bh = (int64_t)b * p.from.kv_heads + h;
-    const int m = p.to_lengths[b];   // written by the selection
-    const int64_t first = (int64_t)at * page;
-    const int32_t *kept = p.kept + bh * p.budget;
-    float *to_w = p.to_weights + bh * p.to_max_pages * page;
-    for (int s = threadIdx.x; s < page; s += kMoveThreads)
-        to_w[first + s] = first + s < m ? p.weights[bh * p.width + kept[first + s]] : 0.0f;
-    if (first >= m)
-        return;
-    const int64_t id = p.to_pages[b * p.to_max_pages + at];
-    if (id < 0 || id >= p.to.num_pages) {
-        if (threadIdx.x == 0)
-            record_page_error();
-        return;
-    }
     constexpr int kPerToken = D / 16;
-    uint4 x[2][kVec];
-    float s[2][kVec];
+    const int page = p.from.page, shift = p.from.page_shift, heads = p.from.kv_heads;
+    const int items = p.items;   // heads fastest, then pages, then sequences
+
+    struct Item {
+        int h, b, at, m, to;     // m: the sequence's new length; to: the new page, -1 for none
+        int from[kVec];          // source page of each vector, -1: none
+        int t[kVec];             // and its token
+        float w;
+    };
+    auto look = [&](int item) {
+        Item x;
+        x.h = item % heads;
+        x.at = item / heads % (int)p.to_max_pages;
+        x.b = item / heads / (int)p.to_max_pages;
+        const int64_t bh = (int64_t)x.b * heads + x.h;
+        const int32_t *kept = p.kept + bh * p.budget;
+        const int first = x.at << shift;
+        // written by the selection: -1 past the new length
+        const int at0 = first + threadIdx.x;
+        const int mine = threadIdx.x < page && at0 < p.budget ? kept[at0] : -1;
 #pragma unroll
-    for (int n = 0; n < kVec; ++n) {
-        const int v = threadIdx.x + n * kMoveThreads, slot = v / kPerToken;
-        x[0][n] = x[1][n] = make_uint4(0, 0, 0, 0);
-        s[0][n] = s[1][n] = 0.0f;
-        if (slot < page && first + slot < m) {
-            const int t = kept[first + slot];
-            const int64_t from = p.pages[b * p.max_pages + (t >> p.from.page_shift)];
-            if (from < 0 || from >= p.from.num_pages) {
+        for (int n = 0; n < kVec; ++n) {
+            const int slot = (threadIdx.x + n * kMoveThreads) / kPerToken;
+            x.t[n] = slot < page && first + slot < p.budget ? kept[first + slot] : -1;
+        }
+        x.m = p.to_lengths[x.b];
+        x.to = p.to_pages[x.b * p.to_max_pages + x.at];
+#pragma unroll
+        for (int n = 0; n < kVec; ++n)
+            x.from[n] = x.t[n] >= 0 ? p.pages[x.b * p.max_pages + (x.t[n] >> shift)] : -1;
+        x.w = mine >= 0 ? p.weights[bh * p.width + mine] : 0.0f;
+        return x;
+    };
+
+    int turn = 0;
+    int item = blockIdx.x;
+    if (item >= items)
+        return;
+    Item next = look(item);
+    for (; item < items; item += gridDim.x) {
+        const Item x = next;
+        const bool ahead = item + (int)gridDim.x < items;
+        const int64_t bh = (int64_t)x.b * heads + x.h;
+        const int first = x.at << shift;
+        const bool there = first < x.m, good = there && x.to >= 0 && x.to < p.to.num_pages;
+        uint4 v[2][kVec];
+        float s[2][kVec];
+#pragma unroll
+        for (int n = 0; n < kVec; ++n) {
+            v[0][n] = v[1][n] = make_uint4(0, 0, 0, 0);
+            s[0][n] = s[1][n] = 0.0f;
+            if (!good || x.t[n] < 0)
+                continue;
+            if (x.from[n] < 0 || x.from[n] >= p.from.num_pages) {
                 record_page_error();
-            } else {
-                const int64_t block = from * p.from.kv_heads + h;
+                continue;
+            }
+            const int64_t block = (int64_t)x.from[n] * heads + x.h;
+            const int64_t at = (block * page + (x.t[n] & (page - 1))) * D + 16 * ((threadIdx.x + n * kMoveThreads) % kPerToken);
 #pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    x[kv][n] = *reinterpret_cast<const uint4 *>(
-                        p.from.values[kv] + (block * page + (t & (page - 1))) * D + 16 * (v % kPerToken));
-                    s[kv][n] = p.from.scales[kv][block];
+            for (int kv = 0; kv < 2; ++kv) {
+                v[kv][n] = *reinterpret_cast<const uint4 *>(p.from.values[kv] + at);
+                s[kv][n] = p.from.scales[kv][block];
+            }
+        }
+        if (ahead)
+            next = look(item + gridDim.x);
+        if (threadIdx.x < page)
+            p.to_weights[bh * p.to_max_pages * page + first + threadIdx.x] = x.w;
+        if (there && !good && threadIdx.x == 0)
+            record_page_error();
+        if (!good)
+            continue;
+        const int64_t block = (int64_t)x.to * heads + x.h;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+            float amax = 0.0f;
+#pragma unroll
+            for (int n = 0; n < kVec; ++n) {
+                const uint32_t w[4] = {v[kv][n].x, v[kv][n].y, v[kv][n].z, v[kv][n].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 f = e4m3x2_to_float2(w[e] & 0xffffu), g = e4m3x2_to_float2(w[e] >> 16);
+                    amax = fmaxf(amax, fmaxf(fmaxf(finite_abs(f.x), finite_abs(f.y)),
+                                             fmaxf(finite_abs(g.x), finite_abs(g.y))) * s[kv][n]);
                 }
             }
-        }
-    }
+            // the words alternate between items: one barrier each
+            amax = block_max(amax, slots[turn][kv]);
+            const float scale = scale_for(amax), inv = inverse_scale(scale);
+            if (threadIdx.x == 0)
+                p.to.scales[kv][block] = scale;
+            uint8_t *dst = p.to.values[kv] + block * page * D;
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-        float amax = 0.0f;
+            for (int n = 0; n < kVec; ++n) {
+                const int i = threadIdx.x + n * kMoveThreads;
+                if (i / kPerToken >= page)
+                    break;
+                const float ratio = s[kv][n] * inv;
+                uint32_t w[4] = {v[kv][n].x, v[kv][n].y, v[kv][n].z, v[kv][n].w};
 #pragma unroll
-        for (int n = 0; n < kVec; ++n) {
-            const uint32_t w[4] = {x[kv][n].x, x[kv][n].y, x[kv][n].z, x[kv][n].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 f = e4m3x2_to_float2(w[e] & 0xffffu), g = e4m3x2_to_float2(w[e] >> 16);
-                amax = fmaxf(amax, fmaxf(fmaxf(finite_abs(f.x), finite_abs(f.y)),
-                                         fmaxf(finite_abs(g.x), finite_abs(g.y))) * s[kv][n]);
+                for (int e = 0; e < 4; ++e) {
+                    const float2 f = e4m3x2_to_float2(w[e] & 0xffffu), g = e4m3x2_to_float2(w[e] >> 16);
+                    w[e] = to_e4m3x2(f.x * ratio, f.y * ratio) | to_e4m3x2(g.x * ratio, g.y * ratio) << 16;
+                }
+                *reinterpret_cast<uint4 *>(dst + 16 * i) = make_uint4(w[0], w[1], w[2], w[3]);
             }
         }
-        amax = block_max(amax, slots[kv]);
-        const float scale = scale_for(amax), inv = inverse_scale(scale);
-        const int64_t block = id * p.to.kv_heads + h;
-        if (threadIdx.x == 0)
-            p.to.scales[kv][block] = scale;
-        uint8_t *dst = p.to.values[kv] + block * page * D;
-#pragma unroll
-        for (int n = 0; n < kVec; ++n) {
-            const int v = threadIdx.x + n * kMoveThreads;
-            if (v / kPerToken >= page)
-                break;
-            const float ratio = s[kv][n] * inv;
-            uint32_t w[4] = {x[kv][n].x, x[kv][n].y, x[kv][n].z, x[kv][n].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 f = e4m3x2_to_float2(w[e] & 0xffffu), g = e4m3x2_to_float2(w[e] >> 16);
-                w[e] = to_e4m3x2(f.x * ratio, f.y * ratio) | to_e4m3x2(g.x * ratio, g.y * ratio) << 16;
-            }
-            *reinterpret_cast<uint4 *>(dst + 16 * v) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+        turn ^= 1;
     }
 }
 

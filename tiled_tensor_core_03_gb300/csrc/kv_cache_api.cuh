@@ -68,14 +68,33 @@ int launch_append(const KC::AppendParams &p, int64_t grid, int dtype, cudaStream
                : launch_kv(KC::kv_append_kernel<D, kVec, false>, grid, KC::kAppendThreads, s, p);
 }
 
+template <int D, int kVec>
+int launch_move_vec(const KC::EvictParams &p, int sms, cudaStream_t s) {
+    // a few blocks an SM walk over the items (2048 threads an SM at most)
+    const int64_t grid = std::min<int64_t>(p.items, (int64_t)sms * 8);
+    return launch_kv(KC::kv_evict_move_kernel<D, kVec>, grid, KC::kMoveThreads, s, p);
+}
+
 template <int D>
-int launch_move(const KC::EvictParams &p, int64_t grid, cudaStream_t s) {
+int launch_move(const KC::EvictParams &p, int sms, cudaStream_t s) {
     // vectors of 16 elements a thread
-    if (p.from.page * D / 16 > 2 * KC::kMoveThreads)
-        return launch_kv(KC::kv_evict_move_kernel<D, 4>, grid, KC::kMoveThreads, s, p);
-    if (p.from.page * D / 16 > KC::kMoveThreads)
-        return launch_kv(KC::kv_evict_move_kernel<D, 2>, grid, KC::kMoveThreads, s, p);
-    return launch_kv(KC::kv_evict_move_kernel<D, 1>, grid, KC::kMoveThreads, s, p);
+    const int vectors = p.from.page * D / 16;
+    return vectors > 2 * KC::kMoveThreads ? launch_move_vec<D, 4>(p, sms, s)
+           : vectors > KC::kMoveThreads   ? launch_move_vec<D, 2>(p, sms, s)
+                                          : launch_move_vec<D, 1>(p, sms, s);
+}
+
+// A cluster of blocks holds a sequence's keys in registers as far as 8 blocks go.
+int launch_select(KC::EvictParams &p, int64_t heads, cudaStream_t s) {
+    constexpr int kSmall = 4, kLarge = 16;
+    const int64_t most = p.max_pages * p.from.page;
+    p.cluster = 1;
+    if (most <= (int64_t)kSmall * KC::kSelectThreads)
+        return launch_kv(KC::kv_evict_select_kernel<kSmall>, heads, KC::kSelectThreads, s, p);
+    while (p.cluster < KC::kMaxSelectCluster && most > (int64_t)p.cluster * kLarge * KC::kSelectThreads)
+        p.cluster *= 2;
+    return launch_kernel(KC::kv_evict_select_kernel<kLarge>, (unsigned)(heads * p.cluster),
+                         KC::kSelectThreads, 0u, s, false, (unsigned)p.cluster, p);
 }
 
 // K or V of a pool as a 4-D tensor of bytes {head_dim, page, kv_heads, num_pages}; boxes
@@ -226,7 +245,7 @@ int kv_cache_evict_e4m3(const kv_cache_pool *cache, const float *weights, int64_
         !aligned(kept, 4))
         return GEMMRELU_ERR_INVALID_ARG;
     const int64_t heads = batch * cache->kv_heads, moves = heads * to_max_pages;
-    if (heads > kMaxGrid || moves > kMaxGrid)
+    if (heads > kMaxGrid / KC::kMaxSelectCluster || moves > kMaxGrid)
         return GEMMRELU_ERR_INVALID_ARG;
     KC::EvictParams p{};
     p.from = device_pool(cache);
@@ -242,6 +261,7 @@ int kv_cache_evict_e4m3(const kv_cache_pool *cache, const float *weights, int64_
     p.budget = (int)budget;
     p.sinks = (int)sinks;
     p.recent = (int)recent;
+    p.items = (int)moves;
     p.to_lengths = to_lengths;
     p.to_weights = to_weights;
     p.kept = kept;
@@ -250,10 +270,10 @@ int kv_cache_evict_e4m3(const kv_cache_pool *cache, const float *weights, int64_
     if (rc != GEMMRELU_OK)
         return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    rc = launch_kv(KC::kv_evict_select_kernel, heads, KC::kSelectThreads, s, p);
+    rc = launch_select(p, heads, s);
     if (rc != GEMMRELU_OK)
         return rc;
-    return cache->head_dim == 64 ? launch_move<64>(p, moves, s) : launch_move<128>(p, moves, s);
+    return cache->head_dim == 64 ? launch_move<64>(p, ds->sms, s) : launch_move<128>(p, ds->sms, s);
 }
 
 size_t kv_cache_attention_x16_workspace_bytes(int64_t batch, int64_t tokens, int64_t q_heads,
