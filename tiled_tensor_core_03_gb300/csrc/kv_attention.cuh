@@ -203,11 +203,6 @@ __device__ __forceinline__ uint32_t turned(uint32_t x) {
     return r;
 }
 
-__device__ __forceinline__ uint32_t half2_of(float a, float b) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
 __device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
     uint2 v;
     asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");

@@ -78,6 +78,45 @@ __device__ __forceinline__ float storable(float x) {
     return fabsf(x) < INFINITY ? x : __uint_as_float(0x7fffffffu);
 }
 
+// Elementwise larger of two pairs of magnitudes; a NaN gives way to the other.
+template <bool kBf16>
+__device__ __forceinline__ uint32_t larger2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (kBf16)
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else
+        asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Two fp16 values to e4m3, low byte first: round to nearest even; NaN stays NaN.
+__device__ __forceinline__ uint32_t half2_to_e4m3x2(uint32_t h) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+    return r;
+}
+
+// Two fp32 values to an fp16 pair, low half = a.
+__device__ __forceinline__ uint32_t half2_of(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Four e4m3 values times `ratio`, rounded to e4m3 again.
+__device__ __forceinline__ uint32_t rescaled(uint32_t four, float ratio) {
+    const float2 f = e4m3x2_to_float2(four & 0xffffu), g = e4m3x2_to_float2(four >> 16);
+    return to_e4m3x2(f.x * ratio, f.y * ratio) | to_e4m3x2(g.x * ratio, g.y * ratio) << 16;
+}
+
+// The same for a power of two in [2^-14, 2^15] and results of at most 448: fp16 holds the
+// products exactly, but for bits below 2^-24, far below e4m3's smallest half step of 2^-10.
+__device__ __forceinline__ uint32_t rescaled_exact(uint32_t four, uint32_t ratio2) {
+    uint32_t a = e4m3x2_to_half2(four & 0xffffu), b = e4m3x2_to_half2(four >> 16);
+    asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(a) : "r"(ratio2));
+    asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(b) : "r"(ratio2));
+    return half2_to_e4m3x2(a) | half2_to_e4m3x2(b) << 16;
+}
+
 // Largest of the block's non-negative values; `slots` has one word per warp.
 // The barrier inside also orders earlier reads of the block before later writes.
 __device__ __forceinline__ float block_max(float x, uint32_t *slots) {
@@ -154,7 +193,6 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
     constexpr int kPerToken = D / 8;
     const uint16_t *src = p.x[kv] + b * p.stride[kv][0] + h * p.stride[kv][2];
     uint4 x[kVec];
-    float amax = 0.0f;
 #pragma unroll
     for (int n = 0; n < kVec; ++n) {
         const int v = threadIdx.x + n * kAppendThreads, slot = v / kPerToken;
@@ -163,18 +201,31 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
             x[n] = *reinterpret_cast<const uint4 *>(src + (first + slot - start) * p.stride[kv][1] +
                                                     8 * (v % kPerToken));
     }
-#pragma unroll
-    for (int n = 0; n < kVec; ++n) {
-        const uint32_t w[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 f = pair_to_float2<kBf16>(w[e]);
-            amax = fmaxf(amax, fmaxf(finite_abs(f.x), finite_abs(f.y)));
-        }
-    }
     float *scale_at = p.pool.scales[kv] + id * p.pool.kv_heads + h;
     const float held = lo > 0 ? *scale_at : 0.0f;   // 0: a fresh page
-    amax = block_max(amax, slots);
+    uint32_t top = 0;
+#pragma unroll
+    for (int n = 0; n < kVec; ++n) {
+        top = larger2<kBf16>(top, larger2<kBf16>(x[n].x & 0x7fff7fffu, x[n].y & 0x7fff7fffu));
+        top = larger2<kBf16>(top, larger2<kBf16>(x[n].z & 0x7fff7fffu, x[n].w & 0x7fff7fffu));
+    }
+    const float2 tops = pair_to_float2<kBf16>(top);
+    float amax = block_max(fmaxf(tops.x, tops.y), slots);
+    const bool infinite = amax == INFINITY;   // seldom: look again, and store them as NaN
+    if (infinite) {
+        amax = 0.0f;
+#pragma unroll
+        for (int n = 0; n < kVec; ++n) {
+            const uint32_t w[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 f = pair_to_float2<kBf16>(w[e]);
+                amax = fmaxf(amax, fmaxf(finite_abs(f.x), finite_abs(f.y)));
+            }
+        }
+        __syncthreads();
+        amax = block_max(amax, slots);
+    }
     const float scale = fmaxf(held, scale_for(amax));
     const float inv = inverse_scale(scale);
     if (threadIdx.x == 0 && scale != held)
@@ -188,21 +239,17 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
             uint32_t q[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float2 f = pair_to_float2<kBf16>(w[e]);
-                q[e] = to_e4m3x2(storable(f.x) * inv, storable(f.y) * inv);
+                float2 f = pair_to_float2<kBf16>(w[e]);
+                if (infinite)
+                    f = make_float2(storable(f.x), storable(f.y));
+                q[e] = to_e4m3x2(f.x * inv, f.y * inv);
             }
             *reinterpret_cast<uint2 *>(dst + 8 * v) = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
         } else if (slot < lo && scale != held) {
             // an older token of a page whose scale grew
-            uint2 old = *reinterpret_cast<const uint2 *>(dst + 8 * v);
+            const uint2 old = *reinterpret_cast<const uint2 *>(dst + 8 * v);
             const float ratio = held * inv;
-            uint32_t o[2] = {old.x, old.y};
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float2 f = e4m3x2_to_float2(o[e] & 0xffffu), g = e4m3x2_to_float2(o[e] >> 16);
-                o[e] = to_e4m3x2(f.x * ratio, f.y * ratio) | to_e4m3x2(g.x * ratio, g.y * ratio) << 16;
-            }
-            *reinterpret_cast<uint2 *>(dst + 8 * v) = make_uint2(o[0], o[1]);
+            *reinterpret_cast<uint2 *>(dst + 8 * v) = make_uint2(rescaled(old.x, ratio), rescaled(old.y, ratio));
         }
     }
 }
@@ -241,29 +288,35 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-constexpr int kSelectThreads = 1024;
+constexpr int kSelectThreads = 512;
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kMaxSelectCluster = 8;
+constexpr int kShortList = 512;   // keys that one warp finishes alone
 
 // Which tokens stay, a cluster of 1 to 8 blocks per (sequence, head), each with a stretch of
 // the tokens.  Between the sinks and the recent tokens the k heaviest are those above the
 // k-th largest key and the first few equal to it.  The keys are read once into registers
 // (kKeys a thread; what does not fit is read again from L2), and the k-th largest is built
 // two bits at a time from the top: of three candidates the largest that k keys reach.
-// Counting takes 16 rounds of compares whatever the weights are; a histogram of
-// digits had its atomics collide, since weights share exponents: 23 us at 2000 tokens and
-// 51 us at 16384, against 4 and 9 us for this.
+// What bounds it is the rounds' latency and, with many keys, their compares, so once 512
+// keys or fewer share the bits found one warp takes those and finishes alone.
+// Counting takes the same time whatever the weights are; a histogram of digits had its
+// atomics collide, since weights share exponents: 23 us at 2000 tokens and 51 us at 16384.
+// 1024 threads with 16 keys each took 13 and 29 us, most of it in 17 rounds of barriers.
 template <int kKeys>
 __global__ void __launch_bounds__(kSelectThreads, 1) kv_evict_select_kernel(const EvictParams p) {
-    __shared__ int warp_count[2][3][kSelectWarps];
+    __shared__ uint2 warp_count[2][kSelectWarps];
     __shared__ int block_count[2][kMaxSelectCluster][3];
     __shared__ int slot_sure[kKeys * kSelectWarps], slot_tie[kKeys * kSelectWarps];
+    __shared__ uint32_t list[kShortList];
+    __shared__ int shared[4];   // list length, k-th key, keys above it; totals
     pdl_launch_dependents();
     pdl_wait_primary();
     const int cluster = p.cluster, rank = cluster > 1 ? (int)cluster_ctarank() : 0;
     const int64_t bh = blockIdx.x / cluster;
     const int h = (int)(bh % p.from.kv_heads), b = (int)(bh / p.from.kv_heads);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t below = (1u << lane) - 1;
     const int n = checked_length(p.lengths, b, p.max_pages * p.from.page);
     const int m = n < p.budget ? n : p.budget;
     const float *w = p.weights + bh * p.width;
@@ -298,22 +351,42 @@ __global__ void __launch_bounds__(kSelectThreads, 1) kv_evict_select_kernel(cons
             x[1] += key[s] >= c2;
             x[2] += key[s] >= c3;
         }
-        for (int i = t0 + kGroup + tid; i < t1; i += kSelectThreads) {
-            const uint32_t k = key_at(i);
-            x[0] += k >= c1;
-            x[1] += k >= c2;
-            x[2] += k >= c3;
-        }
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            x[i] = __reduce_add_sync(0xffffffffu, x[i]);
+        if (stretch <= kGroup) {
+            // a block's counts stay below 2^16: two in one word
+            const uint32_t two = __reduce_add_sync(0xffffffffu, (uint32_t)x[0] | (uint32_t)x[1] << 16);
+            const uint32_t one = __reduce_add_sync(0xffffffffu, (uint32_t)x[2]);
             if (lane == 0)
-                warp_count[turn][i][warp] = x[i];
-        }
-        __syncthreads();
+                warp_count[turn][warp] = make_uint2(two, one);
+            __syncthreads();
+            uint32_t sum_two = 0, sum_one = 0;
 #pragma unroll
-        for (int i = 0; i < 3; ++i)
-            got[i] = __reduce_add_sync(0xffffffffu, warp_count[turn][i][lane]);
+            for (int i = 0; i < kSelectWarps; ++i) {
+                const uint2 c = warp_count[turn][i];
+                sum_two += c.x;
+                sum_one += c.y;
+            }
+            got[0] = (int)(sum_two & 0xffffu);
+            got[1] = (int)(sum_two >> 16);
+            got[2] = (int)sum_one;
+        } else {
+            for (int i = t0 + kGroup + tid; i < t1; i += kSelectThreads) {
+                const uint32_t k = key_at(i);
+                x[0] += k >= c1;
+                x[1] += k >= c2;
+                x[2] += k >= c3;
+            }
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                x[i] = __reduce_add_sync(0xffffffffu, x[i]);
+                if (lane == 0)
+                    warp_count[turn][warp] = make_uint2((uint32_t)x[i], 0u);
+                __syncthreads();
+                got[i] = 0;
+                for (int k = 0; k < kSelectWarps; ++k)
+                    got[i] += (int)warp_count[turn][k].x;
+                __syncthreads();
+            }
+        }
         if (cluster > 1) {
             if (warp == 0 && lane < cluster) {
                 const uint32_t at = mapa_shared(smem_addr(&block_count[turn][rank][0]), (uint32_t)lane);
@@ -336,15 +409,72 @@ __global__ void __launch_bounds__(kSelectThreads, 1) kv_evict_select_kernel(cons
     uint32_t kth = 0xffffffffu;   // no weight has this key
     int ties_kept = 0;
     if (need > 0) {
+        // `above` keys exceed all those that share the bits found, which `reach` - above do
+        int above = 0, reach = hi - lo, shift = 30;
         kth = 0;
-        for (int shift = 30; shift >= 0; shift -= 2) {
+        for (; shift >= 0; shift -= 2) {
             int got[3];
             count(kth | 1u << shift, kth | 2u << shift, kth | 3u << shift, got);
-            kth |= (uint32_t)(got[2] >= need ? 3 : got[1] >= need ? 2 : got[0] >= need ? 1 : 0) << shift;
+            const int digit = got[2] >= need ? 3 : got[1] >= need ? 2 : got[0] >= need ? 1 : 0;
+            above = digit == 3 ? above : got[digit];
+            reach = digit == 0 ? reach : got[digit - 1];
+            kth |= (uint32_t)digit << shift;
+            if (cluster == 1 && stretch <= kGroup && reach - above <= kShortList)
+                break;
         }
-        int got[3];   // kth < 0xffffffff, which no weight has
-        count(kth + 1, kth + 1, kth + 1, got);
-        ties_kept = need - got[0];
+        if (shift >= 2) {   // (cluster is 1) the keys that share the bits, in no order
+            if (tid == 0)
+                shared[0] = 0;
+            __syncthreads();
+            const uint32_t mask = ~0u << shift;
+#pragma unroll
+            for (int s = 0; s < kKeys; ++s) {
+                const bool in = key[s] != 0 && (key[s] & mask) == kth;
+                const uint32_t who = __ballot_sync(0xffffffffu, in);
+                if (who == 0)
+                    continue;
+                int at = 0;
+                if (lane == 0)
+                    at = atomicAdd(&shared[0], __popc(who));
+                at = __shfl_sync(0xffffffffu, at, 0);
+                if (in)
+                    list[at + __popc(who & below)] = key[s];
+            }
+            __syncthreads();
+            if (warp == 0) {
+                uint32_t mine[kShortList / 32];
+                const int length = shared[0];
+#pragma unroll
+                for (int s = 0; s < kShortList / 32; ++s)
+                    mine[s] = s * 32 + lane < length ? list[s * 32 + lane] : 0u;
+                const int want = need - above;
+                int over = 0;
+                for (shift -= 2; shift >= 0; shift -= 2) {
+                    int x[3] = {0, 0, 0};
+#pragma unroll
+                    for (int s = 0; s < kShortList / 32; ++s) {
+                        x[0] += mine[s] >= (kth | 1u << shift);
+                        x[1] += mine[s] >= (kth | 2u << shift);
+                        x[2] += mine[s] >= (kth | 3u << shift);
+                    }
+                    const uint32_t two = __reduce_add_sync(0xffffffffu, (uint32_t)x[0] | (uint32_t)x[1] << 16);
+                    x[0] = (int)(two & 0xffffu);
+                    x[1] = (int)(two >> 16);
+                    x[2] = (int)__reduce_add_sync(0xffffffffu, (uint32_t)x[2]);
+                    const int digit = x[2] >= want ? 3 : x[1] >= want ? 2 : x[0] >= want ? 1 : 0;
+                    over = digit == 3 ? over : x[digit];
+                    kth |= (uint32_t)digit << shift;
+                }
+                if (lane == 0) {
+                    shared[1] = (int)kth;
+                    shared[2] = above + over;
+                }
+            }
+            __syncthreads();
+            kth = (uint32_t)shared[1];
+            above = shared[2];
+        }
+        ties_kept = need - above;
     }
 
     // survivors and equal keys of the blocks before
@@ -362,13 +492,14 @@ __global__ void __launch_bounds__(kSelectThreads, 1) kv_evict_select_kernel(cons
             look(i, key_at(i));
         sure = __reduce_add_sync(0xffffffffu, sure);
         tie = __reduce_add_sync(0xffffffffu, tie);
-        if (lane == 0) {
-            warp_count[turn][0][warp] = sure;
-            warp_count[turn][1][warp] = tie;
-        }
+        if (lane == 0)
+            warp_count[turn][warp] = make_uint2((uint32_t)sure, (uint32_t)tie);
         __syncthreads();
-        sure = __reduce_add_sync(0xffffffffu, warp_count[turn][0][lane]);
-        tie = __reduce_add_sync(0xffffffffu, warp_count[turn][1][lane]);
+        sure = tie = 0;
+        for (int i = 0; i < kSelectWarps; ++i) {
+            sure += (int)warp_count[turn][i].x;
+            tie += (int)warp_count[turn][i].y;
+        }
         if (warp == 0 && lane < cluster) {
             const uint32_t at = mapa_shared(smem_addr(&block_count[turn][rank][0]), (uint32_t)lane);
             st_cluster_f32(at, __int_as_float(sure));
@@ -383,62 +514,65 @@ __global__ void __launch_bounds__(kSelectThreads, 1) kv_evict_select_kernel(cons
     }
     // write this block's survivors in order, kGroup tokens at a time
     for (int g0 = t0; g0 < t1; g0 += kGroup) {
-        uint32_t sure[kKeys], tie[kKeys];
+        if (g0 > t0) {
+#pragma unroll
+            for (int s = 0; s < kKeys; ++s)
+                key[s] = key_at(g0 + s * kSelectThreads + tid);
+        }
+        auto sure_of = [&](int s) {
+            const int i = g0 + s * kSelectThreads + tid;
+            return __ballot_sync(0xffffffffu, i < t1 && (i < lo || i >= hi || key[s] > kth));
+        };
+        auto tie_of = [&](int s) {
+            const int i = g0 + s * kSelectThreads + tid;
+            return __ballot_sync(0xffffffffu, i < t1 && i >= lo && i < hi && key[s] == kth);
+        };
 #pragma unroll
         for (int s = 0; s < kKeys; ++s) {
-            const int i = g0 + s * kSelectThreads + tid;
-            const uint32_t k = g0 == t0 ? key[s] : key_at(i);
-            const bool in = i < t1, compete = i >= lo && i < hi;
-            sure[s] = __ballot_sync(0xffffffffu, in && (!compete || k > kth));
-            tie[s] = __ballot_sync(0xffffffffu, in && compete && k == kth);
+            const uint32_t sure = sure_of(s), tie = tie_of(s);
             if (lane == 0) {
-                slot_sure[s * kSelectWarps + warp] = __popc(sure[s]);
-                slot_tie[s * kSelectWarps + warp] = __popc(tie[s]);
+                slot_sure[s * kSelectWarps + warp] = __popc(sure);
+                slot_tie[s * kSelectWarps + warp] = __popc(tie);
             }
         }
         __syncthreads();
-        if (warp == 0) {   // exclusive sums in token order, kKeys entries a lane
-            int a[kKeys], c[kKeys], sum_a = 0, sum_c = 0;
+        if (warp < 2) {   // exclusive sums in token order, one warp each
+            int *slot = warp == 0 ? slot_sure : slot_tie;
+            constexpr int kEach = kKeys * kSelectWarps / 32;
+            int a[kEach], sum = 0;
 #pragma unroll
-            for (int s = 0; s < kKeys; ++s) {
-                a[s] = slot_sure[lane * kKeys + s];
-                c[s] = slot_tie[lane * kKeys + s];
-                sum_a += a[s];
-                sum_c += c[s];
+            for (int s = 0; s < kEach; ++s) {
+                a[s] = slot[lane * kEach + s];
+                sum += a[s];
             }
-            int run_a = sum_a, run_c = sum_c;
+            int run = sum;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int x = __shfl_up_sync(0xffffffffu, run_a, o), y = __shfl_up_sync(0xffffffffu, run_c, o);
-                run_a += lane >= o ? x : 0;
-                run_c += lane >= o ? y : 0;
+                const int x = __shfl_up_sync(0xffffffffu, run, o);
+                run += lane >= o ? x : 0;
             }
-            int at_a = run_a - sum_a, at_c = run_c - sum_c;
+            int at = run - sum;
 #pragma unroll
-            for (int s = 0; s < kKeys; ++s) {
-                slot_sure[lane * kKeys + s] = at_a;
-                slot_tie[lane * kKeys + s] = at_c;
-                at_a += a[s];
-                at_c += c[s];
+            for (int s = 0; s < kEach; ++s) {
+                slot[lane * kEach + s] = at;
+                at += a[s];
             }
-            if (lane == 31) {
-                warp_count[0][0][0] = run_a;
-                warp_count[0][0][1] = run_c;
-            }
+            if (lane == 31)
+                shared[2 + warp] = run;
         }
         __syncthreads();
-        const uint32_t below = (1u << lane) - 1;
         const int kept_before = min(ties, ties_kept);
 #pragma unroll
         for (int s = 0; s < kKeys; ++s) {
-            const int rank_tie = ties + slot_tie[s * kSelectWarps + warp] + __popc(tie[s] & below);
-            const int at = out + slot_sure[s * kSelectWarps + warp] + __popc(sure[s] & below) +
+            const uint32_t sure = sure_of(s), tie = tie_of(s);
+            const int rank_tie = ties + slot_tie[s * kSelectWarps + warp] + __popc(tie & below);
+            const int at = out + slot_sure[s * kSelectWarps + warp] + __popc(sure & below) +
                            min(rank_tie, ties_kept) - kept_before;
-            const bool stays = (sure[s] >> lane & 1u) || ((tie[s] >> lane & 1u) && rank_tie < ties_kept);
+            const bool stays = (sure >> lane & 1u) || ((tie >> lane & 1u) && rank_tie < ties_kept);
             if (stays)
                 kept[at] = g0 + s * kSelectThreads + tid;
         }
-        const int more_sure = warp_count[0][0][0], more_ties = warp_count[0][0][1];
+        const int more_sure = shared[2], more_ties = shared[3];
         ties += more_ties;
         out += more_sure + min(ties, ties_kept) - kept_before;
         __syncthreads();
@@ -453,7 +587,7 @@ constexpr int kMoveThreads = 256;
 // away (its position, its page, itself), so a block walks over items and reads the next
 // item's positions and pages while this one's bytes are under way.
 template <int D, int kVec>
-__global__ void __launch_bounds__(kMoveThreads) kv_evict_move_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(kMoveThreads, kVec == 4 ? 2 : 4) kv_evict_move_kernel(const EvictParams p) {
     __shared__ uint32_t slots[2][2][kMoveThreads / 32];
     pdl_launch_dependents();
     pdl_wait_primary();
@@ -538,12 +672,14 @@ __global__ void __launch_bounds__(kMoveThreads) kv_evict_move_kernel(const Evict
 #pragma unroll
             for (int n = 0; n < kVec; ++n) {
                 const uint32_t w[4] = {v[kv][n].x, v[kv][n].y, v[kv][n].z, v[kv][n].w};
+                uint32_t top = 0;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float2 f = e4m3x2_to_float2(w[e] & 0xffffu), g = e4m3x2_to_float2(w[e] >> 16);
-                    amax = fmaxf(amax, fmaxf(fmaxf(finite_abs(f.x), finite_abs(f.y)),
-                                             fmaxf(finite_abs(g.x), finite_abs(g.y))) * s[kv][n]);
+                    top = larger2<false>(top, e4m3x2_to_half2(w[e] & 0x7f7fu));
+                    top = larger2<false>(top, e4m3x2_to_half2(w[e] >> 16 & 0x7f7fu));
                 }
+                const float2 f = pair_to_float2<false>(top);
+                amax = fmaxf(amax, fmaxf(f.x, f.y) * s[kv][n]);
             }
             // the words alternate between items: one barrier each
             amax = block_max(amax, slots[turn][kv]);
@@ -558,10 +694,17 @@ __global__ void __launch_bounds__(kMoveThreads) kv_evict_move_kernel(const Evict
                     break;
                 const float ratio = s[kv][n] * inv;
                 uint32_t w[4] = {v[kv][n].x, v[kv][n].y, v[kv][n].z, v[kv][n].w};
+                // a power of two that fp16 holds (or 0: nothing there)
+                const uint32_t r = __float_as_uint(ratio);
+                if ((r & 0x7fffffu) == 0 && ratio <= 32768.0f && (ratio >= 0x1p-14f || r == 0)) {
+                    const uint32_t ratio2 = half2_of(ratio, ratio);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 f = e4m3x2_to_float2(w[e] & 0xffffu), g = e4m3x2_to_float2(w[e] >> 16);
-                    w[e] = to_e4m3x2(f.x * ratio, f.y * ratio) | to_e4m3x2(g.x * ratio, g.y * ratio) << 16;
+                    for (int e = 0; e < 4; ++e)
+                        w[e] = rescaled_exact(w[e], ratio2);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        w[e] = rescaled(w[e], ratio);
                 }
                 *reinterpret_cast<uint4 *>(dst + 16 * i) = make_uint4(w[0], w[1], w[2], w[3]);
             }

@@ -86,7 +86,7 @@ int launch_move(const KC::EvictParams &p, int sms, cudaStream_t s) {
 
 // A cluster of blocks holds a sequence's keys in registers as far as 8 blocks go.
 int launch_select(KC::EvictParams &p, int64_t heads, cudaStream_t s) {
-    constexpr int kSmall = 4, kLarge = 16;
+    constexpr int kSmall = 8, kLarge = 32;   // keys a thread
     const int64_t most = p.max_pages * p.from.page;
     p.cluster = 1;
     if (most <= (int64_t)kSmall * KC::kSelectThreads)
