@@ -19,6 +19,12 @@
 //    never loaded, so the work is proportional to the window.  Where the two tiles are
 //    at different queries the list is the union, and each tile skips the blocks that it does
 //    not see.
+//  - A CTA stays and walks over work items, and every hand-off is counted across them: the
+//    next item's Q, K and V arrive and its first scores are computed while this one's last
+//    softmax and its output are still under way.  With a CTA per item, a window of 8
+//    blocks spent a quarter of its time starting and ending.
+//  - Of a block whose window part is past only the sinks are left; up to 32 of them
+//    are computed as a block of 32 keys instead of 128.
 //  - Scores are masked only in blocks where some row does not see some key: the
 //    diagonal's, the window's low end, the sinks'.
 //  - A key that a row does not see has weight 0, and 0 times a NaN or an infinity in its V
@@ -43,6 +49,7 @@ struct WindowParams {
     uint16_t *o;                   // [batch][n_q][q_heads][d]
     int n_q, n_kv, q_heads, group;
     int q_tiles, items;            // items = q_tiles * group: tiles of one K/V head
+    int kv_heads, batch;
     int pairs, window, sinks;
     float scale;                   // log2(e) / sqrt(d)
     int drop_arrive;
@@ -142,63 +149,131 @@ __device__ __noinline__ void window_row(const WindowParams &p, int batch, int he
     }
 }
 
+// Shared memory of flash_attention.cuh with more barriers: q_full, q_empty, k_full[kKV],
+// v_full[kKV], kv_empty[kKV], s_full[2], p_full[2], o_full[2], o_empty[2], drain.
+template <int HD>
+struct WindowCfg : Cfg<HD> {
+    static constexpr uint32_t kNumBars = 2 + 3 * kKV + 8 + 1;
+    static constexpr uint32_t kOffMisc = Cfg<HD>::kOffBar + kNumBars * 8;
+    static constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;
+    static constexpr int kNarrow = 32;   // keys of a block with few sinks only
+    static constexpr uint32_t kIdescNarrow = make_idesc_f16_f32(BM, kNarrow, 0, 0);
+};
+
+// Three warpgroups: two of softmax, one with the producer's and the issuer's warp.  384 threads
+// launch with 168 registers; the third warpgroup keeps 72 and the others take 216 each, which
+// holds a row's 128 scores and the loop around them: 2 * 216 + 72 = 3 * 168.
+constexpr int kWindowThreads = 384;
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 216, kOtherRegs = 72;
+static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kLaunchRegs, "registers given back cover those taken");
+
+// wait_bounded_eager by a whole warp, with one answer.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, uint64_t limit_ns,
+                                          volatile uint32_t *abort_flag, unsigned where) {
+    return __all_sync(0xffffffffu, wait_bounded_eager(bar, parity, limit_ns, abort_flag, where));
+}
+
+// The entries of a block list that a tile takes part in: [0, head) and [from, to).
+struct Turns {
+    int head, from, to;
+    __device__ __forceinline__ bool has(int j) const { return j < head || (j >= from && j < to); }
+    __device__ __forceinline__ int count() const { return head + to - from; }
+};
+
+// A work item: two neighbouring tiles of one K/V head, and the list of the blocks that either
+// sees: entries 0 .. sinks - 1 are the first blocks, the others follow from block low.
+struct WindowItem {
+    int kvh, batch;
+    int tile0, tile1, head0, head1;
+    bool two;
+    int sinks, low, nb;
+    int narrow;              // the entry with no more than 32 sinks and nothing else, or -1
+    Turns t0, t1;
+    __device__ __forceinline__ int block(int j) const { return j < sinks ? j : low + (j - sinks); }
+};
+
+template <int HD>
+__device__ __forceinline__ WindowItem window_item(const WindowParams &p, int index) {
+    WindowItem w;
+    // the last queries see the most keys: they go first
+    const int pair = p.pairs - 1 - index % p.pairs, off = p.n_kv - p.n_q, item = 2 * pair;
+    index /= p.pairs;
+    w.kvh = index % p.kv_heads;
+    w.batch = index / p.kv_heads;
+    w.two = item + 1 < p.items;
+    w.tile0 = item / p.group;
+    const int g = item - w.tile0 * p.group;
+    w.head0 = w.kvh * p.group + g;
+    const bool same = g + 1 < p.group;   // the second tile: the next head, or the next queries
+    w.tile1 = same ? w.tile0 : w.tile0 + 1;
+    w.head1 = same ? w.head0 + 1 : w.kvh * p.group;
+    auto seen_by = [&](int tile) {
+        return blocks_seen(tile * BM + off, min(tile * BM + BM, p.n_q) - 1 + off, p.window, p.sinks);
+    };
+    const Blocks b0 = seen_by(w.tile0), b1 = !w.two ? Blocks{0, 0, 0} : same ? b0 : seen_by(w.tile1);
+    Blocks all = b0;
+    if (b1.count() > 0) {
+        if (b0.count() == 0) {
+            all = b1;
+        } else {
+            all.low = min(b0.low, b1.low);
+            all.high = max(b0.high, b1.high);
+            all.sinks = min(max(b0.sinks, b1.sinks), all.low);
+        }
+    }
+    auto turns_of = [&](const Blocks &b) {
+        if (b.count() == 0)
+            return Turns{0, 0, 0};
+        // (a tile's first blocks may reach into the part from `low` on)
+        const int head = b.sinks <= all.sinks ? b.sinks : all.sinks + max(0, b.sinks - all.low);
+        return Turns{head, all.sinks + b.low - all.low, all.sinks + b.high - all.low};
+    };
+    w.sinks = all.sinks;
+    w.low = all.low;
+    w.nb = all.count();
+    w.t0 = turns_of(b0);
+    w.t1 = turns_of(b1);
+    const int last = p.sinks / BN, left = p.sinks - last * BN;
+    w.narrow = left > 0 && left <= WindowCfg<HD>::kNarrow && last < all.sinks ? last : -1;
+    return w;
+}
+
 template <int HD, bool kBf16>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kWindowThreads, 1)
     flash_attention_window_kernel(const __grid_constant__ CUtensorMap tmQ,
                                   const __grid_constant__ CUtensorMap tmK,
                                   const __grid_constant__ CUtensorMap tmV,
                                   const __grid_constant__ WindowParams p) {
-    using G = Cfg<HD>;
+    using G = WindowCfg<HD>;
     constexpr uint32_t kIdescS = with_type(G::kIdescS, kBf16);
     constexpr uint32_t kIdescO = with_type(G::kIdescO, kBf16);
+    constexpr uint32_t kIdescNarrow = with_type(G::kIdescNarrow, kBf16);
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *gbase = smem_raw + (base - raw);
 
     const uint32_t bar0 = base + G::kOffBar;
-    const uint32_t q_full = bar0;
-    auto k_full = [&](uint32_t s) { return bar0 + 8u * (1 + s); };
-    auto v_full = [&](uint32_t s) { return bar0 + 8u * (1 + kKV + s); };
-    auto kv_empty = [&](uint32_t s) { return bar0 + 8u * (1 + 2 * kKV + s); };
-    auto s_full = [&](uint32_t t) { return bar0 + 8u * (1 + 3 * kKV + t); };
-    auto p_full = [&](uint32_t t) { return bar0 + 8u * (3 + 3 * kKV + t); };
-    const uint32_t o_full = bar0 + 8u * (5 + 3 * kKV);
-    const uint32_t drain_bar = bar0 + 8u * (6 + 3 * kKV);
+    const uint32_t q_full = bar0, q_empty = bar0 + 8u;
+    auto k_full = [&](uint32_t s) { return bar0 + 8u * (2 + s); };
+    auto v_full = [&](uint32_t s) { return bar0 + 8u * (2 + kKV + s); };
+    auto kv_empty = [&](uint32_t s) { return bar0 + 8u * (2 + 2 * kKV + s); };
+    auto s_full = [&](uint32_t t) { return bar0 + 8u * (2 + 3 * kKV + t); };
+    auto p_full = [&](uint32_t t) { return bar0 + 8u * (4 + 3 * kKV + t); };
+    auto o_full = [&](uint32_t t) { return bar0 + 8u * (6 + 3 * kKV + t); };
+    auto o_empty = [&](uint32_t t) { return bar0 + 8u * (8 + 3 * kKV + t); };
+    const uint32_t drain_bar = bar0 + 8u * (10 + 3 * kKV);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + G::kOffMisc);
     volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(gbase + G::kOffMisc + 4);
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);   // uniform
     const int lane = threadIdx.x & 31;
-    const int kvh = blockIdx.y, batch = blockIdx.z;
     const int off = p.n_kv - p.n_q;
-    // the last queries see the most keys: they go first
-    const int item0 = 2 * (p.pairs - 1 - (int)blockIdx.x);
-    const bool two = item0 + 1 < p.items;
-    const int tile0 = item0 / p.group, tile1 = (item0 + 1) / p.group;
-    const int head0 = kvh * p.group + item0 % p.group, head1 = kvh * p.group + (item0 + 1) % p.group;
-    auto seen_by = [&](int tile) {
-        const int last = min(tile * BM + BM, p.n_q) - 1;
-        return blocks_seen(tile * BM + off, last + off, p.window, p.sinks);
-    };
-    const Blocks s0 = seen_by(tile0);
-    const Blocks s1 = two ? seen_by(tile1) : Blocks{0, 0, 0};
-    // the list: the union, in order
-    Blocks all = s0;
-    if (s1.count() > 0) {
-        if (s0.count() == 0) {
-            all = s1;
-        } else {
-            all.low = min(s0.low, s1.low);
-            all.high = max(s0.high, s1.high);
-            all.sinks = min(max(s0.sinks, s1.sinks), all.low);
-        }
-    }
-    const int nb = all.count();
-    auto block_of = [&](int j) { return j < all.sinks ? j : all.low + (j - all.sinks); };
+    const int total = p.pairs * p.kv_heads * p.batch;
 
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1u);
+        mbar_init(q_empty, 1u);
         for (uint32_t s = 0; s < (uint32_t)kKV; ++s) {
             mbar_init(k_full(s), 1u);
             mbar_init(v_full(s), 1u);
@@ -207,8 +282,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (uint32_t t = 0; t < (uint32_t)kTiles; ++t) {
             mbar_init(s_full(t), 1u);
             mbar_init(p_full(t), 4u);
+            mbar_init(o_full(t), 1u);
+            mbar_init(o_empty(t), 4u);
         }
-        mbar_init(o_full, 1u);
         mbar_init(drain_bar, 1u);
         *abort_flag = 0u;
         fence_mbar_init();
@@ -229,248 +305,333 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
     pdl_wait_primary();  // the previous grid of the stream has completed
 
-    if (warp == kProducerWarp) {
+    if (warp >= kProducerWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         // ============================================================ TMA producer
-        if (lane == 0 && nb > 0) {
-            uint32_t issued = 0, parity = 0;  // K/V stages with copies in flight
-            bool q_issued = false;
-            if (!(p.drop_arrive && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)) {
-                mbar_arrive_expect_tx(q_full, (two ? 2u : 1u) * G::kQBytes);
-                for (int t = 0; t < (two ? 2 : 1); ++t)
+        if (warp == kProducerWarp && lane == 0) {
+            uint32_t queries = 0, blocks = 0;   // Q loads and K/V blocks issued
+            bool ok = !(p.drop_arrive && blockIdx.x == 0);
+            for (int index = blockIdx.x; ok && index < total; index += gridDim.x) {
+                const WindowItem w = window_item<HD>(p, index);
+                if (w.nb == 0)
+                    continue;
+                if (!wait_bounded_eager(q_empty, (queries & 1u) ^ 1u, p.wait_limit_ns, abort_flag,
+                                        kSiteProducerEmpty))
+                    break;
+                mbar_arrive_expect_tx(q_full, (w.two ? 2u : 1u) * G::kQBytes);
+                for (int t = 0; t < (w.two ? 2 : 1); ++t)
 #pragma unroll
                     for (int d = 0; d < G::kDSub; ++d)
                         tma_load_4d(&tmQ, base + G::kOffQ + t * G::kQBytes + d * kSub, q_full,
-                                    64 * d, t ? head1 : head0, (t ? tile1 : tile0) * BM, batch);
-                q_issued = true;
-            }
-            for (int j = 0; j < nb; ++j) {
-                const uint32_t st = (uint32_t)(j % kKV), ph = (uint32_t)((j / kKV) & 1);
-                if (!wait_bounded_eager(kv_empty(st), ph ^ 1u, p.wait_limit_ns, abort_flag,
-                                  kSiteProducerEmpty))
-                    break;
-                const int key = block_of(j) * BN;
-                mbar_arrive_expect_tx(k_full(st), G::kKBytes);
+                                    64 * d, t ? w.head1 : w.head0, (t ? w.tile1 : w.tile0) * BM, w.batch);
+                ++queries;
+                for (int j = 0; j < w.nb; ++j) {
+                    const uint32_t st = blocks % kKV, ph = blocks / kKV & 1u;
+                    ok = wait_bounded_eager(kv_empty(st), ph ^ 1u, p.wait_limit_ns, abort_flag,
+                                            kSiteProducerEmpty);
+                    if (!ok)
+                        break;
+                    const int key = w.block(j) * BN;
+                    mbar_arrive_expect_tx(k_full(st), G::kKBytes);
 #pragma unroll
-                for (int d = 0; d < G::kDSub; ++d)
-                    tma_load_4d(&tmK, base + G::kOffK + st * G::kKBytes + d * kSub, k_full(st),
-                                64 * d, kvh, key, batch);
-                mbar_arrive_expect_tx(v_full(st), G::kVBytes);
+                    for (int d = 0; d < G::kDSub; ++d)
+                        tma_load_4d(&tmK, base + G::kOffK + st * G::kKBytes + d * kSub, k_full(st),
+                                    64 * d, w.kvh, key, w.batch);
+                    mbar_arrive_expect_tx(v_full(st), G::kVBytes);
 #pragma unroll
-                for (int d = 0; d < G::kDSub; ++d)
-                    tma_load_4d(&tmV, base + G::kOffV + st * G::kVBytes + d * kSub, v_full(st),
-                                64 * d, kvh, key, batch);
-                issued |= 1u << st;
-                parity = (parity & ~(1u << st)) | (ph << st);
+                    for (int d = 0; d < G::kDSub; ++d)
+                        tma_load_4d(&tmV, base + G::kOffV + st * G::kVBytes + d * kSub, v_full(st),
+                                    64 * d, w.kvh, key, w.batch);
+                    ++blocks;
+                }
             }
             // every copy issued must have landed before the CTA may exit
-            if (q_issued)
-                wait_drain(q_full, 0u, p.wait_limit_ns, abort_flag);
-            for (uint32_t s = 0; s < (uint32_t)kKV; ++s)
-                if (issued & (1u << s)) {
-                    wait_drain(k_full(s), (parity >> s) & 1u, p.wait_limit_ns, abort_flag);
-                    wait_drain(v_full(s), (parity >> s) & 1u, p.wait_limit_ns, abort_flag);
-                }
+            if (queries > 0)
+                wait_drain(q_full, (queries - 1) & 1u, p.wait_limit_ns, abort_flag);
+            for (uint32_t i = blocks > (uint32_t)kKV ? blocks - kKV : 0u; i < blocks; ++i) {
+                wait_drain(k_full(i % kKV), i / kKV & 1u, p.wait_limit_ns, abort_flag);
+                wait_drain(v_full(i % kKV), i / kKV & 1u, p.wait_limit_ns, abort_flag);
+            }
         }
-    } else if (warp == kMmaWarp) {
         // ============================================================ MMA issuer
-        if (lane == 0 && nb > 0) {
-            bool ok = wait_bounded_eager(q_full, 0u, p.wait_limit_ns, abort_flag, kSiteMmaFull);
-            uint32_t done0 = 0, done1 = 0;   // P V products of each tile so far
-            // S_t = Q_t K_j^T
-            auto score = [&](int t, int j) -> bool {
-                const uint32_t st = (uint32_t)(j % kKV), ph = (uint32_t)((j / kKV) & 1);
-                if (!wait_bounded_eager(k_full(st), ph, p.wait_limit_ns, abort_flag, kSiteMmaFull))
+        if (warp == kMmaWarp) {
+            // One thread issues, but the whole warp walks along: control flow and operands are
+            // then uniform, and the MMAs' descriptors stay in uniform registers.  Inside a
+            // branch of one lane each of them was moved there instruction by instruction, and
+            // issuing bound the kernel (2600 to 4100 cycles a block of 128 keys against 2048 for
+            // the MMAs).  An item's list is worked out during the item before it.
+            const bool leader = lane == 0;
+            const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0);
+            const uint64_t q_desc = make_sdesc_sw128(base + G::kOffQ, 16, 1024);
+            const uint64_t k_desc = make_sdesc_sw128(base + G::kOffK, 16, 1024);
+            const uint64_t v_desc = make_sdesc_sw128(base + G::kOffV, kSub, 1024);
+            bool ok = true;
+            uint32_t queries = 0;                 // items with blocks so far
+            uint32_t blocks = 0;                  // K/V blocks before the one in hand
+            uint32_t turns0 = 0, turns1 = 0;      // P V products of each tile so far
+            uint32_t outs0 = 0, outs1 = 0;        // items of each tile with an output so far
+            // S_t = Q_t K^T of block number i
+            auto score = [&](const uint32_t t, uint32_t i, bool narrow) -> bool {
+                const uint32_t st = i % kKV;
+                if (!wait_warp(k_full(st), i / kKV & 1u, p.wait_limit_ns, abort_flag, kSiteMmaFull))
                     return false;
                 tc_fence_after_sync();
-                const uint64_t qd = make_sdesc_sw128(base + G::kOffQ + t * G::kQBytes, 16, 1024);
-                const uint64_t kd = make_sdesc_sw128(base + G::kOffK + st * G::kKBytes, 16, 1024);
-                const uint32_t d_s = tmem_base + G::kTmemS + t * BN;
+                const uint64_t qd = q_desc + t * (G::kQBytes >> 4), kd = k_desc + st * (G::kKBytes >> 4);
+                const uint32_t idesc = narrow ? kIdescNarrow : kIdescS;
 #pragma unroll
                 for (int kk = 0; kk < HD / UKA; ++kk) {
-                    const uint64_t o = (uint64_t)((kk / 4) * (kSub >> 4) + (kk % 4) * 2);
-                    umma_f16(d_s, qd + o, kd + o, kIdescS, kk > 0 ? 1u : 0u);
+                    const uint32_t o = (kk / 4) * (kSub >> 4) + (kk % 4) * 2;
+                    if (leader)
+                        umma_f16(tmem + G::kTmemS + t * BN, qd + o, kd + o, idesc, kk > 0 ? 1u : 0u);
                 }
-                umma_commit(s_full(t));
+                if (leader)
+                    umma_commit(s_full(t));
                 return true;
             };
-            // O_t += P_t V_j, P_t from TMEM (over S_t)
-            auto pv = [&](int t, int j, uint32_t &done) -> bool {
-                const uint32_t st = (uint32_t)(j % kKV), ph = (uint32_t)((j / kKV) & 1);
-                if (!wait_bounded_eager(p_full(t), done & 1u, p.wait_limit_ns, abort_flag,
-                                  kSiteMmaAccEmpty) ||
-                    !wait_bounded_eager(v_full(st), ph, p.wait_limit_ns, abort_flag, kSiteMmaFull))
+            // O_t += P_t V of block number i, P_t from TMEM (over S_t); O_t starts afresh with
+            // an item's first block, and is complete with its last
+            auto pv = [&](const uint32_t t, uint32_t i, bool narrow, bool fresh, bool complete,
+                          uint32_t &turns, uint32_t &outs) -> bool {
+                const uint32_t st = i % kKV;
+                if (!wait_warp(v_full(st), i / kKV & 1u, p.wait_limit_ns, abort_flag, kSiteMmaFull) ||
+                    (fresh && !wait_warp(o_empty(t), (outs & 1u) ^ 1u, p.wait_limit_ns, abort_flag,
+                                                  kSiteMmaAccEmpty)) ||
+                    !wait_warp(p_full(t), turns & 1u, p.wait_limit_ns, abort_flag, kSiteMmaAccEmpty))
                     return false;
                 tc_fence_after_sync();
-                const uint64_t vd = make_sdesc_sw128(base + G::kOffV + st * G::kVBytes, kSub, 1024);
-                const uint32_t d_o = tmem_base + G::kTmemO + t * HD;
-                const uint32_t a_p = tmem_base + G::kTmemS + t * BN;
+                const uint64_t vd = v_desc + st * (G::kVBytes >> 4);
+                const uint32_t d_o = tmem + G::kTmemO + t * HD, a_p = tmem + G::kTmemS + t * BN;
+                if (leader)
+                    umma_f16_ts(d_o, a_p, vd, kIdescO, fresh ? 0u : 1u);
 #pragma unroll
-                for (int kk = 0; kk < BN / UKA; ++kk)
-                    umma_f16_ts(d_o, a_p + kk * (UKA / 2), vd + (uint64_t)(kk * ((UKA * 128) >> 4)),
-                                kIdescO, (done > 0 || kk > 0) ? 1u : 0u);
-                ++done;
+                for (int kk = 1; kk < G::kNarrow / UKA; ++kk)
+                    if (leader)
+                        umma_f16_ts(d_o, a_p + kk * (UKA / 2), vd + kk * ((UKA * 128) >> 4), kIdescO, 1u);
+                if (!narrow) {
+#pragma unroll
+                    for (int kk = G::kNarrow / UKA; kk < BN / UKA; ++kk)
+                        if (leader)
+                            umma_f16_ts(d_o, a_p + kk * (UKA / 2), vd + kk * ((UKA * 128) >> 4), kIdescO, 1u);
+                }
+                ++turns;
+                if (complete) {
+                    if (leader)
+                        umma_commit(o_full(t));
+                    ++outs;
+                }
                 return true;
             };
-            if (ok && s0.has(block_of(0)))
-                ok = score(0, 0);
-            if (ok && s1.has(block_of(0)))
-                ok = score(1, 0);
-            for (int j = 0; ok && j < nb; ++j) {
-                const int blk = block_of(j), next = j + 1 < nb ? block_of(j + 1) : -1;
-                if (s0.has(blk))
-                    ok = pv(0, j, done0);
-                if (ok && next >= 0 && s0.has(next))
-                    ok = score(0, j + 1);
-                if (ok && s1.has(blk))
-                    ok = pv(1, j, done1);
-                if (!ok)
-                    break;
-                umma_commit(kv_empty((uint32_t)(j % kKV)));
-                if (next >= 0 && s1.has(next))
-                    ok = score(1, j + 1);
+            WindowItem w{};
+            if ((int)blockIdx.x < total)
+                w = window_item<HD>(p, blockIdx.x);
+            for (int index = blockIdx.x; ok && index < total;) {
+                const int nb = w.nb, narrow = w.narrow;
+                const Turns t0 = w.t0, t1 = w.t1;
+                if (nb > 0) {
+                    ok = wait_warp(q_full, queries & 1u, p.wait_limit_ns, abort_flag, kSiteMmaFull);
+                    ++queries;
+                    if (ok && t0.has(0))
+                        ok = score(0, blocks, narrow == 0);
+                    if (ok && t1.has(0))
+                        ok = score(1, blocks, narrow == 0);
+                    if (ok && nb == 1 && leader)
+                        umma_commit(q_empty);
+                }
+                index += gridDim.x;
+                if (index < total)
+                    w = window_item<HD>(p, index);
+                bool fresh0 = true, fresh1 = true;
+                for (int j = 0; ok && j < nb; ++j, ++blocks) {
+                    const bool here = j == narrow, there = j + 1 == narrow, more = j + 1 < nb;
+                    if (t0.has(j)) {
+                        ok = pv(0, blocks, here, fresh0, j + 1 == t0.to, turns0, outs0);
+                        fresh0 = false;
+                    }
+                    if (ok && more && t0.has(j + 1))
+                        ok = score(0, blocks + 1, there);
+                    if (ok && t1.has(j)) {
+                        ok = pv(1, blocks, here, fresh1, j + 1 == t1.to, turns1, outs1);
+                        fresh1 = false;
+                    }
+                    if (!ok)
+                        break;
+                    if (leader)
+                        umma_commit(kv_empty(blocks % kKV));
+                    if (more && t1.has(j + 1))
+                        ok = score(1, blocks + 1, there);
+                    if (ok && j + 2 == nb && leader)
+                        umma_commit(q_empty);   // the item's last scores
+                }
             }
-            if (ok)
-                umma_commit(o_full);
             // all MMAs of this thread complete before TMEM can be released
-            umma_commit(drain_bar);
+            if (leader)
+                umma_commit(drain_bar);
             wait_drain(drain_bar, 0u, p.wait_limit_ns, abort_flag);
         }
+        // (the other two warps complete the warpgroup)
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         // ============================================================ softmax / output
         const int t = warp >> 2;                        // tile
         const int q = warp & 3;                         // TMEM lanes 32q .. 32q+31
-        const int tile = t ? tile1 : tile0, head = t ? head1 : head0;
-        const Blocks mine = t ? s1 : s0;
-        const int qi = tile * BM + 32 * q + lane;       // query index
-        const int pos = qi + off;
-        const int first = tile * BM + off, last = min(tile * BM + BM, p.n_q) - 1 + off;
         const uint32_t lane_base = (uint32_t)(32 * q) << 16;
         const uint32_t s_addr = tmem_base + lane_base + G::kTmemS + t * BN;
         const uint32_t o_addr = tmem_base + lane_base + G::kTmemO + t * HD;
-        float m = -INFINITY, l = 0.0f;
+        uint32_t turns = 0, outputs = 0;
         bool alive = true;
-        uint32_t turn = 0;
-        for (int j = 0; j < nb; ++j) {
-            const int blk = block_of(j);
-            if (!mine.has(blk))
+        for (int index = blockIdx.x; alive && index < total; index += gridDim.x) {
+            const WindowItem w = window_item<HD>(p, index);
+            if (t == 1 && !w.two)
                 continue;
-            const bool ok = wait_bounded_eager(s_full((uint32_t)t), turn & 1u, p.wait_limit_ns,
-                                         abort_flag, kSiteEpiAccFull);
-            if (!__all_sync(0xffffffffu, ok)) {
-                alive = false;
-                break;
-            }
-            tc_fence_after_sync();
-            const int key0 = blk * BN;
-            // some row does not see some key of the block
-            const bool masked = key0 + BN - 1 > first ||
-                                (p.window > 0 && key0 <= last - p.window && key0 + BN > p.sinks);
-            uint32_t v[BN];
+            const int tile = t ? w.tile1 : w.tile0, head = t ? w.head1 : w.head0;
+            const Turns mine = t ? w.t1 : w.t0;
+            const int qi = tile * BM + 32 * q + lane;       // query index
+            const int pos = qi + off;
+            const int first = tile * BM + off, last = min(tile * BM + BM, p.n_q) - 1 + off;
+            float m = -INFINITY, l = 0.0f;
+            uint32_t done = 0;
+            // one block of kKeys keys: scores from TMEM, P as 16-bit pairs over them
+            auto softmax = [&](auto keys, int key0, bool masked) {
+                constexpr int kKeys = decltype(keys)::value;
+                uint32_t v[kKeys];
 #pragma unroll
-            for (int c0 = 0; c0 < BN; c0 += 32)
-                tmem_ld_x32(s_addr + c0, *reinterpret_cast<uint32_t(*)[32]>(&v[c0]));
+                for (int c0 = 0; c0 < kKeys; c0 += 32)
+                    tmem_ld_x32(s_addr + c0, *reinterpret_cast<uint32_t(*)[32]>(&v[c0]));
 #pragma unroll
-            for (int c0 = 0; c0 < BN; c0 += 32)
-                tmem_ld_wait_regs(*reinterpret_cast<uint32_t(*)[32]>(&v[c0]));
-            if (masked) {
-                const int hi = pos - key0;
-                const int lo = p.window > 0 ? hi - p.window : -1;   // seen above it, or below `head`
-                const int head_end = p.sinks - key0;
+                for (int c0 = 0; c0 < kKeys; c0 += 32)
+                    tmem_ld_wait_regs(*reinterpret_cast<uint32_t(*)[32]>(&v[c0]));
+                if (masked) {
+                    const int hi = pos - key0;
+                    const int lo = p.window > 0 ? hi - p.window : -1;   // seen above it, or below `head`
+                    const int head_end = p.sinks - key0;
 #pragma unroll
-                for (int i = 0; i < BN; ++i)
-                    v[i] = i <= hi && (i > lo || i < head_end) ? v[i] : __float_as_uint(-INFINITY);
-            }
-            float mx0 = -INFINITY, mx1 = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < BN; i += 2) {
-                mx0 = fmaxf(mx0, __uint_as_float(v[i]));
-                mx1 = fmaxf(mx1, __uint_as_float(v[i + 1]));
-            }
-            const float m_blk = fmaxf(mx0, mx1) * p.scale;   // scale > 0
-            // move the reference only when the maximum grew by more than kRescaleLog2;
-            // -infinity until the row has seen a key
-            const bool move = m_blk > m + kRescaleLog2;
-            const float m_new = move ? m_blk : m;
-            const float alpha = move ? fast_exp2(m - m_new) : 1.0f;   // 0 at the first block
-            const float m_ref = m_new == -INFINITY ? 0.0f : m_new;
-            const float2 sc2 = make_float2(p.scale, p.scale), nm2 = make_float2(-m_ref, -m_ref);
-            float2 sa = make_float2(0.0f, 0.0f), sb = make_float2(0.0f, 0.0f);
-#pragma unroll
-            for (int c0 = 0; c0 < BN; c0 += 32) {
-                uint32_t ph[16];
-#pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                    const float2 x01 = __ffma2_rn(
-                        make_float2(__uint_as_float(v[c0 + i]), __uint_as_float(v[c0 + i + 1])), sc2, nm2);
-                    const float2 x23 = __ffma2_rn(
-                        make_float2(__uint_as_float(v[c0 + i + 2]), __uint_as_float(v[c0 + i + 3])), sc2, nm2);
-                    const float2 e01 = make_float2(fast_exp2(x01.x), fast_exp2(x01.y));
-                    const float2 e23 = make_float2(fast_exp2(x23.x), fast_exp2(x23.y));
-                    sa = __fadd2_rn(sa, e01);
-                    sb = __fadd2_rn(sb, e23);
-                    ph[i / 2] = pack_pair<kBf16>(e01.x, e01.y);
-                    ph[i / 2 + 1] = pack_pair<kBf16>(e23.x, e23.y);
+                    for (int i = 0; i < kKeys; ++i)
+                        v[i] = i <= hi && (i > lo || i < head_end) ? v[i] : __float_as_uint(-INFINITY);
                 }
-                tmem_st_x16(s_addr + c0 / 2, ph);
-            }
-            l = l * alpha + ((sa.x + sa.y) + (sb.x + sb.y));
-            m = m_new;
-            // rescale this warp's output rows when any of their references moved
-            // (the previous P V of this tile completed before S_j was written)
-            if (turn > 0 && __any_sync(0xffffffffu, move)) {
+                float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < kKeys; i += 2) {
+                    mx0 = fmaxf(mx0, __uint_as_float(v[i]));
+                    mx1 = fmaxf(mx1, __uint_as_float(v[i + 1]));
+                }
+                const float m_blk = fmaxf(mx0, mx1) * p.scale;   // scale > 0
+                // move the reference only when the maximum grew by more than kRescaleLog2;
+                // -infinity until the row has seen a key
+                const bool move = m_blk > m + kRescaleLog2;
+                const float m_new = move ? m_blk : m;
+                const float alpha = move ? fast_exp2(m - m_new) : 1.0f;   // 0 at the first block
+                const float m_ref = m_new == -INFINITY ? 0.0f : m_new;
+                const float2 sc2 = make_float2(p.scale, p.scale), nm2 = make_float2(-m_ref, -m_ref);
+                float2 sa = make_float2(0.0f, 0.0f), sb = make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int c0 = 0; c0 < kKeys; c0 += 32) {
+                    uint32_t ph[16];
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        const float2 x01 = __ffma2_rn(
+                            make_float2(__uint_as_float(v[c0 + i]), __uint_as_float(v[c0 + i + 1])), sc2, nm2);
+                        const float2 x23 = __ffma2_rn(
+                            make_float2(__uint_as_float(v[c0 + i + 2]), __uint_as_float(v[c0 + i + 3])), sc2, nm2);
+                        const float2 e01 = make_float2(fast_exp2(x01.x), fast_exp2(x01.y));
+                        const float2 e23 = make_float2(fast_exp2(x23.x), fast_exp2(x23.y));
+                        sa = __fadd2_rn(sa, e01);
+                        sb = __fadd2_rn(sb, e23);
+                        ph[i / 2] = pack_pair<kBf16>(e01.x, e01.y);
+                        ph[i / 2 + 1] = pack_pair<kBf16>(e23.x, e23.y);
+                    }
+                    tmem_st_x16(s_addr + c0 / 2, ph);
+                }
+                l = l * alpha + ((sa.x + sa.y) + (sb.x + sb.y));
+                m = m_new;
+                // rescale this warp's output rows when any of their references moved
+                // (the previous P V of this tile completed before S_j was written)
+                if (done > 0 && __any_sync(0xffffffffu, move)) {
 #pragma unroll 1
-                for (int c0 = 0; c0 < HD; c0 += 32) {
-                    uint32_t w[32];
-                    tmem_ld_x32_sync(o_addr + c0, w);
+                    for (int c0 = 0; c0 < HD; c0 += 32) {
+                        uint32_t o[32];
+                        tmem_ld_x32_sync(o_addr + c0, o);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        w[i] = __float_as_uint(__uint_as_float(w[i]) * alpha);
-                    tmem_st_x32(o_addr + c0, w);
+                        for (int i = 0; i < 32; ++i)
+                            o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                        tmem_st_x32(o_addr + c0, o);
+                    }
                 }
-            }
-            tmem_st_wait();
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(p_full((uint32_t)t));
-            ++turn;
-        }
-        // the last P V of both tiles, then O / l rounded once
-        if (alive && (t == 0 || two)) {
-            const bool done = turn == 0 || wait_bounded_eager(o_full, 0u, p.wait_limit_ns, abort_flag,
-                                                              kSiteEpiAccFull);
-            if (__all_sync(0xffffffffu, done)) {
+                tmem_st_wait();
+            };
+            for (int j = 0; j < w.nb; ++j) {
+                if (!mine.has(j))
+                    continue;
+                const bool ok = wait_bounded_eager(s_full((uint32_t)t), turns & 1u, p.wait_limit_ns,
+                                                   abort_flag, kSiteEpiAccFull);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    alive = false;
+                    break;
+                }
                 tc_fence_after_sync();
-                const float inv_l = l == 0.0f ? 0.0f : 1.0f / l;
-                uint16_t *dst = p.o + (((int64_t)batch * p.n_q + qi) * p.q_heads + head) * HD;
-                bool fine = true;
+                const int key0 = w.block(j) * BN;
+                // some row does not see some key of the block
+                const bool masked = key0 + BN - 1 > first ||
+                                    (p.window > 0 && key0 <= last - p.window && key0 + BN > p.sinks);
+                if (j == w.narrow)
+                    softmax(std::integral_constant<int, G::kNarrow>{}, key0, true);
+                else
+                    softmax(std::integral_constant<int, BN>{}, key0, masked);
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(p_full((uint32_t)t));
+                ++turns;
+                ++done;
+            }
+            if (!alive)
+                break;
+            // the tile's last P V, then O / l rounded once
+            if (done > 0) {
+                const bool ok = wait_bounded_eager(o_full((uint32_t)t), outputs & 1u, p.wait_limit_ns,
+                                                   abort_flag, kSiteEpiAccFull);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    alive = false;
+                    break;
+                }
+                ++outputs;
+                tc_fence_after_sync();
+            }
+            const float inv_l = l == 0.0f ? 0.0f : 1.0f / l;
+            uint16_t *dst = p.o + (((int64_t)w.batch * p.n_q + qi) * p.q_heads + head) * HD;
+            bool fine = true;
 #pragma unroll 1
-                for (int c0 = 0; c0 < HD; c0 += 32) {
-                    uint32_t w[32];
-                    uint32_t h[16];
-                    if (turn > 0)
-                        tmem_ld_x32_sync(o_addr + c0, w);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float x = turn > 0 ? __uint_as_float(w[2 * i]) * inv_l : 0.0f;
-                        const float y = turn > 0 ? __uint_as_float(w[2 * i + 1]) * inv_l : 0.0f;
-                        fine = fine && fabsf(x) < INFINITY && fabsf(y) < INFINITY;
-                        h[i] = pack_pair<kBf16>(x, y);
-                    }
-                    if (qi < p.n_q) {
-                        uint4 *d4 = reinterpret_cast<uint4 *>(dst + c0);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            d4[i] = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+            for (int c0 = 0; c0 < HD; c0 += 32) {
+                uint32_t o[32];
+                uint32_t h[16];
+                if (done > 0) {
+                    tmem_ld_x32_sync(o_addr + c0, o);
+                    if (c0 + 32 == HD) {   // O_t may be written again
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(o_empty((uint32_t)t));
                     }
                 }
-                uint32_t again = __ballot_sync(0xffffffffu, !fine && qi < p.n_q);
-                while (again) {
-                    const int r = __ffs(again) - 1;
-                    again &= again - 1;
-                    __syncwarp();
-                    window_row<HD, kBf16>(p, batch, head, tile * BM + 32 * q + r, lane);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float x = done > 0 ? __uint_as_float(o[2 * i]) * inv_l : 0.0f;
+                    const float y = done > 0 ? __uint_as_float(o[2 * i + 1]) * inv_l : 0.0f;
+                    fine = fine && fabsf(x) < INFINITY && fabsf(y) < INFINITY;
+                    h[i] = pack_pair<kBf16>(x, y);
                 }
+                if (qi < p.n_q) {
+                    uint4 *d4 = reinterpret_cast<uint4 *>(dst + c0);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        d4[i] = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+                }
+            }
+            uint32_t again = __ballot_sync(0xffffffffu, !fine && qi < p.n_q);
+            while (again) {
+                const int r = __ffs(again) - 1;
+                again &= again - 1;
+                __syncwarp();
+                window_row<HD, kBf16>(p, w.batch, head, tile * BM + 32 * q + r, lane);
             }
         }
     }

@@ -39,15 +39,14 @@ bool window_strides_ok(const int64_t *s, int64_t batch, int64_t seq, int64_t hea
 
 template <int HD, bool kBf16>
 int launch_window(const CUtensorMap &mQ, const CUtensorMap &mK, const CUtensorMap &mV,
-                  const FA::WindowParams &p, int64_t kv_heads, int64_t batch, cudaStream_t stream,
-                  bool &attr_done) {
+                  const FA::WindowParams &p, int sms, cudaStream_t stream, bool &attr_done) {
     auto kern = FA::flash_attention_window_kernel<HD, kBf16>;
-    if (!ensure_smem_attr(attr_done, kern, FA::Cfg<HD>::kSmemBytes))
+    if (!ensure_smem_attr(attr_done, kern, FA::WindowCfg<HD>::kSmemBytes))
         return GEMMRELU_ERR_LAUNCH;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)p.pairs, (unsigned)kv_heads, (unsigned)batch);
-    cfg.blockDim = dim3(FA::kThreads);
-    cfg.dynamicSmemBytes = FA::Cfg<HD>::kSmemBytes;
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>(sms, (int64_t)p.pairs * p.kv_heads * p.batch));
+    cfg.blockDim = dim3(FA::kWindowThreads);
+    cfg.dynamicSmemBytes = FA::WindowCfg<HD>::kSmemBytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -108,8 +107,10 @@ extern "C" int flash_attention_window_x16(const void *Q, const void *K, const vo
     p.group = (int)(q_heads / kv_heads);
     p.q_tiles = (int)((q_seq + FA::BM - 1) / FA::BM);
     const int64_t items = (int64_t)p.q_tiles * p.group;
-    if (items >= kMaxDim)
+    if (items >= kMaxDim / (batch * kv_heads))
         return GEMMRELU_ERR_INVALID_ARG;
+    p.kv_heads = (int)kv_heads;
+    p.batch = (int)batch;
     p.items = (int)items;
     p.pairs = (int)((items + 1) / 2);
     p.window = (int)std::min<int64_t>(window, (int64_t)1 << 30);
@@ -119,11 +120,11 @@ extern "C" int flash_attention_window_x16(const void *Q, const void *K, const vo
     p.wait_limit_ns = wait_limit_ns();
     if (head_dim == 64)
         return dtype == GEMMRELU_BF16
-                   ? launch_window<64, true>(mQ, mK, mV, p, kv_heads, batch, s, ds->attr_window[0])
-                   : launch_window<64, false>(mQ, mK, mV, p, kv_heads, batch, s, ds->attr_window[1]);
+                   ? launch_window<64, true>(mQ, mK, mV, p, ds->sms, s, ds->attr_window[0])
+                   : launch_window<64, false>(mQ, mK, mV, p, ds->sms, s, ds->attr_window[1]);
     return dtype == GEMMRELU_BF16
-               ? launch_window<128, true>(mQ, mK, mV, p, kv_heads, batch, s, ds->attr_window[2])
-               : launch_window<128, false>(mQ, mK, mV, p, kv_heads, batch, s, ds->attr_window[3]);
+               ? launch_window<128, true>(mQ, mK, mV, p, ds->sms, s, ds->attr_window[2])
+               : launch_window<128, false>(mQ, mK, mV, p, ds->sms, s, ds->attr_window[3]);
 }
 
 extern "C" int flash_attention_window_debug_blocks(int64_t first, int64_t last, int64_t window,
