@@ -167,6 +167,13 @@ constexpr int kWindowThreads = 384;
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 216, kOtherRegs = 72;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kLaunchRegs, "registers given back cover those taken");
 
+// One thread of the (converged) warp, chosen by the hardware.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(r));
+    return r != 0;
+}
+
 // wait_bounded_eager by a whole warp, with one answer.
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, uint64_t limit_ns,
                                           volatile uint32_t *abort_flag, unsigned where) {
@@ -355,12 +362,13 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
         }
         // ============================================================ MMA issuer
         if (warp == kMmaWarp) {
-            // One thread issues, but the whole warp walks along: control flow and operands are
-            // then uniform, and the MMAs' descriptors stay in uniform registers.  Inside a
+            // One elected thread issues, but the whole warp walks along: control flow and operands
+            // are then uniform, and the MMAs' descriptors stay in uniform registers.  In a
             // branch of one lane each of them was moved there instruction by instruction, and
-            // issuing bound the kernel (2600 to 4100 cycles a block of 128 keys against 2048 for
-            // the MMAs).  An item's list is worked out during the item before it.
-            const bool leader = lane == 0;
+            // issuing bound the kernel (16384 tokens, window 4096, 32 heads of 128: 1077 us
+            // against 781 us).  An item's list is worked out during the item before it, and a
+            // load that the first tile has waited for is not waited for again (136 cycles).
+            const bool leader = elect_one();
             const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0);
             const uint64_t q_desc = make_sdesc_sw128(base + G::kOffQ, 16, 1024);
             const uint64_t k_desc = make_sdesc_sw128(base + G::kOffK, 16, 1024);
@@ -371,9 +379,9 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
             uint32_t turns0 = 0, turns1 = 0;      // P V products of each tile so far
             uint32_t outs0 = 0, outs1 = 0;        // items of each tile with an output so far
             // S_t = Q_t K^T of block number i
-            auto score = [&](const uint32_t t, uint32_t i, bool narrow) -> bool {
+            auto score = [&](const uint32_t t, uint32_t i, bool narrow, bool waited) -> bool {
                 const uint32_t st = i % kKV;
-                if (!wait_warp(k_full(st), i / kKV & 1u, p.wait_limit_ns, abort_flag, kSiteMmaFull))
+                if (!waited && !wait_warp(k_full(st), i / kKV & 1u, p.wait_limit_ns, abort_flag, kSiteMmaFull))
                     return false;
                 tc_fence_after_sync();
                 const uint64_t qd = q_desc + t * (G::kQBytes >> 4), kd = k_desc + st * (G::kKBytes >> 4);
@@ -390,10 +398,10 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
             };
             // O_t += P_t V of block number i, P_t from TMEM (over S_t); O_t starts afresh with
             // an item's first block, and is complete with its last
-            auto pv = [&](const uint32_t t, uint32_t i, bool narrow, bool fresh, bool complete,
+            auto pv = [&](const uint32_t t, uint32_t i, bool narrow, bool waited, bool fresh, bool complete,
                           uint32_t &turns, uint32_t &outs) -> bool {
                 const uint32_t st = i % kKV;
-                if (!wait_warp(v_full(st), i / kKV & 1u, p.wait_limit_ns, abort_flag, kSiteMmaFull) ||
+                if ((!waited && !wait_warp(v_full(st), i / kKV & 1u, p.wait_limit_ns, abort_flag, kSiteMmaFull)) ||
                     (fresh && !wait_warp(o_empty(t), (outs & 1u) ^ 1u, p.wait_limit_ns, abort_flag,
                                                   kSiteMmaAccEmpty)) ||
                     !wait_warp(p_full(t), turns & 1u, p.wait_limit_ns, abort_flag, kSiteMmaAccEmpty))
@@ -431,9 +439,9 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
                     ok = wait_warp(q_full, queries & 1u, p.wait_limit_ns, abort_flag, kSiteMmaFull);
                     ++queries;
                     if (ok && t0.has(0))
-                        ok = score(0, blocks, narrow == 0);
+                        ok = score(0, blocks, narrow == 0, false);
                     if (ok && t1.has(0))
-                        ok = score(1, blocks, narrow == 0);
+                        ok = score(1, blocks, narrow == 0, t0.has(0));
                     if (ok && nb == 1 && leader)
                         umma_commit(q_empty);
                 }
@@ -444,13 +452,13 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
                 for (int j = 0; ok && j < nb; ++j, ++blocks) {
                     const bool here = j == narrow, there = j + 1 == narrow, more = j + 1 < nb;
                     if (t0.has(j)) {
-                        ok = pv(0, blocks, here, fresh0, j + 1 == t0.to, turns0, outs0);
+                        ok = pv(0, blocks, here, false, fresh0, j + 1 == t0.to, turns0, outs0);
                         fresh0 = false;
                     }
                     if (ok && more && t0.has(j + 1))
-                        ok = score(0, blocks + 1, there);
+                        ok = score(0, blocks + 1, there, false);
                     if (ok && t1.has(j)) {
-                        ok = pv(1, blocks, here, fresh1, j + 1 == t1.to, turns1, outs1);
+                        ok = pv(1, blocks, here, t0.has(j), fresh1, j + 1 == t1.to, turns1, outs1);
                         fresh1 = false;
                     }
                     if (!ok)
@@ -458,7 +466,7 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
                     if (leader)
                         umma_commit(kv_empty(blocks % kKV));
                     if (more && t1.has(j + 1))
-                        ok = score(1, blocks + 1, there);
+                        ok = score(1, blocks + 1, there, t0.has(j + 1));
                     if (ok && j + 2 == nb && leader)
                         umma_commit(q_empty);   // the item's last scores
                 }
