@@ -51,13 +51,16 @@ constexpr int kAttnThreads = 160;
 constexpr float kMoveLog2 = 8.0f;    // the reference moves when a score exceeds it by more
 constexpr float kPShift = 128.0f;    // 2^7, see above
 
-// kN groups of 8 query rows a tile: 1 (up to 8 rows: three blocks an SM) or 2 (two).
+// kN groups of 8 query rows a tile.  Two blocks an SM (168 registers a thread); three (128) only
+// where that takes no spills, 64 elements and one group.  Measured, one group: 32 sequences of up to
+// 4096 tokens, 8 heads of 128, 41.1 us with two blocks and 44.0 with three; 16 sequences of up
+// to 8192, window 2000, 16 heads of 64, 4 tokens each, 30.8 and 26.0 us.
 template <int D, int kN>
 struct AttnCfg {
     static constexpr int kRows = 8 * kN;
-    static constexpr int kBlocksPerSm = kN == 1 ? 3 : 2;
+    static constexpr int kBlocksPerSm = kN == 1 && D == 64 ? 3 : 2;
     static constexpr uint32_t kTile = kUnit * D;                 // bytes of K (or V) in a stage
-    static constexpr int kStages = (kN == 1 ? 3 : 4) * (128 / D);
+    static constexpr int kStages = D == 128 ? 4 : kN == 1 ? 6 : 8;
     static constexpr uint32_t kOffK = 0;
     static constexpr uint32_t kOffV = kOffK + kStages * kTile;
     static constexpr int kPitch = D + 4;                         // floats a row of the join buffer
@@ -146,10 +149,10 @@ __host__ __device__ __forceinline__ int range_owner(int x, int total, int grid) 
 }
 
 // How many of the launched blocks work: each takes a unit at least, and a (sequence, head,
-// row tile) is cut into about sqrt(8 units) parts at most.  A part costs its block's start
+// row tile) is cut into about sqrt(4 units) parts at most.  A part costs its block's start
 // and, in the join, a read of its O by one block; a unit in sequence costs its copy.
 __device__ __forceinline__ int blocks_used(int total, int segments, int grid) {
-    const float most = sqrtf(8.0f * (float)total * (float)segments);
+    const float most = sqrtf(4.0f * (float)total * (float)segments);
     int n = total < grid ? total : grid;
     if (most < (float)n)
         n = (int)most;

@@ -123,7 +123,7 @@ struct AttnSpace {
 AttnSpace attention_space(int64_t batch, int64_t rows, int64_t kv_heads, int64_t head_dim,
                           int64_t weights_width, int sms) {
     AttnSpace a{};
-    const size_t slots = 2 * (size_t)sms * std::max(KC::AttnCfg<128, 1>::kBlocksPerSm * 8,
+    const size_t slots = 2 * (size_t)sms * std::max(KC::AttnCfg<64, 1>::kBlocksPerSm * 8,
                                                     KC::AttnCfg<128, 2>::kBlocksPerSm * 16);
     size_t at = a.partial = GEMMRELU_KV_COUNTER_BYTES;
     at += slots * (head_dim + 2) * 4;
