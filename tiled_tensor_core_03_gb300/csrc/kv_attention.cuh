@@ -912,28 +912,42 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
 }
 
 // weights[t] += sum over the rows that see t of softmax_t, from the scores and each row's
-// log-sum-exp; a thread per token.
+// log-sum-exp; a thread per token, the rows kVec at a time.  All that it reads is asked for
+// before the length is known (scores and weights have room for every slot of the table).
 constexpr int kWeightThreads = 256;
 
+template <int kVec>
 __global__ void __launch_bounds__(kWeightThreads) kv_attention_weights_kernel(const AttnParams p) {
     pdl_launch_dependents();
+    const int blocks = (int)((p.width + kWeightThreads - 1) / kWeightThreads);
+    const int bh = blockIdx.x / blocks, b = bh / p.pool.kv_heads;
+    const int t = (blockIdx.x - bh * blocks) * kWeightThreads + threadIdx.x;
     pdl_wait_primary();
-    const int64_t blocks = (p.width + kWeightThreads - 1) / kWeightThreads;
-    const int64_t bh = blockIdx.x / blocks;
-    const int b = (int)(bh / p.pool.kv_heads);
-    const int64_t t = (blockIdx.x % blocks) * kWeightThreads + threadIdx.x;
-    const int n = length_of(p, b);
-    if (t >= n)
+    if (t >= p.width)
         return;
-    const float *s = p.scores + (bh * p.width + t) * p.rows;
-    const float *lse = p.lse + bh * p.rows;
+    const float *s = p.scores + ((int64_t)bh * p.width + t) * p.rows;
+    const float *lse = p.lse + (int64_t)bh * p.rows;
+    float *w = p.weights + (int64_t)bh * p.width + t;
+    const float before = *w;
+    const int n = length_of(p, b);
     float sum = 0.0f;
-    for (int r = 0; r < p.rows; ++r) {
-        const int pos = n - p.tokens + r / p.group;
-        if (sees((int)t, pos, p.window, p.sinks))
-            sum += exp2_fast(s[r] - lse[r]);
+    for (int r = 0; r < p.rows; r += kVec) {
+        float x[kVec], y[kVec];
+        if constexpr (kVec == 4) {
+            const float4 u = *reinterpret_cast<const float4 *>(s + r);
+            const float4 v = *reinterpret_cast<const float4 *>(lse + r);
+            x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
+            y[0] = v.x, y[1] = v.y, y[2] = v.z, y[3] = v.w;
+        } else {
+            x[0] = s[r], y[0] = lse[r];
+        }
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+            if (sees(t, n - p.tokens + (r + i) / p.group, p.window, p.sinks))   // (else x is anything)
+                sum += exp2_fast(x[i] - y[i]);
     }
-    p.weights[bh * p.width + t] += sum;
+    if (t < n)
+        *w = before + sum;
 }
 
 }  // namespace kvc

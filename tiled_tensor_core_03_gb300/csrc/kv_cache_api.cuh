@@ -161,8 +161,9 @@ int launch_kv_attention(const CUtensorMap &mK, const CUtensorMap &mV, KC::AttnPa
     if (rc != GEMMRELU_OK || !kScores)
         return rc;
     const int64_t blocks = (p.width + KC::kWeightThreads - 1) / KC::kWeightThreads;
-    return launch_kv(KC::kv_attention_weights_kernel, (int64_t)p.batch * p.pool.kv_heads * blocks,
-                     KC::kWeightThreads, s, p);
+    const int64_t grid = (int64_t)p.batch * p.pool.kv_heads * blocks;
+    return p.rows % 4 == 0 ? launch_kv(KC::kv_attention_weights_kernel<4>, grid, KC::kWeightThreads, s, p)
+                           : launch_kv(KC::kv_attention_weights_kernel<1>, grid, KC::kWeightThreads, s, p);
 }
 
 template <int D, int kN>

@@ -73,11 +73,11 @@ def _pool(cache, d):
     if dim not in _HEAD_DIMS or page not in _PAGES:
         raise ValueError(f"head_dim must be one of {_HEAD_DIMS}, page one of {_PAGES}: "
                          f"got {tuple(shape)}")
-    if ks.shape != (pages, heads) or vs.shape != (pages, heads) or ks.dtype != torch.float32 \
-            or vs.dtype != torch.float32 or not ks.is_contiguous() or not vs.is_contiguous():
+    shape2 = ks.shape
+    if shape2 != (pages, heads) or vs.shape != shape2 or ks.dtype is not torch.float32 \
+            or vs.dtype is not torch.float32 or not ks.is_contiguous() or not vs.is_contiguous():
         raise ValueError("cache scales must be contiguous float32 [num_pages, kv_heads]")
-    if k.get_device() != d or v.get_device() != d or ks.get_device() != d \
-            or vs.get_device() != d:
+    if not d == k.get_device() == v.get_device() == ks.get_device() == vs.get_device():
         raise ValueError(f"the cache must be on cuda:{d}")
     return Pool(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages, heads, page,
                 dim), shape
@@ -116,14 +116,6 @@ def _current(d):
     return torch._C._cuda_getCurrentRawStream(d)   # current_stream().cuda_stream, directly
 
 
-def _on(stream, f, *args):
-    """f(raw stream, *args); what f allocates belongs to the stream."""
-    if stream is None:
-        return f(_current(torch.cuda.current_device()), *args)
-    with torch.cuda.stream(stream):
-        return f(stream.cuda_stream, *args)
-
-
 def flash_attention_window(q, k, v, window, sinks=0, out=None, stream=None):
     """softmax(q k^T / sqrt(d)) v of a prompt with a sliding window: q [batch, q_seq, q_heads, d],
     k and v [batch, kv_seq, kv_heads, d], fp16 or bf16, any strides between heads, d = 64 or
@@ -150,20 +142,22 @@ def flash_attention_window(q, k, v, window, sinks=0, out=None, stream=None):
     if out is not None and (out.shape != shape or out.dtype != q.dtype or out.get_device() != d
                             or not out.is_contiguous()):
         raise ValueError("out must be a contiguous tensor like q")
+    if stream is not None:
+        with torch.cuda.stream(stream):   # what is allocated belongs to it
+            return flash_attention_window(q, k, v, window, sinks, out)
+    if out is None:
+        out = q.new_empty(shape)
     if q.numel() == 0:
-        return torch.empty_like(q) if out is None else out
+        return out
     qp, qs = _strides(q, "q")
     kp, ks = _strides(k, "k")
     vp, vs = _strides(v, "v")
-
-    def call(s):
-        o = torch.empty(shape, dtype=q.dtype, device=q.device) if out is None else out
-        rc = lib().flash_attention_window_x16(qp, kp, vp, o.data_ptr(), dtype, batch, q_seq, kv_seq,
-                                              q_heads, kv_heads, dim, qs, ks, vs, window, sinks, s)
-        if rc != OK:
-            raise GemmReluError(rc, "flash_attention_window_x16")
-        return o
-    return _on(stream, call)
+    rc = lib().flash_attention_window_x16(qp, kp, vp, out.data_ptr(), dtype, batch, q_seq, kv_seq,
+                                          q_heads, kv_heads, dim, qs, ks, vs, window, sinks,
+                                          _current(d))
+    if rc != OK:
+        raise GemmReluError(rc, "flash_attention_window_x16")
+    return out
 
 
 def kv_cache_append(cache, k, v, pages, lengths, counts=None, stream=None):
@@ -261,20 +255,23 @@ def kv_cache_attention(q, cache, pages, lengths, window=0, sinks=0, weights=None
     if out is not None and (out.shape != shape or out.dtype != q.dtype or out.get_device() != d
                             or not out.is_contiguous()):
         raise ValueError("out must be a contiguous tensor like q")
+    if stream is not None:
+        with torch.cuda.stream(stream):   # what is allocated belongs to it
+            return kv_cache_attention(q, cache, pages, lengths, window, sinks, weights, out,
+                                      workspace)
+    if out is None:
+        out = q.new_empty(shape)
     if batch == 0 or tokens == 0:
-        return torch.empty_like(q) if out is None else out
+        return out
     qp, qs = _strides(q, "q")
-
-    def call(s):
-        o = torch.empty(shape, dtype=q.dtype, device=q.device) if out is None else out
-        w = _workspace(q, cache, weights, s) if workspace is None else workspace
-        rc = lib().kv_cache_attention_x16(
-            ctypes.byref(pool), qp, dtype, batch, tokens, heads, qs, o.data_ptr(), table,
-            max_pages, lens, window, sinks, wp, width, w.data_ptr(), w.nbytes, s)
-        if rc != OK:
-            raise GemmReluError(rc, "kv_cache_attention_x16")
-        return o
-    return _on(stream, call)
+    s = _current(d)
+    w = _workspace(q, cache, weights, s) if workspace is None else workspace
+    rc = lib().kv_cache_attention_x16(ctypes.byref(pool), qp, dtype, batch, tokens, heads, qs,
+                                      out.data_ptr(), table, max_pages, lens, window, sinks, wp,
+                                      width, w.data_ptr(), w.nbytes, s)
+    if rc != OK:
+        raise GemmReluError(rc, "kv_cache_attention_x16")
+    return out
 
 
 def kv_cache_evict(cache, weights, pages, lengths, budget, sinks, recent, to, to_pages,
@@ -308,16 +305,19 @@ def kv_cache_evict(cache, weights, pages, lengths, budget, sinks, recent, to, to
     if to_max * page < budget:
         raise ValueError(f"to_pages has room for {to_max * page} tokens, the budget is {budget}")
 
-    def call(s):
-        new_lengths = torch.empty(batch, dtype=torch.int32, device=weights.device)
-        new_weights = torch.empty((batch, heads, to_max * page), dtype=torch.float32,
-                                  device=weights.device)
-        kept = torch.empty((batch, heads, budget), dtype=torch.int32, device=weights.device)
-        rc = lib().kv_cache_evict_e4m3(
-            ctypes.byref(pool), weights.data_ptr(), width, table, max_pages, lens, batch, budget,
-            sinks, recent, ctypes.byref(dest), to_table, to_max, new_lengths.data_ptr(),
-            new_weights.data_ptr(), kept.data_ptr(), s)
-        if rc != OK:
-            raise GemmReluError(rc, "kv_cache_evict_e4m3")
+    if stream is not None:
+        with torch.cuda.stream(stream):   # what is allocated belongs to it
+            return kv_cache_evict(cache, weights, pages, lengths, budget, sinks, recent, to,
+                                  to_pages)
+    new_lengths = lengths.new_empty(batch)
+    new_weights = weights.new_empty((batch, heads, to_max * page))
+    kept = lengths.new_empty((batch, heads, budget))
+    if batch == 0:
         return new_lengths, new_weights, kept
-    return _on(stream, call)
+    rc = lib().kv_cache_evict_e4m3(
+        ctypes.byref(pool), weights.data_ptr(), width, table, max_pages, lens, batch, budget,
+        sinks, recent, ctypes.byref(dest), to_table, to_max, new_lengths.data_ptr(),
+        new_weights.data_ptr(), kept.data_ptr(), _current(d))
+    if rc != OK:
+        raise GemmReluError(rc, "kv_cache_evict_e4m3")
+    return new_lengths, new_weights, kept
