@@ -183,12 +183,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
         return;
     const int lo = start > first ? (int)(start - first) : 0;                       // new slots
     const int hi = end - first < p.pool.page ? (int)(end - first) : p.pool.page;   // [lo, hi)
-    const int64_t id = p.pages[b * p.max_pages + at];
-    if (id < 0 || id >= p.pool.num_pages) {
-        if (threadIdx.x == 0)
-            record_page_error();
-        return;
-    }
+    const int64_t id = p.pages[b * p.max_pages + at];   // (used once the tokens are on their way)
 
     constexpr int kPerToken = D / 8;
     const uint16_t *src = p.x[kv] + b * p.stride[kv][0] + h * p.stride[kv][2];
@@ -200,6 +195,11 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
         if (slot >= lo && slot < hi)
             x[n] = *reinterpret_cast<const uint4 *>(src + (first + slot - start) * p.stride[kv][1] +
                                                     8 * (v % kPerToken));
+    }
+    if (id < 0 || id >= p.pool.num_pages) {
+        if (threadIdx.x == 0)
+            record_page_error();
+        return;
     }
     float *scale_at = p.pool.scales[kv] + id * p.pool.kv_heads + h;
     const float held = lo > 0 ? *scale_at : 0.0f;   // 0: a fresh page
@@ -294,8 +294,9 @@ constexpr int kMaxSelectCluster = 8;
 constexpr int kShortList = 512;   // keys that one warp finishes alone
 
 // Which tokens stay, a cluster of 1 to 8 blocks per (sequence, head), each with a stretch of
-// the tokens.  Between the sinks and the recent tokens the k heaviest are those above the
-// k-th largest key and the first few equal to it.  The keys are read once into registers
+// the tokens.  Sinks and recent tokens have the largest key there is, so the survivors are
+// the `budget` largest keys: those above the k-th largest, k = budget, and the first few equal
+// to it.  The keys are read once into registers
 // (kKeys a thread; what does not fit is read again from L2), and the k-th largest is built
 // two bits at a time from the top: of three candidates the largest that k keys reach.
 // What bounds it is the rounds' latency and, with many keys, their compares, so once 512
@@ -330,16 +331,28 @@ __global__ void __launch_bounds__(kSelectThreads, 1) kv_evict_select_kernel(cons
             kept[i] = i;
         return;   // all blocks of the cluster
     }
-    const int lo = p.sinks, hi = n - p.recent;   // the tokens that compete
+    const int lo = p.sinks, hi = n - p.recent;   // the tokens that compete for the rest
     const int stretch = (n + cluster - 1) / cluster;
     const int t0 = min(rank * stretch, n), t1 = min(t0 + stretch, n);
     constexpr int kGroup = kKeys * kSelectThreads;
-    // token t0 + s * threads + tid is slot s of this thread; 0, below every key, for the others
-    auto key_at = [&](int i) { return i >= lo && i < hi && i < t1 ? weight_key(w[i]) : 0u; };
+    // token t0 + s * threads + tid is slot s of this thread; past the stretch 0, below every key
+    auto key_of_weight = [&](int i, float x) {
+        return i >= t1 ? 0u : i < lo || i >= hi ? 0xffffffffu : weight_key(x);
+    };
+    auto key_at = [&](int i) { return key_of_weight(i, i < t1 ? w[i] : 0.0f); };
     uint32_t key[kKeys];
+    auto load = [&](int g0) {
+        float x[kKeys];
 #pragma unroll
-    for (int s = 0; s < kKeys; ++s)
-        key[s] = key_at(t0 + s * kSelectThreads + tid);
+        for (int s = 0; s < kKeys; ++s) {
+            const int i = g0 + s * kSelectThreads + tid;
+            x[s] = i < t1 ? w[i] : 0.0f;
+        }
+#pragma unroll
+        for (int s = 0; s < kKeys; ++s)
+            key[s] = key_of_weight(g0 + s * kSelectThreads + tid, x[s]);
+    };
+    load(t0);
 
     int turn = 0;
     // how many of all keys reach three thresholds
@@ -405,13 +418,12 @@ __global__ void __launch_bounds__(kSelectThreads, 1) kv_evict_select_kernel(cons
         turn ^= 1;
     };
 
-    const int need = p.budget - p.sinks - p.recent;
-    uint32_t kth = 0xffffffffu;   // no weight has this key
-    int ties_kept = 0;
-    if (need > 0) {
+    const int need = p.budget;
+    uint32_t kth = 0;
+    int ties_kept;
+    {
         // `above` keys exceed all those that share the bits found, which `reach` - above do
-        int above = 0, reach = hi - lo, shift = 30;
-        kth = 0;
+        int above = 0, reach = n, shift = 30;
         for (; shift >= 0; shift -= 2) {
             int got[3];
             count(kth | 1u << shift, kth | 2u << shift, kth | 3u << shift, got);
@@ -427,18 +439,21 @@ __global__ void __launch_bounds__(kSelectThreads, 1) kv_evict_select_kernel(cons
                 shared[0] = 0;
             __syncthreads();
             const uint32_t mask = ~0u << shift;
+            int mine_too = 0;
+#pragma unroll
+            for (int s = 0; s < kKeys; ++s)
+                mine_too += __popc(__ballot_sync(0xffffffffu, (key[s] & mask) == kth && key[s] != 0));
+            int at = 0;
+            if (lane == 0 && mine_too > 0)
+                at = atomicAdd(&shared[0], mine_too);
+            at = __shfl_sync(0xffffffffu, at, 0);
 #pragma unroll
             for (int s = 0; s < kKeys; ++s) {
-                const bool in = key[s] != 0 && (key[s] & mask) == kth;
+                const bool in = (key[s] & mask) == kth && key[s] != 0;
                 const uint32_t who = __ballot_sync(0xffffffffu, in);
-                if (who == 0)
-                    continue;
-                int at = 0;
-                if (lane == 0)
-                    at = atomicAdd(&shared[0], __popc(who));
-                at = __shfl_sync(0xffffffffu, at, 0);
                 if (in)
                     list[at + __popc(who & below)] = key[s];
+                at += __popc(who);
             }
             __syncthreads();
             if (warp == 0) {
@@ -481,15 +496,15 @@ __global__ void __launch_bounds__(kSelectThreads, 1) kv_evict_select_kernel(cons
     int out = 0, ties = 0;
     if (cluster > 1) {
         int sure = 0, tie = 0;
-        auto look = [&](int i, uint32_t k) {
-            sure += i < t1 && (i < lo || i >= hi || k > kth);
-            tie += i < t1 && k == kth && i >= lo && i < hi;
+        auto look = [&](uint32_t k) {
+            sure += k > kth;
+            tie += k == kth;
         };
 #pragma unroll
         for (int s = 0; s < kKeys; ++s)
-            look(t0 + s * kSelectThreads + tid, key[s]);
+            look(key[s]);
         for (int i = t0 + kGroup + tid; i < t1; i += kSelectThreads)
-            look(i, key_at(i));
+            look(key_at(i));
         sure = __reduce_add_sync(0xffffffffu, sure);
         tie = __reduce_add_sync(0xffffffffu, tie);
         if (lane == 0)
@@ -514,19 +529,10 @@ __global__ void __launch_bounds__(kSelectThreads, 1) kv_evict_select_kernel(cons
     }
     // write this block's survivors in order, kGroup tokens at a time
     for (int g0 = t0; g0 < t1; g0 += kGroup) {
-        if (g0 > t0) {
-#pragma unroll
-            for (int s = 0; s < kKeys; ++s)
-                key[s] = key_at(g0 + s * kSelectThreads + tid);
-        }
-        auto sure_of = [&](int s) {
-            const int i = g0 + s * kSelectThreads + tid;
-            return __ballot_sync(0xffffffffu, i < t1 && (i < lo || i >= hi || key[s] > kth));
-        };
-        auto tie_of = [&](int s) {
-            const int i = g0 + s * kSelectThreads + tid;
-            return __ballot_sync(0xffffffffu, i < t1 && i >= lo && i < hi && key[s] == kth);
-        };
+        if (g0 > t0)
+            load(g0);
+        auto sure_of = [&](int s) { return __ballot_sync(0xffffffffu, key[s] > kth); };
+        auto tie_of = [&](int s) { return __ballot_sync(0xffffffffu, key[s] == kth); };
 #pragma unroll
         for (int s = 0; s < kKeys; ++s) {
             const uint32_t sure = sure_of(s), tie = tie_of(s);

@@ -70,8 +70,8 @@ int launch_append(const KC::AppendParams &p, int64_t grid, int dtype, cudaStream
 
 template <int D, int kVec>
 int launch_move_vec(const KC::EvictParams &p, int sms, cudaStream_t s) {
-    // a few blocks an SM walk over the items (2048 threads an SM at most)
-    const int64_t grid = std::min<int64_t>(p.items, (int64_t)sms * 8);
+    // the blocks that fit at once walk over the items
+    const int64_t grid = std::min<int64_t>(p.items, (int64_t)sms * (kVec == 4 ? 2 : 4));
     return launch_kv(KC::kv_evict_move_kernel<D, kVec>, grid, KC::kMoveThreads, s, p);
 }
 
