@@ -488,12 +488,13 @@ def test_cache_attention_dropped_arrival_times_out_and_recovers():
 # ---------------------------------------------------------------- eviction
 
 
-def _evict(rng, page, d, hkv, lengths, budget, sinks, recent, weights=None, same_pool=False):
+def _evict(rng, page, d, hkv, lengths, budget, sinks, recent, weights=None, same_pool=False,
+           garbage=False):
     import torch
     need = [-(-n // page) for n in lengths]
     keep = [-(-min(n, budget) // page) for n in lengths]
     total = sum(need) + sum(keep) + 1
-    cache, c64 = _cache(rng, total, hkv, page, d, garbage=False)
+    cache, c64 = _cache(rng, total, hkv, page, d, garbage=garbage)
     to, t64 = (cache, c64) if same_pool else _cache(rng, total, hkv, page, d)
     both = _tables(rng, need + keep, total)
     table = both[:len(need), :max(max(need), 1)]
@@ -549,6 +550,33 @@ def test_evict_long(n, budget):
     rng = np.random.default_rng(n)
     w = np.round(np.exp(rng.standard_normal((2, 1, n + 128))) * 50) / 50
     _evict(rng, 128, 64, 1, [n, n // 3], budget, 4, budget // 4, weights=w)
+
+
+def test_evict_keeps_nan():
+    """Any bytes, NaN codes among them: NaN stays NaN and counts for no scale."""
+    _evict(np.random.default_rng(25), 64, 128, 2, [300, 70], 100, 4, 10, garbage=True)
+
+
+def test_evict_scales_far_apart():
+    """Tokens of pages whose scales differ by up to 2^40 in one new page."""
+    import torch
+    rng = np.random.default_rng(26)
+    cache, c64 = _cache(rng, 4, 1, 16, 64, garbage=False)
+    to, _ = _cache(rng, 1, 1, 16, 64)
+    for which in (2, 3):
+        c64[which][:, 0] = [2.0 ** -8, 2.0 ** -20, 2.0 ** -28, 2.0 ** -48]
+        cache[which][:, 0] = torch.tensor(c64[which][:, 0], dtype=torch.float32, device="cuda")
+    for kept in ([0, 17, 33, 50], [17, 33, 34, 49], [48, 49, 62, 63]):
+        w = torch.zeros((1, 1, 64), device="cuda")
+        w[0, 0, kept] = 1.0
+        gr.kv_cache_evict(cache, w, _i32([[0, 1, 2, 3]]), _i32([64]), 4, 0, 0, to, _i32([[0]]))
+        for which in (0, 1):
+            x = np.zeros((16, 64))
+            at = np.array(kept)
+            x[:4] = c64[which][at // 16, 0, at % 16] * c64[which + 2][at // 16, 0][:, None]
+            s = ref.scale_for(ref.finite_amax(x))
+            assert _f64(to[which + 2])[0, 0] == s
+            assert np.array_equal(_f64(to[which].float())[0, 0], ref.e4m3_round(x / s))
 
 
 def test_evict_within_one_pool():

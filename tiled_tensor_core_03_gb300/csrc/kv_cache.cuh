@@ -587,6 +587,30 @@ __global__ void __launch_bounds__(kSelectThreads, 1) kv_evict_select_kernel(cons
 
 constexpr int kMoveThreads = 256;
 
+// Largest magnitude of 16 e4m3 values as a code (0 .. 0x7e), or 0x7f where there is a NaN: e4m3
+// magnitudes ascend with their codes, so two 16-bit lanes compare four bytes at a time.
+__device__ __forceinline__ uint32_t largest_code(const uint4 &x) {
+    const uint32_t hi = __vimax3_u16x2(__vmaxu2(x.x & 0x7f007f00u, x.y & 0x7f007f00u), x.z & 0x7f007f00u,
+                                       x.w & 0x7f007f00u);
+    const uint32_t lo = __vimax3_u16x2(__vmaxu2(x.x & 0x007f007fu, x.y & 0x007f007fu), x.z & 0x007f007fu,
+                                       x.w & 0x007f007fu);
+    const uint32_t m = __vmaxu2(hi >> 8, lo);
+    return max(m >> 16, m & 0xffffu);
+}
+
+// The same with NaN out of the way.
+__device__ __forceinline__ float largest_finite(const uint4 &x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        top = larger2<false>(top, e4m3x2_to_half2(w[e] & 0x7f7fu));
+        top = larger2<false>(top, e4m3x2_to_half2(w[e] >> 16 & 0x7f7fu));
+    }
+    const float2 f = pair_to_float2<false>(top);
+    return fmaxf(f.x, f.y);
+}
+
 // Gathers the kept tokens of (sequence, new page, head) items, 16 elements a thread and
 // vector of K and of V, and stores them under scales of their own.  The bytes stay
 // in registers between the maximum and the rounding.  A token's bytes are three dependent reads
@@ -594,12 +618,15 @@ constexpr int kMoveThreads = 256;
 // item's positions and pages while this one's bytes are under way.
 template <int D, int kVec>
 __global__ void __launch_bounds__(kMoveThreads, kVec == 4 ? 2 : 4) kv_evict_move_kernel(const EvictParams p) {
-    __shared__ uint32_t slots[2][2][kMoveThreads / 32];
+    __shared__ uint2 tops[2][kMoveThreads / 32];
     pdl_launch_dependents();
     pdl_wait_primary();
     constexpr int kPerToken = D / 16;
     const int page = p.from.page, shift = p.from.page_shift, heads = p.from.kv_heads;
-    const int items = p.items;   // heads fastest, then pages, then sequences
+    const int to_max = (int)p.to_max_pages, items = p.items;   // heads fastest, then pages, then sequences
+    // the item in hand, and what a step over gridDim.x items adds, without divisions in the loop
+    int h = blockIdx.x % heads, at = blockIdx.x / heads % to_max, b = blockIdx.x / heads / to_max;
+    const int step_h = gridDim.x % heads, step_at = gridDim.x / heads % to_max, step_b = gridDim.x / heads / to_max;
 
     struct Item {
         int h, b, at, m, to;     // m: the sequence's new length; to: the new page, -1 for none
@@ -607,28 +634,41 @@ __global__ void __launch_bounds__(kMoveThreads, kVec == 4 ? 2 : 4) kv_evict_move
         int t[kVec];             // and its token
         float w;
     };
-    auto look = [&](int item) {
+    auto look = [&]() {
         Item x;
-        x.h = item % heads;
-        x.at = item / heads % (int)p.to_max_pages;
-        x.b = item / heads / (int)p.to_max_pages;
-        const int64_t bh = (int64_t)x.b * heads + x.h;
-        const int32_t *kept = p.kept + bh * p.budget;
-        const int first = x.at << shift;
+        x.h = h;
+        x.at = at;
+        x.b = b;
+        const int64_t bh = (int64_t)b * heads + h;
+        const int first = at << shift;
         // written by the selection: -1 past the new length
-        const int at0 = first + threadIdx.x;
-        const int mine = threadIdx.x < page && at0 < p.budget ? kept[at0] : -1;
+        const int32_t *kept = p.kept + bh * p.budget + first;
+        const int left = min(p.budget - first, page);
+        const int mine = (int)threadIdx.x < left ? kept[threadIdx.x] : -1;
 #pragma unroll
         for (int n = 0; n < kVec; ++n) {
             const int slot = (threadIdx.x + n * kMoveThreads) / kPerToken;
-            x.t[n] = slot < page && first + slot < p.budget ? kept[first + slot] : -1;
+            x.t[n] = slot < left ? kept[slot] : -1;
         }
-        x.m = p.to_lengths[x.b];
-        x.to = p.to_pages[x.b * p.to_max_pages + x.at];
+        x.m = p.to_lengths[b];
+        x.to = p.to_pages[(int64_t)b * to_max + at];
+        const int32_t *pages = p.pages + b * p.max_pages;
 #pragma unroll
         for (int n = 0; n < kVec; ++n)
-            x.from[n] = x.t[n] >= 0 ? p.pages[x.b * p.max_pages + (x.t[n] >> shift)] : -1;
+            x.from[n] = x.t[n] >= 0 ? pages[x.t[n] >> shift] : -1;
         x.w = mine >= 0 ? p.weights[bh * p.width + mine] : 0.0f;
+        // on to the block's next item
+        h += step_h;
+        at += step_at;
+        b += step_b;
+        if (h >= heads) {
+            h -= heads;
+            ++at;
+        }
+        if (at >= to_max) {
+            at -= to_max;
+            ++b;
+        }
         return x;
     };
 
@@ -636,11 +676,9 @@ __global__ void __launch_bounds__(kMoveThreads, kVec == 4 ? 2 : 4) kv_evict_move
     int item = blockIdx.x;
     if (item >= items)
         return;
-    Item next = look(item);
+    Item next = look();
     for (; item < items; item += gridDim.x) {
         const Item x = next;
-        const bool ahead = item + (int)gridDim.x < items;
-        const int64_t bh = (int64_t)x.b * heads + x.h;
         const int first = x.at << shift;
         const bool there = first < x.m, good = there && x.to >= 0 && x.to < p.to.num_pages;
         uint4 v[2][kVec];
@@ -656,40 +694,49 @@ __global__ void __launch_bounds__(kMoveThreads, kVec == 4 ? 2 : 4) kv_evict_move
                 continue;
             }
             const int64_t block = (int64_t)x.from[n] * heads + x.h;
-            const int64_t at = (block * page + (x.t[n] & (page - 1))) * D + 16 * ((threadIdx.x + n * kMoveThreads) % kPerToken);
+            const int64_t from = (block * page + (x.t[n] & (page - 1))) * D + 16 * ((threadIdx.x + n * kMoveThreads) % kPerToken);
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv) {
-                v[kv][n] = *reinterpret_cast<const uint4 *>(p.from.values[kv] + at);
+                v[kv][n] = *reinterpret_cast<const uint4 *>(p.from.values[kv] + from);
                 s[kv][n] = p.from.scales[kv][block];
             }
         }
-        if (ahead)
-            next = look(item + gridDim.x);
-        if (threadIdx.x < page)
-            p.to_weights[bh * p.to_max_pages * page + first + threadIdx.x] = x.w;
+        if (item + (int)gridDim.x < items)
+            next = look();
+        if ((int)threadIdx.x < page)
+            p.to_weights[(((int64_t)x.b * heads + x.h) * to_max << shift) + first + threadIdx.x] = x.w;
         if (there && !good && threadIdx.x == 0)
             record_page_error();
         if (!good)
             continue;
-        const int64_t block = (int64_t)x.to * heads + x.h;
+        uint32_t top[2];
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
             float amax = 0.0f;
 #pragma unroll
             for (int n = 0; n < kVec; ++n) {
-                const uint32_t w[4] = {v[kv][n].x, v[kv][n].y, v[kv][n].z, v[kv][n].w};
-                uint32_t top = 0;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    top = larger2<false>(top, e4m3x2_to_half2(w[e] & 0x7f7fu));
-                    top = larger2<false>(top, e4m3x2_to_half2(w[e] >> 16 & 0x7f7fu));
-                }
-                const float2 f = pair_to_float2<false>(top);
-                amax = fmaxf(amax, fmaxf(f.x, f.y) * s[kv][n]);
+                const uint32_t code = largest_code(v[kv][n]);
+                float f = e4m3x2_to_float2(code).x;
+                if (code == 0x7fu)   // a NaN: look again
+                    f = largest_finite(v[kv][n]);
+                amax = fmaxf(amax, f * s[kv][n]);
             }
-            // the words alternate between items: one barrier each
-            amax = block_max(amax, slots[turn][kv]);
-            const float scale = scale_for(amax), inv = inverse_scale(scale);
+            top[kv] = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
+        }
+        // the words alternate between items: one barrier each
+        if ((threadIdx.x & 31) == 0)
+            tops[turn][threadIdx.x >> 5] = make_uint2(top[0], top[1]);
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kMoveThreads / 32; ++w) {
+            top[0] = max(top[0], tops[turn][w].x);
+            top[1] = max(top[1], tops[turn][w].y);
+        }
+        turn ^= 1;
+        const int64_t block = (int64_t)x.to * heads + x.h;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+            const float scale = scale_for(__uint_as_float(top[kv])), inv = inverse_scale(scale);
             if (threadIdx.x == 0)
                 p.to.scales[kv][block] = scale;
             uint8_t *dst = p.to.values[kv] + block * page * D;
@@ -715,7 +762,6 @@ __global__ void __launch_bounds__(kMoveThreads, kVec == 4 ? 2 : 4) kv_evict_move
                 *reinterpret_cast<uint4 *>(dst + 16 * i) = make_uint4(w[0], w[1], w[2], w[3]);
             }
         }
-        turn ^= 1;
     }
 }
 
