@@ -246,6 +246,11 @@ int gemm_relu_f16_splitk_noalloc(const void *A, const void *B, void *C,
                                  int64_t M, int64_t N, int64_t K, int split_k, void *stream);
 
 /*
+ * gemm_relu_stream_capturing -- whether `stream` is being captured into a graph (host-only).
+ */
+int gemm_relu_stream_capturing(void *stream);
+
+/*
  * gemm_relu_status -- synchronise `stream`, then return and clear the current
  * device's watchdog word: GEMMRELU_OK, or GEMMRELU_ERR_TIMEOUT if a bounded
  * wait inside a kernel expired since the last call (that kernel's output is

@@ -135,10 +135,9 @@ P = 0x1000   # an aligned address that is never read: every call below ends befo
 
 
 def _pool(**kw):
-    from tiled_tensor_core_03_gb300.serving import Pool
     f = dict(k=P, v=P, k_scale=P, v_scale=P, num_pages=4, kv_heads=2, page=64, head_dim=128)
     f.update(kw)
-    return Pool(**f)
+    return gr.KVCachePool(**f)
 
 
 def _strides(*s):
@@ -153,7 +152,7 @@ BAD_STRIDES = [None, _strides(2048, 256, -128), _strides(2048, 252, 128)]
 
 def _append(lib, pool=None, k=P, v=P, dtype=0, batch=2, tokens=8, ks=S, vs=S, pages=P, max_pages=4,
             lengths=P, counts=None):
-    return lib.kv_cache_append_x16(ctypes.byref(pool or _pool()), k, v, dtype, batch, tokens, ks, vs,
+    return gr.kv_cache_append_x16(pool or _pool(), k, v, dtype, batch, tokens, ks, vs,
                                    pages, max_pages, lengths, counts, None)
 
 
@@ -173,7 +172,7 @@ def test_append_refusals(lib):
 
 def _attention(lib, pool=None, q=P, dtype=0, batch=2, tokens=1, q_heads=8, qs=S, out=P, pages=P,
                max_pages=4, lengths=P, window=0, sinks=0, weights=None, width=0, ws=P, ws_bytes=1 << 40):
-    return lib.kv_cache_attention_x16(ctypes.byref(pool or _pool()), q, dtype, batch, tokens, q_heads,
+    return gr.kv_cache_attention_x16(pool or _pool(), q, dtype, batch, tokens, q_heads,
                                       qs, out, pages, max_pages, lengths, window, sinks, weights, width,
                                       ws, ws_bytes, None)
 
@@ -196,8 +195,8 @@ def test_attention_refusals(lib):
 
 def _evict(lib, pool=None, to=None, weights=P, width=256, pages=P, max_pages=4, lengths=P, batch=2,
            budget=100, sinks=4, recent=20, to_pages=P, to_max=2, to_lengths=P, to_weights=P, kept=P):
-    return lib.kv_cache_evict_e4m3(ctypes.byref(pool or _pool()), weights, width, pages, max_pages,
-                                   lengths, batch, budget, sinks, recent, ctypes.byref(to or _pool()),
+    return gr.kv_cache_evict_e4m3(pool or _pool(), weights, width, pages, max_pages,
+                                   lengths, batch, budget, sinks, recent, to or _pool(),
                                    to_pages, to_max, to_lengths, to_weights, kept, None)
 
 
@@ -215,7 +214,7 @@ def test_evict_refusals(lib):
 
 def _window(lib, q=P, k=P, v=P, o=P, dtype=0, batch=1, n_q=8, n_kv=8, hq=4, hkv=2, d=64, qs=S, ks=S,
             vs=S, window=4, sinks=1):
-    return lib.flash_attention_window_x16(q, k, v, o, dtype, batch, n_q, n_kv, hq, hkv, d, qs, ks, vs,
+    return gr.flash_attention_window_x16(q, k, v, o, dtype, batch, n_q, n_kv, hq, hkv, d, qs, ks, vs,
                                           window, sinks, None)
 
 

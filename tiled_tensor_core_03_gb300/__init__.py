@@ -41,6 +41,14 @@ KERNEL_NAMES = {KERNEL_PAIR: "CTA-pair kernel (256 x 256 tiles)",
 _lib = None
 
 
+class KVCachePool(ctypes.Structure):
+    """kv_cache_pool of include/kv_cache.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
+                ("kv_heads", ctypes.c_int64), ("page", ctypes.c_int64),
+                ("head_dim", ctypes.c_int64)]
+
+
 class GemmReluError(RuntimeError):
     def __init__(self, code, what=""):
         self.code = code
@@ -71,6 +79,8 @@ def lib():
         L.gemm_relu_f16_splitk_noalloc.restype = i32
         L.gemm_relu_status.argtypes = [vp]
         L.gemm_relu_status.restype = i32
+        L.gemm_relu_stream_capturing.argtypes = [vp]
+        L.gemm_relu_stream_capturing.restype = i32
         L.gemm_relu_strerror.argtypes = [i32]
         L.gemm_relu_strerror.restype = ctypes.c_char_p
         L.gemm_relu_f16_path.argtypes = [vp, vp, vp, i64, i64, i64]
@@ -153,6 +163,46 @@ def gemm_relu_f16_splitk_noalloc(A, B, C, M, N, K, split_k, stream=None):
 def flash_attention_f16(Q, K, V, O, batch, seq, heads, head_dim, causal, stream=None):
     return lib().flash_attention_f16(Q, K, V, O, batch, seq, heads, head_dim, int(causal),
                                      stream)
+
+
+def flash_attention_window_x16(Q, K, V, O, dtype, batch, q_seq, kv_seq, q_heads, kv_heads,
+                               head_dim, q_strides, k_strides, v_strides, window, sinks,
+                               stream=None):
+    """*_strides: ctypes arrays of three int64 {sequence, token, head}."""
+    return lib().flash_attention_window_x16(Q, K, V, O, dtype, batch, q_seq, kv_seq, q_heads,
+                                            kv_heads, head_dim, q_strides, k_strides, v_strides,
+                                            window, sinks, stream)
+
+
+def kv_cache_append_x16(cache, k, v, dtype, batch, tokens, k_strides, v_strides, pages, max_pages,
+                        lengths, counts, stream=None):
+    """cache: a KVCachePool."""
+    return lib().kv_cache_append_x16(ctypes.byref(cache), k, v, dtype, batch, tokens, k_strides,
+                                     v_strides, pages, max_pages, lengths, counts, stream)
+
+
+def kv_cache_attention_x16_workspace_bytes(batch, tokens, q_heads, kv_heads, head_dim,
+                                           weights_width=0):
+    return lib().kv_cache_attention_x16_workspace_bytes(batch, tokens, q_heads, kv_heads, head_dim,
+                                                        weights_width)
+
+
+def kv_cache_attention_x16(cache, q, dtype, batch, tokens, q_heads, q_strides, out, pages,
+                           max_pages, lengths, window, sinks, weights, weights_width, workspace,
+                           workspace_bytes, stream=None):
+    """cache: a KVCachePool."""
+    return lib().kv_cache_attention_x16(ctypes.byref(cache), q, dtype, batch, tokens, q_heads,
+                                        q_strides, out, pages, max_pages, lengths, window, sinks,
+                                        weights, weights_width, workspace, workspace_bytes, stream)
+
+
+def kv_cache_evict_e4m3(cache, weights, weights_width, pages, max_pages, lengths, batch, budget,
+                        sinks, recent, to, to_pages, to_max_pages, to_lengths, to_weights, kept,
+                        stream=None):
+    """cache and to: KVCachePools."""
+    return lib().kv_cache_evict_e4m3(ctypes.byref(cache), weights, weights_width, pages, max_pages,
+                                     lengths, batch, budget, sinks, recent, ctypes.byref(to),
+                                     to_pages, to_max_pages, to_lengths, to_weights, kept, stream)
 
 
 def gemm_relu_status(stream=None):

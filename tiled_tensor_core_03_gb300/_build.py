@@ -1,7 +1,10 @@
-"""Build libgemmrelu.so in-tree with nvcc for sm_103a (one translation unit)."""
+"""Build in-tree: libgemmrelu.so with nvcc for sm_103a (one translation unit), and beside it the
+CPython extension _serving that hands torch tensors to it (g++, torch's headers)."""
 import os
 import subprocess
 import sys
+import sysconfig
+import threading
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -27,19 +30,57 @@ def nvcc():
     return cand if os.path.exists(cand) else "nvcc"
 
 
+BINDING_SRC = os.path.join(CSRC, "serving_binding.cpp")
+BINDING = os.path.join(PKG, "_serving" + sysconfig.get_config_var("EXT_SUFFIX"))
+BINDING_DEPS = [BINDING_SRC] + [os.path.join(INCLUDE, f) for f in
+                                ("gemm_relu.h", "flash_attention.h", "kv_cache.h")]
+
+
+def _stale(target, deps):
+    return not os.path.exists(target) or any(
+        os.path.getmtime(d) > os.path.getmtime(target) for d in deps)
+
+
 def needs_build():
-    if not os.path.exists(LIB):
-        return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(d) > t for d in DEPS)
+    return _stale(LIB, DEPS) or _stale(BINDING, BINDING_DEPS)
+
+
+def build_binding():
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc, libs = os.path.join(root, "include"), os.path.join(root, "lib")
+    cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-I{INCLUDE}", f"-I{inc}", f"-I{os.path.join(inc, 'torch', 'csrc', 'api', 'include')}",
+           f"-I{sysconfig.get_path('include')}", f"-I{os.path.join(cuda, 'include')}",
+           "-o", BINDING, BINDING_SRC, f"-L{libs}", f"-Wl,-rpath,{libs}",
+           "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    subprocess.run(cmd, check=True)
+    return BINDING
 
 
 def build(verbose=False, extra=()):
-    cmd = [nvcc(), *NVCC_FLAGS, f"-I{INCLUDE}", f"-I{CSRC}", *extra, "-o", LIB, *SOURCES]
-    if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-        print(" ".join(cmd), file=sys.stderr)
-    subprocess.run(cmd, check=True)
+    """Compile both at the same time."""
+    failed = []
+
+    def binding():
+        try:
+            build_binding()
+        except Exception as e:   # raised again below, in the caller's thread
+            failed.append(e)
+    side = threading.Thread(target=binding)
+    side.start()
+    try:
+        cmd = [nvcc(), *NVCC_FLAGS, f"-I{INCLUDE}", f"-I{CSRC}", *extra, "-o", LIB, *SOURCES]
+        if verbose:
+            cmd.insert(1, "-Xptxas=-v")
+            print(" ".join(cmd), file=sys.stderr)
+        subprocess.run(cmd, check=True)
+    finally:
+        side.join()
+    if failed:
+        raise failed[0]
     return LIB
 
 

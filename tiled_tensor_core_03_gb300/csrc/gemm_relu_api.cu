@@ -1192,6 +1192,12 @@ int gemm_relu_status(void *stream) {
     return (int)st;
 }
 
+int gemm_relu_stream_capturing(void *stream) {
+    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+    return cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &st) == cudaSuccess &&
+           st != cudaStreamCaptureStatusNone;
+}
+
 const char *gemm_relu_strerror(int code) {
     switch (code) {
     case GEMMRELU_OK: return "ok";
