@@ -275,6 +275,23 @@ def test_append_numbers_at_the_edges():
     _same_cache(cache, want)
 
 
+@pytest.mark.parametrize("exponent", [-110, -60, -30, -20, 0, 20, 24, 30, 100])
+def test_append_beside_a_far_scale(exponent):
+    """New fp16 tokens of every magnitude in a page whose scale is far from theirs."""
+    import torch
+    rng = np.random.default_rng(exponent + 200)
+    cache, want = _cache(rng, 1, 1, 16, 64, garbage=False)
+    for which in (2, 3):
+        want[which][0, 0] = 2.0 ** max(exponent, -100)
+        cache[which][0, 0] = 2.0 ** max(exponent, -100)
+    mag = torch.tensor([2.0 ** -24, 2.0 ** -14, 1e-3, 1.0, 60000.0], device="cuda")[:, None, None]
+    k = (torch.randn((1, 5, 1, 64), device="cuda").clamp(-1, 1) * mag).half()
+    gr.kv_cache_append(cache, k, k, _i32([[0]]), _i32([12]))
+    for which in (0, 1):
+        ref.append(want[which], want[which + 2], _f64(k)[0], [0], 16, 12, 5)
+    _same_cache(cache, want)
+
+
 def test_append_refuses_what_only_the_device_sees():
     """Pages outside the pool, bad lengths and counts: nothing is written for them, the others
     are, and the status says so."""

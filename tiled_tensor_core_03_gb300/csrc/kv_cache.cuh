@@ -237,12 +237,24 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
         if (slot >= lo && slot < hi) {
             const uint32_t w[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
             uint32_t q[4];
+            if (!kBf16 && !infinite && inv <= 32768.0f && inv >= 0x1p-14f) {
+                // fp16 all the way: 1 / scale is a normal number, and what fp16 rounds off a product lies
+                // below 2^-24, far below e4m3's smallest half step of 2^-10
+                const uint32_t inv2 = half2_of(inv, inv);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float2 f = pair_to_float2<kBf16>(w[e]);
-                if (infinite)
-                    f = make_float2(storable(f.x), storable(f.y));
-                q[e] = to_e4m3x2(f.x * inv, f.y * inv);
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t y = w[e];
+                    asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(y) : "r"(inv2));
+                    q[e] = half2_to_e4m3x2(y);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float2 f = pair_to_float2<kBf16>(w[e]);
+                    if (infinite)
+                        f = make_float2(storable(f.x), storable(f.y));
+                    q[e] = to_e4m3x2(f.x * inv, f.y * inv);
+                }
             }
             *reinterpret_cast<uint2 *>(dst + 8 * v) = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
         } else if (slot < lo && scale != held) {
@@ -747,9 +759,11 @@ __global__ void __launch_bounds__(kMoveThreads, kVec == 4 ? 2 : 4) kv_evict_move
                     break;
                 const float ratio = s[kv][n] * inv;
                 uint32_t w[4] = {v[kv][n].x, v[kv][n].y, v[kv][n].z, v[kv][n].w};
-                // a power of two that fp16 holds (or 0: nothing there)
+                // a power of two that fp16 holds (or 0: nothing there); 1 where a page's scale
+                // stays, which the bytes pass as they are
                 const uint32_t r = __float_as_uint(ratio);
-                if ((r & 0x7fffffu) == 0 && ratio <= 32768.0f && (ratio >= 0x1p-14f || r == 0)) {
+                if (__all_sync(__activemask(), ratio == 1.0f)) {
+                } else if ((r & 0x7fffffu) == 0 && ratio <= 32768.0f && (ratio >= 0x1p-14f || r == 0)) {
                     const uint32_t ratio2 = half2_of(ratio, ratio);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
