@@ -61,7 +61,9 @@ KERNEL_CHOICES = {"auto": 0, "one_cta_256": 1, "one_cta_128": 2, "pair": 3, "gem
 
 KERNEL_SOURCES = ("gemm_relu_api.cu", "gemm_relu_kernels.cuh", "gemm_relu_splitk.cuh",
                   "gemm_relu_2sm.cuh", "gemm_relu_gemv.cuh", "flash_attention.cuh", "sm103.cuh",
-                  "gemm_relu_stage.cuh")
+                  "gemm_relu_stage.cuh", "flash_attention_window.cuh",
+                  "flash_attention_window_api.cuh", "kv_cache.cuh", "kv_attention.cuh",
+                  "kv_cache_api.cuh")
 
 
 def kernel_source_hash():
