@@ -632,6 +632,42 @@ def test_evict_refuses_what_only_the_device_sees():
                               a["recent"], to, _i32([[0]] * 3))
 
 
+def test_pages_past_four_gib():
+    """Pages whose bytes start past 2^32 in the pool: written, read and moved like any other."""
+    import torch
+    rng = np.random.default_rng(27)
+    num, hkv, page, d = 66000, 4, 128, 128            # 4.3 GB each of K and V
+    cache = gr.KVCache.empty(num, hkv, d, page)
+    far = num - 1 - np.arange(6)
+    assert int(far.min()) * hkv * page * d > 2 ** 32
+    n = 300
+    k, k64 = _rand(rng, (1, n, hkv, d), "bf16")
+    v, v64 = _rand(rng, (1, n, hkv, d), "bf16")
+    q, q64 = _rand(rng, (1, 2, 2 * hkv, d), "bf16")
+    pages, lengths = _i32([far[:3]]), _i32([n])
+    gr.kv_cache_append(cache, k, v, pages, lengths)
+    w = torch.zeros((1, hkv, 3 * page), device="cuda")
+    out = gr.kv_cache_attention(q, cache, pages, lengths, weights=w)
+    held = []
+    for x, which in ((k64, 0), (v64, 1)):
+        c, s = np.zeros((3, hkv, page, d)), np.ones((3, hkv))
+        ref.append(c, s, x[0], [0, 1, 2], page, n, n)
+        assert np.array_equal(_f64(cache[which][pages[0].long()].float())[:2], c[:2])
+        assert np.array_equal(_f64(cache[which + 2][pages[0].long()]), s)
+        held.append((c * s[..., None, None]).transpose(0, 2, 1, 3).reshape(-1, hkv, d)[:n])
+    o, absv, _, size = ref.attend(q64[0], held[0], held[1], 0, 0)
+    _check(_f64(out)[0], o, absv, size, d, "bf16", 2.0 ** -11)
+    n2, _, kept = gr.kv_cache_evict(cache, w, pages, lengths, 200, 2, 20, cache, _i32([far[3:5]]))
+    assert n2.item() == 200
+    again = gr.kv_cache_attention(q, cache, _i32([far[3:5]]), n2)
+    for h in range(hkv):
+        at = kept[0, h].cpu().numpy()
+        # the kept tokens' values are stored as they were, or rounded again under another scale
+        got = _f64(cache[0][far[3], h].float()) * float(cache[2][far[3], h])
+        assert np.allclose(got, held[0][at[:128], h], rtol=2.0 ** -4, atol=2.0 ** -9)
+    assert torch.isfinite(again).all()
+
+
 # ---------------------------------------------------------------- together
 
 
