@@ -180,6 +180,11 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, uint64_
     return __all_sync(0xffffffffu, wait_bounded_eager(bar, parity, limit_ns, abort_flag, where));
 }
 
+// The lowest n of 32 bits (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t keys_below(int n) {
+    return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1;
+}
+
 // The entries of a block list that a tile takes part in: [0, head) and [from, to).
 struct Turns {
     int head, from, to;
@@ -509,12 +514,17 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
                 for (int c0 = 0; c0 < kKeys; c0 += 32)
                     tmem_ld_wait_regs(*reinterpret_cast<uint32_t(*)[32]>(&v[c0]));
                 if (masked) {
+                    // a bit per key, 32 at a time: seen up to `hi`, above `lo` or below `head`
                     const int hi = pos - key0;
-                    const int lo = p.window > 0 ? hi - p.window : -1;   // seen above it, or below `head`
-                    const int head_end = p.sinks - key0;
+                    const int lo = p.window > 0 ? hi - p.window : -1;
+                    const int head = p.sinks - key0;
 #pragma unroll
-                    for (int i = 0; i < kKeys; ++i)
-                        v[i] = i <= hi && (i > lo || i < head_end) ? v[i] : __float_as_uint(-INFINITY);
+                    for (int c0 = 0; c0 < kKeys; c0 += 32) {
+                        const uint32_t seen = keys_below(hi + 1 - c0) & (~keys_below(lo + 1 - c0) | keys_below(head - c0));
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            v[c0 + i] = seen & (1u << i) ? v[c0 + i] : __float_as_uint(-INFINITY);
+                    }
                 }
                 float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
