@@ -292,7 +292,7 @@ __device__ __forceinline__ void write_row(const AttnParams &p, int b, int h, int
 // Releases this block's part (whose writers a barrier precedes), acquires the others'.
 __device__ __forceinline__ unsigned count_part(unsigned *word, unsigned n) {
     unsigned old;
-    asm volatile("fence.acq_rel.gpu;\n\tatom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;\n\tfence.acq_rel.gpu;"
+    asm volatile("fence.acq_rel.gpu;\n\tatom.relaxed.gpu.global.inc.u32 %0, [%1], %2;\n\tfence.acq_rel.gpu;"
                  : "=r"(old)
                  : "l"(word), "r"(n)
                  : "memory");
@@ -853,12 +853,13 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
 #pragma unroll
                 for (int j = 0; j < kF; ++j)
                     y[j] = 0.0f;
-                // four parts are read at a time
-                for (int c = c0; c <= c1; c += 4) {
-                    float2 ml[4];
-                    float4 z[4][kF / 4];
+                // a few parts are read at a time: each round waits for L2 once
+                constexpr int kAtOnce = kN == 1 ? 8 : 4;
+                for (int c = c0; c <= c1; c += kAtOnce) {
+                    float2 ml[kAtOnce];
+                    float4 z[kAtOnce][kF / 4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < kAtOnce; ++k) {
                         ml[k] = make_float2(-INFINITY, 0.0f);
                         if (c + k <= c1) {
                             const int64_t at = slot(c + k);
@@ -868,7 +869,10 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
                                 z[k][j] = __ldcg(reinterpret_cast<const float4 *>(p.partial + at * D + d0) + j);
                         }
                     }
-                    const float top = fmaxf(fmaxf(ref, fmaxf(ml[0].x, ml[1].x)), fmaxf(ml[2].x, ml[3].x));
+                    float top = ref;
+#pragma unroll
+                    for (int k = 0; k < kAtOnce; ++k)
+                        top = fmaxf(top, ml[k].x);
                     if (top > ref) {
                         const float f = exp2_fast(ref - top);   // 0 at first
                         sum *= f;
@@ -878,7 +882,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
                         ref = top;
                     }
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < kAtOnce; ++k) {
                         if (c + k > c1)
                             break;
                         const float f = exp2_fast(ml[k].x - (ref == -INFINITY ? 0.0f : ref));
