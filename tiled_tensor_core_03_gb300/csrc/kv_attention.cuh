@@ -51,8 +51,8 @@ constexpr int kAttnThreads = 160;
 constexpr float kMoveLog2 = 8.0f;    // the reference moves when a score exceeds it by more
 constexpr float kPShift = 128.0f;    // 2^7, see above
 
-// kN groups of 8 query rows a tile.  Two blocks an SM (168 registers a thread); three (128) only
-// where that takes no spills, 64 elements and one group.  Measured, one group: 32 sequences of up to
+// kN groups of 8 query rows a tile (two for heads of 64 only).  Two blocks an SM (168 registers a
+// thread); three (128) for 64 elements and one group.  Measured, one group: 32 sequences of up to
 // 4096 tokens, 8 heads of 128, 41.1 us with two blocks and 44.0 with three; 16 sequences of up
 // to 8192, window 2000, 16 heads of 64, 4 tokens each, 30.8 and 26.0 us.
 template <int D, int kN>

@@ -124,7 +124,7 @@ AttnSpace attention_space(int64_t batch, int64_t rows, int64_t kv_heads, int64_t
                           int64_t weights_width, int sms) {
     AttnSpace a{};
     const size_t slots = 2 * (size_t)sms * std::max(KC::AttnCfg<64, 1>::kBlocksPerSm * 8,
-                                                    KC::AttnCfg<128, 2>::kBlocksPerSm * 16);
+                                                    KC::AttnCfg<64, 2>::kBlocksPerSm * 16);
     size_t at = a.partial = GEMMRELU_KV_COUNTER_BYTES;
     at += slots * (head_dim + 2) * 4;
     a.lse = at = round256(at);
@@ -353,12 +353,15 @@ int kv_cache_attention_x16(const kv_cache_pool *cache, const void *q, int dtype,
     p.wait_limit_ns = wait_limit_ns();
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool bf16 = dtype == GEMMRELU_BF16;
-    // up to 8 rows fit one group of 8; two groups share the conversion of K and V
-    if (cache->head_dim == 64)
-        return rows <= 8 ? launch_kv_attention_as<64, 1>(bf16, mK, mV, p, s, ds->sms, ds->attr_kv)
-                         : launch_kv_attention_as<64, 2>(bf16, mK, mV, p, s, ds->sms, ds->attr_kv);
-    return rows <= 8 ? launch_kv_attention_as<128, 1>(bf16, mK, mV, p, s, ds->sms, ds->attr_kv)
-                     : launch_kv_attention_as<128, 2>(bf16, mK, mV, p, s, ds->sms, ds->attr_kv);
+    // Up to 8 rows fit one group of 8.  Beyond, two groups a tile share the conversion of K and V, which
+    // pays for heads of 64 (32 sequences of up to 4096 tokens, 8 K/V heads: 16 rows 41.9 us with two
+    // groups, 44.8 with a tile per group; 64 rows 124 and 143) but not for heads of 128, whose
+    // accumulators and query fragments spill at 168 registers (16 rows 76 to 107 us with two
+    // groups, 66.4 with a tile per group; 64 rows 233 to 365 and 222).
+    if (cache->head_dim == 128)
+        return launch_kv_attention_as<128, 1>(bf16, mK, mV, p, s, ds->sms, ds->attr_kv);
+    return rows <= 8 ? launch_kv_attention_as<64, 1>(bf16, mK, mV, p, s, ds->sms, ds->attr_kv)
+                     : launch_kv_attention_as<64, 2>(bf16, mK, mV, p, s, ds->sms, ds->attr_kv);
 }
 
 int kv_cache_debug_span(int64_t length, int64_t tokens, int64_t window, int64_t sinks, int *out) {
