@@ -31,9 +31,16 @@
 //    would still be NaN.  A row whose result is not finite (never, with finite inputs) is
 //    therefore computed again from its visible keys alone, a warp per row.
 //
-// Bound: the tensor cores' 4 d flops a visible pair and, on the other pipe, one exponential
-// a pair; blocks are 128 keys wide, so a window of W keys costs up to W + 255 keys and the
-// sinks one block.
+// Bound: the tensor cores' 4 d flops a pair; blocks are 128 keys wide, so a window of W keys
+// costs up to W + 255 keys and the sinks one block.  A tile's turn is a chain, S, softmax, P V, next
+// S over the same TMEM columns: about 3300 cycles a block with two tiles in turn, for 2048 cycles
+// of products.  Measured, 32 query heads on 8 of 128: 16384 tokens, window 4096, 739 to 770 us (the power
+// limit moves it), 1.27 to 1.32 PFLOP/s of visible pairs, 0.69 of the measured burst; 4 x 4096 tokens,
+// window 1024, 238 us, 1.01 PFLOP/s (9.3 blocks an item for 8 of keys, and 2500 cycles for an
+// item's output); a prompt of 203 tokens 7.0 us, launch and latency.
+// Not kept: 2^x by range reduction and a polynomial for a share of the pairs (a quarter: 262 -> 306 us;
+// exponentials are not the bound on this GPU), two threads a row on 16 softmax warps (326 us and more:
+// registers), separate K and V rings (272 us), 192 or 168 registers for the softmax (285 us).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -514,7 +521,8 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
                 for (int c0 = 0; c0 < kKeys; c0 += 32)
                     tmem_ld_wait_regs(*reinterpret_cast<uint32_t(*)[32]>(&v[c0]));
                 if (masked) {
-                    // a bit per key, 32 at a time: seen up to `hi`, above `lo` or below `head`
+                    // a bit per key, 32 at a time: seen up to `hi`, above `lo` or below `head` (three
+                    // compares a key instead: 262 us for 241 at window 1024)
                     const int hi = pos - key0;
                     const int lo = p.window > 0 ? hi - p.window : -1;
                     const int head = p.sinks - key0;

@@ -4,11 +4,16 @@
 //
 // over the tokens t that row r sees (t <= p_r; with a window W also t > p_r - W
 // or t < sinks), p_r the row's position.  The rows of one K/V head are
-// its group's query heads of every new token, 16 rows a tile.
+// its group's query heads of every new token, 8 rows a tile (16 for heads of 64).
 //
 // What bounds it: every visible token's 2 D bytes are read once per row tile and
-// used for 4 D flops a row, so up to some tens of rows it is a stream from HBM.  The
-// kernel is built around that stream:
+// used for 4 D flops a row, so one tile is a stream from HBM: 64 sequences of up to 32768
+// tokens, 8 heads of 128, 3.1 GB in 461 us, 6.7 TB/s (0.99 of a measured copy).  About 13 us of a
+// call are fixed: 3 to the first bytes (lengths, page numbers, pages, one after the other), 5 between
+// the first and the last block's end, 4 for counting and joining; so 32 sequences of up to 4096
+// tokens, 183 MB, take 41 us, and one sequence of 1000 tokens 9.5 us.  More row tiles are bound by
+// the conversions and products: 26 us for every further 8 rows at those 183 MB.  The
+// kernel is built around the stream:
 //
 //  - Work is cut into units of 64 tokens of one (sequence, head, row tile); the
 //    units of all of them, in order, are dealt to the blocks in equal contiguous

@@ -154,7 +154,11 @@ constexpr int kAppendThreads = 256;
 
 // One block per (sequence, touched page, head, K or V): the new tokens' elements stay in
 // registers (kVec vectors of 8 a thread) between the block's maximum and
-// the rounding, so they are read once.
+// the rounding, so they are read once.  A prompt is bound by HBM and, near it, by the issue of
+// conversions (69% of issue slots, the ALU pipe full): 4 prompts of up to 4096 tokens, 8 heads of 128,
+// fp16, 82.7 MB in 16.5 us, 5.0 TB/s.  Hence maxima on packed pairs (21.7 -> 19.0 us), the
+// page number read behind the tokens (-> 17.9) and fp16 scaled and rounded as it is (-> 16.5).
+// One token for each of 64 sequences takes 4.2 us, launch and three dependent reads.
 template <int D, int kVec, bool kBf16>
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendParams p) {
     __shared__ uint32_t slots[kAppendThreads / 32];
@@ -312,10 +316,13 @@ constexpr int kShortList = 512;   // keys that one warp finishes alone
 // (kKeys a thread; what does not fit is read again from L2), and the k-th largest is built
 // two bits at a time from the top: of three candidates the largest that k keys reach.
 // What bounds it is the rounds' latency and, with many keys, their compares, so once 512
-// keys or fewer share the bits found one warp takes those and finishes alone.
-// Counting takes the same time whatever the weights are; a histogram of digits had its
-// atomics collide, since weights share exponents: 23 us at 2000 tokens and 51 us at 16384.
-// 1024 threads with 16 keys each took 13 and 29 us, most of it in 17 rounds of barriers.
+// keys or fewer share the bits found one warp takes those and finishes alone (not across a
+// cluster: 8 sequences of up to 32768 tokens took 73.6 us that way and 65.8 this way, one took
+// 32.4 and 39.7).
+// Measured for one sequence of 2000 tokens and for 16 of up to 16384, 8 heads: with the move
+// 10.3 and 72 us, of which this is about 5 and 22.  Counting takes the same time whatever the
+// weights are; a histogram of digits had its atomics collide, since weights share exponents (23 and
+// 51 us); 1024 threads with 16 keys each took 13 and 29 us, most of it in 17 rounds of barriers.
 template <int kKeys>
 __global__ void __launch_bounds__(kSelectThreads, 1) kv_evict_select_kernel(const EvictParams p) {
     __shared__ uint2 warp_count[2][kSelectWarps];
@@ -627,7 +634,10 @@ __device__ __forceinline__ float largest_finite(const uint4 &x) {
 // vector of K and of V, and stores them under scales of their own.  The bytes stay
 // in registers between the maximum and the rounding.  A token's bytes are three dependent reads
 // away (its position, its page, itself), so a block walks over items and reads the next
-// item's positions and pages while this one's bytes are under way.
+// item's positions and pages while this one's bytes are under way.  Bound by HBM on rows of D
+// bytes and by issue (60% of the slots): 16 sequences cut from up to 16384 to 4096 tokens, 8
+// heads of 128, 134 MB read and 134 written in about 50 us; an item per block and fp32
+// arithmetic took 70.
 template <int D, int kVec>
 __global__ void __launch_bounds__(kMoveThreads, kVec == 4 ? 2 : 4) kv_evict_move_kernel(const EvictParams p) {
     __shared__ uint2 tops[2][kMoveThreads / 32];

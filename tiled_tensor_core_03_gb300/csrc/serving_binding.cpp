@@ -17,7 +17,7 @@
 #include <mutex>
 #include <sstream>
 #include <string>
-#include <tuple>
+#include <utility>
 
 #include "flash_attention.h"
 #include "gemm_relu.h"
@@ -218,24 +218,32 @@ PyObject *append_impl(PyObject *const *a) {
     Py_RETURN_NONE;
 }
 
-at::Tensor new_workspace(const at::Tensor &q, int64_t kv_heads, int64_t width) {
-    const size_t n = f_workspace_bytes(q.size(0), q.size(1), q.size(2), kv_heads, q.size(3), width);
-    at::Tensor w = at::empty({(int64_t)std::max<size_t>(n, GEMMRELU_KV_COUNTER_BYTES)}, q.options().dtype(at::kByte));
+size_t workspace_bytes(const at::Tensor &q, int64_t kv_heads, int64_t width) {
+    return std::max<size_t>(f_workspace_bytes(q.size(0), q.size(1), q.size(2), kv_heads, q.size(3), width),
+                            GEMMRELU_KV_COUNTER_BYTES);
+}
+
+at::Tensor new_workspace(const at::Tensor &q, size_t bytes) {
+    at::Tensor w = at::empty({(int64_t)bytes}, q.options().dtype(at::kByte));
     w.narrow(0, 0, GEMMRELU_KV_COUNTER_BYTES).zero_();
     return w;
 }
 
-// Workspaces of calls that bring none and collect no weights (a few MB whose size depends on
-// head_dim alone), one per device, stream and head_dim: calls on a stream follow one another.
-// Calls being captured get their own, since their graph may run anywhere.  Never destroyed:
-// they may outlive torch's allocator otherwise.
+// Workspaces of calls that bring none, one per device and stream, as large as its calls needed so
+// far: calls on a stream follow one another, and one that is replaced goes back to torch's
+// allocator for that stream.  Calls being captured get their own, since their graph may run
+// anywhere, and so do those that need more than kKeep (scores of many weights), which torch then
+// has back at once.  The map is never destroyed: at exit torch's allocator may be gone before it.
+constexpr size_t kKeep = (size_t)64 << 20;
+
 at::Tensor workspace_for(const at::Tensor &q, int64_t kv_heads, int64_t width, int d, void *stream) {
-    if (width > 0 || f_capturing(stream))
-        return new_workspace(q, kv_heads, width);
-    static auto *kept = new std::map<std::tuple<int, void *, int64_t>, at::Tensor>;
-    at::Tensor &w = (*kept)[{d, stream, q.size(3)}];   // (the GIL is held)
-    if (!w.defined())
-        w = new_workspace(q, kv_heads, 0);
+    const size_t bytes = workspace_bytes(q, kv_heads, width);
+    if (bytes > kKeep || f_capturing(stream))
+        return new_workspace(q, bytes);
+    static auto *kept = new std::map<std::pair<int, void *>, at::Tensor>;
+    at::Tensor &w = (*kept)[{d, stream}];   // (the GIL is held)
+    if (!w.defined() || w.nbytes() < bytes)
+        w = new_workspace(q, bytes);
     return w;
 }
 
@@ -293,7 +301,7 @@ PyObject *workspace_impl(PyObject *const *a) {
         refuse(PyExc_ValueError, "q must be [batch, tokens, q_heads, head_dim]");
     const kv_cache_pool pool = pool_of(a[1], d);
     const int64_t width = a[2] == Py_None ? 0 : tensor(a[2], "weights").size(-1);
-    return THPVariable_Wrap(new_workspace(q, pool.kv_heads, width));
+    return THPVariable_Wrap(new_workspace(q, workspace_bytes(q, pool.kv_heads, width)));
 }
 
 PyObject *evict_impl(PyObject *const *a) {

@@ -92,8 +92,8 @@ def kv_cache_attention(q, cache, pages, lengths, window=0, sinks=0, weights=None
     `weights` (fp32 [batch, kv_heads, at least max_pages * page]) each token's softmax
     weights, summed over the query tokens and heads of its group, are added to it.
 
-    Without a `workspace` the call uses one that is kept per stream, or its own where it
-    collects weights or is being captured."""
+    Without a `workspace` the call uses one that is kept per stream (up to 64 MB), or its
+    own where it needs more or is being captured."""
     if stream is not None:
         with torch.cuda.stream(stream):   # what is allocated belongs to it
             return _serving.attention(cache, q, pages, lengths, window, sinks, weights, out,
