@@ -105,6 +105,28 @@ def test_window_without_window_is_causal_attention():
     assert torch.equal(a.view(torch.int16), b.view(torch.int16))
 
 
+@pytest.mark.parametrize("batch,n_q,n_kv,group,kvh,d,window", [
+    (1, 300, 32768, 1, 7, 128, 900),     # 16 MB of K and V a head: four heads together, then three
+    (1, 900, 70000, 3, 3, 64, 0),        # five tiles of two heads; 18 MB a head
+    (5, 700, 700, 3, 7, 64, 100),        # all heads together, several rounds of a grid
+    (1, 300, 260000, 2, 3, 128, 5000),   # no two heads fit
+])
+def test_window_order_of_heads(batch, n_q, n_kv, group, kvh, d, window):
+    """Heads whose work is interleaved give the bits that each gives alone."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(n_q)
+    q = torch.randn(batch, n_q, kvh * group, d, device="cuda", dtype=torch.float16, generator=g)
+    k, v = (torch.randn(batch, n_kv, kvh, d, device="cuda", dtype=torch.float16, generator=g)
+            for _ in range(2))
+    out = gr.flash_attention_window(q, k, v, window, 4)
+    for b in range(batch):
+        for h in range(kvh):
+            alone = gr.flash_attention_window(q[b:b + 1, :, h * group:(h + 1) * group], k[b:b + 1, :, h:h + 1],
+                                              v[b:b + 1, :, h:h + 1], window, 4)
+            mine = out[b:b + 1, :, h * group:(h + 1) * group]
+            assert torch.equal(mine.view(torch.int16), alone.view(torch.int16)), (b, h)
+
+
 def test_window_strides_and_stream():
     """Slices of a fused projection, heads before tokens, an axis of one with an odd stride; on a
     side stream."""

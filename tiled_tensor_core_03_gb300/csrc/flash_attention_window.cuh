@@ -34,10 +34,10 @@
 // Bound: the tensor cores' 4 d flops a pair; blocks are 128 keys wide, so a window of W keys
 // costs up to W + 255 keys and the sinks one block.  A tile's turn is a chain, S, softmax, P V, next
 // S over the same TMEM columns: about 3300 cycles a block with two tiles in turn, for 2048 cycles
-// of products.  Measured, 32 query heads on 8 of 128: 16384 tokens, window 4096, 739 to 770 us (the power
-// limit moves it), 1.27 to 1.32 PFLOP/s of visible pairs, 0.69 of the measured burst; 4 x 4096 tokens,
-// window 1024, 238 us, 1.01 PFLOP/s (9.3 blocks an item for 8 of keys, and 2500 cycles for an
-// item's output); a prompt of 203 tokens 7.0 us, launch and latency.
+// of products.  Measured, 32 query heads on 8 of 128: 16384 tokens, window 4096, 691 to 702 us (the power
+// limit moves it), 1.39 to 1.41 PFLOP/s of visible pairs, 0.75 of the measured burst; 4 x 4096 tokens,
+// window 1024, 223 us, 1.08 PFLOP/s (9.3 blocks an item for 8 of keys, and 2500 cycles for an
+// item's output); a prompt of 203 tokens 6.9 us, launch and latency.
 // Not kept: 2^x by range reduction and a polynomial for a share of the pairs (a quarter: 262 -> 306 us;
 // exponentials are not the bound on this GPU), two threads a row on 16 softmax warps (326 us and more:
 // registers), separate K and V rings (272 us), 192 or 168 registers for the softmax (285 us).
@@ -50,6 +50,29 @@
 namespace gemmrelu {
 namespace attn {
 
+// n / d for 0 <= n < 2^31 by a product (Granlund and Montgomery, Division by Invariant Integers using
+// Multiplication, 1994): with l = ceil(log2 d) and m = floor(2^32 (2^l - d) / d) + 1 it is
+// (hi(m n) + n) >> l.  A work item needs four, and the compiler's long division delayed the next
+// item's scores: 4 x 4096 tokens, 32 heads on 8 of 128, window 128 114 us, now 107.
+struct Divisor {
+    uint32_t m;
+    int l;
+    static Divisor of(uint32_t d) {
+        Divisor v{0, 0};
+        while (v.l < 31 && (1u << v.l) < d)
+            ++v.l;
+        v.m = (uint32_t)(((((uint64_t)1 << v.l) - d) << 32) / d) + 1;
+        return v;
+    }
+    __host__ __device__ int quotient(int n) const {
+#ifdef __CUDA_ARCH__
+        return (int)((__umulhi(m, (uint32_t)n) + (uint32_t)n) >> l);
+#else
+        return (int)(((uint32_t)((uint64_t)m * (uint32_t)n >> 32) + (uint32_t)n) >> l);
+#endif
+    }
+};
+
 struct WindowParams {
     const uint16_t *q, *k, *v;
     int64_t qs[3], ks[3], vs[3];   // sequence, token, head
@@ -58,6 +81,8 @@ struct WindowParams {
     int q_tiles, items;            // items = q_tiles * group: tiles of one K/V head
     int kv_heads, batch;
     int pairs, window, sinks;
+    int chunk, chunk_items;        // K/V heads of all sequences whose items mix, and their items
+    Divisor by_chunk, by_last, by_chunk_items, by_kv_heads, by_group;   // (last: the rest of heads)
     float scale;                   // log2(e) / sqrt(d)
     int drop_arrive;
     uint64_t wait_limit_ns;
@@ -211,16 +236,37 @@ struct WindowItem {
     __device__ __forceinline__ int block(int j) const { return j < sinks ? j : low + (j - sinks); }
 };
 
+// The items of this CTA, one a round.  Within a chunk of heads their cost falls, so that with
+// rounds dealt out forwards and backwards in turn every CTA gets about the same sum.
+struct WindowWalk {
+    int base, total;
+    bool back;
+    __device__ __forceinline__ WindowWalk(const WindowParams &p)
+        : base(0), total(p.pairs * p.kv_heads * p.batch), back(false) {}
+    __device__ __forceinline__ bool more() const { return base + (int)blockIdx.x < total; }
+    __device__ __forceinline__ int index() const {
+        return back ? min(base + (int)gridDim.x, total) - 1 - (int)blockIdx.x : base + (int)blockIdx.x;
+    }
+    __device__ __forceinline__ void next() {
+        base += gridDim.x;
+        back = !back;
+    }
+};
+
 template <int HD>
 __device__ __forceinline__ WindowItem window_item(const WindowParams &p, int index) {
     WindowItem w;
     // the last queries see the most keys: they go first
-    const int pair = p.pairs - 1 - index % p.pairs, off = p.n_kv - p.n_q, item = 2 * pair;
-    index /= p.pairs;
-    w.kvh = index % p.kv_heads;
-    w.batch = index / p.kv_heads;
+    const int chunk = p.by_chunk_items.quotient(index), first = chunk * p.chunk;
+    const int heads = min(p.chunk, p.kv_heads * p.batch - first);
+    index -= chunk * p.chunk_items;
+    const int rank = (heads == p.chunk ? p.by_chunk : p.by_last).quotient(index);
+    const int pair = p.pairs - 1 - rank, off = p.n_kv - p.n_q, item = 2 * pair;
+    index = first + index - rank * heads;
+    w.batch = p.by_kv_heads.quotient(index);
+    w.kvh = index - w.batch * p.kv_heads;
     w.two = item + 1 < p.items;
-    w.tile0 = item / p.group;
+    w.tile0 = p.by_group.quotient(item);
     const int g = item - w.tile0 * p.group;
     w.head0 = w.kvh * p.group + g;
     const bool same = g + 1 < p.group;   // the second tile: the next head, or the next queries
@@ -288,7 +334,6 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);   // uniform
     const int lane = threadIdx.x & 31;
     const int off = p.n_kv - p.n_q;
-    const int total = p.pairs * p.kv_heads * p.batch;
 
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1u);
@@ -330,8 +375,8 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
         if (warp == kProducerWarp && lane == 0) {
             uint32_t queries = 0, blocks = 0;   // Q loads and K/V blocks issued
             bool ok = !(p.drop_arrive && blockIdx.x == 0);
-            for (int index = blockIdx.x; ok && index < total; index += gridDim.x) {
-                const WindowItem w = window_item<HD>(p, index);
+            for (WindowWalk walk(p); ok && walk.more(); walk.next()) {
+                const WindowItem w = window_item<HD>(p, walk.index());
                 if (w.nb == 0)
                     continue;
                 if (!wait_bounded_eager(q_empty, (queries & 1u) ^ 1u, p.wait_limit_ns, abort_flag,
@@ -441,10 +486,11 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
                 }
                 return true;
             };
+            WindowWalk walk(p);
             WindowItem w{};
-            if ((int)blockIdx.x < total)
-                w = window_item<HD>(p, blockIdx.x);
-            for (int index = blockIdx.x; ok && index < total;) {
+            if (walk.more())
+                w = window_item<HD>(p, walk.index());
+            while (ok && walk.more()) {
                 const int nb = w.nb, narrow = w.narrow;
                 const Turns t0 = w.t0, t1 = w.t1;
                 if (nb > 0) {
@@ -457,9 +503,9 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
                     if (ok && nb == 1 && leader)
                         umma_commit(q_empty);
                 }
-                index += gridDim.x;
-                if (index < total)
-                    w = window_item<HD>(p, index);
+                walk.next();
+                if (walk.more())
+                    w = window_item<HD>(p, walk.index());
                 bool fresh0 = true, fresh1 = true;
                 for (int j = 0; ok && j < nb; ++j, ++blocks) {
                     const bool here = j == narrow, there = j + 1 == narrow, more = j + 1 < nb;
@@ -499,8 +545,8 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
         const uint32_t o_addr = tmem_base + lane_base + G::kTmemO + t * HD;
         uint32_t turns = 0, outputs = 0;
         bool alive = true;
-        for (int index = blockIdx.x; alive && index < total; index += gridDim.x) {
-            const WindowItem w = window_item<HD>(p, index);
+        for (WindowWalk walk(p); alive && walk.more(); walk.next()) {
+            const WindowItem w = window_item<HD>(p, walk.index());
             if (t == 1 && !w.two)
                 continue;
             const int tile = t ? w.tile1 : w.tile0, head = t ? w.head1 : w.head0;

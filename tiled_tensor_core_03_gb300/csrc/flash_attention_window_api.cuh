@@ -58,6 +58,15 @@ int launch_window(const CUtensorMap &mQ, const CUtensorMap &mK, const CUtensorMa
 
 }  // namespace
 
+// The order of the work.  The first queries see fewer keys than the last, and with one head after the
+// other a CTA whose stride shares a factor with a head's items gets the same few places in each.  So
+// heads go together, the last queries of all of them first, as many heads as have K and V in 96 MB
+// of the L2 cache (129 MB).  Measured, 32 heads on 8 of 128, one head after the other against this: 4 x 4096
+// tokens without a window 440 -> 405 us, with 1024 237 -> 223; 2048 tokens 51.3 -> 40.9; 16384 tokens
+// without a window 1590 -> 1444 us, with 4096 710 -> 666; 4 x 4096 and 32 heads on 32 557 -> 453 us
+// (485 with all heads together).  What it costs: 16384 tokens with a window of 512 173 -> 186 us.
+constexpr int64_t kWindowChunkBytes = (int64_t)96 << 20;
+
 extern "C" int flash_attention_window_x16(const void *Q, const void *K, const void *V, void *O,
                                           int dtype, int64_t batch, int64_t q_seq, int64_t kv_seq,
                                           int64_t q_heads, int64_t kv_heads, int64_t head_dim,
@@ -113,6 +122,16 @@ extern "C" int flash_attention_window_x16(const void *Q, const void *K, const vo
     p.batch = (int)batch;
     p.items = (int)items;
     p.pairs = (int)((items + 1) / 2);
+    const int64_t heads = batch * kv_heads;
+    const int64_t fit = std::max<int64_t>(1, kWindowChunkBytes / (kv_seq * head_dim * 4));
+    const int64_t chunks = (heads + fit - 1) / fit;
+    p.chunk = (int)((heads + chunks - 1) / chunks);
+    p.chunk_items = p.chunk * p.pairs;
+    p.by_chunk = FA::Divisor::of(p.chunk);
+    p.by_last = FA::Divisor::of(heads % p.chunk ? heads % p.chunk : p.chunk);
+    p.by_chunk_items = FA::Divisor::of(p.chunk_items);
+    p.by_kv_heads = FA::Divisor::of(p.kv_heads);
+    p.by_group = FA::Divisor::of(p.group);
     p.window = (int)std::min<int64_t>(window, (int64_t)1 << 30);
     p.sinks = (int)std::min<int64_t>(sinks, (int64_t)1 << 30);
     p.scale = (float)(1.4426950408889634 / std::sqrt((double)head_dim));
