@@ -393,6 +393,17 @@ def test_cache_attention_weights(page, d, hkv, group, tokens, lengths, window, s
     _attend(rng, page, d, hkv, group, tokens, lengths, window, sinks, "fp16", weights=True)
 
 
+@pytest.mark.parametrize("weights", [False, True])
+@pytest.mark.parametrize("page,d,hkv,group,tokens,lengths,window,sinks", [
+    (64, 128, 1, 8, 17, [700, 64, 17, 9], 0, 0),     # 17 tiles of 8 rows: nine at a time, the last one empty
+    (32, 64, 2, 8, 33, [500, 40], 100, 3),           # 17 tiles of 16
+    (16, 128, 2, 3, 90, [400, 95, 0], 0, 0),         # 34 tiles in three passes of twelve
+    (128, 128, 1, 4, 8, [6000], 0, 0)])              # four tiles, each cut into many parts
+def test_cache_attention_many_row_tiles(page, d, hkv, group, tokens, lengths, window, sinks, weights):
+    rng = np.random.default_rng(page + d + tokens + sum(lengths))
+    _attend(rng, page, d, hkv, group, tokens, lengths, window, sinks, "bf16", weights=weights)
+
+
 def test_cache_attention_many_sequences_and_large_scores():
     """More sequences than threads that count them, most of them empty or short, a table wider than
     any needs; scores of tens of units."""

@@ -246,10 +246,10 @@ bool ensure_smem_attr(bool &done, Kern kernel, uint32_t bytes) {
 // memory.  `cooperative` guarantees co-residency of all CTAs (stream-K);
 // cluster_x > 1 sets a cluster shape at launch.
 template <typename... KArgs, typename... Args>
-int launch_kernel(void (*kern)(KArgs...), unsigned grid, unsigned block, uint32_t smem,
+int launch_kernel(void (*kern)(KArgs...), dim3 grid, unsigned block, uint32_t smem,
                   cudaStream_t stream, bool cooperative, unsigned cluster_x, Args &&...args) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;

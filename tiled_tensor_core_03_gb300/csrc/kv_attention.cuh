@@ -12,12 +12,17 @@
 // call are fixed: 3 to the first bytes (lengths, page numbers, pages, one after the other), 5 between
 // the first and the last block's end, 4 for counting and joining; so 32 sequences of up to 4096
 // tokens, 183 MB, take 41 us, and one sequence of 1000 tokens 9.5 us.  More row tiles are bound by
-// the conversions and products: 26 us for every further 8 rows at those 183 MB.  The
+// the chain of conversions and products of a unit: 25 us for every further 8 rows at those 183 MB.  The
 // kernel is built around the stream:
 //
-//  - Work is cut into units of 64 tokens of one (sequence, head, row tile); the
+//  - Work is cut into units of 64 tokens of one (sequence, head); the
 //    units of all of them, in order, are dealt to the blocks in equal contiguous
-//    ranges whatever the lengths are.  A block finishes what lies
+//    ranges whatever the lengths are.  Each range has a block per row tile (grid.y, up to 16; further
+//    tiles in further passes): they read the same units at about the same time, from
+//    HBM once, and their strips of the scores meet in L2.  With the tiles one after the other in one
+//    block's range 32 sequences of up to 4096 tokens, 8 heads of 128, took 66.3 us, not 64.3, with 16 rows,
+//    222 and 216 with 64, and with weights 202 and 165 with 28; one tile pays 0.3 us of 41.
+//    A block finishes what lies
 //    inside its range; a (sequence, head, row tile) that is cut leaves one fp32
 //    partial (O, m, l) per block in the workspace, and the block that comes last joins
 //    them, in the order of the ranges.  No block waits for another and nothing depends on
@@ -53,6 +58,7 @@ constexpr int kUnit = 64;            // tokens of a stage
 constexpr int kWarps = 4;            // computing warps
 constexpr int kFeedWarp = 4;
 constexpr int kAttnThreads = 160;
+constexpr int kMostAbreast = 16;     // row tiles that share the stream of a head
 constexpr float kMoveLog2 = 8.0f;    // the reference moves when a score exceeds it by more
 constexpr float kPShift = 128.0f;    // 2^7, see above
 
@@ -86,13 +92,14 @@ struct AttnParams {
     const int32_t *pages, *lengths;
     int64_t max_pages;
     int batch, tokens, q_heads, group;
-    int rows, row_tiles;               // tokens * group, in tiles of 8 or 16
+    int rows;                          // tokens * group, in tiles of 8 or 16: `abreast` at a time,
+    int abreast, passes;               // `passes` times
     int window, sinks;
     float scale_log2;                  // log2(e) / sqrt(D)
     float *partial;                    // [2 * grid][kRows][D], then [2 * grid][kRows][2] (m, l)
-    int grid;
-    unsigned *arrived;                 // [grid] parts that are there of the segment that leaves
-                                       // block i; all 0 between calls
+    int grid;                          // ranges * abreast
+    unsigned *arrived;                 // [ranges][abreast] parts that are there of the segment that
+                                       // leaves the block's range; all 0 between calls
     float *scores;                     // with weights: [batch][kv_heads][width][rows], base 2
     float *lse;                        //               [batch][kv_heads][rows], base 2
     float *weights;                    // [batch][kv_heads][width]
@@ -153,8 +160,8 @@ __host__ __device__ __forceinline__ int range_owner(int x, int total, int grid) 
     return x < longer ? x / (q + 1) : r + (x - longer) / q;
 }
 
-// How many of the launched blocks work: each takes a unit at least, and a (sequence, head,
-// row tile) is cut into about sqrt(4 units) parts at most.  A part costs its block's start
+// How many of the launched ranges have work: each has a unit at least, and a (sequence, head,
+// pass) is cut into about sqrt(4 units) parts at most.  A part costs its block's start
 // and, in the join, a read of its O by one block; a unit in sequence costs its copy.
 __device__ __forceinline__ int blocks_used(int total, int segments, int grid) {
     const float most = sqrtf(4.0f * (float)total * (float)segments);
@@ -348,9 +355,10 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
     }
     pdl_wait_primary();
 
-    // this block's range of units, and the sequence that it starts in: every thread counts a
+    // this block's range of units of 64 tokens, and the sequence that it starts in: every thread counts a
     // slice of the sequences
-    const int per_seq = p.pool.kv_heads * p.row_tiles;   // (head, row tile) pairs
+    const int range = blockIdx.x, lane_tile = blockIdx.y;
+    const int per_seq = p.pool.kv_heads * p.passes;   // (head, pass) pairs
     const int slice = (p.batch + kAttnThreads - 1) / kAttnThreads;
     const int b0 = min(tid * slice, p.batch), b1 = min(b0 + slice, p.batch);
     int mine = 0;
@@ -373,9 +381,9 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
     }
     total *= per_seq;
     seq_at *= per_seq;
-    const int blocks = blocks_used(total, p.batch * per_seq, p.grid);
-    const int start = (int)blockIdx.x < blocks ? range_start(blockIdx.x, total, blocks) : total;
-    const int stop = (int)blockIdx.x < blocks ? range_start(blockIdx.x + 1, total, blocks) : total;
+    const int ranges = blocks_used(total, p.batch * per_seq, gridDim.x);
+    const int start = range < ranges ? range_start(range, total, ranges) : total;
+    const int stop = range < ranges ? range_start(range + 1, total, ranges) : total;
     if (start < stop && start >= seq_at && start < seq_at + mine * per_seq) {
         int i = b0;
         for (; slice > 1; ++i) {
@@ -415,7 +423,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
                     s = span_of(n, p.tokens, p.window, p.sinks);
                 }
                 const int local = (unit - lat) / s.units;
-                h = local / p.row_tiles;
+                h = local / p.passes;
                 const int token = s.chunk((unit - lat) % s.units) * kUnit +
                                   (lane % pieces) * piece_tokens;
                 slot = token & (p.pool.page - 1);
@@ -485,7 +493,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
         // and the one that it ends in
         int cut_b[2], cut_local[2], cut_seg0[2], cut_seg1[2], cuts = 0;
         while (unit < stop) {
-            // the (sequence, head, row tile) of this unit, and its units in this block
+            // the (sequence, head, pass) of this unit, and its units in this block
             int n = length_of(p, b);
             Span s = span_of(n, p.tokens, p.window, p.sinks);
             while (unit >= seq_at + s.units * per_seq) {
@@ -494,7 +502,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
                 s = span_of(n, p.tokens, p.window, p.sinks);
             }
             const int local = (unit - seq_at) / s.units;
-            const int h = local / p.row_tiles, tile = local % p.row_tiles;
+            const int h = local / p.passes, tile = local % p.passes * p.abreast + lane_tile;
             const int seg0 = seq_at + local * s.units, seg1 = seg0 + s.units;
             const int end = seg1 < stop ? seg1 : stop;
             const int row0 = tile * kRows;
@@ -814,7 +822,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
                         write_row<D, kF, kBf16, kScores>(p, b, h, row0 + r, d0, y, ref, sum);
                 } else {
                     // a part: slot 0 where it starts this block's range, else slot 1
-                    const int64_t at = ((int64_t)blockIdx.x * 2 + (seg0 > start ? 1 : 0)) * kRows + r;
+                    const int64_t at = ((int64_t)(range * p.abreast + lane_tile) * 2 + (seg0 > start ? 1 : 0)) * kRows + r;
                     float *dst = p.partial + at * D + d0;
 #pragma unroll
                     for (int j = 0; j < kF; j += 4)
@@ -837,9 +845,10 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
             named_bar_sync(1, 32 * kWarps);
             if (lane == 0 && warp < cuts) {
                 const int i = warp;
-                const int c0 = range_owner(i ? cut_seg0[1] : cut_seg0[0], total, blocks);
-                const int c1 = range_owner((i ? cut_seg1[1] : cut_seg1[0]) - 1, total, blocks);
-                last[i] = count_part(p.arrived + c0, (unsigned)(c1 - c0)) == (unsigned)(c1 - c0);
+                const int c0 = range_owner(i ? cut_seg0[1] : cut_seg0[0], total, ranges);
+                const int c1 = range_owner((i ? cut_seg1[1] : cut_seg1[0]) - 1, total, ranges);
+                last[i] = count_part(p.arrived + c0 * p.abreast + lane_tile, (unsigned)(c1 - c0)) ==
+                          (unsigned)(c1 - c0);
             }
             named_bar_sync(1, 32 * kWarps);
 #pragma unroll 1
@@ -848,12 +857,14 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
                     continue;
                 const int seg0 = i ? cut_seg0[1] : cut_seg0[0], seg1 = i ? cut_seg1[1] : cut_seg1[0];
                 const int local = i ? cut_local[1] : cut_local[0], bb = i ? cut_b[1] : cut_b[0];
-                const int c0 = range_owner(seg0, total, blocks), c1 = range_owner(seg1 - 1, total, blocks);
+                const int c0 = range_owner(seg0, total, ranges), c1 = range_owner(seg1 - 1, total, ranges);
                 constexpr int kF = D * kN / 16;
                 const int r = tid * kN / 16, d0 = tid % (16 / kN) * kF;
                 // a part's row: only the first part can start inside its block's range
-                const int first = (c0 * 2 + (seg0 > range_start(c0, total, blocks) ? 1 : 0)) * kRows + r;
-                auto slot = [&](int c) { return (int64_t)(c == c0 ? first : c * 2 * kRows + r); };
+                const int first = seg0 > range_start(c0, total, ranges) ? 1 : 0;
+                auto slot = [&](int c) {
+                    return (int64_t)((c * p.abreast + lane_tile) * 2 + (c == c0 ? first : 0)) * kRows + r;
+                };
                 float ref = -INFINITY, sum = 0.0f, y[kF];
 #pragma unroll
                 for (int j = 0; j < kF; ++j)
@@ -903,9 +914,9 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
                 }
                 if (ref == -INFINITY)
                     ref = 0.0f;
-                const int row = local % p.row_tiles * kRows + r;
+                const int row = (local % p.passes * p.abreast + lane_tile) * kRows + r;
                 if (alive && row < p.rows)
-                    write_row<D, kF, kBf16, kScores>(p, bb, local / p.row_tiles, row, d0, y, ref, sum);
+                    write_row<D, kF, kBf16, kScores>(p, bb, local / p.passes, row, d0, y, ref, sum);
             }
         }
     }

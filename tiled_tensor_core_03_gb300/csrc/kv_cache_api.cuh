@@ -155,9 +155,14 @@ int launch_kv_attention(const CUtensorMap &mK, const CUtensorMap &mV, KC::AttnPa
     bool &attr_done = attr[(D == 128 ? 8 : 0) + (kN == 2 ? 4 : 0) + (kBf16 ? 2 : 0) + (kScores ? 1 : 0)];
     if (!ensure_smem_attr(attr_done, kern, G::kSmem))
         return GEMMRELU_ERR_LAUNCH;
-    p.row_tiles = (p.rows + G::kRows - 1) / G::kRows;
-    p.grid = std::min(sms * G::kBlocksPerSm, (int)(GEMMRELU_KV_COUNTER_BYTES / sizeof(unsigned)));
-    const int rc = launch_kernel(kern, (unsigned)p.grid, KC::kAttnThreads, G::kSmem, s, false, 1u, mK, mV, p);
+    const int tiles = (p.rows + G::kRows - 1) / G::kRows;
+    p.passes = (tiles + KC::kMostAbreast - 1) / KC::kMostAbreast;
+    p.abreast = (tiles + p.passes - 1) / p.passes;
+    const int ranges = std::max(1, std::min(sms * G::kBlocksPerSm,
+                                            (int)(GEMMRELU_KV_COUNTER_BYTES / sizeof(unsigned))) / p.abreast);
+    p.grid = ranges * p.abreast;
+    const int rc = launch_kernel(kern, dim3((unsigned)ranges, (unsigned)p.abreast), KC::kAttnThreads, G::kSmem, s,
+                                 false, 1u, mK, mV, p);
     if (rc != GEMMRELU_OK || !kScores)
         return rc;
     const int64_t blocks = (p.width + KC::kWeightThreads - 1) / KC::kWeightThreads;
