@@ -330,9 +330,11 @@ __global__ void __launch_bounds__(kSelectThreads, 1) kv_evict_select_kernel(cons
     __shared__ int slot_sure[kKeys * kSelectWarps], slot_tie[kKeys * kSelectWarps];
     __shared__ uint32_t list[kShortList];
     __shared__ int shared[4];   // list length, k-th key, keys above it; totals
+    const int cluster = p.cluster, rank = cluster > 1 ? (int)cluster_ctarank() : 0;
+    if (cluster > 1)
+        cluster_arrive();   // this block runs: the others may store into its shared memory
     pdl_launch_dependents();
     pdl_wait_primary();
-    const int cluster = p.cluster, rank = cluster > 1 ? (int)cluster_ctarank() : 0;
     const int64_t bh = blockIdx.x / cluster;
     const int h = (int)(bh % p.from.kv_heads), b = (int)(bh / p.from.kv_heads);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -348,6 +350,8 @@ __global__ void __launch_bounds__(kSelectThreads, 1) kv_evict_select_kernel(cons
     if (n <= p.budget) {
         for (int i = rank * kSelectThreads + tid; i < n; i += cluster * kSelectThreads)
             kept[i] = i;
+        if (cluster > 1)
+            cluster_wait();
         return;   // all blocks of the cluster
     }
     const int lo = p.sinks, hi = n - p.recent;   // the tokens that compete for the rest
@@ -372,6 +376,8 @@ __global__ void __launch_bounds__(kSelectThreads, 1) kv_evict_select_kernel(cons
             key[s] = key_of_weight(g0 + s * kSelectThreads + tid, x[s]);
     };
     load(t0);
+    if (cluster > 1)
+        cluster_wait();   // the others have started (behind the loads: no time of its own)
 
     int turn = 0;
     // how many of all keys reach three thresholds
