@@ -114,6 +114,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
+    cluster_arrive();  // this CTA runs: the others may store into its shared memory
     const int n0 = (int)(blockIdx.x / (unsigned)csize) * kCols;
     const int s0 = (int)(((int64_t)rank * p.num_stages) / csize);
     const int s1 = (int)(((int64_t)(rank + 1) * p.num_stages) / csize);
@@ -232,6 +233,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                      __float_as_uint(acc[m][3].x), __float_as_uint(acc[m][3].y));
     }
     __syncthreads();
+    cluster_wait();  // every CTA of the cluster has started
     // column t: the warps' partials in order w = 0..7, then to the CTA of the
     // cluster that owns column t (kCols / csize columns each), slot = rank
     const uint32_t per_owner = (uint32_t)(kCols / csize);
