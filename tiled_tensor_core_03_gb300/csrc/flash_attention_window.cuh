@@ -150,7 +150,7 @@ __device__ __noinline__ void window_row(const WindowParams &p, int batch, int he
         o[e] = 0.0f;
     }
     const int low = p.window > 0 && pos - p.window + 1 > 0 ? pos - p.window + 1 : 0;
-    for (int j = p.sinks < low ? 0 : low; j <= pos; ++j) {
+    for (int j = p.sinks > 0 ? 0 : low; j <= pos; ++j) {   // the sinks, then the window
         if (j < low && j >= p.sinks)
             j = low;
         const uint16_t *k = p.k + batch * p.ks[0] + j * p.ks[1] + kvh * p.ks[2] + lane;
