@@ -41,3 +41,23 @@ def test_window_not_finite_beside_rows_that_left_sinks_behind(sinks, d, dtype):
         _check(got[~sees], o[~sees], absv[~sees], size[~sees], d, dtype, _half_step(dtype))
         got, o, absv = (np.delete(x, 5, 2) for x in (got, o, absv))
         _check(got, o, absv, size, d, dtype, _half_step(dtype))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_window_first_score_minus_infinity(dtype):
+    """A key whose score is -infinity has weight 0, also where it is the first that a row sees and
+    a V that the row does not see is not finite."""
+    rng = np.random.default_rng(41)
+    n, d = 200, 64
+    q, q64 = _rand(rng, (1, n, 1, d), dtype)
+    k, k64 = _rand(rng, (1, n, 1, d), dtype)
+    v, v64 = _rand(rng, (1, n, 1, d), dtype)
+    q, q64 = q.abs(), np.abs(q64)
+    k[0, :2, 0, 5], k64[0, :2, 0, 5] = -np.inf, -np.inf
+    v[0, 199, 0, 7], v64[0, 199, 0, 7] = np.nan, np.nan
+    for window, sinks in ((0, 0), (50, 2)):
+        got = _f64(gr.flash_attention_window(q, k, v, window, sinks))[0, 2:199]
+        with np.errstate(invalid="ignore"):
+            o, absv, _, _ = ref.attend(q64[0], k64[0], v64[0], window, sinks)
+        size = ref.attend(q64[0], np.where(np.isinf(k64[0]), 0, k64[0]), v64[0], window, sinks)[3]
+        _check(got, o[2:199], absv[2:199], size[2:199], d, dtype, _half_step(dtype))

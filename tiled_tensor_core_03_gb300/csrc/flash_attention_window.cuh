@@ -164,7 +164,8 @@ __device__ __noinline__ void window_row(const WindowParams &p, int batch, int he
             s += __shfl_xor_sync(0xffffffffu, s, x);
         s *= p.scale;
         const float to = fmaxf(m, s);
-        const float f = to > m ? exp2f(m - to) : 1.0f, w = exp2f(s - to);
+        // (a score of -infinity has weight 0, also as the first)
+        const float f = to > m ? exp2f(m - to) : 1.0f, w = s == -INFINITY ? 0.0f : exp2f(s - to);
         l = l * f + w;
 #pragma unroll
         for (int e = 0; e < E; ++e)
