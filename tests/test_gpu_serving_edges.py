@@ -61,3 +61,54 @@ def test_window_first_score_minus_infinity(dtype):
             o, absv, _, _ = ref.attend(q64[0], k64[0], v64[0], window, sinks)
         size = ref.attend(q64[0], np.where(np.isinf(k64[0]), 0, k64[0]), v64[0], window, sinks)[3]
         _check(got, o[2:199], absv[2:199], size[2:199], d, dtype, _half_step(dtype))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,window,sinks,everywhere", [(3000, 0, 0, False), (3000, 700, 4, False), (700, 300, 70, True)])
+def test_window_not_finite_holds_nobody_up(n, window, sinks, everywhere, dtype):
+    """An infinity in V of the first token, which every row sees, or one in every fifth token: no wait
+    inside the kernel gets long (their limit is 20 ms here), and every row is written."""
+    import torch
+    rng = np.random.default_rng(42)
+    d, hq = 128, 4
+    q, _ = _rand(rng, (1, n, hq, d), dtype)
+    k, _ = _rand(rng, (1, n, 1, d), dtype)
+    v, _ = _rand(rng, (1, n, 1, d), dtype)
+    at = torch.arange(0, n, 5, device="cuda") if everywhere else torch.zeros(1, dtype=torch.long, device="cuda")
+    clean = v.clone()
+    clean[0, at, 0, 9] = 0
+    dirty = clean.clone()
+    dirty[0, at, 0, 9] = float("inf")
+    gr.gemm_relu_debug_set(0, 20_000_000)
+    try:
+        want = gr.flash_attention_window(q, k, clean, window, sinks)
+        got = gr.flash_attention_window(q, k, dirty, window, sinks)
+        assert gr.status() == gr.OK
+    finally:
+        gr.gemm_relu_debug_set(0, 0)
+    keep = [c for c in range(d) if c != 9]
+    assert torch.equal(got[..., keep], want[..., keep])
+    sees = torch.from_numpy(np.any([_sees(n, int(a), window, sinks) for a in at.cpu()], axis=0)).cuda()
+    assert not torch.isfinite(got[0, sees][..., 9]).any()
+    assert torch.equal(got[0, ~sees], want[0, ~sees])
+
+
+def test_window_not_finite_in_many_heads_and_sequences():
+    """Garbage of every kind past the prompts of a padded batch, more items than CTAs: what comes before
+    the padding is as if the padding were 0."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(43)
+    b, n, hq, hkv, d = 4, 1500, 12, 6, 64
+    q, k, v = (torch.randn(b, n, h, d, device="cuda", dtype=torch.bfloat16, generator=g) for h in (hq, hkv, hkv))
+    lengths = [1500, 1401, 77, 900]
+    k0, v0 = k.clone(), v.clone()
+    for i, m in enumerate(lengths):
+        k0[i, m:], v0[i, m:] = 0, 0
+        bytes_ = torch.randint(-2 ** 15, 2 ** 15, k[i, m:].shape, device="cuda", generator=g).short()
+        k[i, m:], v[i, m:] = bytes_.view(torch.bfloat16), bytes_.flip(0).view(torch.bfloat16)
+        v[i, m:, :, ::3] = float("nan")
+    for window, sinks in ((0, 0), (200, 3)):
+        got = gr.flash_attention_window(q, k, v, window, sinks)
+        want = gr.flash_attention_window(q, k0, v0, window, sinks)
+        for i, m in enumerate(lengths):
+            assert torch.equal(got[i, :m], want[i, :m])

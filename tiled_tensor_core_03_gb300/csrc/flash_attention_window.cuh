@@ -28,8 +28,12 @@
 //  - Scores are masked only in blocks where some row does not see some key: the
 //    diagonal's, the window's low end, the sinks'.
 //  - A key that a row does not see has weight 0, and 0 times a NaN or an infinity in its V
-//    would still be NaN.  A row whose result is not finite (never, with finite inputs) is
-//    therefore computed again from its visible keys alone, a warp per row.
+//    would still be NaN.  A CTA that finds a row with finite weights but without a finite result
+//    (an element of some V is not finite) therefore walks over its items a second time.  There, in
+//    the blocks that some row sees in part, such elements of V become 0 in shared memory and are
+//    added by hand to the rows that see them.  That costs about what the first walk did and some
+//    microseconds for each of those few blocks, whatever the rows' lengths are, so that no
+//    wait inside the pipeline gets long.
 //
 // Bound: the tensor cores' 4 d flops a pair; blocks are 128 keys wide, so a window of W keys
 // costs up to W + 255 keys and the sinks one block.  A tile's turn is a chain, S, softmax, P V, next
@@ -74,8 +78,8 @@ struct Divisor {
 };
 
 struct WindowParams {
-    const uint16_t *q, *k, *v;
-    int64_t qs[3], ks[3], vs[3];   // sequence, token, head
+    const uint16_t *v;
+    int64_t vs[3];                 // sequence, token, head
     uint16_t *o;                   // [batch][n_q][q_heads][d]
     int n_q, n_kv, q_heads, group;
     int q_tiles, items;            // items = q_tiles * group: tiles of one K/V head
@@ -118,6 +122,14 @@ __host__ __device__ inline Blocks blocks_seen(int first, int last, int window, i
 }
 
 template <bool kBf16>
+__device__ __forceinline__ float to_float(uint32_t x16) {
+    if constexpr (kBf16)
+        return __uint_as_float(x16 << 16);
+    else
+        return __half2float(__ushort_as_half((unsigned short)x16));
+}
+
+template <bool kBf16>
 __device__ __forceinline__ uint32_t pack_pair(float a, float b) {
     if constexpr (kBf16) {
         const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -127,68 +139,89 @@ __device__ __forceinline__ uint32_t pack_pair(float a, float b) {
     }
 }
 
+// The halves of a pair that are an infinity or a NaN (all exponent bits set): 0x8000 in their place.
 template <bool kBf16>
-__device__ __forceinline__ float load_x16(const uint16_t *p) {
-    if constexpr (kBf16)
-        return __uint_as_float((uint32_t)*p << 16);
-    else
-        return __half2float(*reinterpret_cast<const __half *>(p));
+__device__ __forceinline__ uint32_t not_finite(uint32_t pair) {
+    return kBf16 ? ((pair & 0x7f807f80u) + 0x00800080u) & 0x80008000u
+                 : ((pair & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
 }
 
-// One row from its visible keys alone, by a warp: the plain one-pass softmax, a key at a
-// time.  Only rows whose result was not finite come here.
+template <bool kBf16>
+__device__ __forceinline__ uint32_t finite_part(uint32_t pair) {
+    return pair & ~((not_finite<kBf16>(pair) >> 15) * 0xffffu);
+}
+
+// One key of a block per thread: whether its V row (in global memory; nullptr past the last key) has
+// elements that are not finite.  Those become 0 in the block's copy in shared memory, whose
+// row `r` of 64 elements a sub-tile starts at `smem_row`.
 template <int HD, bool kBf16>
-__device__ __noinline__ void window_row(const WindowParams &p, int batch, int head, int qi,
-                                        int lane) {
-    const int pos = qi + p.n_kv - p.n_q, kvh = head / p.group;
-    constexpr int E = HD / 32;
-    float q[E], o[E], m = -INFINITY, l = 0.0f;
-    const uint16_t *src = p.q + batch * p.qs[0] + qi * p.qs[1] + head * p.qs[2] + lane;
+__device__ __noinline__ bool clean_row(const uint16_t *row, uint32_t smem_row, int r) {
+    uint32_t bad = 0;
+    if (row != nullptr)
+#pragma unroll 4
+        for (int c = 0; c < HD / 8; ++c) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(row + 8 * c);
+            bad |= not_finite<kBf16>(x.x) | not_finite<kBf16>(x.y) | not_finite<kBf16>(x.z) | not_finite<kBf16>(x.w);
+        }
+    if (bad)
+#pragma unroll 1
+        for (int c = 0; c < HD / 8; ++c) {
+            const uint32_t at = smem_row + (c >> 3) * kSub + ((uint32_t)((c & 7) ^ (r & 7)) << 4);
+            const uint4 x = ld_shared_v4(at);
+            st_shared_v4(at, finite_part<kBf16>(x.x), finite_part<kBf16>(x.y), finite_part<kBf16>(x.z),
+                         finite_part<kBf16>(x.w));
+        }
+    return bad != 0;
+}
+
+// Add what clean_row took out of a block to the warp's 32 rows of O in TMEM: `keys` has a bit for each of the
+// block's keys with such elements, `v` points at the first one's row.  Their sum (an infinity, or a NaN)
+// takes the place of what weights above 0 would give.
+template <int HD, bool kBf16>
+__device__ __noinline__ void add_not_finite(const WindowParams &p, const uint16_t *v, const uint32_t *keys, int key0,
+                                            int pos, uint32_t o_addr) {
+#pragma unroll 1
+    for (int c0 = 0; c0 < HD; c0 += 32) {
+        uint32_t o[32];
+        tmem_ld_x32_sync(o_addr + c0, o);
+#pragma unroll 1
+        for (int w = 0; w < BN / 32; ++w) {
+#pragma unroll 1
+            for (uint32_t left = keys[w]; left; left &= left - 1) {
+                const int i = 32 * w + __ffs(left) - 1, key = key0 + i;
+                if (key > pos || (p.window > 0 && key <= pos - p.window && key >= p.sinks))
+                    continue;
+                const uint4 *row = reinterpret_cast<const uint4 *>(v + i * p.vs[1] + c0);
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        q[e] = load_x16<kBf16>(src + 32 * e);
-        o[e] = 0.0f;
+                for (int c = 0; c < 4; ++c) {
+                    const uint4 y = row[c];
+                    const uint32_t x[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t bad = not_finite<kBf16>(x[e]);
+                        uint32_t &lo = o[8 * c + 2 * e], &hi = o[8 * c + 2 * e + 1];
+                        if (bad & 0x8000u)
+                            lo = __float_as_uint(__uint_as_float(lo) + to_float<kBf16>(x[e] & 0xffffu));
+                        if (bad & 0x80000000u)
+                            hi = __float_as_uint(__uint_as_float(hi) + to_float<kBf16>(x[e] >> 16));
+                    }
+                }
+            }
+            __syncwarp();
+        }
+        tmem_st_x32(o_addr + c0, o);
     }
-    const int low = p.window > 0 && pos - p.window + 1 > 0 ? pos - p.window + 1 : 0;
-    for (int j = p.sinks > 0 ? 0 : low; j <= pos; ++j) {   // the sinks, then the window
-        if (j < low && j >= p.sinks)
-            j = low;
-        const uint16_t *k = p.k + batch * p.ks[0] + j * p.ks[1] + kvh * p.ks[2] + lane;
-        const uint16_t *v = p.v + batch * p.vs[0] + j * p.vs[1] + kvh * p.vs[2] + lane;
-        float s = 0.0f;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            s += q[e] * load_x16<kBf16>(k + 32 * e);
-#pragma unroll
-        for (int x = 16; x; x >>= 1)
-            s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= p.scale;
-        const float to = fmaxf(m, s);
-        // (a score of -infinity has weight 0, also as the first)
-        const float f = to > m ? exp2f(m - to) : 1.0f, w = s == -INFINITY ? 0.0f : exp2f(s - to);
-        l = l * f + w;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            o[e] = o[e] * f + w * load_x16<kBf16>(v + 32 * e);
-        m = to;
-        if (l != l)
-            break;   // a NaN score: the row is NaN
-    }
-    uint16_t *dst = p.o + (((int64_t)batch * p.n_q + qi) * p.q_heads + head) * HD + lane;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const float x = l == 0.0f ? 0.0f : o[e] / l + (l != l ? l : 0.0f);
-        dst[32 * e] = (uint16_t)(pack_pair<kBf16>(x, 0.0f) & 0xffffu);
-    }
+    tmem_st_wait();
 }
 
 // Shared memory of flash_attention.cuh with more barriers: q_full, q_empty, k_full[kKV],
-// v_full[kKV], kv_empty[kKV], s_full[2], p_full[2], o_full[2], o_empty[2], drain.
+// v_full[kKV], kv_empty[kKV], s_full[2], p_full[2], o_full[2], o_empty[2], v_clean[2], drain.
 template <int HD>
 struct WindowCfg : Cfg<HD> {
-    static constexpr uint32_t kNumBars = 2 + 3 * kKV + 8 + 1;
+    static constexpr uint32_t kNumBars = 2 + 3 * kKV + 10 + 1;
     static constexpr uint32_t kOffMisc = Cfg<HD>::kOffBar + kNumBars * 8;
-    static constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;
+    static constexpr uint32_t kOffKeys = kOffMisc + 16;   // [kTiles][2][BN / 32]: keys with V that is not finite
+    static constexpr uint32_t kSmemBytes = kOffKeys + kTiles * 2 * (BN / 32) * 4 + 1024;
     static constexpr int kNarrow = 32;   // keys of a block with few sinks only
     static constexpr uint32_t kIdescNarrow = make_idesc_f16_f32(BM, kNarrow, 0, 0);
 };
@@ -328,9 +361,11 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
     auto p_full = [&](uint32_t t) { return bar0 + 8u * (4 + 3 * kKV + t); };
     auto o_full = [&](uint32_t t) { return bar0 + 8u * (6 + 3 * kKV + t); };
     auto o_empty = [&](uint32_t t) { return bar0 + 8u * (8 + 3 * kKV + t); };
-    const uint32_t drain_bar = bar0 + 8u * (10 + 3 * kKV);
+    auto v_clean = [&](uint32_t t) { return bar0 + 8u * (10 + 3 * kKV + t); };
+    const uint32_t drain_bar = bar0 + 8u * (12 + 3 * kKV);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + G::kOffMisc);
     volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(gbase + G::kOffMisc + 4);
+    volatile uint32_t *redo_flag = reinterpret_cast<volatile uint32_t *>(gbase + G::kOffMisc + 8);
 
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);   // uniform
     const int lane = threadIdx.x & 31;
@@ -349,9 +384,11 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
             mbar_init(p_full(t), 4u);
             mbar_init(o_full(t), 1u);
             mbar_init(o_empty(t), 4u);
+            mbar_init(v_clean(t), 4u);
         }
         mbar_init(drain_bar, 1u);
         *abort_flag = 0u;
+        *redo_flag = 0u;
         fence_mbar_init();
         pdl_launch_dependents();
     }
@@ -370,52 +407,66 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
     const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
     pdl_wait_primary();  // the previous grid of the stream has completed
 
+    // The end of a walk over the items, for every warp: whether a second one follows.
+    auto once_more = [&](int pass) {
+        __syncwarp();
+        tc_fence_before_sync();
+        named_bar_sync(1, kWindowThreads);
+        tc_fence_after_sync();
+        return pass == 0 && *redo_flag != 0u && *abort_flag == 0u;
+    };
+
     if (warp >= kProducerWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         // ============================================================ TMA producer
-        if (warp == kProducerWarp && lane == 0) {
+        if (warp == kProducerWarp) {
             uint32_t queries = 0, blocks = 0;   // Q loads and K/V blocks issued
             bool ok = !(p.drop_arrive && blockIdx.x == 0);
-            for (WindowWalk walk(p); ok && walk.more(); walk.next()) {
-                const WindowItem w = window_item<HD>(p, walk.index());
-                if (w.nb == 0)
-                    continue;
-                if (!wait_bounded_eager(q_empty, (queries & 1u) ^ 1u, p.wait_limit_ns, abort_flag,
-                                        kSiteProducerEmpty))
-                    break;
-                mbar_arrive_expect_tx(q_full, (w.two ? 2u : 1u) * G::kQBytes);
-                for (int t = 0; t < (w.two ? 2 : 1); ++t)
-#pragma unroll
-                    for (int d = 0; d < G::kDSub; ++d)
-                        tma_load_4d(&tmQ, base + G::kOffQ + t * G::kQBytes + d * kSub, q_full,
-                                    64 * d, t ? w.head1 : w.head0, (t ? w.tile1 : w.tile0) * BM, w.batch);
-                ++queries;
-                for (int j = 0; j < w.nb; ++j) {
-                    const uint32_t st = blocks % kKV, ph = blocks / kKV & 1u;
-                    ok = wait_bounded_eager(kv_empty(st), ph ^ 1u, p.wait_limit_ns, abort_flag,
+            for (int pass = 0;; ++pass) {
+                for (WindowWalk walk(p); lane == 0 && ok && walk.more(); walk.next()) {
+                    const WindowItem w = window_item<HD>(p, walk.index());
+                    if (w.nb == 0)
+                        continue;
+                    ok = wait_bounded_eager(q_empty, (queries & 1u) ^ 1u, p.wait_limit_ns, abort_flag,
                                             kSiteProducerEmpty);
                     if (!ok)
                         break;
-                    const int key = w.block(j) * BN;
-                    mbar_arrive_expect_tx(k_full(st), G::kKBytes);
+                    mbar_arrive_expect_tx(q_full, (w.two ? 2u : 1u) * G::kQBytes);
+                    for (int t = 0; t < (w.two ? 2 : 1); ++t)
 #pragma unroll
-                    for (int d = 0; d < G::kDSub; ++d)
-                        tma_load_4d(&tmK, base + G::kOffK + st * G::kKBytes + d * kSub, k_full(st),
-                                    64 * d, w.kvh, key, w.batch);
-                    mbar_arrive_expect_tx(v_full(st), G::kVBytes);
+                        for (int d = 0; d < G::kDSub; ++d)
+                            tma_load_4d(&tmQ, base + G::kOffQ + t * G::kQBytes + d * kSub, q_full,
+                                        64 * d, t ? w.head1 : w.head0, (t ? w.tile1 : w.tile0) * BM, w.batch);
+                    ++queries;
+                    for (int j = 0; j < w.nb; ++j) {
+                        const uint32_t st = blocks % kKV, ph = blocks / kKV & 1u;
+                        ok = wait_bounded_eager(kv_empty(st), ph ^ 1u, p.wait_limit_ns, abort_flag,
+                                                kSiteProducerEmpty);
+                        if (!ok)
+                            break;
+                        const int key = w.block(j) * BN;
+                        mbar_arrive_expect_tx(k_full(st), G::kKBytes);
 #pragma unroll
-                    for (int d = 0; d < G::kDSub; ++d)
-                        tma_load_4d(&tmV, base + G::kOffV + st * G::kVBytes + d * kSub, v_full(st),
-                                    64 * d, w.kvh, key, w.batch);
-                    ++blocks;
+                        for (int d = 0; d < G::kDSub; ++d)
+                            tma_load_4d(&tmK, base + G::kOffK + st * G::kKBytes + d * kSub, k_full(st),
+                                        64 * d, w.kvh, key, w.batch);
+                        mbar_arrive_expect_tx(v_full(st), G::kVBytes);
+#pragma unroll
+                        for (int d = 0; d < G::kDSub; ++d)
+                            tma_load_4d(&tmV, base + G::kOffV + st * G::kVBytes + d * kSub, v_full(st),
+                                        64 * d, w.kvh, key, w.batch);
+                        ++blocks;
+                    }
                 }
-            }
-            // every copy issued must have landed before the CTA may exit
-            if (queries > 0)
-                wait_drain(q_full, (queries - 1) & 1u, p.wait_limit_ns, abort_flag);
-            for (uint32_t i = blocks > (uint32_t)kKV ? blocks - kKV : 0u; i < blocks; ++i) {
-                wait_drain(k_full(i % kKV), i / kKV & 1u, p.wait_limit_ns, abort_flag);
-                wait_drain(v_full(i % kKV), i / kKV & 1u, p.wait_limit_ns, abort_flag);
+                // every copy issued must have landed before the CTA may exit
+                if (queries > 0)   // (lane 0)
+                    wait_drain(q_full, (queries - 1) & 1u, p.wait_limit_ns, abort_flag);
+                for (uint32_t i = blocks > (uint32_t)kKV ? blocks - kKV : 0u; i < blocks; ++i) {
+                    wait_drain(k_full(i % kKV), i / kKV & 1u, p.wait_limit_ns, abort_flag);
+                    wait_drain(v_full(i % kKV), i / kKV & 1u, p.wait_limit_ns, abort_flag);
+                }
+                if (!once_more(pass))
+                    break;
             }
         }
         // ============================================================ MMA issuer
@@ -487,55 +538,62 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
                 }
                 return true;
             };
-            WindowWalk walk(p);
-            WindowItem w{};
-            if (walk.more())
-                w = window_item<HD>(p, walk.index());
-            while (ok && walk.more()) {
-                const int nb = w.nb, narrow = w.narrow;
-                const Turns t0 = w.t0, t1 = w.t1;
-                if (nb > 0) {
-                    ok = wait_warp(q_full, queries & 1u, p.wait_limit_ns, abort_flag, kSiteMmaFull);
-                    ++queries;
-                    if (ok && t0.has(0))
-                        ok = score(0, blocks, narrow == 0, false);
-                    if (ok && t1.has(0))
-                        ok = score(1, blocks, narrow == 0, t0.has(0));
-                    if (ok && nb == 1 && leader)
-                        umma_commit(q_empty);
-                }
-                walk.next();
+            for (int pass = 0;; ++pass) {
+                WindowWalk walk(p);
+                WindowItem w{};
                 if (walk.more())
                     w = window_item<HD>(p, walk.index());
-                bool fresh0 = true, fresh1 = true;
-                for (int j = 0; ok && j < nb; ++j, ++blocks) {
-                    const bool here = j == narrow, there = j + 1 == narrow, more = j + 1 < nb;
-                    if (t0.has(j)) {
-                        ok = pv(0, blocks, here, false, fresh0, j + 1 == t0.to, turns0, outs0);
-                        fresh0 = false;
+                while (ok && walk.more()) {
+                    const int nb = w.nb, narrow = w.narrow;
+                    const Turns t0 = w.t0, t1 = w.t1;
+                    if (nb > 0) {
+                        ok = wait_warp(q_full, queries & 1u, p.wait_limit_ns, abort_flag, kSiteMmaFull);
+                        ++queries;
+                        if (ok && t0.has(0))
+                            ok = score(0, blocks, narrow == 0, false);
+                        if (ok && t1.has(0))
+                            ok = score(1, blocks, narrow == 0, t0.has(0));
+                        if (ok && nb == 1 && leader)
+                            umma_commit(q_empty);
                     }
-                    if (ok && more && t0.has(j + 1))
-                        ok = score(0, blocks + 1, there, false);
-                    if (ok && t1.has(j)) {
-                        ok = pv(1, blocks, here, t0.has(j), fresh1, j + 1 == t1.to, turns1, outs1);
-                        fresh1 = false;
+                    walk.next();
+                    if (walk.more())
+                        w = window_item<HD>(p, walk.index());
+                    bool fresh0 = true, fresh1 = true;
+                    for (int j = 0; ok && j < nb; ++j, ++blocks) {
+                        const bool here = j == narrow, there = j + 1 == narrow, more = j + 1 < nb;
+                        if (t0.has(j)) {
+                            ok = pv(0, blocks, here, false, fresh0, j + 1 == t0.to, turns0, outs0);
+                            fresh0 = false;
+                        }
+                        if (ok && more && t0.has(j + 1))
+                            ok = score(0, blocks + 1, there, false);
+                        if (ok && t1.has(j)) {
+                            ok = pv(1, blocks, here, t0.has(j), fresh1, j + 1 == t1.to, turns1, outs1);
+                            fresh1 = false;
+                        }
+                        if (!ok)
+                            break;
+                        if (leader)
+                            umma_commit(kv_empty(blocks % kKV));
+                        if (more && t1.has(j + 1))
+                            ok = score(1, blocks + 1, there, t0.has(j + 1));
+                        if (ok && j + 2 == nb && leader)
+                            umma_commit(q_empty);   // the item's last scores
                     }
-                    if (!ok)
-                        break;
-                    if (leader)
-                        umma_commit(kv_empty(blocks % kKV));
-                    if (more && t1.has(j + 1))
-                        ok = score(1, blocks + 1, there, t0.has(j + 1));
-                    if (ok && j + 2 == nb && leader)
-                        umma_commit(q_empty);   // the item's last scores
                 }
+                // all MMAs of this thread complete before TMEM can be released
+                if (leader)
+                    umma_commit(drain_bar);
+                wait_drain(drain_bar, pass & 1u, p.wait_limit_ns, abort_flag);
+                if (!once_more(pass))
+                    break;
             }
-            // all MMAs of this thread complete before TMEM can be released
-            if (leader)
-                umma_commit(drain_bar);
-            wait_drain(drain_bar, 0u, p.wait_limit_ns, abort_flag);
         }
-        // (the other two warps complete the warpgroup)
+        // the other two warps complete the warpgroup
+        for (int pass = 0; warp > kMmaWarp; ++pass)
+            if (!once_more(pass))
+                break;
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         // ============================================================ softmax / output
@@ -545,178 +603,231 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
         const uint32_t s_addr = tmem_base + lane_base + G::kTmemS + t * BN;
         const uint32_t o_addr = tmem_base + lane_base + G::kTmemO + t * HD;
         uint32_t turns = 0, outputs = 0;
+        uint32_t blocks = 0;                            // K/V blocks before the item in hand
         bool alive = true;
-        for (WindowWalk walk(p); alive && walk.more(); walk.next()) {
-            const WindowItem w = window_item<HD>(p, walk.index());
-            if (t == 1 && !w.two)
-                continue;
-            const int tile = t ? w.tile1 : w.tile0, head = t ? w.head1 : w.head0;
-            const Turns mine = t ? w.t1 : w.t0;
-            const int qi = tile * BM + 32 * q + lane;       // query index
-            const int pos = qi + off;
-            const int first = tile * BM + off, last = min(tile * BM + BM, p.n_q) - 1 + off;
-            float m = -INFINITY, l = 0.0f;
-            uint32_t done = 0;
-            // one block of kKeys keys: scores from TMEM, P as 16-bit pairs over them
-            auto softmax = [&](auto keys, int key0, bool masked) {
-                constexpr int kKeys = decltype(keys)::value;
-                uint32_t v[kKeys];
+        // the second walk over the items (see above)
+        uint32_t *keys = reinterpret_cast<uint32_t *>(gbase + G::kOffKeys) + t * 2 * (BN / 32);
+        uint32_t redo = 0, cleaned = 0;
+        auto reached = [&](uint32_t bar, uint32_t phase) {
+            return __all_sync(0xffffffffu, wait_bounded(bar, phase & 1u, p.wait_limit_ns, abort_flag, kSiteEpiAccFull));
+        };
+        // (compiled once for each walk: the second one's code between the turns cost the first 2.7%)
+        auto walk_items = [&](auto again) __attribute__((always_inline)) {
+            constexpr bool kAgain = decltype(again)::value;
+            for (WindowWalk walk(p); alive && walk.more(); walk.next()) {
+                const WindowItem w = window_item<HD>(p, walk.index());
+                const uint32_t block0 = blocks;
+                blocks += w.nb;
+                if (t == 1 && !w.two)
+                    continue;
+                const int tile = t ? w.tile1 : w.tile0, head = t ? w.head1 : w.head0;
+                const Turns mine = t ? w.t1 : w.t0;
+                const int qi = tile * BM + 32 * q + lane;       // query index
+                const int pos = qi + off;
+                const int first = tile * BM + off, last = min(tile * BM + BM, p.n_q) - 1 + off;
+                // some row of a tile does not see some key of the block
+                auto masked_for = [&](int first, int last, int key0) {
+                    return key0 + BN - 1 > first ||
+                           (p.window > 0 && key0 <= last - p.window && key0 + BN > p.sinks);
+                };
+                const int tile_b = t ? w.tile0 : w.tile1;       // the item's other tile
+                const Turns other = t ? w.t0 : w.t1;
+                const uint16_t *v_head = p.v + w.batch * p.vs[0] + w.kvh * p.vs[2];
+                // the first key of a block whose elements that are not finite are still to be added
+                int taken = -1;
+                auto add_taken = [&]() {
+                    if (taken >= 0)
+                        add_not_finite<HD, kBf16>(p, v_head + taken * p.vs[1],
+                                                  keys + ((turns - 1u) & 1u) * (BN / 32), taken, pos, o_addr);
+                    taken = -1;
+                };
+                float m = -INFINITY, l = 0.0f;
+                uint32_t done = 0;
+                // one block of kKeys keys: scores from TMEM, P as 16-bit pairs over them
+                auto softmax = [&](auto keys, int key0, bool masked) {
+                    constexpr int kKeys = decltype(keys)::value;
+                    uint32_t v[kKeys];
 #pragma unroll
-                for (int c0 = 0; c0 < kKeys; c0 += 32)
-                    tmem_ld_x32(s_addr + c0, *reinterpret_cast<uint32_t(*)[32]>(&v[c0]));
+                    for (int c0 = 0; c0 < kKeys; c0 += 32)
+                        tmem_ld_x32(s_addr + c0, *reinterpret_cast<uint32_t(*)[32]>(&v[c0]));
 #pragma unroll
-                for (int c0 = 0; c0 < kKeys; c0 += 32)
-                    tmem_ld_wait_regs(*reinterpret_cast<uint32_t(*)[32]>(&v[c0]));
-                if (masked) {
-                    // a bit per key, 32 at a time: seen up to `hi`, above `lo` or below `head` (three
-                    // compares a key instead: 262 us for 241 at window 1024)
-                    const int hi = pos - key0;
-                    const int lo = p.window > 0 ? hi - p.window : -1;
-                    const int head = p.sinks - key0;
+                    for (int c0 = 0; c0 < kKeys; c0 += 32)
+                        tmem_ld_wait_regs(*reinterpret_cast<uint32_t(*)[32]>(&v[c0]));
+                    if (masked) {
+                        // a bit per key, 32 at a time: seen up to `hi`, above `lo` or below `head` (three
+                        // compares a key instead: 262 us for 241 at window 1024)
+                        const int hi = pos - key0;
+                        const int lo = p.window > 0 ? hi - p.window : -1;
+                        const int head = p.sinks - key0;
+#pragma unroll
+                        for (int c0 = 0; c0 < kKeys; c0 += 32) {
+                            const uint32_t seen = keys_below(hi + 1 - c0) & (~keys_below(lo + 1 - c0) | keys_below(head - c0));
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                v[c0 + i] = seen & (1u << i) ? v[c0 + i] : __float_as_uint(-INFINITY);
+                        }
+                    }
+                    float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < kKeys; i += 2) {
+                        mx0 = fmaxf(mx0, __uint_as_float(v[i]));
+                        mx1 = fmaxf(mx1, __uint_as_float(v[i + 1]));
+                    }
+                    const float m_blk = fmaxf(mx0, mx1) * p.scale;   // scale > 0
+                    // move the reference only when the maximum grew by more than kRescaleLog2;
+                    // -infinity until the row has seen a key
+                    const bool move = m_blk > m + kRescaleLog2;
+                    const float m_new = move ? m_blk : m;
+                    const float alpha = move ? fast_exp2(m - m_new) : 1.0f;   // 0 at the first block
+                    const float m_ref = m_new == -INFINITY ? 0.0f : m_new;
+                    const float2 sc2 = make_float2(p.scale, p.scale), nm2 = make_float2(-m_ref, -m_ref);
+                    float2 sa = make_float2(0.0f, 0.0f), sb = make_float2(0.0f, 0.0f);
 #pragma unroll
                     for (int c0 = 0; c0 < kKeys; c0 += 32) {
-                        const uint32_t seen = keys_below(hi + 1 - c0) & (~keys_below(lo + 1 - c0) | keys_below(head - c0));
+                        uint32_t ph[16];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            v[c0 + i] = seen & (1u << i) ? v[c0 + i] : __float_as_uint(-INFINITY);
+                        for (int i = 0; i < 32; i += 4) {
+                            const float2 x01 = __ffma2_rn(
+                                make_float2(__uint_as_float(v[c0 + i]), __uint_as_float(v[c0 + i + 1])), sc2, nm2);
+                            const float2 x23 = __ffma2_rn(
+                                make_float2(__uint_as_float(v[c0 + i + 2]), __uint_as_float(v[c0 + i + 3])), sc2, nm2);
+                            const float2 e01 = make_float2(fast_exp2(x01.x), fast_exp2(x01.y));
+                            const float2 e23 = make_float2(fast_exp2(x23.x), fast_exp2(x23.y));
+                            sa = __fadd2_rn(sa, e01);
+                            sb = __fadd2_rn(sb, e23);
+                            ph[i / 2] = pack_pair<kBf16>(e01.x, e01.y);
+                            ph[i / 2 + 1] = pack_pair<kBf16>(e23.x, e23.y);
+                        }
+                        tmem_st_x16(s_addr + c0 / 2, ph);
                     }
-                }
-                float mx0 = -INFINITY, mx1 = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < kKeys; i += 2) {
-                    mx0 = fmaxf(mx0, __uint_as_float(v[i]));
-                    mx1 = fmaxf(mx1, __uint_as_float(v[i + 1]));
-                }
-                const float m_blk = fmaxf(mx0, mx1) * p.scale;   // scale > 0
-                // move the reference only when the maximum grew by more than kRescaleLog2;
-                // -infinity until the row has seen a key
-                const bool move = m_blk > m + kRescaleLog2;
-                const float m_new = move ? m_blk : m;
-                const float alpha = move ? fast_exp2(m - m_new) : 1.0f;   // 0 at the first block
-                const float m_ref = m_new == -INFINITY ? 0.0f : m_new;
-                const float2 sc2 = make_float2(p.scale, p.scale), nm2 = make_float2(-m_ref, -m_ref);
-                float2 sa = make_float2(0.0f, 0.0f), sb = make_float2(0.0f, 0.0f);
-#pragma unroll
-                for (int c0 = 0; c0 < kKeys; c0 += 32) {
-                    uint32_t ph[16];
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        const float2 x01 = __ffma2_rn(
-                            make_float2(__uint_as_float(v[c0 + i]), __uint_as_float(v[c0 + i + 1])), sc2, nm2);
-                        const float2 x23 = __ffma2_rn(
-                            make_float2(__uint_as_float(v[c0 + i + 2]), __uint_as_float(v[c0 + i + 3])), sc2, nm2);
-                        const float2 e01 = make_float2(fast_exp2(x01.x), fast_exp2(x01.y));
-                        const float2 e23 = make_float2(fast_exp2(x23.x), fast_exp2(x23.y));
-                        sa = __fadd2_rn(sa, e01);
-                        sb = __fadd2_rn(sb, e23);
-                        ph[i / 2] = pack_pair<kBf16>(e01.x, e01.y);
-                        ph[i / 2 + 1] = pack_pair<kBf16>(e23.x, e23.y);
-                    }
-                    tmem_st_x16(s_addr + c0 / 2, ph);
-                }
-                l = l * alpha + ((sa.x + sa.y) + (sb.x + sb.y));
-                m = m_new;
-                // rescale this warp's output rows when any of their references moved
-                // (the previous P V of this tile completed before S_j was written)
-                if (done > 0 && __any_sync(0xffffffffu, move)) {
+                    l = l * alpha + ((sa.x + sa.y) + (sb.x + sb.y));
+                    m = m_new;
+                    // rescale this warp's output rows when any of their references moved
+                    // (the previous P V of this tile completed before S_j was written)
+                    if (done > 0 && __any_sync(0xffffffffu, move)) {
 #pragma unroll 1
-                    for (int c0 = 0; c0 < HD; c0 += 32) {
-                        uint32_t o[32];
-                        tmem_ld_x32_sync(o_addr + c0, o);
+                        for (int c0 = 0; c0 < HD; c0 += 32) {
+                            uint32_t o[32];
+                            tmem_ld_x32_sync(o_addr + c0, o);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                        tmem_st_x32(o_addr + c0, o);
+                            for (int i = 0; i < 32; ++i)
+                                o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                            tmem_st_x32(o_addr + c0, o);
+                        }
                     }
+                    tmem_st_wait();
+                };
+                for (int j = 0; j < w.nb; ++j) {
+                    if (!mine.has(j))
+                        continue;
+                    const bool ok = wait_bounded_eager(s_full((uint32_t)t), turns & 1u, p.wait_limit_ns,
+                                                       abort_flag, kSiteEpiAccFull);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        alive = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    const int key0 = w.block(j) * BN;
+                    if constexpr (kAgain) {
+                        add_taken();   // (the P V before this turn is done)
+                        // where every row of both tiles sees every key the products do it all
+                        const int first_b = tile_b * BM + off, last_b = min(tile_b * BM + BM, p.n_q) - 1 + off;
+                        if (masked_for(first, last, key0) || (other.has(j) && masked_for(first_b, last_b, key0))) {
+                            const uint32_t i = block0 + j, st = i % kKV;
+                            alive = reached(v_full(st), i / kKV);
+                            if (!alive)
+                                break;
+                            const int r = 32 * q + lane, key = key0 + r;
+                            const bool bad = clean_row<HD, kBf16>(key < p.n_kv ? v_head + key * p.vs[1] : nullptr,
+                                                                  base + G::kOffV + st * G::kVBytes + r * 128, r);
+                            fence_proxy_async_smem();
+                            uint32_t *words = keys + (turns & 1u) * (BN / 32);
+                            const uint32_t word = __ballot_sync(0xffffffffu, bad);
+                            if (lane == 0) {
+                                words[q] = word;
+                                mbar_arrive(v_clean((uint32_t)t));
+                            }
+                            __syncwarp();
+                            // (bounded, unlike a named barrier: another warp of the tile may have given up)
+                            alive = reached(v_clean((uint32_t)t), cleaned++);
+                            if (!alive)
+                                break;
+                            if (words[0] | words[1] | words[2] | words[3])
+                                taken = key0;
+                        }
+                    }
+                    const bool masked = masked_for(first, last, key0);
+                    if (j == w.narrow)
+                        softmax(std::integral_constant<int, G::kNarrow>{}, key0, true);
+                    else
+                        softmax(std::integral_constant<int, BN>{}, key0, masked);
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(p_full((uint32_t)t));
+                    ++turns;
+                    ++done;
                 }
-                tmem_st_wait();
-            };
-            for (int j = 0; j < w.nb; ++j) {
-                if (!mine.has(j))
-                    continue;
-                const bool ok = wait_bounded_eager(s_full((uint32_t)t), turns & 1u, p.wait_limit_ns,
-                                                   abort_flag, kSiteEpiAccFull);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    alive = false;
+                if (!alive)
                     break;
-                }
-                tc_fence_after_sync();
-                const int key0 = w.block(j) * BN;
-                // some row does not see some key of the block
-                const bool masked = key0 + BN - 1 > first ||
-                                    (p.window > 0 && key0 <= last - p.window && key0 + BN > p.sinks);
-                if (j == w.narrow)
-                    softmax(std::integral_constant<int, G::kNarrow>{}, key0, true);
-                else
-                    softmax(std::integral_constant<int, BN>{}, key0, masked);
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(p_full((uint32_t)t));
-                ++turns;
-                ++done;
-            }
-            if (!alive)
-                break;
-            // the tile's last P V, then O / l rounded once
-            if (done > 0) {
-                const bool ok = wait_bounded_eager(o_full((uint32_t)t), outputs & 1u, p.wait_limit_ns,
-                                                   abort_flag, kSiteEpiAccFull);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    alive = false;
-                    break;
-                }
-                ++outputs;
-                tc_fence_after_sync();
-            }
-            const float inv_l = l == 0.0f ? 0.0f : 1.0f / l;
-            uint16_t *dst = p.o + (((int64_t)w.batch * p.n_q + qi) * p.q_heads + head) * HD;
-            bool fine = true;
-#pragma unroll 1
-            for (int c0 = 0; c0 < HD; c0 += 32) {
-                uint32_t o[32];
-                uint32_t h[16];
+                // the tile's last P V, then O / l rounded once
                 if (done > 0) {
-                    tmem_ld_x32_sync(o_addr + c0, o);
-                    if (c0 + 32 == HD) {   // O_t may be written again
-                        tc_fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(o_empty((uint32_t)t));
+                    const bool ok = wait_bounded_eager(o_full((uint32_t)t), outputs & 1u, p.wait_limit_ns,
+                                                       abort_flag, kSiteEpiAccFull);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        alive = false;
+                        break;
+                    }
+                    ++outputs;
+                    tc_fence_after_sync();
+                    if constexpr (kAgain)
+                        add_taken();
+                }
+                const float inv_l = l == 0.0f ? 0.0f : 1.0f / l;
+                uint16_t *dst = p.o + (((int64_t)w.batch * p.n_q + qi) * p.q_heads + head) * HD;
+                bool fine = true;
+#pragma unroll 1
+                for (int c0 = 0; c0 < HD; c0 += 32) {
+                    uint32_t o[32];
+                    uint32_t h[16];
+                    if (done > 0) {
+                        tmem_ld_x32_sync(o_addr + c0, o);
+                        if (c0 + 32 == HD) {   // O_t may be written again
+                            tc_fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0)
+                                mbar_arrive(o_empty((uint32_t)t));
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float x = done > 0 ? __uint_as_float(o[2 * i]) * inv_l : 0.0f;
+                        const float y = done > 0 ? __uint_as_float(o[2 * i + 1]) * inv_l : 0.0f;
+                        fine = fine && fabsf(x) < INFINITY && fabsf(y) < INFINITY;
+                        h[i] = pack_pair<kBf16>(x, y);
+                    }
+                    if (qi < p.n_q) {
+                        uint4 *d4 = reinterpret_cast<uint4 *>(dst + c0);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            d4[i] = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
                     }
                 }
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float x = done > 0 ? __uint_as_float(o[2 * i]) * inv_l : 0.0f;
-                    const float y = done > 0 ? __uint_as_float(o[2 * i + 1]) * inv_l : 0.0f;
-                    fine = fine && fabsf(x) < INFINITY && fabsf(y) < INFINITY;
-                    h[i] = pack_pair<kBf16>(x, y);
-                }
-                if (qi < p.n_q) {
-                    uint4 *d4 = reinterpret_cast<uint4 *>(dst + c0);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        d4[i] = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
-                }
+                redo |= !fine && l == l && qi < p.n_q;   // (a NaN among its weights: the row is NaN)
             }
-            uint32_t again = __ballot_sync(0xffffffffu, !fine && qi < p.n_q);
-            while (again) {
-                const int r = __ffs(again) - 1;
-                again &= again - 1;
-                __syncwarp();
-                window_row<HD, kBf16>(p, w.batch, head, tile * BM + 32 * q + r, lane);
-            }
+        };
+        walk_items(std::false_type{});
+        if (redo != 0u)
+            *redo_flag = 1u;
+        if (once_more(0)) {
+            walk_items(std::true_type{});
+            once_more(1);
         }
     }
 
     // ---------------------------------------------------------------- teardown
-    __syncwarp();
-    tc_fence_before_sync();
-    __syncthreads();
-    if (warp == kMmaWarp) {
-        tc_fence_after_sync();
+    if (warp == kMmaWarp)
         tmem_dealloc(tmem_base, G::kTmemCols);
-    }
 }
 
 }  // namespace attn

@@ -101,15 +101,10 @@ extern "C" int flash_attention_window_x16(const void *Q, const void *K, const vo
         !make_strided_map(&mV, V, dtype, batch, kv_seq, kv_heads, head_dim, v_strides))
         return GEMMRELU_ERR_LAUNCH;
     FA::WindowParams p{};
-    p.q = static_cast<const uint16_t *>(Q);
-    p.k = static_cast<const uint16_t *>(K);
     p.v = static_cast<const uint16_t *>(V);
     p.o = static_cast<uint16_t *>(O);
-    for (int i = 0; i < 3; ++i) {
-        p.qs[i] = q_strides[i];
-        p.ks[i] = k_strides[i];
+    for (int i = 0; i < 3; ++i)
         p.vs[i] = v_strides[i];
-    }
     p.n_q = (int)q_seq;
     p.n_kv = (int)kv_seq;
     p.q_heads = (int)q_heads;
