@@ -64,7 +64,10 @@ int flash_attention_f16(const void *Q, const void *K, const void *V, void *O,
  *
  * Softmax statistics and sums are fp32; the softmax weights are rounded to
  * `dtype` for the product with V, the result once.  NaN and infinities
- * reach exactly the queries that see them.  The summation order is fixed: the
+ * reach exactly the queries that see them, and finite V give finite results
+ * but for those that round past the type's largest number.  (bf16 scores that
+ * leave fp32 are infinities; bf16 V below 2^-117 times the number of visible
+ * keys may lose bits.)  The summation order is fixed: the
  * same call gives the same bits.  Asynchronous on `stream`, allocates nothing.
  */
 int flash_attention_window_x16(const void *Q, const void *K, const void *V, void *O, int dtype,

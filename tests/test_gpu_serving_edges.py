@@ -112,3 +112,18 @@ def test_window_not_finite_in_many_heads_and_sequences():
         want = gr.flash_attention_window(q, k0, v0, window, sinks)
         for i, m in enumerate(lengths):
             assert torch.equal(got[i, :m], want[i, :m])
+
+
+@pytest.mark.parametrize("n,window,sinks,scale", [(600, 0, 0, 0.1), (600, 0, 0, 2.0), (900, 300, 130, 0.1)])
+@pytest.mark.parametrize("size_of_v", [1e37, 1e30, 1e-30])
+def test_window_very_large_and_small_values(n, window, sinks, scale, size_of_v):
+    """Sums of finite bf16 V would leave fp32 before they are divided: the mean does not."""
+    import torch
+    rng = np.random.default_rng(44)
+    d = 64
+    q, q64 = _rand(rng, (1, n, 2, d), "bf16", scale)
+    k, k64 = _rand(rng, (1, n, 1, d), "bf16")
+    v = torch.from_numpy(rng.uniform(0.5, 4.0, (1, n, 1, d)) * size_of_v).to(torch.bfloat16)
+    got = _f64(gr.flash_attention_window(q, k, v.cuda(), window, sinks))[0] / size_of_v
+    o, absv, _, size = ref.attend(q64[0], k64[0], v.double().numpy()[0] / size_of_v, window, sinks)
+    _check(got, o, absv, size, d, "bf16", _half_step("bf16"))

@@ -88,6 +88,7 @@ struct WindowParams {
     int chunk, chunk_items;        // K/V heads of all sequences whose items mix, and their items
     Divisor by_chunk, by_last, by_chunk_items, by_kv_heads, by_group;   // (last: the rest of heads)
     float scale;                   // log2(e) / sqrt(d)
+    float shift;                   // bf16: what a row's reference stands above its largest score
     int drop_arrive;
     uint64_t wait_limit_ns;
 };
@@ -673,7 +674,9 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
                         mx0 = fmaxf(mx0, __uint_as_float(v[i]));
                         mx1 = fmaxf(mx1, __uint_as_float(v[i + 1]));
                     }
-                    const float m_blk = fmaxf(mx0, mx1) * p.scale;   // scale > 0
+                    // scale > 0; with bf16 a sum of weights stays below 1, so that O, which is a sum with
+                    // weights until it is divided, stays within the largest V and fp32
+                    const float m_blk = fmaxf(mx0, mx1) * p.scale + (kBf16 ? p.shift : 0.0f);
                     // move the reference only when the maximum grew by more than kRescaleLog2;
                     // -infinity until the row has seen a key
                     const bool move = m_blk > m + kRescaleLog2;

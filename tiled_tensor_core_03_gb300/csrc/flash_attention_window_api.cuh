@@ -130,6 +130,10 @@ extern "C" int flash_attention_window_x16(const void *Q, const void *K, const vo
     p.window = (int)std::min<int64_t>(window, (int64_t)1 << 30);
     p.sinks = (int)std::min<int64_t>(sinks, (int64_t)1 << 30);
     p.scale = (float)(1.4426950408889634 / std::sqrt((double)head_dim));
+    // Weights stay below 2^8 times a row's largest: 9 + log2(keys that a row can see) keeps their sum
+    // below 1/2.  fp16 values are far from fp32's range, and its weights have none to spare.
+    const int64_t seen = window > 0 ? std::min(kv_seq, std::min(window, kv_seq) + std::min(sinks, kv_seq)) : kv_seq;
+    p.shift = dtype == GEMMRELU_BF16 ? 9.0f + std::ceil(std::log2((float)seen)) : 0.0f;
     p.drop_arrive = g_drop_arrive.load();
     p.wait_limit_ns = wait_limit_ns();
     if (head_dim == 64)
