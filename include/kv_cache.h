@@ -111,9 +111,10 @@ size_t kv_cache_attention_x16_workspace_bytes(int64_t batch, int64_t tokens, int
  * Sizes whose 64-token units, batch * kv_heads * ceil(tokens * group / 8) *
  * ceil(max_pages * page / 64), reach 2^31 are refused.
  *
- * Scores, softmax statistics and sums are fp32, the softmax weights are rounded
- * to fp16 for the product with V.  The order of all sums is fixed: the same call
- * gives the same bits.
+ * Scores, softmax statistics and sums are fp32.  For the product with V a softmax weight
+ * times its page's scale is rounded to fp16, relative to the largest such product of
+ * the row: exact to 2^-11 of itself down to 2^-21 of that, and to 2^-32 of that
+ * below.  The order of all sums is fixed: the same call gives the same bits.
  */
 int kv_cache_attention_x16(const kv_cache_pool *cache, const void *q, int dtype, int64_t batch,
                            int64_t tokens, int64_t q_heads, const int64_t *q_strides, void *out,

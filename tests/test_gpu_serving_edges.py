@@ -127,3 +127,79 @@ def test_window_very_large_and_small_values(n, window, sinks, scale, size_of_v):
     got = _f64(gr.flash_attention_window(q, k, v.cuda(), window, sinks))[0] / size_of_v
     o, absv, _, size = ref.attend(q64[0], k64[0], v.double().numpy()[0] / size_of_v, window, sinks)
     _check(got, o, absv, size, d, "bf16", _half_step("bf16"))
+
+# ---------------------------------------------------------------- attention over the cache
+
+
+def _cache_check(out, q64, c64, ids, n, d, dtype, window=0, sinks=0):
+    """As _check, without its absolute term: values of every size count."""
+    hkv = c64[0].shape[1]
+    k, v = ((x[ids] * s[ids][..., None, None]).transpose(0, 2, 1, 3).reshape(-1, hkv, d)[:n]
+            for x, s in ((c64[0], c64[2]), (c64[1], c64[3])))
+    o, absv, _, size = ref.attend(q64, k, v, window, sinks)
+    top = 2.0 ** np.floor(np.log2(np.maximum(absv.max(), 2.0 ** -120)))     # so that 2^-25 counts for nothing
+    rows = absv.max(-1, keepdims=True)
+    rows = 2.0 ** np.floor(np.log2(np.where(rows > 0, rows, top)))
+    _check(out / rows, o / rows, absv / rows, size, d, dtype, 2.0 ** -11)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("group", [1, 5, 12])
+@pytest.mark.parametrize("exponent", [-20, -33, -40, -90])
+def test_cache_attention_small_scale_with_all_the_weight(exponent, group, d):
+    """A page with a tiny V scale holds nearly all the weight beside one whose V scale is larger by
+    2^20 to 2^90, read before or after it or both: the result has the bits of the small page."""
+    import torch
+    rng = np.random.default_rng(51)
+    cache, c64 = _cache(rng, 3, 1, 64, d, garbage=False)
+    for h, s in ((0, 1.0), (1, 2.0 ** exponent), (2, 1.0)):
+        for which, x in ((2, 2.0 ** -3), (3, s)):
+            cache[which][h, 0] = x
+            c64[which][h, 0] = x
+        # every score of pages 0 and 2 lies some 100 nats below page 1's
+        values = torch.from_numpy(np.abs(c64[0][h]) % 8 + 8).to(torch.float8_e4m3fn) if h == 1 else \
+            torch.from_numpy(-(np.abs(c64[0][h]) % 8) - 8).to(torch.float8_e4m3fn)
+        cache[0][h] = values.cuda()
+        c64[0][h] = values.double().numpy()
+    q = _rand(rng, (1, 1, group, d), "bf16")[0].abs() + 3
+    q64 = _f64(q)
+    # 64 units of 64 tokens go to 16 blocks: each warp reads pages of both scales
+    for order in ([0, 1] * 32, [1, 2] * 32, [0, 2, 0, 1] * 16, [0] * 63 + [1], [1] + [2] * 63):
+        out = gr.kv_cache_attention(q, cache, _i32([order]), _i32([64 * len(order)]))
+        _cache_check(_f64(out)[0], q64[0], c64, order, 64 * len(order), d, "bf16")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("page,d,hkv,group,tokens,lengths", [
+    (64, 128, 2, 4, 1, [3000, 200]), (16, 64, 1, 8, 3, [1500, 40]), (128, 64, 2, 1, 1, [5000]),
+    (32, 128, 1, 16, 2, [900, 4000])])
+def test_cache_attention_scales_of_every_size(page, d, hkv, group, tokens, lengths, dtype):
+    """V scales between 2^-70 and 2^7 (2^-4 for fp16 outputs) in every order, scores of tens of nats, so that
+    any page may carry the result; sequences cut into several parts."""
+    import torch
+    rng = np.random.default_rng(page + d + group)
+    need = [-(-n // page) for n in lengths]
+    cache, c64 = _cache(rng, sum(need), hkv, page, d, garbage=False)
+    s = 2.0 ** rng.integers(-70 if dtype == "bf16" else -4, 8, (sum(need), hkv))
+    cache[3].copy_(torch.from_numpy(s.astype(np.float32)))
+    c64[3][...] = s
+    table = _tables(rng, need, sum(need))
+    for scale in (0.05, 10.0, 200.0):
+        q, q64 = _rand(rng, (len(lengths), tokens, hkv * group, d), dtype, scale)
+        out = _f64(gr.kv_cache_attention(q, cache, _i32(table), _i32(lengths)))
+        for i, n in enumerate(lengths):
+            _cache_check(out[i], q64[i], c64, table[i, :need[i]], n, d, dtype)
+
+
+def test_cache_attention_zero_pages():
+    """Pages of zeros carry the least scale there is; they count in the softmax and add nothing."""
+    rng = np.random.default_rng(53)
+    cache, c64 = _cache(rng, 6, 1, 16, 64, garbage=False)
+    for i in (0, 2, 3):
+        cache[1][i] = 0
+        cache[3][i] = 2.0 ** -100
+        c64[1][i], c64[3][i] = 0, 2.0 ** -100
+    q, q64 = _rand(rng, (1, 1, 4, 64), "bf16")
+    for order in ([0, 1, 2, 3, 4, 5] * 40, [1, 0, 4, 2] * 60, [0, 2, 3] * 50, [5, 0] * 100):
+        out = gr.kv_cache_attention(q, cache, _i32([order]), _i32([16 * len(order) - 3]))
+        _cache_check(_f64(out)[0], q64[0], c64, order, 16 * len(order) - 3, 64, "bf16")

@@ -44,9 +44,12 @@
 //  - Softmax in one pass, base 2, a running reference m per row that moves only when
 //    a score exceeds it by 2^8; fp32 statistics and accumulators.  P is
 //    rounded to fp16 for the second product (relative 2^-11, like the output's own
-//    rounding).  V's scale is folded into P relative to the
-//    largest scale met so far, 2^7 above one: P stays below 2^15 and normal down to
-//    2^-21 of the row's largest weight.
+//    rounding).  V's scale is folded into P, and O has a reference of its own, r above m and moved
+//    likewise: P = 2^(7 - r) * vs * weight stays below 2^15 and normal down to 2^-21 of the row's
+//    largest weight times scale, whatever scales come in what order (but for weights below 2^-111 under
+//    scales 2^111 above the others).  m and r are whole, so that factors and moves are exact
+//    for scales that are powers of two.  (With P relative to the largest scale met so far a
+//    page with the weight but a scale 2^30 below another's lost its bits.)
 #pragma once
 
 #include "kv_cache.cuh"
@@ -60,7 +63,7 @@ constexpr int kFeedWarp = 4;
 constexpr int kAttnThreads = 160;
 constexpr int kMostAbreast = 16;     // row tiles that share the stream of a head
 constexpr float kMoveLog2 = 8.0f;    // the reference moves when a score exceeds it by more
-constexpr float kPShift = 128.0f;    // 2^7, see above
+constexpr float kPLog2 = 7.0f;       // see above
 
 // kN groups of 8 query rows a tile (two for heads of 64 only).  Two blocks an SM (168 registers a
 // thread); three (128) for 64 elements and one group.  Measured, one group: 32 sequences of up to
@@ -76,9 +79,9 @@ struct AttnCfg {
     static constexpr uint32_t kOffV = kOffK + kStages * kTile;
     static constexpr int kPitch = D + 4;                         // floats a row of the join buffer
     static constexpr uint32_t kOffJoin = kOffV + kStages * kTile;   // [4 warps][kRows][kPitch]
-    static constexpr uint32_t kOffStat = kOffJoin + kWarps * kRows * kPitch * 4;   // m, l [4][kRows], vref [4]
-    static constexpr uint32_t kOffMeta = kOffStat + (2 * kWarps * kRows + kWarps) * 4;
-    static constexpr uint32_t kOffScan = kOffMeta + kStages * 4 * 8;   // (ks, vs) per 16 tokens
+    static constexpr uint32_t kOffStat = kOffJoin + kWarps * kRows * kPitch * 4;   // m, l, r [4][kRows]
+    static constexpr uint32_t kOffMeta = kOffStat + 3 * kWarps * kRows * 4;
+    static constexpr uint32_t kOffScan = kOffMeta + kStages * 4 * 8;   // (ks, log2 vs) per 16 tokens
     static constexpr uint32_t kOffBar = kOffScan + 16 * 4;
     static constexpr uint32_t kOffMisc = kOffBar + 2 * kStages * 8;
     static constexpr uint32_t kSmem = kOffMisc + 16 + 1024;
@@ -96,7 +99,7 @@ struct AttnParams {
     int abreast, passes;               // `passes` times
     int window, sinks;
     float scale_log2;                  // log2(e) / sqrt(D)
-    float *partial;                    // [2 * grid][kRows][D], then [2 * grid][kRows][2] (m, l)
+    float *partial;                    // [2 * grid][kRows][D], then [2 * grid][kRows][4] (m, l, r, unused)
     int grid;                          // ranges * abreast
     unsigned *arrived;                 // [ranges][abreast] parts that are there of the segment that
                                        // leaves the block's range; all 0 between calls
@@ -285,17 +288,23 @@ __device__ __forceinline__ int64_t out_row(const AttnParams &p, int b, int h, in
     return ((int64_t)b * p.tokens + row / p.group) * p.q_heads + h * p.group + row % p.group;
 }
 
-// kF elements of a row of the result from their sum y and the row's sum of weights, relative
-// to the reference ref; with scores also the row's log-sum-exp.
+// a - b, but -infinity less anything is -infinity.
+__device__ __forceinline__ float less(float a, float b) { return a - (b == -INFINITY ? 0.0f : b); }
+
+// kF elements of a row of the result from the row's sum of weights, relative to the reference ref, and their
+// own sum y, whose reference is r above that; with scores also the row's log-sum-exp.
 template <int D, int kF, bool kBf16, bool kScores>
 __device__ __forceinline__ void write_row(const AttnParams &p, int b, int h, int row, int d0,
-                                          const float (&y)[kF], float ref, float sum) {
+                                          const float (&y)[kF], float ref, float r, float sum) {
     const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;   // 0: the row sees nothing
+    // (its square: r may span the range of all scales)
+    const float f = r == -INFINITY ? 0.0f : exp2f(0.5f * (r - kPLog2));
     uint16_t *dst = p.out + out_row(p, b, h, row) * D + d0;
 #pragma unroll
     for (int j = 0; j < kF; j += 4)
         *reinterpret_cast<uint2 *>(dst + j) =
-            make_uint2(pack_out<kBf16>(y[j] * inv, y[j + 1] * inv), pack_out<kBf16>(y[j + 2] * inv, y[j + 3] * inv));
+            make_uint2(pack_out<kBf16>(y[j] * inv * f * f, y[j + 1] * inv * f * f),
+                       pack_out<kBf16>(y[j + 2] * inv * f * f, y[j + 3] * inv * f * f));
     if (kScores && d0 == 0)
         p.lse[((int64_t)b * p.pool.kv_heads + h) * p.rows + row] = sum == 0.0f ? INFINITY : ref + log2f(sum);
 }
@@ -440,6 +449,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
                 b = lb;
                 seq_at = lat;
             }
+            const float lv = log2f(fmaxf(vs, kMinScale));
             // the next batch starts in the sequence of this one's last unit
             const int last = min(per_batch, stop - u0) * pieces - 1;
             b = __shfl_sync(0xffffffffu, b, last);
@@ -462,7 +472,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
                 }
                 if (in)
                     for (int s = 0; s < piece_tokens / 16; ++s)
-                        meta[stage * 4 + (lane % pieces) * (piece_tokens / 16) + s] = make_float2(ks, vs);
+                        meta[stage * 4 + (lane % pieces) * (piece_tokens / 16) + s] = make_float2(ks, lv);
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(full(stage));
@@ -484,8 +494,8 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
         const int g = lane >> 2, c = lane & 3;
         float *join = reinterpret_cast<float *>(gbase + G::kOffJoin);
         float *stat = reinterpret_cast<float *>(gbase + G::kOffStat);
-        float *stat_m = stat, *stat_l = stat + kWarps * kRows, *stat_v = stat + 2 * kWarps * kRows;
-        float *stats = p.partial + (int64_t)p.grid * 2 * kRows * D;   // the parts' (m, l)
+        float *stat_m = stat, *stat_l = stat + kWarps * kRows, *stat_r = stat + 2 * kWarps * kRows;
+        float *stats = p.partial + (int64_t)p.grid * 2 * kRows * D;   // the parts' (m, l, r)
         bool alive = true;
         uint32_t stage = 0, phase = 0;
         int unit = start;
@@ -533,17 +543,16 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
 
             // o[t][j]: elements 2j (0, 1) and 2j + 1 (2, 3) of the lane's piece, rows 2c, 2c + 1
             float o[kN][D / 16][4];
-            float m[kN][2], l[kN][2];
+            float m[kN][2], md[kN][2], l[kN][2];   // (md: 7 - r)
 #pragma unroll
             for (int t = 0; t < kN; ++t) {
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j)
                     o[t][j][0] = o[t][j][1] = o[t][j][2] = o[t][j][3] = 0.0f;
                 m[t][0] = m[t][1] = -INFINITY;
+                md[t][0] = md[t][1] = 0.0f;
                 l[t][0] = l[t][1] = 0.0f;
             }
-            float vref = 0.0f, vinv = 0.0f;
-
             const int units_here = end - unit, u0 = unit - seg0;
             for (int u = 0; u < units_here; ++u) {
                 const int t0 = s.chunk(u0 + u) * kUnit + 16 * warp;
@@ -599,7 +608,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
                     const bool masked = !(t0 + 15 <= pos_min &&
                                           (p.window == 0 || t0 > pos_max - p.window || t0 + 15 < p.sinks));
                     const int ta = t0 + key_of(g), tb = ta + 8;   // the lane's tokens
-                    float x[kN][4];
+                    float x[kN][4], d[kN][2];   // exponents of the weights, and what P's exceed them by
                     bool high = false;
 #pragma unroll
                     for (int t = 0; t < kN; ++t) {
@@ -619,7 +628,11 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
                             if (masked && !sees(i < 2 ? ta : tb, pos[t][e], p.window, p.sinks))
                                 x[t][i] = acc[t][i] = -INFINITY;
                         }
-                        high |= fmaxf(fmaxf(x[t][0], x[t][1]), fmaxf(x[t][2], x[t][3])) > kMoveLog2;
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            d[t][e] = fminf(md[t][e] + sc.y, 126.0f);
+                            high |= fmaxf(x[t][e], x[t][2 + e]) > fminf(kMoveLog2, kMoveLog2 + kPLog2 - d[t][e]);
+                        }
                     }
                     if (__any_sync(0xffffffffu, high)) {
                         // move the rows' references to their largest score so far
@@ -632,16 +645,22 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
                                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                                const float to = fmaxf(m[t][e], top);
+                                const float to = fmaxf(m[t][e], rintf(top));
                                 const float a = to > m[t][e] ? exp2_fast(m[t][e] - to) : 1.0f;   // 0 at first
                                 l[t][e] *= a;
+                                // o's old reference and this unit's, from the new m
+                                const float ref = to == -INFINITY ? 0.0f : to;
+                                const float r0 = m[t][e] - ref + (kPLog2 - md[t][e]);
+                                const float r1 = fmaxf(r0, rintf(top - ref + sc.y));
+                                const float ao = r1 > r0 ? exp2_fast(r0 - r1) : 1.0f;
 #pragma unroll
                                 for (int j = 0; j < D / 16; ++j) {
-                                    o[t][j][e] *= a;
-                                    o[t][j][2 + e] *= a;
+                                    o[t][j][e] *= ao;
+                                    o[t][j][2 + e] *= ao;
                                 }
                                 m[t][e] = to;
-                                const float ref = to == -INFINITY ? 0.0f : to;
+                                md[t][e] = less(kPLog2, r1);
+                                d[t][e] = fminf(md[t][e] + sc.y, 126.0f);
 #pragma unroll
                                 for (int i = 0; i < 2; ++i)
                                     x[t][2 * i + e] = acc[t][2 * i + e] == -INFINITY
@@ -649,33 +668,18 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
                                                           : fmaf(acc[t][2 * i + e], f, -ref);
                             }
                     }
-                    const float vs = fmaxf(sc.y, kMinScale);
-                    if (vs > vref) {   // uniform in the warp
-                        const float f = vref / vs;
-#pragma unroll
-                        for (int t = 0; t < kN; ++t)
-#pragma unroll
-                            for (int j = 0; j < D / 16; ++j) {
-                                o[t][j][0] *= f;
-                                o[t][j][1] *= f;
-                                o[t][j][2] *= f;
-                                o[t][j][3] *= f;
-                            }
-                        vref = vs;
-                        vinv = kPShift / vs;
-                    }
                     // ---- P^T as the second product's B operand: {rows 2c, 2c + 1} of a token to
                     // {tokens 2c, 2c + 1} of a row
-                    const float pf = vs * vinv;
                     uint32_t pt[kN][2];
 #pragma unroll
                     for (int t = 0; t < kN; ++t) {
                         const float e0 = exp2_fast(x[t][0]), e1 = exp2_fast(x[t][1]);
                         const float e2 = exp2_fast(x[t][2]), e3 = exp2_fast(x[t][3]);
+                        const float f0 = exp2_fast(d[t][0]), f1 = exp2_fast(d[t][1]);
                         l[t][0] += e0 + e2;
                         l[t][1] += e1 + e3;
-                        pt[t][0] = turned(half2_of(e0 * pf, e1 * pf));
-                        pt[t][1] = turned(half2_of(e2 * pf, e3 * pf));
+                        pt[t][0] = turned(half2_of(e0 * f0, e1 * f1));
+                        pt[t][1] = turned(half2_of(e2 * f0, e3 * f1));
                     }
                     // ---- O^T += V^T P^T: the lane's four tokens c, c + 4, c + 8, c + 12
                     constexpr int kW = D / 32;   // words of a lane's piece
@@ -767,7 +771,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
             }
             unit = end;
 
-            // ---- join the four warps: each leaves (O, m, l), then 16 / kN threads take a row
+            // ---- join the four warps: each leaves (O, m, l, r), then 16 / kN threads take a row
 #pragma unroll
             for (int t = 0; t < kN; ++t)
 #pragma unroll
@@ -784,28 +788,29 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
                     if (g == 0) {
                         stat_m[row] = m[t][e];
                         stat_l[row] = l[t][e];
+                        stat_r[row] = kPLog2 - md[t][e];
                     }
                 }
-            if (lane == 0)
-                stat_v[warp] = vref / kPShift;
             named_bar_sync(1, 32 * kWarps);
             {
                 constexpr int kF = D * kN / 16;   // elements a thread
                 const int r = tid * kN / 16, d0 = tid % (16 / kN) * kF;
-                float top = -INFINITY, sum = 0.0f;
+                float top = -INFINITY, top_r = -INFINITY, sum = 0.0f;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w)
                     top = fmaxf(top, stat_m[w * kRows + r]);
-                const float ref = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w)
+                    top_r = fmaxf(top_r, less(stat_m[w * kRows + r], top) + stat_r[w * kRows + r]);
                 float y[kF];
 #pragma unroll
                 for (int j = 0; j < kF; ++j)
                     y[j] = 0.0f;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
-                    const float f = exp2_fast(stat_m[w * kRows + r] - ref);
-                    const float fv = f * stat_v[w];
-                    sum += f * stat_l[w * kRows + r];
+                    const float below = less(stat_m[w * kRows + r], top);
+                    const float fv = exp2_fast(less(below + stat_r[w * kRows + r], top_r));
+                    sum += exp2_fast(below) * stat_l[w * kRows + r];
                     const float4 *src = reinterpret_cast<const float4 *>(
                         join + (w * kRows + r) * G::kPitch + d0);
 #pragma unroll
@@ -819,7 +824,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
                 }
                 if (seg0 >= start && seg1 <= stop) {   // the whole of it
                     if (alive && row0 + r < p.rows)
-                        write_row<D, kF, kBf16, kScores>(p, b, h, row0 + r, d0, y, ref, sum);
+                        write_row<D, kF, kBf16, kScores>(p, b, h, row0 + r, d0, y, top, top_r, sum);
                 } else {
                     // a part: slot 0 where it starts this block's range, else slot 1
                     const int64_t at = ((int64_t)(range * p.abreast + lane_tile) * 2 + (seg0 > start ? 1 : 0)) * kRows + r;
@@ -828,7 +833,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
                     for (int j = 0; j < kF; j += 4)
                         *reinterpret_cast<float4 *>(dst + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
                     if (d0 == 0)
-                        *reinterpret_cast<float2 *>(stats + at * 2) = make_float2(top, sum);
+                        *reinterpret_cast<float4 *>(stats + at * 4) = make_float4(top, sum, top_r, 0.0f);
                     cut_b[cuts & 1] = b;
                     cut_local[cuts & 1] = local;
                     cut_seg0[cuts & 1] = seg0;
@@ -841,7 +846,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
 
         // ---- count the parts; who counts the last one of a segment joins it
         if (cuts > 0) {
-            int *last = reinterpret_cast<int *>(stat_v);
+            int *last = reinterpret_cast<int *>(stat_r);
             named_bar_sync(1, 32 * kWarps);
             if (lane == 0 && warp < cuts) {
                 const int i = warp;
@@ -865,21 +870,21 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
                 auto slot = [&](int c) {
                     return (int64_t)((c * p.abreast + lane_tile) * 2 + (c == c0 ? first : 0)) * kRows + r;
                 };
-                float ref = -INFINITY, sum = 0.0f, y[kF];
+                float ref = -INFINITY, ref_r = -INFINITY, sum = 0.0f, y[kF];
 #pragma unroll
                 for (int j = 0; j < kF; ++j)
                     y[j] = 0.0f;
                 // a few parts are read at a time: each round waits for L2 once
                 constexpr int kAtOnce = kN == 1 ? 8 : 4;
                 for (int c = c0; c <= c1; c += kAtOnce) {
-                    float2 ml[kAtOnce];
+                    float4 ml[kAtOnce];   // (m, l, r)
                     float4 z[kAtOnce][kF / 4];
 #pragma unroll
                     for (int k = 0; k < kAtOnce; ++k) {
-                        ml[k] = make_float2(-INFINITY, 0.0f);
+                        ml[k] = make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
                         if (c + k <= c1) {
                             const int64_t at = slot(c + k);
-                            ml[k] = __ldcg(reinterpret_cast<const float2 *>(stats + at * 2));
+                            ml[k] = __ldcg(reinterpret_cast<const float4 *>(stats + at * 4));
 #pragma unroll
                             for (int j = 0; j < kF / 4; ++j)
                                 z[k][j] = __ldcg(reinterpret_cast<const float4 *>(p.partial + at * D + d0) + j);
@@ -889,20 +894,25 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
 #pragma unroll
                     for (int k = 0; k < kAtOnce; ++k)
                         top = fmaxf(top, ml[k].x);
-                    if (top > ref) {
-                        const float f = exp2_fast(ref - top);   // 0 at first
-                        sum *= f;
+                    const float r0 = less(ref, top) + ref_r;   // (-infinity at first, as in ref)
+                    float r1 = r0;
 #pragma unroll
-                        for (int j = 0; j < kF; ++j)
-                            y[j] *= f;
-                        ref = top;
-                    }
+                    for (int k = 0; k < kAtOnce; ++k)
+                        r1 = fmaxf(r1, less(ml[k].x, top) + ml[k].z);
+                    sum *= exp2_fast(less(ref, top));
+                    const float fy = exp2_fast(less(r0, r1));
+#pragma unroll
+                    for (int j = 0; j < kF; ++j)
+                        y[j] *= fy;
+                    ref = top;
+                    ref_r = r1;
 #pragma unroll
                     for (int k = 0; k < kAtOnce; ++k) {
                         if (c + k > c1)
                             break;
-                        const float f = exp2_fast(ml[k].x - (ref == -INFINITY ? 0.0f : ref));
-                        sum += f * ml[k].y;
+                        const float below = less(ml[k].x, ref);
+                        sum += exp2_fast(below) * ml[k].y;
+                        const float f = exp2_fast(less(below + ml[k].z, ref_r));
 #pragma unroll
                         for (int j = 0; j < kF / 4; ++j) {
                             y[4 * j] += f * z[k][j].x;
@@ -912,11 +922,9 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
                         }
                     }
                 }
-                if (ref == -INFINITY)
-                    ref = 0.0f;
                 const int row = (local % p.passes * p.abreast + lane_tile) * kRows + r;
                 if (alive && row < p.rows)
-                    write_row<D, kF, kBf16, kScores>(p, bb, local / p.passes, row, d0, y, ref, sum);
+                    write_row<D, kF, kBf16, kScores>(p, bb, local / p.passes, row, d0, y, ref, ref_r, sum);
             }
         }
     }

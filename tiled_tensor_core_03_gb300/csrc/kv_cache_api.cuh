@@ -126,7 +126,7 @@ AttnSpace attention_space(int64_t batch, int64_t rows, int64_t kv_heads, int64_t
     const size_t slots = 2 * (size_t)sms * std::max(KC::AttnCfg<64, 1>::kBlocksPerSm * 8,
                                                     KC::AttnCfg<64, 2>::kBlocksPerSm * 16);
     size_t at = a.partial = GEMMRELU_KV_COUNTER_BYTES;
-    at += slots * (head_dim + 2) * 4;
+    at += slots * (head_dim + 4) * 4;
     a.lse = at = round256(at);
     if (weights_width > 0) {
         at += (size_t)batch * kv_heads * rows * 4;
