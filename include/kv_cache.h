@@ -99,7 +99,8 @@ size_t kv_cache_attention_x16_workspace_bytes(int64_t batch, int64_t tokens, int
  *            token i has position p = length - tokens + i.  It sees the tokens
  *            t <= p; with a window > 0 only those with t > p - window or
  *            t < sinks.  A token at a negative position (a sequence shorter
- *            than `tokens`) sees nothing: its output is 0.
+ *            than `tokens`) sees nothing: its output is 0.  Pages of which no
+ *            query sees a token are not looked up: their numbers may be anything.
  * weights  : fp32 [batch][kv_heads][weights_width] or NULL.  weights[t] grows by the
  *            sum, over the query tokens and the head's group of query heads,
  *            of the softmax weight of token t; weights_width >= max_pages * page.

@@ -203,3 +203,31 @@ def test_cache_attention_zero_pages():
     for order in ([0, 1, 2, 3, 4, 5] * 40, [1, 0, 4, 2] * 60, [0, 2, 3] * 50, [5, 0] * 100):
         out = gr.kv_cache_attention(q, cache, _i32([order]), _i32([16 * len(order) - 3]))
         _cache_check(_f64(out)[0], q64[0], c64, order, 16 * len(order) - 3, 64, "bf16")
+
+
+@pytest.mark.parametrize("weights", [False, True])
+@pytest.mark.parametrize("page,tokens,n,window,sinks", [
+    (16, 1, 300, 100, 0), (16, 3, 300, 100, 20), (32, 1, 1000, 400, 4), (16, 1, 70, 1, 1), (32, 2, 500, 33, 65)])
+def test_cache_attention_freed_pages(page, tokens, n, window, sinks, weights):
+    """Pages of which no query sees a token are never asked for: a sequence may have given them up."""
+    import torch
+    rng = np.random.default_rng(page + n + window)
+    need, d, hkv = -(-n // page), 64, 2
+    cache, c64 = _cache(rng, need, hkv, page, d, garbage=False)
+    table = _tables(rng, [need], need)
+    low = n - tokens - window + 1            # the first token that the first query's window holds
+    freed = [i for i in range(need) if (i + 1) * page <= low and i * page >= sinks]
+    assert freed
+    given = table.copy()
+    given[0, freed] = rng.choice([-1, need, 2 ** 31 - 1], len(freed))
+    q, q64 = _rand(rng, (1, tokens, 2 * hkv, d), "fp16")
+    w = torch.zeros((1, hkv, need * page), device="cuda") if weights else None
+    out = _f64(gr.kv_cache_attention(q, cache, _i32(given), _i32([n]), window, sinks, weights=w))
+    assert gr.status() == gr.OK
+    k, v = ((x[table[0]] * s[table[0]][..., None, None]).transpose(0, 2, 1, 3).reshape(-1, hkv, d)[:n]
+            for x, s in ((c64[0], c64[2]), (c64[1], c64[3])))
+    o, absv, mass, size = ref.attend(q64[0], k, v, window, sinks)
+    _check(out[0], o, absv, size, d, "fp16", 2.0 ** -11)
+    if weights:
+        rel = ref.weight_error(size.max(), d) + 2.0 ** -20
+        assert (np.abs(_f64(w)[0, :, :n] - mass) <= rel * mass).all()

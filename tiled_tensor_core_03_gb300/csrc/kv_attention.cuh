@@ -436,7 +436,11 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
                 const int token = s.chunk((unit - lat) % s.units) * kUnit +
                                   (lane % pieces) * piece_tokens;
                 slot = token & (p.pool.page - 1);
-                if (token < n) {
+                // (a page of 16 or 32 tokens may lie in a unit that rows see and be seen by none itself: the
+                // sequence may have given it up)
+                const bool seen = p.window == 0 || token < p.sinks ||
+                                  token + piece_tokens > max(n - p.tokens, 0) - p.window + 1;
+                if (token < n && seen) {
                     id = p.pages[lb * p.max_pages + (token >> p.pool.page_shift)];
                     if (id < 0 || id >= p.pool.num_pages) {
                         record_page_error();
