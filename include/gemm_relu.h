@@ -254,8 +254,10 @@ int gemm_relu_stream_capturing(void *stream);
  * gemm_relu_status -- synchronise `stream`, then return and clear the current
  * device's watchdog word: GEMMRELU_OK, or GEMMRELU_ERR_TIMEOUT if a bounded
  * wait inside a kernel expired since the last call (that kernel's output is
- * then unspecified; the CUDA context stays usable).  Returns GEMMRELU_ERR_CUDA
- * if the synchronisation or the read fails.
+ * then unspecified; the CUDA context stays usable), or GEMMRELU_ERR_PAGE if a
+ * cache call met a page number, length or count out of range (kv_cache.h; its
+ * other outputs are right).  With both the status is the timeout.  Returns
+ * GEMMRELU_ERR_CUDA if the synchronisation or the read fails.
  */
 int gemm_relu_status(void *stream);
 

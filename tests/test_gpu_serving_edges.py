@@ -231,3 +231,31 @@ def test_cache_attention_freed_pages(page, tokens, n, window, sinks, weights):
     if weights:
         rel = ref.weight_error(size.max(), d) + 2.0 ** -20
         assert (np.abs(_f64(w)[0, :, :n] - mass) <= rel * mass).all()
+
+# ---------------------------------------------------------------- status and streams
+
+
+@pytest.mark.parametrize("page_first", [True, False])
+def test_status_a_timeout_outranks_a_bad_page(page_first):
+    """A bad page leaves the other outputs right, a timeout leaves a call's outputs unspecified: with
+    both since the last look, the status is the timeout, whichever came first."""
+    rng = np.random.default_rng(61)
+    cache, _ = _cache(rng, 2, 1, 16, 64)
+    x, _ = _rand(rng, (1, 4, 1, 64), "fp16")
+    q, _ = _rand(rng, (1, 300, 2, 64), "fp16")
+
+    def bad_page():
+        gr.kv_cache_append(cache, x, x, _i32([[7]]), _i32([4]))
+
+    def timeout():
+        gr.gemm_relu_debug_set(1, 20_000_000)
+        try:
+            gr.flash_attention_window(q, q, q, 100, 4)
+        finally:
+            gr.gemm_relu_debug_set(0, 0)
+    for step in (bad_page, timeout) if page_first else (timeout, bad_page):
+        step()
+    assert gr.status() == gr.ERR_TIMEOUT
+    assert gr.status() == gr.OK
+    bad_page()
+    assert gr.status() == gr.ERR_PAGE

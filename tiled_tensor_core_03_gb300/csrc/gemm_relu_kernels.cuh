@@ -38,8 +38,9 @@ using namespace sm103;
 
 // ------------------------------------------------------------------ status
 
-// Device watchdog word: 0, or the first error code recorded since the host
-// last read it.  `g_status_where` tells which wait expired (debugging aid).
+// Device watchdog word: 0, or the gravest error code recorded since the host
+// last read it: a timeout leaves outputs unspecified, a bad page does not.
+// `g_status_where` tells which wait expired (debugging aid).
 __device__ unsigned int g_status;
 __device__ unsigned int g_status_where;
 
@@ -57,7 +58,7 @@ enum WaitSite : unsigned {
 
 __device__ __forceinline__ void record_timeout(volatile uint32_t *abort_flag, unsigned where) {
     *abort_flag = 1u;
-    if (atomicCAS(&g_status, 0u, kStatusTimeout) == 0u)
+    if (atomicExch(&g_status, kStatusTimeout) != kStatusTimeout)
         g_status_where = where;
 }
 

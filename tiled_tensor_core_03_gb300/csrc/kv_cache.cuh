@@ -19,6 +19,7 @@ namespace kvc {
 
 constexpr unsigned kStatusPage = 8;   // == GEMMRELU_ERR_PAGE
 
+// (a timeout that is there already stays)
 __device__ __forceinline__ void record_page_error() { atomicCAS(&g_status, 0u, kStatusPage); }
 
 // ---------------------------------------------------------------- the number format
