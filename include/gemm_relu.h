@@ -251,6 +251,13 @@ int gemm_relu_f16_splitk_noalloc(const void *A, const void *B, void *C,
 int gemm_relu_stream_capturing(void *stream);
 
 /*
+ * gemm_relu_stream_id -- a number that names `stream` for the life of the process.  Its handle
+ * does not: a destroyed stream's handle may come back, and cudaStreamPerThread is another
+ * stream in every host thread (host-only; GEMMRELU_ERR_CUDA if CUDA does not know the stream).
+ */
+int gemm_relu_stream_id(void *stream, uint64_t *id);
+
+/*
  * gemm_relu_status -- synchronise `stream`, then return and clear the current
  * device's watchdog word: GEMMRELU_OK, or GEMMRELU_ERR_TIMEOUT if a bounded
  * wait inside a kernel expired since the last call (that kernel's output is

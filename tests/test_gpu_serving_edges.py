@@ -259,3 +259,90 @@ def test_status_a_timeout_outranks_a_bad_page(page_first):
     assert gr.status() == gr.OK
     bad_page()
     assert gr.status() == gr.ERR_PAGE
+
+
+def _stream_id(handle):
+    import ctypes
+    out = ctypes.c_uint64()
+    assert gr.lib().gemm_relu_stream_id(ctypes.c_void_p(handle), ctypes.byref(out)) == gr.OK
+    return out.value
+
+
+PER_THREAD = 2      # cudaStreamPerThread
+
+
+def test_stream_ids_tell_streams_with_one_handle_apart():
+    import ctypes
+    import threading
+    import torch
+    handles = [0] + [torch.cuda.Stream().cuda_stream for _ in range(3)]
+    ids = [_stream_id(h) for h in handles]
+    assert len(set(ids)) == len(set(handles)) and ids == [_stream_id(h) for h in handles]
+    assert gr.lib().gemm_relu_stream_id(None, None) == gr.ERR_INVALID_ARG
+    seen = []
+    for _ in range(20):        # created and destroyed: the handle may come back, the id does not
+        s = ctypes.c_void_p()
+        torch.cuda.cudart().cudaStreamCreate(ctypes.addressof(s))
+        seen.append(_stream_id(s.value))
+        torch.cuda.cudart().cudaStreamDestroy(s.value)
+    assert len(set(seen)) == 20 and not set(seen) & set(ids)
+    mine = []
+
+    def look():
+        torch.cuda.set_device(0)
+        mine.append(_stream_id(PER_THREAD))
+    for _ in range(2):
+        t = threading.Thread(target=look)
+        t.start()
+        t.join()
+    look()
+    assert len(set(mine)) == 3
+
+
+def test_cache_attention_on_streams_of_one_handle():
+    """Two threads, each on its own cudaStreamPerThread, whose calls overlap on the GPU: each has a
+    workspace of its own.  Then more streams than workspaces are kept."""
+    import ctypes
+    import threading
+    import torch
+    rng = np.random.default_rng(62)
+    cache, _ = _cache(rng, 400, 2, 64, 128, garbage=False)
+    work, want = [], []
+    for n in (9000, 25000):
+        q, _ = _rand(rng, (1, 1, 8, 128), "bf16")
+        pages = _i32(np.arange(-(-n // 64))[None])
+        args = (q, cache, pages, _i32([n]))
+        want.append(gr.kv_cache_attention(*args))
+        work.append((args, [torch.empty_like(q) for _ in range(200)]))
+    torch.cuda.synchronize()
+    start = threading.Barrier(2)
+    failed = []
+
+    def go(args, outs):
+        try:
+            torch.cuda.set_device(0)
+            stream = torch.cuda.ExternalStream(PER_THREAD)
+            start.wait(60)
+            for out in outs:
+                gr.kv_cache_attention(*args, out=out, stream=stream)
+            stream.synchronize()
+        except Exception as e:      # shown by the test, not by the thread
+            failed.append(e)
+    threads = [threading.Thread(target=go, args=w) for w in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    for (_, outs), x in zip(work, want):
+        assert all(torch.equal(o, x) for o in outs)
+    args, _ = work[0]
+    handles = [ctypes.c_void_p() for _ in range(70)]
+    for h in handles:
+        assert int(torch.cuda.cudart().cudaStreamCreate(ctypes.addressof(h))) == 0
+        s = torch.cuda.ExternalStream(h.value)
+        o = gr.kv_cache_attention(*args, stream=s)
+        s.synchronize()
+        assert torch.equal(o, want[0])
+    for h in handles:
+        torch.cuda.cudart().cudaStreamDestroy(h.value)

@@ -81,6 +81,8 @@ def lib():
         L.gemm_relu_status.restype = i32
         L.gemm_relu_stream_capturing.argtypes = [vp]
         L.gemm_relu_stream_capturing.restype = i32
+        L.gemm_relu_stream_id.argtypes = [vp, vp]
+        L.gemm_relu_stream_id.restype = i32
         L.gemm_relu_strerror.argtypes = [i32]
         L.gemm_relu_strerror.restype = ctypes.c_char_p
         L.gemm_relu_f16_path.argtypes = [vp, vp, vp, i64, i64, i64]

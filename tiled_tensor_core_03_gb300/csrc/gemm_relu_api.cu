@@ -1198,6 +1198,16 @@ int gemm_relu_stream_capturing(void *stream) {
            st != cudaStreamCaptureStatusNone;
 }
 
+int gemm_relu_stream_id(void *stream, uint64_t *id) {
+    if (!id)
+        return GEMMRELU_ERR_INVALID_ARG;
+    unsigned long long v = 0;
+    if (cudaStreamGetId(static_cast<cudaStream_t>(stream), &v) != cudaSuccess)
+        return GEMMRELU_ERR_CUDA;
+    *id = v;
+    return GEMMRELU_OK;
+}
+
 const char *gemm_relu_strerror(int code) {
     switch (code) {
     case GEMMRELU_OK: return "ok";

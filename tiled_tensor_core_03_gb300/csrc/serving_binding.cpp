@@ -31,6 +31,7 @@ decltype(&kv_cache_attention_x16) f_attention;
 decltype(&kv_cache_attention_x16_workspace_bytes) f_workspace_bytes;
 decltype(&kv_cache_evict_e4m3) f_evict;
 decltype(&gemm_relu_stream_capturing) f_capturing;
+decltype(&gemm_relu_stream_id) f_stream_id;
 PyObject *g_error;   // GemmReluError
 
 struct Refusal {
@@ -231,17 +232,23 @@ at::Tensor new_workspace(const at::Tensor &q, size_t bytes) {
 
 // Workspaces of calls that bring none, one per device and stream, as large as its calls needed so
 // far: calls on a stream follow one another, and one that is replaced goes back to torch's
-// allocator for that stream.  Calls being captured get their own, since their graph may run
-// anywhere, and so do those that need more than kKeep (scores of many weights), which torch then
-// has back at once.  The map is never destroyed: at exit torch's allocator may be gone before it.
+// allocator for that stream.  A stream is known by its id, since two may share a handle.  Calls being
+// captured get their own, since their graph may run anywhere, and so do those that need more
+// than kKeep (scores of many weights), which torch then has back at once.  So that streams that
+// are gone do not hold memory for ever, all go back once there are kMostKept.  The map is
+// never destroyed: at exit torch's allocator may be gone before it.
 constexpr size_t kKeep = (size_t)64 << 20;
+constexpr size_t kMostKept = 64;
 
 at::Tensor workspace_for(const at::Tensor &q, int64_t kv_heads, int64_t width, int d, void *stream) {
     const size_t bytes = workspace_bytes(q, kv_heads, width);
-    if (bytes > kKeep || f_capturing(stream))
+    uint64_t id;
+    if (bytes > kKeep || f_capturing(stream) || f_stream_id(stream, &id) != GEMMRELU_OK)
         return new_workspace(q, bytes);
-    static auto *kept = new std::map<std::pair<int, void *>, at::Tensor>;
-    at::Tensor &w = (*kept)[{d, stream}];   // (the GIL is held)
+    static auto *kept = new std::map<std::pair<int, uint64_t>, at::Tensor>;   // (the GIL is held)
+    if (kept->size() >= kMostKept && kept->count({d, id}) == 0)
+        kept->clear();
+    at::Tensor &w = (*kept)[{d, id}];
     if (!w.defined() || w.nbytes() < bytes)
         w = new_workspace(q, bytes);
     return w;
@@ -363,11 +370,11 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     return nullptr;
 }
 
-// bind(GemmReluError, addresses of the six library functions in the order below)
+// bind(GemmReluError, addresses of the seven library functions in the order below)
 PyObject *bind(PyObject *, PyObject *args) {
     PyObject *error;
-    unsigned long long f[6];
-    if (!PyArg_ParseTuple(args, "OKKKKKK", &error, &f[0], &f[1], &f[2], &f[3], &f[4], &f[5]))
+    unsigned long long f[7];
+    if (!PyArg_ParseTuple(args, "OKKKKKKK", &error, &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6]))
         return nullptr;
     f_window = reinterpret_cast<decltype(f_window)>((uintptr_t)f[0]);
     f_append = reinterpret_cast<decltype(f_append)>((uintptr_t)f[1]);
@@ -375,6 +382,7 @@ PyObject *bind(PyObject *, PyObject *args) {
     f_workspace_bytes = reinterpret_cast<decltype(f_workspace_bytes)>((uintptr_t)f[3]);
     f_evict = reinterpret_cast<decltype(f_evict)>((uintptr_t)f[4]);
     f_capturing = reinterpret_cast<decltype(f_capturing)>((uintptr_t)f[5]);
+    f_stream_id = reinterpret_cast<decltype(f_stream_id)>((uintptr_t)f[6]);
     Py_INCREF(error);
     g_error = error;
     Py_RETURN_NONE;

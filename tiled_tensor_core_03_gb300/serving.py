@@ -27,7 +27,7 @@ _serving.bind(GemmReluError, *(
     ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value
     for name in ("flash_attention_window_x16", "kv_cache_append_x16", "kv_cache_attention_x16",
                  "kv_cache_attention_x16_workspace_bytes", "kv_cache_evict_e4m3",
-                 "gemm_relu_stream_capturing")))
+                 "gemm_relu_stream_capturing", "gemm_relu_stream_id")))
 
 
 class KVCache(NamedTuple):
