@@ -1,5 +1,7 @@
 """Build in-tree: libgemmrelu.so with nvcc for sm_103a (one translation unit), and beside it the
-CPython extension _serving that hands torch tensors to it (g++, torch's headers)."""
+CPython extension _serving that hands torch tensors to it (g++, torch's headers; left out where
+there is no torch, which the library itself does not need)."""
+import importlib.util
 import os
 import subprocess
 import sys
@@ -41,8 +43,15 @@ def _stale(target, deps):
         os.path.getmtime(d) > os.path.getmtime(target) for d in deps)
 
 
+def _has_torch():
+    try:
+        return importlib.util.find_spec("torch") is not None
+    except ValueError:   # a placeholder in sys.modules
+        return False
+
+
 def needs_build():
-    return _stale(LIB, DEPS) or _stale(BINDING, BINDING_DEPS)
+    return _stale(LIB, DEPS) or (_has_torch() and _stale(BINDING, BINDING_DEPS))
 
 
 def build_binding():
@@ -61,7 +70,7 @@ def build_binding():
 
 
 def build(verbose=False, extra=()):
-    """Compile both at the same time."""
+    """Compile both at the same time, the library alone without torch."""
     failed = []
 
     def binding():
@@ -70,7 +79,10 @@ def build(verbose=False, extra=()):
         except Exception as e:   # raised again below, in the caller's thread
             failed.append(e)
     side = threading.Thread(target=binding)
-    side.start()
+    if _has_torch():
+        side.start()
+    else:
+        print("no torch: the serving operators' extension is not built", file=sys.stderr)
     try:
         cmd = [nvcc(), *NVCC_FLAGS, f"-I{INCLUDE}", f"-I{CSRC}", *extra, "-o", LIB, *SOURCES]
         if verbose:
@@ -78,7 +90,8 @@ def build(verbose=False, extra=()):
             print(" ".join(cmd), file=sys.stderr)
         subprocess.run(cmd, check=True)
     finally:
-        side.join()
+        if side.ident is not None:
+            side.join()
     if failed:
         raise failed[0]
     return LIB
