@@ -59,10 +59,10 @@ def build_binding():
     root = os.path.dirname(torch.__file__)
     inc, libs = os.path.join(root, "include"), os.path.join(root, "lib")
     cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-Wextra",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           f"-I{INCLUDE}", f"-I{inc}", f"-I{os.path.join(inc, 'torch', 'csrc', 'api', 'include')}",
-           f"-I{sysconfig.get_path('include')}", f"-I{os.path.join(cuda, 'include')}",
+           f"-I{INCLUDE}", "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_path("include"), "-isystem", os.path.join(cuda, "include"),
            "-o", BINDING, BINDING_SRC, f"-L{libs}", f"-Wl,-rpath,{libs}",
            "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
     subprocess.run(cmd, check=True)
