@@ -231,6 +231,7 @@ struct WindowCfg : Cfg<HD> {
 // launch with 168 registers; the third warpgroup keeps 72 and the others take 216 each, which
 // holds a row's 128 scores and the loop around them: 2 * 216 + 72 = 3 * 168.
 constexpr int kWindowThreads = 384;
+constexpr float kHugeLog2 = 16777216.0f;   // 2^24: scores from here on are rounded before they are referred
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 216, kOtherRegs = 72;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kLaunchRegs, "registers given back cover those taken");
 
@@ -676,14 +677,23 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
                     }
                     // scale > 0; with bf16 a sum of weights stays below 1, so that O, which is a sum with
                     // weights until it is divided, stays within the largest V and fp32
-                    const float m_blk = fmaxf(mx0, mx1) * p.scale + (kBf16 ? p.shift : 0.0f);
+                    const float m_blk = __fadd_rn(__fmul_rn(fmaxf(mx0, mx1), p.scale), kBf16 ? p.shift : 0.0f);
                     // move the reference only when the maximum grew by more than kRescaleLog2;
                     // -infinity until the row has seen a key
                     const bool move = m_blk > m + kRescaleLog2;
                     const float m_new = move ? m_blk : m;
                     const float alpha = move ? fast_exp2(m - m_new) : 1.0f;   // 0 at the first block
                     const float m_ref = m_new == -INFINITY ? 0.0f : m_new;
-                    const float2 sc2 = make_float2(p.scale, p.scale), nm2 = make_float2(-m_ref, -m_ref);
+                    // The products below take score * scale unrounded, the reference is rounded: from 2^24 on
+                    // their difference at a row's largest key would be half a unit and more, at 2^31 an overflow.
+                    float sc = p.scale;
+                    if (__any_sync(0xffffffffu, fabsf(m_ref) >= kHugeLog2)) {
+#pragma unroll
+                        for (int i = 0; i < kKeys; ++i)
+                            v[i] = __float_as_uint(__fmul_rn(__uint_as_float(v[i]), p.scale));
+                        sc = 1.0f;
+                    }
+                    const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-m_ref, -m_ref);
                     float2 sa = make_float2(0.0f, 0.0f), sb = make_float2(0.0f, 0.0f);
 #pragma unroll
                     for (int c0 = 0; c0 < kKeys; c0 += 32) {
