@@ -232,6 +232,28 @@ def test_cache_attention_zero_pages():
         _cache_check(_f64(out)[0], q64[0], c64, order, 16 * len(order) - 3, 64, "bf16")
 
 
+@pytest.mark.parametrize("scale", [2.0 ** 10, 2.0 ** 30])
+def test_cache_attention_huge_scores_and_small_scales(scale):
+    """Scores up to 2^40 (one token takes all the weight) and V scales around 2^-60."""
+    import torch
+    rng = np.random.default_rng(54)
+    cache, c64 = _cache(rng, 40, 1, 64, 64, garbage=False)
+    for which, e in ((2, 2), (3, -60)):
+        s = 2.0 ** (e + rng.integers(-2, 3, (40, 1)))
+        c64[which][...] = s
+        cache[which].copy_(torch.from_numpy(s.astype(np.float32)))
+    q, q64 = _rand(rng, (1, 1, 3, 64), "bf16", scale)
+    order = list(range(40))
+    out = gr.kv_cache_attention(q, cache, _i32([order]), _i32([2550]))
+    k = (c64[0] * c64[2][..., None, None]).transpose(0, 2, 1, 3).reshape(-1, 64)[:2550]
+    v = (c64[1] * c64[3][..., None, None]).transpose(0, 2, 1, 3).reshape(-1, 64)[:2550]
+    for h in range(3):
+        x = np.sort(k @ q64[0, 0, h])
+        assert (x[-1] - x[-2]) / 8 > 100
+        want = v[np.argmax(k @ q64[0, 0, h])]
+        assert np.array_equal(_f64(out)[0, 0, h], want)
+
+
 @pytest.mark.parametrize("weights", [False, True])
 @pytest.mark.parametrize("page,tokens,n,window,sinks", [
     (16, 1, 300, 100, 0), (16, 3, 300, 100, 20), (32, 1, 1000, 400, 4), (16, 1, 70, 1, 1), (32, 2, 500, 33, 65)])

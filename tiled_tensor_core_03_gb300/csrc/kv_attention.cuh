@@ -47,9 +47,12 @@
 //    rounding).  V's scale is folded into P, and O has a reference of its own, r above m and moved
 //    likewise: P = 2^(7 - r) * vs * weight stays below 2^15 and normal down to 2^-21 of the row's
 //    largest weight times scale, whatever scales come in what order (but for weights below 2^-111 under
-//    scales 2^111 above the others).  m and r are whole, so that factors and moves are exact
-//    for scales that are powers of two.  (With P relative to the largest scale met so far a
+//    scales 2^111 above the others).  (With P relative to the largest scale met so far a
 //    page with the weight but a scale 2^30 below another's lost its bits.)
+//    m is a score before its factor log2(e) / sqrt(D), which multiplies differences alone: with scales that
+//    are powers of two the largest score's difference is then 0 at any size.  (Multiplied first, the
+//    reference is rounded and the fused product is not: off by half a unit at 2^24, an overflow at 2^31.  The
+//    multiplication more costs 0 to 1%.)
 #pragma once
 
 #include "kv_cache.cuh"
@@ -306,7 +309,7 @@ __device__ __forceinline__ void write_row(const AttnParams &p, int b, int h, int
             make_uint2(pack_out<kBf16>(y[j] * inv * f * f, y[j + 1] * inv * f * f),
                        pack_out<kBf16>(y[j + 2] * inv * f * f, y[j + 3] * inv * f * f));
     if (kScores && d0 == 0)
-        p.lse[((int64_t)b * p.pool.kv_heads + h) * p.rows + row] = sum == 0.0f ? INFINITY : ref + log2f(sum);
+        p.lse[((int64_t)b * p.pool.kv_heads + h) * p.rows + row] = sum == 0.0f ? INFINITY : ref * p.scale_log2 + log2f(sum);
 }
 
 // Count a part of a segment of n + 1: the number counted before; wraps to 0 with the last.
@@ -522,7 +525,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
             const int row0 = tile * kRows;
 
             // the query rows as fragments (lane g's row of each group of 8), and what the lane
-            // knows of the rows of its scores, 2c and 2c + 1: position (-1: sees nothing), scale
+            // knows of the rows of its scores, 2c and 2c + 1: position (-1: sees nothing), scale (a power of two)
             uint32_t q[kN][D / 8];
             int pos[kN][2];
             float row_scale[kN][2];
@@ -537,9 +540,9 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
                 for (int e = 0; e < 2; ++e) {
                     const int row = row0 + 8 * t + 2 * c + e;
                     pos[t][e] = row < p.rows ? n - p.tokens + row / p.group : -1;
-                    row_scale[t][e] = p.scale_log2;
+                    row_scale[t][e] = 1.0f;
                     if constexpr (kBf16)
-                        row_scale[t][e] *= __shfl_sync(0xffffffffu, back, 4 * (2 * c + e));
+                        row_scale[t][e] = __shfl_sync(0xffffffffu, back, 4 * (2 * c + e));
                 }
             }
             const int pos_min = n - p.tokens + row0 / p.group;
@@ -623,12 +626,12 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
                             for (int i = 0; i < 4; ++i)
                                 if (pos[t][i & 1] >= 0 && (i < 2 ? ta : tb) < n)
                                     dst[(i >> 1) * 8 * p.rows + (i & 1)] =
-                                        acc[t][i] * (sc.x * row_scale[t][i & 1]);
+                                        acc[t][i] * (sc.x * row_scale[t][i & 1]) * p.scale_log2;
                         }
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int e = i & 1;
-                            x[t][i] = fmaf(acc[t][i], sc.x * row_scale[t][e], -m[t][e]);
+                            x[t][i] = fmaf(acc[t][i], sc.x * row_scale[t][e], -m[t][e]) * p.scale_log2;
                             if (masked && !sees(i < 2 ? ta : tb, pos[t][e], p.window, p.sinks))
                                 x[t][i] = acc[t][i] = -INFINITY;
                         }
@@ -649,13 +652,13 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
                                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                                const float to = fmaxf(m[t][e], rintf(top));
-                                const float a = to > m[t][e] ? exp2_fast(m[t][e] - to) : 1.0f;   // 0 at first
+                                const float to = fmaxf(m[t][e], top);
+                                const float a = to > m[t][e] ? exp2_fast((m[t][e] - to) * p.scale_log2) : 1.0f;   // 0 at first
                                 l[t][e] *= a;
                                 // o's old reference and this unit's, from the new m
                                 const float ref = to == -INFINITY ? 0.0f : to;
-                                const float r0 = m[t][e] - ref + (kPLog2 - md[t][e]);
-                                const float r1 = fmaxf(r0, rintf(top - ref + sc.y));
+                                const float r0 = (m[t][e] - ref) * p.scale_log2 + (kPLog2 - md[t][e]);
+                                const float r1 = fmaxf(r0, rintf((top - ref) * p.scale_log2 + sc.y));
                                 const float ao = r1 > r0 ? exp2_fast(r0 - r1) : 1.0f;
 #pragma unroll
                                 for (int j = 0; j < D / 16; ++j) {
@@ -669,7 +672,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
                                 for (int i = 0; i < 2; ++i)
                                     x[t][2 * i + e] = acc[t][2 * i + e] == -INFINITY
                                                           ? -INFINITY
-                                                          : fmaf(acc[t][2 * i + e], f, -ref);
+                                                          : fmaf(acc[t][2 * i + e], f, -ref) * p.scale_log2;
                             }
                     }
                     // ---- P^T as the second product's B operand: {rows 2c, 2c + 1} of a token to
@@ -805,14 +808,14 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
                     top = fmaxf(top, stat_m[w * kRows + r]);
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w)
-                    top_r = fmaxf(top_r, less(stat_m[w * kRows + r], top) + stat_r[w * kRows + r]);
+                    top_r = fmaxf(top_r, less(stat_m[w * kRows + r], top) * p.scale_log2 + stat_r[w * kRows + r]);
                 float y[kF];
 #pragma unroll
                 for (int j = 0; j < kF; ++j)
                     y[j] = 0.0f;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
-                    const float below = less(stat_m[w * kRows + r], top);
+                    const float below = less(stat_m[w * kRows + r], top) * p.scale_log2;
                     const float fv = exp2_fast(less(below + stat_r[w * kRows + r], top_r));
                     sum += exp2_fast(below) * stat_l[w * kRows + r];
                     const float4 *src = reinterpret_cast<const float4 *>(
@@ -898,12 +901,12 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
 #pragma unroll
                     for (int k = 0; k < kAtOnce; ++k)
                         top = fmaxf(top, ml[k].x);
-                    const float r0 = less(ref, top) + ref_r;   // (-infinity at first, as in ref)
+                    const float r0 = less(ref, top) * p.scale_log2 + ref_r;   // (-infinity at first, as in ref)
                     float r1 = r0;
 #pragma unroll
                     for (int k = 0; k < kAtOnce; ++k)
-                        r1 = fmaxf(r1, less(ml[k].x, top) + ml[k].z);
-                    sum *= exp2_fast(less(ref, top));
+                        r1 = fmaxf(r1, less(ml[k].x, top) * p.scale_log2 + ml[k].z);
+                    sum *= exp2_fast(less(ref, top) * p.scale_log2);
                     const float fy = exp2_fast(less(r0, r1));
 #pragma unroll
                     for (int j = 0; j < kF; ++j)
@@ -914,7 +917,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, kN>::kBlocksPerSm)
                     for (int k = 0; k < kAtOnce; ++k) {
                         if (c + k > c1)
                             break;
-                        const float below = less(ml[k].x, ref);
+                        const float below = less(ml[k].x, ref) * p.scale_log2;
                         sum += exp2_fast(below) * ml[k].y;
                         const float f = exp2_fast(less(below + ml[k].z, ref_r));
 #pragma unroll
