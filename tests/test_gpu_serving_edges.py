@@ -395,3 +395,15 @@ def test_cache_attention_on_streams_of_one_handle():
         assert torch.equal(o, want[0])
     for h in handles:
         torch.cuda.cudart().cudaStreamDestroy(h.value)
+
+
+def test_no_memory_is_torchs_error():
+    """Scores of 2^20 tokens and 2^17 rows for the weights would take 512 GiB."""
+    import torch
+    cache = gr.KVCache.empty(1, 1, 64, 128)
+    q = torch.zeros((1, 2048, 64, 64), dtype=torch.float16, device="cuda")
+    pages = torch.zeros((1, 8192), dtype=torch.int32, device="cuda")
+    weights = torch.zeros((1, 1, 2 ** 20), device="cuda")
+    with pytest.raises(torch.OutOfMemoryError):
+        gr.kv_cache_attention(q, cache, pages, _i32([1]), weights=weights)
+    assert not weights.any()

@@ -33,7 +33,7 @@ decltype(&kv_cache_attention_x16_workspace_bytes) f_workspace_bytes;
 decltype(&kv_cache_evict_e4m3) f_evict;
 decltype(&gemm_relu_stream_capturing) f_capturing;
 decltype(&gemm_relu_stream_id) f_stream_id;
-PyObject *g_error;   // GemmReluError
+PyObject *g_error, *g_no_memory;   // GemmReluError, torch.OutOfMemoryError
 
 struct Refusal {
     PyObject *type;
@@ -361,6 +361,8 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     } catch (const Raised &) {
     } catch (const Refusal &r) {
         PyErr_SetString(r.type, r.what.c_str());
+    } catch (const c10::OutOfMemoryError &e) {   // what a caller who sheds load catches
+        PyErr_SetString(g_no_memory, e.what_without_backtrace());
     } catch (const std::bad_alloc &) {
         PyErr_NoMemory();
     } catch (const std::exception &e) {
@@ -371,11 +373,11 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     return nullptr;
 }
 
-// bind(GemmReluError, addresses of the seven library functions in the order below)
+// bind(GemmReluError, torch.OutOfMemoryError, addresses of the seven library functions in the order below)
 PyObject *bind(PyObject *, PyObject *args) {
-    PyObject *error;
+    PyObject *error, *no_memory;
     unsigned long long f[7];
-    if (!PyArg_ParseTuple(args, "OKKKKKKK", &error, &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6]))
+    if (!PyArg_ParseTuple(args, "OOKKKKKKK", &error, &no_memory, &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6]))
         return nullptr;
     f_window = reinterpret_cast<decltype(f_window)>((uintptr_t)f[0]);
     f_append = reinterpret_cast<decltype(f_append)>((uintptr_t)f[1]);
@@ -385,7 +387,9 @@ PyObject *bind(PyObject *, PyObject *args) {
     f_capturing = reinterpret_cast<decltype(f_capturing)>((uintptr_t)f[5]);
     f_stream_id = reinterpret_cast<decltype(f_stream_id)>((uintptr_t)f[6]);
     Py_INCREF(error);
+    Py_INCREF(no_memory);
     g_error = error;
+    g_no_memory = no_memory;
     Py_RETURN_NONE;
 }
 

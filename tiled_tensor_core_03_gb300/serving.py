@@ -23,7 +23,7 @@ except ImportError as e:
 _HEAD_DIMS = (64, 128)
 _PAGES = (16, 32, 64, 128)
 
-_serving.bind(GemmReluError, *(
+_serving.bind(GemmReluError, torch.OutOfMemoryError, *(
     ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value
     for name in ("flash_attention_window_x16", "kv_cache_append_x16", "kv_cache_attention_x16",
                  "kv_cache_attention_x16_workspace_bytes", "kv_cache_evict_e4m3",
