@@ -31,17 +31,18 @@
 //    would still be NaN.  A CTA that finds a row with finite weights but without a finite result
 //    (an element of some V is not finite) therefore walks over its items a second time.  There, in
 //    the blocks that some row sees in part, such elements of V become 0 in shared memory and are
-//    added by hand to the rows that see them.  That costs about what the first walk did and some
-//    microseconds for each of those few blocks, whatever the rows' lengths are, so that no
-//    wait inside the pipeline gets long.
+//    added by hand to the rows that see them.  That costs about what the first walk did and 3 us for
+//    each of those few blocks (0.1 ms where all of V is not finite), whatever the rows' lengths are,
+//    so that no wait inside the pipeline gets long: 4 x 4096 tokens, window 1024, one infinity in V 555 us.
 //
 // Bound: the tensor cores' 4 d flops a pair; blocks are 128 keys wide, so a window of W keys
 // costs up to W + 255 keys and the sinks one block.  A tile's turn is a chain, S, softmax, P V, next
 // S over the same TMEM columns: about 3300 cycles a block with two tiles in turn, for 2048 cycles
-// of products.  Measured, 32 query heads on 8 of 128: 16384 tokens, window 4096, 691 to 702 us (the power
-// limit moves it), 1.39 to 1.41 PFLOP/s of visible pairs, 0.75 of the measured burst; 4 x 4096 tokens,
-// window 1024, 223 us, 1.08 PFLOP/s (9.3 blocks an item for 8 of keys, and 2500 cycles for an
-// item's output); a prompt of 203 tokens 6.9 us, launch and latency.
+// of products (window 1024: tensor pipe active in 52% of the cycles).  Measured, 32 query heads on 8 of
+// 128: 16384 tokens, window 4096, 685 to 702 us (the power limit moves it), 1.39 to 1.42 PFLOP/s of visible
+// pairs, 0.71 to 0.73 of the measured burst of 1951.5 TFLOP/s; 4 x 4096 tokens, window 1024, 223 us,
+// 1.08 PFLOP/s (9.3 blocks an item for 8 of keys, and 2500 cycles for an item's output); a prompt of 203
+// tokens 6.9 us, launch and latency.
 // Not kept: 2^x by range reduction and a polynomial for a share of the pairs (a quarter: 262 -> 306 us;
 // exponentials are not the bound on this GPU), two threads a row on 16 softmax warps (326 us and more:
 // registers), separate K and V rings (272 us), 192 or 168 registers for the softmax (285 us).

@@ -8,10 +8,10 @@
 //
 // What bounds it: every visible token's 2 D bytes are read once per row tile and
 // used for 4 D flops a row, so one tile is a stream from HBM: 64 sequences of up to 32768
-// tokens, 8 heads of 128, 3.1 GB in 461 us, 6.7 TB/s (0.99 of a measured copy).  About 13 us of a
+// tokens, 8 heads of 128, 3.1 GB in 468 us, 6.6 TB/s (0.98 of a measured copy).  About 13 us of a
 // call are fixed: 3 to the first bytes (lengths, page numbers, pages, one after the other), 5 between
 // the first and the last block's end, 4 for counting and joining; so 32 sequences of up to 4096
-// tokens, 183 MB, take 41 us, and one sequence of 1000 tokens 9.5 us.  More row tiles are bound by
+// tokens, 183 MB, take 42 us, and one sequence of 1000 tokens 9.7 us.  More row tiles are bound by
 // the chain of conversions and products of a unit: 25 us for every further 8 rows at those 183 MB.  The
 // kernel is built around the stream:
 //
@@ -21,7 +21,8 @@
 //    tiles in further passes): they read the same units at about the same time, from
 //    HBM once, and their strips of the scores meet in L2.  With the tiles one after the other in one
 //    block's range 32 sequences of up to 4096 tokens, 8 heads of 128, took 66.3 us, not 64.3, with 16 rows,
-//    222 and 216 with 64, and with weights 202 and 165 with 28; one tile pays 0.3 us of 41.
+//    222 and 216 with 64, and with weights 202 and 165 with 28; one tile pays 0.3 us of 41.  (Now 65.4,
+//    217.6 and 170: references of their own for O, and scores before their factor.)
 //    A block finishes what lies
 //    inside its range; a (sequence, head, row tile) that is cut leaves one fp32
 //    partial (O, m, l) per block in the workspace, and the block that comes last joins
@@ -70,8 +71,8 @@ constexpr float kPLog2 = 7.0f;       // see above
 
 // kN groups of 8 query rows a tile (two for heads of 64 only).  Two blocks an SM (168 registers a
 // thread); three (128) for 64 elements and one group.  Measured, one group: 32 sequences of up to
-// 4096 tokens, 8 heads of 128, 41.1 us with two blocks and 44.0 with three; 16 sequences of up
-// to 8192, window 2000, 16 heads of 64, 4 tokens each, 30.8 and 26.0 us.
+// 4096 tokens, 8 heads of 128, 42.2 us with two blocks and 45.3 with three; 16 sequences of up
+// to 8192, window 2000, 16 heads of 64, 4 tokens each, 33.2 and 27.7 us.
 template <int D, int kN>
 struct AttnCfg {
     static constexpr int kRows = 8 * kN;

@@ -359,10 +359,10 @@ int kv_cache_attention_x16(const kv_cache_pool *cache, const void *q, int dtype,
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool bf16 = dtype == GEMMRELU_BF16;
     // Up to 8 rows fit one group of 8.  Beyond, two groups a tile share the conversion of K and V, which
-    // pays for heads of 64 (32 sequences of up to 4096 tokens, 8 K/V heads: 16 rows 41.9 us with two
-    // groups, 44.8 with a tile per group; 64 rows 124 and 143) but not for heads of 128, whose
+    // pays for heads of 64 (32 sequences of up to 4096 tokens, 8 K/V heads: 16 rows 42.5 us with two
+    // groups, 46.5 with a tile per group; 64 rows 131 and 147) but not for heads of 128, whose
     // accumulators and query fragments spill at 168 registers (16 rows 76 to 107 us with two
-    // groups, 66.4 with a tile per group; 64 rows 233 to 365 and 222).
+    // groups, 65.4 with a tile per group; 64 rows 233 to 365 and 218).
     if (cache->head_dim == 128)
         return launch_kv_attention_as<128, 1>(bf16, mK, mV, p, s, ds->sms, ds->attr_kv);
     return rows <= 8 ? launch_kv_attention_as<64, 1>(bf16, mK, mV, p, s, ds->sms, ds->attr_kv)

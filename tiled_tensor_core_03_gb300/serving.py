@@ -51,8 +51,9 @@ class KVCache(NamedTuple):
 
 def flash_attention_window(q, k, v, window, sinks=0, out=None, stream=None):
     """softmax(q k^T / sqrt(d)) v of a prompt with a sliding window: q [batch, q_seq, q_heads, d],
-    k and v [batch, kv_seq, kv_heads, d], fp16 or bf16, any strides between heads, d = 64 or
-    128; query head h reads K/V head h // (q_heads // kv_heads).
+    k and v [batch, kv_seq, kv_heads, d], fp16 or bf16, d = 64 or 128; query head h reads K/V
+    head h // (q_heads // kv_heads).  Strides between heads are positive multiples of 8 elements:
+    an expanded axis (stride 0) is refused with GemmReluError.
 
     Query i stands at p = i + kv_seq - q_seq and sees the keys j <= p; with a window > 0
     only those with j > p - window or j < sinks.  A query that sees nothing gets 0."""
@@ -63,8 +64,8 @@ def flash_attention_window(q, k, v, window, sinks=0, out=None, stream=None):
 
 
 def kv_cache_append(cache, k, v, pages, lengths, counts=None, stream=None):
-    """Write new tokens' k and v (fp16 or bf16 [batch, tokens, kv_heads, head_dim], any
-    strides between heads) into their sequences' pages.
+    """Write new tokens' k and v (fp16 or bf16 [batch, tokens, kv_heads, head_dim], strides
+    between heads any multiples of 8, 0 among them) into their sequences' pages.
 
     pages int32 [batch, max_pages]; lengths int32 [batch] INCLUDES the new tokens;
     counts int32 [batch] says how many of the `tokens` rows are new ones (default: all):
@@ -84,16 +85,17 @@ def kv_cache_attention_workspace(q, cache, weights=None):
 def kv_cache_attention(q, cache, pages, lengths, window=0, sinks=0, weights=None, out=None,
                        workspace=None, stream=None):
     """softmax(q K^T / sqrt(head_dim)) V of the last tokens of every sequence over the cache:
-    q fp16 or bf16 [batch, tokens, q_heads, head_dim] (any strides between heads), query
-    head h reading K/V head h // (q_heads // kv_heads).
+    q fp16 or bf16 [batch, tokens, q_heads, head_dim] (strides between heads any
+    multiples of 8), query head h reading K/V head h // (q_heads // kv_heads).
 
     lengths int32 [batch] includes these tokens; token i sees the tokens t <= p = length -
-    tokens + i, with a window > 0 only those with t > p - window or t < sinks.  With
+    tokens + i, with a window > 0 only those with t > p - window or t < sinks (pages that
+    no query sees a token of may have been given up: their numbers are not read).  With
     `weights` (fp32 [batch, kv_heads, at least max_pages * page]) each token's softmax
     weights, summed over the query tokens and heads of its group, are added to it.
 
-    Without a `workspace` the call uses one that is kept per stream (up to 64 MB), or its
-    own where it needs more or is being captured."""
+    Without a `workspace` the call uses one that is kept per stream (up to 64 MB, for up to 64
+    streams), or its own where it needs more or is being captured."""
     if stream is not None:
         with torch.cuda.stream(stream):   # what is allocated belongs to it
             return _serving.attention(cache, q, pages, lengths, window, sinks, weights, out,
