@@ -155,6 +155,26 @@ def test_window_huge_scores(window, sinks, dtype, scale):
                 assert (np.abs(got[i, h] - want) <= ((1 + half) ** 2 - 1) * np.abs(want)).all(), (i, h)
     assert clear > n
 
+
+def test_window_waits_that_run_out_beside_values_that_are_not_finite():
+    """A CTA that never gets its data gives up while others go over their items again: the call ends with
+    a timeout, the next one is right."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(46)
+    q, k, v = (torch.randn(2, 900, h, 64, device="cuda", dtype=torch.bfloat16, generator=g) for h in (8, 4, 4))
+    want = gr.flash_attention_window(q, k, v, 100, 4)
+    dirty = v.clone()
+    dirty[:, 7::50] = float("nan")
+    for limit in (20_000_000, 1_000_000):
+        gr.gemm_relu_debug_set(1, limit)
+        try:
+            gr.flash_attention_window(q, k, dirty, 100, 4)
+            assert gr.status() == gr.ERR_TIMEOUT
+        finally:
+            gr.gemm_relu_debug_set(0, 0)
+        assert torch.equal(gr.flash_attention_window(q, k, v, 100, 4), want)
+        assert gr.status() == gr.OK
+
 # ---------------------------------------------------------------- attention over the cache
 
 

@@ -416,7 +416,11 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
         tc_fence_before_sync();
         named_bar_sync(1, kWindowThreads);
         tc_fence_after_sync();
-        return pass == 0 && *redo_flag != 0u && *abort_flag == 0u;
+        if (pass != 0 || *redo_flag == 0u)
+            return false;
+        const bool go = *abort_flag == 0u;
+        named_bar_sync(1, kWindowThreads);   // all have read it before a wait of the second walk may set it
+        return go;
     };
 
     if (warp >= kProducerWarp) {
