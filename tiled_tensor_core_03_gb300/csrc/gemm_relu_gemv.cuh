@@ -114,7 +114,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
-    cluster_arrive();  // this CTA runs: the others may store into its shared memory
     const int n0 = (int)(blockIdx.x / (unsigned)csize) * kCols;
     const int s0 = (int)(((int64_t)rank * p.num_stages) / csize);
     const int s1 = (int)(((int64_t)(rank + 1) * p.num_stages) / csize);
@@ -169,6 +168,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int j = 0; feeding && j < kStages - 1 && j < n_st; ++j)
             feeding = issue(j);
 
+    // this CTA runs: the others may store into its shared memory (relaxed: 19.1 us with a release
+    // here at 1 x 8192 x 8192, 18.7 without)
+    cluster_arrive_relaxed();
     float2 acc[MV][4];  // columns 8l + 2j, 8l + 2j + 1
 #pragma unroll
     for (int m = 0; m < MV; ++m)

@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1) kv_evict_select_kernel(cons
     __shared__ int shared[4];   // list length, k-th key, keys above it; totals
     const int cluster = p.cluster, rank = cluster > 1 ? (int)cluster_ctarank() : 0;
     if (cluster > 1)
-        cluster_arrive();   // this block runs: the others may store into its shared memory
+        cluster_arrive_relaxed();   // this block runs: the others may store into its shared memory
     pdl_launch_dependents();
     pdl_wait_primary();
     const int64_t bh = blockIdx.x / cluster;
