@@ -77,6 +77,23 @@ int flash_attention_window_x16(const void *Q, const void *K, const void *V, void
                                int64_t sinks, void *stream);
 
 /*
+ * flash_attention_cross_x16 -- attention to an encoder's states: O = softmax(Q K^T / sqrt(d)) V,
+ * where query i of sequence b sees the keys j < lengths[b], whatever i is.
+ *
+ * Arguments, types, numerics and errors are flash_attention_window_x16's, but:
+ * lengths    : DEVICE int32 [batch], each in [0, kv_seq], or NULL: all kv_seq.  A
+ *              sequence without keys gets 0; a number out of range counts as 0, and
+ *              gemm_relu_status reports GEMMRELU_ERR_PAGE.
+ * q_heads    : at most 128 times kv_heads.
+ * What stands behind a sequence's keys in K and V, NaN and infinities among it, reaches no query.
+ */
+int flash_attention_cross_x16(const void *Q, const void *K, const void *V, void *O, int dtype,
+                              int64_t batch, int64_t q_seq, int64_t kv_seq, int64_t q_heads,
+                              int64_t kv_heads, int64_t head_dim, const int64_t *q_strides,
+                              const int64_t *k_strides, const int64_t *v_strides,
+                              const int32_t *lengths, void *stream);
+
+/*
  * Host-only test hook: the blocks of 128 keys that flash_attention_window_x16 visits
  * for rows at positions first .. last: [0, out[0]) and [out[1], out[2]).
  */

@@ -47,6 +47,7 @@ extern "C" {
 #endif
 
 #define GEMMRELU_KV_COUNTER_BYTES 4096   /* of kv_cache_attention_x16's workspace */
+#define GEMMRELU_RAGGED_COUNTER_BYTES 8192   /* of kv_cache_attention_ragged_x16's */
 
 typedef struct {
     void *k, *v;               /* e4m3 [num_pages][kv_heads][page][head_dim], 16-byte aligned */
@@ -122,6 +123,54 @@ int kv_cache_attention_x16(const kv_cache_pool *cache, const void *q, int dtype,
                            const int32_t *pages, int64_t max_pages, const int32_t *lengths,
                            int64_t window, int64_t sinks, float *weights, int64_t weights_width,
                            void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * kv_cache_attention_ragged_x16_workspace_bytes -- bytes of device workspace that
+ * kv_cache_attention_ragged_x16 needs on the current device for heads of
+ * head_dim elements, whatever the call's other sizes.  0 for invalid
+ * arguments, or when no CUDA device is available.
+ */
+size_t kv_cache_attention_ragged_x16_workspace_bytes(int64_t head_dim);
+
+/*
+ * kv_cache_attention_ragged_x16 -- kv_cache_attention_x16 for sequences that bring different
+ * numbers of tokens (chunks of prompts, drafts and single tokens in one call):
+ * each query token attends over its sequence's pages.
+ *
+ * q        : [rows][q_heads][head_dim] of `dtype`, q_strides its {token, head},
+ *            multiples of 8 (0 among them); q_heads a multiple of kv_heads.
+ * out      : [rows][q_heads][head_dim] of `dtype`, contiguous, 16-byte aligned.
+ * starts   : int32 [batch + 1], ascending: sequence b's query tokens are the rows
+ *            starts[b] .. starts[b + 1] - 1 (none where they are equal).  Rows of no
+ *            sequence keep what they hold in `out`.
+ * lengths  : int32 [batch], each sequence's length including its query tokens, which
+ *            are its last ones: row starts[b] + i has position lengths[b] -
+ *            (starts[b + 1] - starts[b]) + i and sees what kv_cache_attention_x16 says.
+ *            Rows that see nothing become 0.
+ * workspace: at least kv_cache_attention_ragged_x16_workspace_bytes(head_dim), 16-byte aligned.
+ *            Its first GEMMRELU_RAGGED_COUNTER_BYTES must be 0 before its first
+ *            call; every call leaves them 0, whatever its sizes.  Calls that may
+ *            overlap on the GPU need different workspaces.
+ *
+ * batch is at most 16384, rows at most 2^24, rows * q_heads at most 2^30; sizes whose blocks of 128 tokens,
+ * (rows * group / 256 + batch) * kv_heads * (max_pages * page / 128 + 1), reach 2^31 are
+ * refused.  A sequence whose rows are not inside [0, rows) or descend is skipped and
+ * reported as GEMMRELU_ERR_PAGE, and so is the whole call where rows that several sequences claim
+ * make that many blocks.
+ *
+ * Scores, softmax statistics and sums are fp32.  For the products bf16 queries become
+ * fp16, scaled by a power of two per row (exact but for elements below 2^-29 of the row's
+ * largest), and a softmax weight times its page's scale is rounded to fp16, relative to the
+ * largest such product of the row, as in kv_cache_attention_x16.  A weight whose product
+ * with its page's V scale is below 2^-132 of the row's largest is left out of the sum of
+ * weights.  NaN of V reach exactly the rows that see them.  The order of all sums is
+ * fixed: the same call gives the same bits.
+ */
+int kv_cache_attention_ragged_x16(const kv_cache_pool *cache, const void *q, int dtype, int64_t rows,
+                                  int64_t q_heads, const int64_t *q_strides, void *out,
+                                  int64_t batch, const int32_t *starts, const int32_t *pages,
+                                  int64_t max_pages, const int32_t *lengths, int64_t window,
+                                  int64_t sinks, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * kv_cache_evict_e4m3 -- keep `budget` tokens of every sequence and head, by

@@ -27,6 +27,7 @@ ERR_PAGE = 8
 NOALLOC_SCRATCH_BYTES = 8 << 20
 F16, BF16 = 0, 1   # types of 16-bit tensors
 KV_COUNTER_BYTES = 4096   # zeroed once in kv_cache_attention's workspaces
+RAGGED_COUNTER_BYTES = 8192   # and in kv_cache_attention_ragged's
 
 PATH_NONE, PATH_TMA, PATH_LSU = 0, 1, 2
 (KERNEL_PAIR, KERNEL_ONE_CTA_256, KERNEL_ONE_CTA_128, KERNEL_PREDICATED, KERNEL_GEMV,
@@ -47,6 +48,12 @@ class KVCachePool(ctypes.Structure):
                 ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
                 ("kv_heads", ctypes.c_int64), ("page", ctypes.c_int64),
                 ("head_dim", ctypes.c_int64)]
+
+
+class RotaryTensor(ctypes.Structure):
+    """rotary_tensor of include/rotary.h."""
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("heads", ctypes.c_int64),
+                ("x_strides", ctypes.c_int64 * 3), ("y_strides", ctypes.c_int64 * 3)]
 
 
 class GemmReluError(RuntimeError):
@@ -101,6 +108,8 @@ def lib():
         L.flash_attention_window_x16.argtypes = [vp, vp, vp, vp, i32] + [i64] * 6 + [vp] * 3 + \
             [i64, i64, vp]
         L.flash_attention_window_x16.restype = i32
+        L.flash_attention_cross_x16.argtypes = [vp, vp, vp, vp, i32] + [i64] * 6 + [vp] * 5
+        L.flash_attention_cross_x16.restype = i32
         L.flash_attention_window_debug_blocks.argtypes = [i64] * 4 + [vp]
         L.flash_attention_window_debug_blocks.restype = i32
         L.kv_cache_debug_span.argtypes = [i64] * 4 + [vp]
@@ -114,6 +123,14 @@ def lib():
         L.kv_cache_attention_x16.argtypes = [vp, vp, i32, i64, i64, i64, vp, vp, vp, i64, vp, i64,
                                              i64, vp, i64, vp, sz, vp]
         L.kv_cache_attention_x16.restype = i32
+        L.kv_cache_attention_ragged_x16_workspace_bytes.argtypes = [i64]
+        L.kv_cache_attention_ragged_x16_workspace_bytes.restype = sz
+        L.kv_cache_attention_ragged_x16.argtypes = [vp, vp, i32, i64, i64, vp, vp, i64, vp, vp, i64, vp,
+                                                    i64, i64, vp, sz, vp]
+        L.kv_cache_attention_ragged_x16.restype = i32
+        L.rotary_x16.argtypes = [vp, vp, i32, i64, i64, i64, i64, i32, vp, i32, vp, i32,
+                                 ctypes.c_double, i32, vp]
+        L.rotary_x16.restype = i32
         L.kv_cache_evict_e4m3.argtypes = [vp, vp, i64, vp, i64, vp, i64, i64, i64, i64, vp, vp,
                                           i64, vp, vp, vp, vp]
         L.kv_cache_evict_e4m3.restype = i32
@@ -196,6 +213,36 @@ def kv_cache_attention_x16(cache, q, dtype, batch, tokens, q_heads, q_strides, o
     return lib().kv_cache_attention_x16(ctypes.byref(cache), q, dtype, batch, tokens, q_heads,
                                         q_strides, out, pages, max_pages, lengths, window, sinks,
                                         weights, weights_width, workspace, workspace_bytes, stream)
+
+
+def flash_attention_cross_x16(Q, K, V, O, dtype, batch, q_seq, kv_seq, q_heads, kv_heads,
+                              head_dim, q_strides, k_strides, v_strides, lengths, stream=None):
+    """*_strides: ctypes arrays of three int64 {sequence, token, head}."""
+    return lib().flash_attention_cross_x16(Q, K, V, O, dtype, batch, q_seq, kv_seq, q_heads,
+                                           kv_heads, head_dim, q_strides, k_strides, v_strides,
+                                           lengths, stream)
+
+
+def kv_cache_attention_ragged_x16_workspace_bytes(head_dim):
+    return lib().kv_cache_attention_ragged_x16_workspace_bytes(head_dim)
+
+
+def kv_cache_attention_ragged_x16(cache, q, dtype, rows, q_heads, q_strides, out, batch, starts,
+                                  pages, max_pages, lengths, window, sinks, workspace,
+                                  workspace_bytes, stream=None):
+    """cache: a KVCachePool; q_strides: a ctypes array of two int64 {token, head}."""
+    return lib().kv_cache_attention_ragged_x16(ctypes.byref(cache), q, dtype, rows, q_heads,
+                                               q_strides, out, batch, starts, pages, max_pages,
+                                               lengths, window, sinks, workspace, workspace_bytes,
+                                               stream)
+
+
+def rotary_x16(q, k, dtype, batch, tokens, head_dim, rot, interleaved, positions, pos_type,
+               inv_freq, freq_type, amplitude=1.0, inverse=False, stream=None):
+    """q and k: RotaryTensors."""
+    return lib().rotary_x16(ctypes.byref(q), ctypes.byref(k), dtype, batch, tokens, head_dim, rot,
+                            int(interleaved), positions, pos_type, inv_freq, freq_type, amplitude,
+                            int(inverse), stream)
 
 
 def kv_cache_evict_e4m3(cache, weights, weights_width, pages, max_pages, lengths, batch, budget,
@@ -402,7 +449,9 @@ def flash_attention(q, k, v, causal=False, out=None, stream=None):
 def __getattr__(name):
     # the serving operators' front end needs torch at import; the rest of this module does not
     if name in ("flash_attention_window", "KVCache", "kv_cache_append", "kv_cache_attention",
-                "kv_cache_attention_workspace", "kv_cache_evict"):
+                "kv_cache_attention_workspace", "kv_cache_evict", "flash_attention_cross",
+                "kv_cache_attention_ragged", "kv_cache_attention_ragged_workspace", "rotary",
+                "rotary_frequencies"):
         from . import serving
         return globals().setdefault(name, getattr(serving, name))
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -55,6 +55,8 @@
 namespace gemmrelu {
 namespace attn {
 
+constexpr unsigned kStatusLength = 8;   // == GEMMRELU_ERR_PAGE
+
 // n / d for 0 <= n < 2^31 by a product (Granlund and Montgomery, Division by Invariant Integers using
 // Multiplication, 1994): with l = ceil(log2 d) and m = floor(2^32 (2^l - d) / d) + 1 it is
 // (hi(m n) + n) >> l.  A work item needs four, and the compiler's long division delayed the next
@@ -88,6 +90,8 @@ struct WindowParams {
     int pairs, window, sinks;
     int chunk, chunk_items;        // K/V heads of all sequences whose items mix, and their items
     Divisor by_chunk, by_last, by_chunk_items, by_kv_heads, by_group;   // (last: the rest of heads)
+    const int32_t *states;         // cross attention: keys of each sequence (or nullptr: n_kv)
+    int tile_tokens;               //                  queries of a tile, each with all heads of the group
     float scale;                   // log2(e) / sqrt(d)
     float shift;                   // bf16: what a row's reference stands above its largest score
     int drop_arrive;
@@ -290,7 +294,19 @@ struct WindowWalk {
     }
 };
 
-template <int HD>
+// Keys of a sequence in cross attention: none where the number is out of range.
+__device__ __forceinline__ int states_of(const WindowParams &p, int batch) {
+    if (p.states == nullptr)
+        return p.n_kv;
+    const int n = p.states[batch];
+    if (n < 0 || n > p.n_kv) {
+        atomicCAS(&g_status, 0u, kStatusLength);
+        return 0;
+    }
+    return n;
+}
+
+template <int HD, bool kCross>
 __device__ __forceinline__ WindowItem window_item(const WindowParams &p, int index) {
     WindowItem w;
     // the last queries see the most keys: they go first
@@ -303,6 +319,17 @@ __device__ __forceinline__ WindowItem window_item(const WindowParams &p, int ind
     w.batch = p.by_kv_heads.quotient(index);
     w.kvh = index - w.batch * p.kv_heads;
     w.two = item + 1 < p.items;
+    if constexpr (kCross) {   // every row sees every key that there is
+        w.tile0 = item;
+        w.tile1 = item + 1;
+        w.head0 = w.head1 = w.kvh * p.group;
+        w.sinks = w.low = 0;
+        w.nb = (states_of(p, w.batch) + BN - 1) / BN;
+        w.narrow = -1;
+        w.t0 = Turns{0, 0, w.nb};
+        w.t1 = Turns{0, 0, w.two ? w.nb : 0};
+        return w;
+    }
     w.tile0 = p.by_group.quotient(item);
     const int g = item - w.tile0 * p.group;
     w.head0 = w.kvh * p.group + g;
@@ -340,7 +367,9 @@ __device__ __forceinline__ WindowItem window_item(const WindowParams &p, int ind
     return w;
 }
 
-template <int HD, bool kBf16>
+// kCross: cross attention.  Queries see all keys of their sequence (states_of), and a tile's rows are
+// tile_tokens queries with all heads of one K/V head's group.
+template <int HD, bool kBf16, bool kCross = false>
 __global__ void __launch_bounds__(kWindowThreads, 1)
     flash_attention_window_kernel(const __grid_constant__ CUtensorMap tmQ,
                                   const __grid_constant__ CUtensorMap tmK,
@@ -431,19 +460,21 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
             bool ok = !(p.drop_arrive && blockIdx.x == 0);
             for (int pass = 0;; ++pass) {
                 for (WindowWalk walk(p); lane == 0 && ok && walk.more(); walk.next()) {
-                    const WindowItem w = window_item<HD>(p, walk.index());
+                    const WindowItem w = window_item<HD, kCross>(p, walk.index());
                     if (w.nb == 0)
                         continue;
                     ok = wait_bounded_eager(q_empty, (queries & 1u) ^ 1u, p.wait_limit_ns, abort_flag,
                                             kSiteProducerEmpty);
                     if (!ok)
                         break;
-                    mbar_arrive_expect_tx(q_full, (w.two ? 2u : 1u) * G::kQBytes);
+                    const uint32_t q_bytes = kCross ? (uint32_t)(p.tile_tokens * p.group) * HD * 2u : G::kQBytes;
+                    const int q_step = kCross ? p.tile_tokens : BM;
+                    mbar_arrive_expect_tx(q_full, (w.two ? 2u : 1u) * q_bytes);
                     for (int t = 0; t < (w.two ? 2 : 1); ++t)
 #pragma unroll
                         for (int d = 0; d < G::kDSub; ++d)
                             tma_load_4d(&tmQ, base + G::kOffQ + t * G::kQBytes + d * kSub, q_full,
-                                        64 * d, t ? w.head1 : w.head0, (t ? w.tile1 : w.tile0) * BM, w.batch);
+                                        64 * d, t ? w.head1 : w.head0, (t ? w.tile1 : w.tile0) * q_step, w.batch);
                     ++queries;
                     for (int j = 0; j < w.nb; ++j) {
                         const uint32_t st = blocks % kKV, ph = blocks / kKV & 1u;
@@ -549,7 +580,7 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
                 WindowWalk walk(p);
                 WindowItem w{};
                 if (walk.more())
-                    w = window_item<HD>(p, walk.index());
+                    w = window_item<HD, kCross>(p, walk.index());
                 while (ok && walk.more()) {
                     const int nb = w.nb, narrow = w.narrow;
                     const Turns t0 = w.t0, t1 = w.t1;
@@ -565,7 +596,7 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
                     }
                     walk.next();
                     if (walk.more())
-                        w = window_item<HD>(p, walk.index());
+                        w = window_item<HD, kCross>(p, walk.index());
                     bool fresh0 = true, fresh1 = true;
                     for (int j = 0; ok && j < nb; ++j, ++blocks) {
                         const bool here = j == narrow, there = j + 1 == narrow, more = j + 1 < nb;
@@ -622,16 +653,23 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
         auto walk_items = [&](auto again) __attribute__((always_inline)) {
             constexpr bool kAgain = decltype(again)::value;
             for (WindowWalk walk(p); alive && walk.more(); walk.next()) {
-                const WindowItem w = window_item<HD>(p, walk.index());
+                const WindowItem w = window_item<HD, kCross>(p, walk.index());
                 const uint32_t block0 = blocks;
                 blocks += w.nb;
                 if (t == 1 && !w.two)
                     continue;
-                const int tile = t ? w.tile1 : w.tile0, head = t ? w.head1 : w.head0;
+                const int tile = t ? w.tile1 : w.tile0;
+                int head = t ? w.head1 : w.head0;
                 const Turns mine = t ? w.t1 : w.t0;
-                const int qi = tile * BM + 32 * q + lane;       // query index
-                const int pos = qi + off;
-                const int first = tile * BM + off, last = min(tile * BM + BM, p.n_q) - 1 + off;
+                int qi = tile * BM + 32 * q + lane;             // query index
+                int pos = qi + off;
+                int first = tile * BM + off, last = min(tile * BM + BM, p.n_q) - 1 + off;
+                if constexpr (kCross) {
+                    const int r = 32 * q + lane, nth = p.by_group.quotient(r);
+                    head += r - nth * p.group;
+                    qi = nth < p.tile_tokens ? tile * p.tile_tokens + nth : p.n_q;
+                    pos = first = last = states_of(p, w.batch) - 1;
+                }
                 // some row of a tile does not see some key of the block
                 auto masked_for = [&](int first, int last, int key0) {
                     return key0 + BN - 1 > first ||
@@ -749,7 +787,8 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
                     if constexpr (kAgain) {
                         add_taken();   // (the P V before this turn is done)
                         // where every row of both tiles sees every key the products do it all
-                        const int first_b = tile_b * BM + off, last_b = min(tile_b * BM + BM, p.n_q) - 1 + off;
+                        const int first_b = kCross ? first : tile_b * BM + off;
+                        const int last_b = kCross ? last : min(tile_b * BM + BM, p.n_q) - 1 + off;
                         if (masked_for(first, last, key0) || (other.has(j) && masked_for(first_b, last_b, key0))) {
                             const uint32_t i = block0 + j, st = i % kKV;
                             alive = reached(v_full(st), i / kKV);

@@ -7,17 +7,18 @@
 namespace {
 
 // A [batch][seq][heads][d] tensor of 16-bit elements with strides {sequence, token,
-// head}: boxes of 64 d x 1 head x 128 tokens, 128-byte swizzle, zero fill outside.  An axis of
-// one element is never stepped over, whatever its stride.
+// head}: boxes of 64 d x 1 head x 128 tokens (or box_heads x box_tokens), 128-byte swizzle, zero fill
+// outside.  An axis of one element is never stepped over, whatever its stride.
 bool make_strided_map(CUtensorMap *map, const void *ptr, int dtype, int64_t batch, int64_t seq,
-                      int64_t heads, int64_t d, const int64_t *strides) {
+                      int64_t heads, int64_t d, const int64_t *strides, int box_heads = 1,
+                      int box_tokens = FA::BM) {
     EncodeTiledFn enc = encode_fn();
     if (!enc)
         return false;
     auto bytes = [&](int64_t n, int64_t stride) { return (cuuint64_t)(n == 1 ? d : stride) * 2; };
     cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)seq, (cuuint64_t)batch};
     cuuint64_t step[3] = {bytes(heads, strides[2]), bytes(seq, strides[1]), bytes(batch, strides[0])};
-    cuuint32_t box[4] = {64, 1, (cuuint32_t)FA::BM, 1};
+    cuuint32_t box[4] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens, 1};
     cuuint32_t estr[4] = {1, 1, 1, 1};
     return enc(map, dtype == GEMMRELU_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                4, const_cast<void *>(ptr), dims, step, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -37,10 +38,10 @@ bool window_strides_ok(const int64_t *s, int64_t batch, int64_t seq, int64_t hea
     return true;
 }
 
-template <int HD, bool kBf16>
+template <int HD, bool kBf16, bool kCross>
 int launch_window(const CUtensorMap &mQ, const CUtensorMap &mK, const CUtensorMap &mV,
                   const FA::WindowParams &p, int sms, cudaStream_t stream, bool &attr_done) {
-    auto kern = FA::flash_attention_window_kernel<HD, kBf16>;
+    auto kern = FA::flash_attention_window_kernel<HD, kBf16, kCross>;
     if (!ensure_smem_attr(attr_done, kern, FA::WindowCfg<HD>::kSmemBytes))
         return GEMMRELU_ERR_LAUNCH;
     cudaLaunchConfig_t cfg{};
@@ -56,6 +57,16 @@ int launch_window(const CUtensorMap &mQ, const CUtensorMap &mK, const CUtensorMa
     return launch_status(cudaLaunchKernelEx(&cfg, kern, mQ, mK, mV, p));
 }
 
+template <bool kCross>
+int launch_window_as(int dtype, int64_t head_dim, const CUtensorMap &mQ, const CUtensorMap &mK, const CUtensorMap &mV,
+                     const FA::WindowParams &p, int sms, cudaStream_t s, bool *attr) {
+    if (head_dim == 64)
+        return dtype == GEMMRELU_BF16 ? launch_window<64, true, kCross>(mQ, mK, mV, p, sms, s, attr[0])
+                                      : launch_window<64, false, kCross>(mQ, mK, mV, p, sms, s, attr[1]);
+    return dtype == GEMMRELU_BF16 ? launch_window<128, true, kCross>(mQ, mK, mV, p, sms, s, attr[2])
+                                  : launch_window<128, false, kCross>(mQ, mK, mV, p, sms, s, attr[3]);
+}
+
 }  // namespace
 
 // The order of the work.  The first queries see fewer keys than the last, and with one head after the
@@ -67,12 +78,13 @@ int launch_window(const CUtensorMap &mQ, const CUtensorMap &mK, const CUtensorMa
 // (485 with all heads together).  What it costs: 16384 tokens with a window of 512 173 -> 186 us.
 constexpr int64_t kWindowChunkBytes = (int64_t)96 << 20;
 
-extern "C" int flash_attention_window_x16(const void *Q, const void *K, const void *V, void *O,
-                                          int dtype, int64_t batch, int64_t q_seq, int64_t kv_seq,
-                                          int64_t q_heads, int64_t kv_heads, int64_t head_dim,
-                                          const int64_t *q_strides, const int64_t *k_strides,
-                                          const int64_t *v_strides, int64_t window, int64_t sinks,
-                                          void *stream) {
+// flash_attention_window_x16, and flash_attention_cross_x16 (kCross: no window or sinks; `states` keys a
+// sequence).
+template <bool kCross>
+static int attention_strided(const void *Q, const void *K, const void *V, void *O, int dtype, int64_t batch,
+                             int64_t q_seq, int64_t kv_seq, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                             const int64_t *q_strides, const int64_t *k_strides, const int64_t *v_strides,
+                             int64_t window, int64_t sinks, const int32_t *states, void *stream) {
     if ((dtype != GEMMRELU_F16 && dtype != GEMMRELU_BF16) || batch < 0 || batch > 65535 ||
         q_seq < 0 || kv_seq < 0 || q_seq > ((int64_t)1 << 30) || kv_seq > ((int64_t)1 << 30) ||
         q_heads < 0 || q_heads > 65535 || kv_heads < 0 || kv_heads > 65535 ||
@@ -82,6 +94,9 @@ extern "C" int flash_attention_window_x16(const void *Q, const void *K, const vo
         return GEMMRELU_OK;
     if (kv_heads == 0 || q_heads % kv_heads != 0 || !O || !aligned(O, 16) ||
         q_seq > ((int64_t)1 << 40) / (batch * q_heads * head_dim))
+        return GEMMRELU_ERR_INVALID_ARG;
+    const int64_t group = q_heads / kv_heads;
+    if (kCross && (group > FA::BM || !aligned(states, 4)))
         return GEMMRELU_ERR_INVALID_ARG;
     if (kv_seq > 0 && (!Q || !K || !V || !aligned(Q, 16) || !aligned(K, 16) || !aligned(V, 16) ||
                        !window_strides_ok(q_strides, batch, q_seq, q_heads) ||
@@ -95,8 +110,10 @@ extern "C" int flash_attention_window_x16(const void *Q, const void *K, const vo
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (kv_seq == 0)   // nobody sees anything
         return launch_status(cudaMemsetAsync(O, 0, (size_t)(batch * q_seq * q_heads * head_dim) * 2, s));
+    const int tile_tokens = kCross ? (int)(FA::BM / group) : FA::BM;
     CUtensorMap mQ, mK, mV;
-    if (!make_strided_map(&mQ, Q, dtype, batch, q_seq, q_heads, head_dim, q_strides) ||
+    if (!make_strided_map(&mQ, Q, dtype, batch, q_seq, q_heads, head_dim, q_strides, kCross ? (int)group : 1,
+                          tile_tokens) ||
         !make_strided_map(&mK, K, dtype, batch, kv_seq, kv_heads, head_dim, k_strides) ||
         !make_strided_map(&mV, V, dtype, batch, kv_seq, kv_heads, head_dim, v_strides))
         return GEMMRELU_ERR_LAUNCH;
@@ -108,9 +125,11 @@ extern "C" int flash_attention_window_x16(const void *Q, const void *K, const vo
     p.n_q = (int)q_seq;
     p.n_kv = (int)kv_seq;
     p.q_heads = (int)q_heads;
-    p.group = (int)(q_heads / kv_heads);
-    p.q_tiles = (int)((q_seq + FA::BM - 1) / FA::BM);
-    const int64_t items = (int64_t)p.q_tiles * p.group;
+    p.group = (int)group;
+    p.states = states;
+    p.tile_tokens = tile_tokens;
+    p.q_tiles = (int)((q_seq + tile_tokens - 1) / tile_tokens);
+    const int64_t items = kCross ? p.q_tiles : (int64_t)p.q_tiles * p.group;
     if (items >= kMaxDim / (batch * kv_heads))
         return GEMMRELU_ERR_INVALID_ARG;
     p.kv_heads = (int)kv_heads;
@@ -136,13 +155,27 @@ extern "C" int flash_attention_window_x16(const void *Q, const void *K, const vo
     p.shift = dtype == GEMMRELU_BF16 ? 9.0f + std::ceil(std::log2((float)seen)) : 0.0f;
     p.drop_arrive = g_drop_arrive.load();
     p.wait_limit_ns = wait_limit_ns();
-    if (head_dim == 64)
-        return dtype == GEMMRELU_BF16
-                   ? launch_window<64, true>(mQ, mK, mV, p, ds->sms, s, ds->attr_window[0])
-                   : launch_window<64, false>(mQ, mK, mV, p, ds->sms, s, ds->attr_window[1]);
-    return dtype == GEMMRELU_BF16
-               ? launch_window<128, true>(mQ, mK, mV, p, ds->sms, s, ds->attr_window[2])
-               : launch_window<128, false>(mQ, mK, mV, p, ds->sms, s, ds->attr_window[3]);
+    return launch_window_as<kCross>(dtype, head_dim, mQ, mK, mV, p, ds->sms, s,
+                                    kCross ? ds->attr_cross : ds->attr_window);
+}
+
+extern "C" int flash_attention_window_x16(const void *Q, const void *K, const void *V, void *O,
+                                          int dtype, int64_t batch, int64_t q_seq, int64_t kv_seq,
+                                          int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                          const int64_t *q_strides, const int64_t *k_strides,
+                                          const int64_t *v_strides, int64_t window, int64_t sinks,
+                                          void *stream) {
+    return attention_strided<false>(Q, K, V, O, dtype, batch, q_seq, kv_seq, q_heads, kv_heads, head_dim, q_strides,
+                                    k_strides, v_strides, window, sinks, nullptr, stream);
+}
+
+extern "C" int flash_attention_cross_x16(const void *Q, const void *K, const void *V, void *O, int dtype,
+                                         int64_t batch, int64_t q_seq, int64_t kv_seq, int64_t q_heads,
+                                         int64_t kv_heads, int64_t head_dim, const int64_t *q_strides,
+                                         const int64_t *k_strides, const int64_t *v_strides,
+                                         const int32_t *lengths, void *stream) {
+    return attention_strided<true>(Q, K, V, O, dtype, batch, q_seq, kv_seq, q_heads, kv_heads, head_dim, q_strides,
+                                   k_strides, v_strides, 0, 0, lengths, stream);
 }
 
 extern "C" int flash_attention_window_debug_blocks(int64_t first, int64_t last, int64_t window,

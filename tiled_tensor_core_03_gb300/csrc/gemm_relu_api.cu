@@ -107,6 +107,8 @@ struct DeviceState {
     bool attr_gemv[4] = {false, false, false, false};
     bool attr_attn[2] = {false, false};
     bool attr_window[4] = {};
+    bool attr_cross[4] = {};
+    bool attr_ragged[4] = {};
     bool attr_kv[16] = {};   // kv_cache_attention: head_dim x row groups x type x weights or not
 };
 constexpr int kMaxDevices = 64;
@@ -1309,3 +1311,4 @@ int gemm_relu_debug_set(int drop_arrive, int64_t wait_limit_ns_arg) {
 
 #include "flash_attention_window_api.cuh"
 #include "kv_cache_api.cuh"
+#include "rotary_api.cuh"

@@ -5,6 +5,7 @@
 #include "kv_cache.h"
 #include "kv_cache.cuh"
 #include "kv_attention.cuh"
+#include "kv_ragged.cuh"
 
 namespace {
 
@@ -169,6 +170,21 @@ int launch_kv_attention(const CUtensorMap &mK, const CUtensorMap &mV, KC::AttnPa
     const int64_t grid = (int64_t)p.batch * p.pool.kv_heads * blocks;
     return p.rows % 4 == 0 ? launch_kv(KC::kv_attention_weights_kernel<4>, grid, KC::kWeightThreads, s, p)
                            : launch_kv(KC::kv_attention_weights_kernel<1>, grid, KC::kWeightThreads, s, p);
+}
+
+// Workspace of kv_cache_attention_ragged_x16: counters, then two parts for each CTA.
+size_t ragged_bytes(int64_t head_dim, int ctas) {
+    return GEMMRELU_RAGGED_COUNTER_BYTES + (size_t)ctas * 2 * 8 * 32 * (head_dim + 4) * sizeof(float);
+}
+
+int ragged_ctas(int sms) { return std::min(sms, KC::kRaggedMaxCtas); }
+
+template <int D, bool kBf16>
+int launch_ragged(const KC::RaggedParams &p, int ctas, cudaStream_t s, bool &attr_done) {
+    auto kern = KC::kv_attention_ragged_kernel<D, kBf16>;
+    if (!ensure_smem_attr(attr_done, kern, KC::RaggedCfg<D>::kSmem))
+        return GEMMRELU_ERR_LAUNCH;
+    return launch_kernel(kern, (unsigned)ctas, (unsigned)KC::kRaggedThreads, KC::RaggedCfg<D>::kSmem, s, false, 1u, p);
 }
 
 template <int D, int kN>
@@ -367,6 +383,71 @@ int kv_cache_attention_x16(const kv_cache_pool *cache, const void *q, int dtype,
         return launch_kv_attention_as<128, 1>(bf16, mK, mV, p, s, ds->sms, ds->attr_kv);
     return rows <= 8 ? launch_kv_attention_as<64, 1>(bf16, mK, mV, p, s, ds->sms, ds->attr_kv)
                      : launch_kv_attention_as<64, 2>(bf16, mK, mV, p, s, ds->sms, ds->attr_kv);
+}
+
+size_t kv_cache_attention_ragged_x16_workspace_bytes(int64_t head_dim) {
+    DeviceState *ds = nullptr;
+    if ((head_dim != 64 && head_dim != 128) || current_device_state(&ds) != GEMMRELU_OK)
+        return 0;
+    return ragged_bytes(head_dim, ragged_ctas(ds->sms));
+}
+
+int kv_cache_attention_ragged_x16(const kv_cache_pool *cache, const void *q, int dtype, int64_t rows,
+                                  int64_t q_heads, const int64_t *q_strides, void *out,
+                                  int64_t batch, const int32_t *starts, const int32_t *pages,
+                                  int64_t max_pages, const int32_t *lengths, int64_t window,
+                                  int64_t sinks, void *workspace, size_t workspace_bytes, void *stream) {
+    if (!pool_ok(cache) || (dtype != GEMMRELU_F16 && dtype != GEMMRELU_BF16) || window < 0 || sinks < 0 ||
+        rows < 0 || rows > ((int64_t)1 << 24) || batch < 0 || batch > KC::kRaggedMaxBatch || q_heads < 1 ||
+        q_heads > 65535 || q_heads % cache->kv_heads != 0 || rows * q_heads > ((int64_t)1 << 30))
+        return GEMMRELU_ERR_INVALID_ARG;
+    if (batch == 0 || rows == 0)
+        return GEMMRELU_OK;
+    if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || !q_strides ||
+        !table_ok(pages, batch, max_pages, cache->page) || !lengths || !aligned(lengths, 4) || !starts ||
+        !aligned(starts, 4))
+        return GEMMRELU_ERR_INVALID_ARG;
+    for (int i = 0; i < 2; ++i)
+        if (q_strides[i] < 0 || q_strides[i] % 8 != 0 || q_strides[i] > ((int64_t)1 << 34))
+            return GEMMRELU_ERR_INVALID_ARG;
+    const int64_t group = q_heads / cache->kv_heads;
+    if ((rows * group / 256 + batch) * cache->kv_heads > kMaxGrid / (max_pages * cache->page / 128 + 1))
+        return GEMMRELU_ERR_INVALID_ARG;
+    DeviceState *ds = nullptr;
+    const int rc = current_device_state(&ds);
+    if (rc != GEMMRELU_OK)
+        return rc;
+    const int ctas = ragged_ctas(ds->sms);
+    if (!workspace || workspace_bytes < ragged_bytes(cache->head_dim, ctas) || !aligned(workspace, 16))
+        return GEMMRELU_ERR_WORKSPACE;
+    KC::RaggedParams p{};
+    p.pool = device_pool(cache);
+    p.q = static_cast<const uint16_t *>(q);
+    p.q_stride[0] = q_strides[0];
+    p.q_stride[1] = q_strides[1];
+    p.out = static_cast<uint16_t *>(out);
+    p.pages = pages;
+    p.lengths = lengths;
+    p.starts = starts;
+    p.max_pages = max_pages;
+    p.batch = (int)batch;
+    p.rows = (int)rows;
+    p.q_heads = (int)q_heads;
+    p.group = (int)group;
+    p.by_group = FA::Divisor::of((uint32_t)group);
+    p.window = (int)std::min<int64_t>(window, kMaxTokens);
+    p.sinks = (int)std::min<int64_t>(sinks, kMaxTokens);
+    p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)cache->head_dim));
+    p.arrived = static_cast<unsigned *>(workspace);
+    p.partial = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + GEMMRELU_RAGGED_COUNTER_BYTES);
+    p.drop_arrive = g_drop_arrive.load();
+    p.wait_limit_ns = wait_limit_ns();
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (cache->head_dim == 128)
+        return dtype == GEMMRELU_BF16 ? launch_ragged<128, true>(p, ctas, s, ds->attr_ragged[0])
+                                      : launch_ragged<128, false>(p, ctas, s, ds->attr_ragged[1]);
+    return dtype == GEMMRELU_BF16 ? launch_ragged<64, true>(p, ctas, s, ds->attr_ragged[2])
+                                  : launch_ragged<64, false>(p, ctas, s, ds->attr_ragged[3]);
 }
 
 int kv_cache_debug_span(int64_t length, int64_t tokens, int64_t window, int64_t sinks, int *out) {

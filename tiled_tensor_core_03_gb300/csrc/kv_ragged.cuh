@@ -1,0 +1,1025 @@
+// kv_ragged.cuh -- attention of a batch of chunks over the paged 8-bit cache:
+//
+//   O[r] = sum_t softmax_t(q_r . k_t / sqrt(D)) v_t,  k_t = ks * K8[t], v_t = vs * V8[t]
+//
+// over the tokens t that row r sees, rows packed: sequence b has the query tokens starts[b] ..
+// starts[b + 1] - 1, the last of its lengths[b] tokens.  The rows of one K/V head are its group's query
+// heads of every new token, token by token; 128 of them are a tile, two neighbouring tiles an item.
+#pragma once
+
+#include "flash_attention_window.cuh"
+#include "kv_attention.cuh"
+
+namespace gemmrelu {
+namespace kvc {
+
+using attn::BM;
+using attn::BN;
+using attn::kSub;
+
+constexpr int kRaggedThreads = attn::kWindowThreads;
+constexpr int kConvWarp = 10, kConvWarps = 2;   // converting warps: 10, 11
+constexpr int kGroups = BN / 16;                // pieces of 16 tokens of a block: the smallest page
+constexpr int kRaggedMaxCtas = GEMMRELU_RAGGED_COUNTER_BYTES / (8 * (int)sizeof(unsigned));
+constexpr int kRaggedMaxBatch = 16384;          // sequences whose units fit the scratch of the start
+constexpr float kBigLog2 = 2048.0f;             // 2^11: scores from here on are referred before V's scale is added
+
+// Scales of a block, a pair (ks, log2 vs) for each 16 tokens, and a bit for each that is not there.
+struct RaggedMeta {
+    float2 scale[kGroups];
+    uint32_t missing;
+    uint32_t pad;
+};
+
+template <int HD>
+struct RaggedCfg {
+    static constexpr int kDSub = HD / 64;
+    static constexpr int kRaw = HD == 128 ? 1 : 4;               // stages of e4m3 bytes
+    // Blocks whose scales are kept.  Block i's are written when the bytes of block i - kRaw have been converted: then the
+    // scores of block i - kRaw - 2 are done, and with them both tiles' softmax of block i - kRaw - 3.
+    static constexpr int kMetas = HD == 128 ? 4 : 8;
+    static_assert(kMetas >= kRaw + 3, "scales stay until they have been read");
+    static constexpr uint32_t kTile16 = kDSub * kSub;            // a block of K or V in fp16; a tile of Q
+    static constexpr uint32_t kTile8 = BN * HD;                  // in e4m3
+    static constexpr uint32_t kOffQ = 0;
+    static constexpr uint32_t kOffK = kOffQ + 2 * kTile16;
+    static constexpr uint32_t kOffV = kOffK + 2 * kTile16;
+    static constexpr uint32_t kOffRawK = kOffV + 2 * kTile16;
+    static constexpr uint32_t kOffRawV = kOffRawK + kRaw * kTile8;
+    static constexpr uint32_t kOffMeta = kOffRawV + kRaw * kTile8;
+    static constexpr uint32_t kOffBar = kOffMeta + kMetas * (uint32_t)sizeof(RaggedMeta);
+    // raw_k_full, raw_v_full, raw_k_empty, raw_v_empty [kRaw]; k_full, v_full, k_empty, v_empty [2];
+    // meta_full[kMetas]; q_full, s_full, p_full, o_full [2]; drain
+    static constexpr uint32_t kNumBars = 4 * kRaw + 8 + kMetas + 8 + 1;
+    static constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;
+    static constexpr uint32_t kSmem = kOffMisc + 256 + 1024;
+    static constexpr uint32_t kTmemS = 0, kTmemO = 2 * BN;
+    static constexpr uint32_t kIdescS = make_idesc_f16_f32(BM, BN, 0, 0);
+    static constexpr uint32_t kIdescO = make_idesc_f16_f32(BM, HD, 0, 1);
+    static_assert(kSmem <= 232448, "shared memory of a block");
+};
+
+struct RaggedParams {
+    Pool pool;
+    const uint16_t *q;
+    int64_t q_stride[2];               // token, head
+    uint16_t *out;                     // [rows][q_heads][D]
+    const int32_t *pages, *lengths, *starts;
+    int64_t max_pages;
+    int batch, rows, q_heads, group;
+    attn::Divisor by_group;
+    int window, sinks;
+    float scale_log2;                  // log2(e) / sqrt(D)
+    float *partial;                    // [2 * CTAs][8 warps][D + 4][32 rows]
+    unsigned *arrived;                 // [CTAs][8 warps]; all 0 between calls
+    int drop_arrive;
+    uint64_t wait_limit_ns;
+};
+
+// ---------------------------------------------------------------- the work
+
+// A sequence's part of the call: rows [start, start + count), tokens [0, n), items of one head.
+struct RaggedSeq {
+    int start, count, n, items;
+};
+
+// (what is out of range is taken as nothing, and reported where `report` is set)
+__device__ __forceinline__ RaggedSeq ragged_seq(const RaggedParams &p, int b, bool report) {
+    RaggedSeq s{0, 0, 0, 0};
+    const int s0 = p.starts[b], s1 = p.starts[b + 1], n = p.lengths[b];
+    bool ok = s0 >= 0 && s1 >= s0 && s1 <= p.rows;
+    if (ok) {
+        s.start = s0;
+        s.count = s1 - s0;
+    }
+    if (n < 0 || n > p.max_pages * p.pool.page)
+        ok = false;
+    else
+        s.n = n;
+    if (!ok && report)
+        record_page_error();
+    s.items = (s.count * p.group + 2 * BM - 1) / (2 * BM);
+    return s;
+}
+
+// Positions of an item's (or a tile's) first and last row, and the blocks that some row of it sees; an item
+// whose rows see nothing has one block all the same, so that somebody writes its output.
+struct RaggedItem {
+    int first, last;
+    attn::Blocks blocks;
+    __device__ __forceinline__ int count() const { return max(1, blocks.count()); }
+    __device__ __forceinline__ int key0(int j) const {
+        return (j < blocks.sinks ? j : blocks.low + (j - blocks.sinks)) * BN;
+    }
+};
+
+__device__ __forceinline__ RaggedItem ragged_item(const RaggedParams &p, const RaggedSeq &s, int item) {
+    RaggedItem it;
+    const int r0 = item * 2 * BM, r1 = min(r0 + 2 * BM, s.count * p.group) - 1;
+    it.first = s.n - s.count + p.by_group.quotient(r0);
+    it.last = s.n - s.count + p.by_group.quotient(r1);
+    it.blocks = attn::blocks_seen(it.first, it.last, p.window, p.sinks);
+    return it;
+}
+
+// Some row at positions first .. last does not see some key of the block.
+__device__ __forceinline__ bool ragged_masked(const RaggedParams &p, int first, int last, int key0) {
+    return key0 + BN - 1 > first || (p.window > 0 && key0 <= last - p.window && key0 + BN > p.sinks);
+}
+
+// Whether some row of the item sees some of `tokens` tokens from `token` on.
+__device__ __forceinline__ bool ragged_sees(const RaggedParams &p, const RaggedItem &it, int token, int tokens) {
+    return token <= it.last && (p.window == 0 || token < p.sinks ||
+                                token + tokens > max(it.first, 0) - p.window + 1);
+}
+
+// The segments (runs of blocks of one item) of a CTA's range of units, in order.
+struct RaggedWalk {
+    int b, head, item, j, left;      // where it stands; units left of the range, this segment's too
+    int unit0;                       // first unit of the item
+    RaggedSeq seq;
+    RaggedItem it;
+    int j1, nb;                      // this segment is the blocks j .. j1 - 1 of nb
+    __device__ __forceinline__ void describe(const RaggedParams &p) {
+        it = ragged_item(p, seq, item);
+        nb = it.count();
+        j1 = min(nb, j + left);
+    }
+    __device__ __forceinline__ int rows(const RaggedParams &p) const { return seq.count * p.group - item * 2 * BM; }
+    // The next segment; false at the end of the range.
+    __device__ __forceinline__ bool next(const RaggedParams &p) {
+        left -= j1 - j;
+        if (left <= 0)
+            return false;
+        unit0 += nb;
+        j = 0;
+        if (++item == seq.items) {
+            item = 0;
+            if (++head == p.pool.kv_heads) {
+                head = 0;
+                do
+                    seq = ragged_seq(p, ++b, false);
+                while (seq.items == 0);
+            }
+        }
+        describe(p);
+        return true;
+    }
+};
+
+// What the start works out, in shared memory.
+struct RaggedPlan {
+    int b, head, item, j, unit0, start, stop, total, ranges;
+};
+
+// ---------------------------------------------------------------- V that is not finite
+
+// The NaN of V in blocks that some row sees in part were taken out (0 in their place); the rows that see one get
+// it back here, in the warp's 32 rows of O in TMEM: blocks j0 .. j1 - 1 of an item, `pos` the lane's row's position.
+template <int HD>
+__device__ __noinline__ void ragged_add_nan(const RaggedParams &p, int b, int head, int item, int j0, int j1, int pos,
+                                            uint32_t o_addr) {
+    const int lane = threadIdx.x & 31, page = p.pool.page;
+    const RaggedSeq seq = ragged_seq(p, b, false);
+    const RaggedItem it = ragged_item(p, seq, item);
+#pragma unroll 1
+    for (int j = j0; j < j1; ++j) {
+#pragma unroll 1
+        for (int k0 = it.key0(j); k0 < it.key0(j) + BN; k0 += 32) {
+            const int key = k0 + lane;
+            const uint8_t *row = nullptr;
+            if (key < seq.n && ragged_sees(p, it, key & ~(page - 1), page)) {
+                const int64_t id = p.pages[b * p.max_pages + (key >> p.pool.page_shift)];
+                if (id >= 0 && id < p.pool.num_pages)
+                    row = p.pool.values[1] + ((id * p.pool.kv_heads + head) * page + (key & (page - 1))) * HD;
+            }
+            uint32_t bad = 0;
+            if (row != nullptr)
+#pragma unroll 1
+                for (int c = 0; c < HD; c += 16) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(row + c);
+                    bad |= nan_bytes(x.x) | nan_bytes(x.y) | nan_bytes(x.z) | nan_bytes(x.w);
+                }
+            const uint32_t low = (uint32_t)reinterpret_cast<uintptr_t>(row);
+            const uint32_t high = (uint32_t)(reinterpret_cast<uintptr_t>(row) >> 32);
+#pragma unroll 1
+            for (uint32_t keys = __ballot_sync(0xffffffffu, bad != 0); keys; keys &= keys - 1) {
+                const int i = __ffs(keys) - 1;
+                const uintptr_t at = (uintptr_t)__shfl_sync(0xffffffffu, low, i) |
+                                     (uintptr_t)__shfl_sync(0xffffffffu, high, i) << 32;
+                const bool mine = sees(k0 + i, pos, p.window, p.sinks);
+#pragma unroll 1
+                for (int c0 = 0; c0 < HD; c0 += 32) {
+                    uint32_t o[32];
+                    tmem_ld_x32_sync(o_addr + c0, o);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const uint32_t x = nan_bytes(reinterpret_cast<const uint32_t *>(at + c0)[c]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            o[4 * c + e] = mine && x & (0x80u << 8 * e) ? 0x7fffffffu : o[4 * c + e];
+                    }
+                    tmem_st_x32(o_addr + c0, o);
+                    tmem_st_wait();
+                }
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- e4m3 to fp16
+
+// Rows [row0, row0 + 64) of a block: bytes at `src` (rows of HD) become fp16 in the sub-tiles of 64
+// columns at `dst`, 128-byte swizzled, the layout of both products' B operands.  Four lanes take 64 bytes
+// of an even row and four the other half of the next one, so that eight lanes that load or store
+// together touch all banks once.  kCheck: rows past the sequence's end or of pages that are not there become 0
+// and so do NaN; true if the lane met one.
+template <int HD, bool kCheck>
+__device__ __forceinline__ bool convert_rows(uint32_t src, uint32_t dst, int row0, int valid, uint32_t missing) {
+    const int lane = threadIdx.x & 31;
+    const int odd = (lane >> 2) & 1, c4 = lane & 3;
+    uint32_t bad = 0;
+    constexpr int kHalves = HD / 64;
+#pragma unroll 4
+    for (int i = 0; i < 64 / 8 * kHalves; ++i) {
+        const int row = row0 + (i / kHalves) * 8 + 2 * (lane >> 3) + odd;
+        const int half = kHalves == 1 ? 0 : (odd ^ (i & 1));
+        const uint4 x = ld_shared_v4(src + row * HD + half * 64 + c4 * 16);
+        uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        if constexpr (kCheck) {
+            const bool there = row < valid && !(missing >> (row >> 4) & 1u);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                w[e] = there ? w[e] : 0u;
+                const uint32_t n = nan_bytes(w[e]);
+                bad |= n;
+                w[e] &= ~((n >> 7) * 0xffu);
+            }
+        }
+        uint32_t h[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            h[2 * e] = e4m3x2_to_half2(w[e] & 0xffffu);
+            h[2 * e + 1] = e4m3x2_to_half2(w[e] >> 16);
+        }
+        const uint32_t at = dst + half * kSub + row * 128;
+        const uint32_t chunk = (uint32_t)((2 * c4) ^ (row & 7)) << 4;
+        st_shared_v4(at + chunk, h[0], h[1], h[2], h[3]);
+        st_shared_v4(at + (chunk ^ 16u), h[4], h[5], h[6], h[7]);
+    }
+    return bad != 0;
+}
+
+// ---------------------------------------------------------------- the kernel
+
+template <int HD, bool kBf16>
+__global__ void __launch_bounds__(kRaggedThreads, 1)
+    kv_attention_ragged_kernel(const __grid_constant__ RaggedParams p) {
+    using G = RaggedCfg<HD>;
+    using namespace attn;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *gbase = smem_raw + (base - raw);
+
+    const uint32_t bar0 = base + G::kOffBar;
+    auto raw_full = [&](int kv, uint32_t s) { return bar0 + 8u * (kv * G::kRaw + s); };
+    auto raw_empty = [&](int kv, uint32_t s) { return bar0 + 8u * ((2 + kv) * G::kRaw + s); };
+    constexpr uint32_t kB1 = 4 * G::kRaw;
+    auto full = [&](int kv, uint32_t s) { return bar0 + 8u * (kB1 + 2 * kv + s); };
+    auto empty = [&](int kv, uint32_t s) { return bar0 + 8u * (kB1 + 4 + 2 * kv + s); };
+    auto meta_full = [&](uint32_t s) { return bar0 + 8u * (kB1 + 8 + s); };
+    constexpr uint32_t kB2 = kB1 + 8 + G::kMetas;
+    auto q_full = [&](uint32_t t) { return bar0 + 8u * (kB2 + t); };
+    auto s_full = [&](uint32_t t) { return bar0 + 8u * (kB2 + 2 + t); };
+    auto p_full = [&](uint32_t t) { return bar0 + 8u * (kB2 + 4 + t); };
+    auto o_full = [&](uint32_t t) { return bar0 + 8u * (kB2 + 6 + t); };
+    const uint32_t drain_bar = bar0 + 8u * (kB2 + 8);
+    RaggedMeta *metas = reinterpret_cast<RaggedMeta *>(gbase + G::kOffMeta);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + G::kOffMisc);
+    volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(gbase + G::kOffMisc + 4);
+    volatile uint32_t *dirty = reinterpret_cast<volatile uint32_t *>(gbase + G::kOffMisc + 16);   // [2][4]
+    RaggedPlan *plan = reinterpret_cast<RaggedPlan *>(gbase + G::kOffMisc + 48);
+    long long *sums = reinterpret_cast<long long *>(gbase + G::kOffMisc + 96);                    // [12]
+
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);   // uniform
+    const int lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (uint32_t s = 0; s < (uint32_t)G::kRaw; ++s)
+            for (int kv = 0; kv < 2; ++kv) {
+                mbar_init(raw_full(kv, s), 1u);
+                mbar_init(raw_empty(kv, s), kConvWarps);
+            }
+        for (uint32_t s = 0; s < 2; ++s) {
+            for (int kv = 0; kv < 2; ++kv) {
+                mbar_init(full(kv, s), kConvWarps);
+                mbar_init(empty(kv, s), 1u);
+            }
+            mbar_init(q_full(s), 4u);
+            mbar_init(s_full(s), 1u);
+            mbar_init(p_full(s), 4u);
+            mbar_init(o_full(s), 1u);
+        }
+        for (uint32_t s = 0; s < (uint32_t)G::kMetas; ++s)
+            mbar_init(meta_full(s), 1u);
+        mbar_init(drain_bar, 1u);
+        *abort_flag = 0u;
+        fence_mbar_init();
+        pdl_launch_dependents();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(smem_addr(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    pdl_wait_primary();
+
+    // ---- this CTA's range of units.  A unit is a block of 128 keys of an item.  Units of one head of every
+    // sequence, a lane each; those of long chunks are summed by a warp.
+    int *units = reinterpret_cast<int *>(gbase + G::kOffK);
+    {
+        long long mine = 0;
+        for (int b0 = warp * 32; b0 < p.batch; b0 += kRaggedThreads) {
+            const int b = b0 + lane;
+            RaggedSeq s{0, 0, 0, 0};
+            if (b < p.batch)
+                s = ragged_seq(p, b, blockIdx.x == 0);
+            long long u = 0;
+            if (s.items <= 4)
+                for (int i = 0; i < s.items; ++i)
+                    u += ragged_item(p, s, i).count();
+            for (uint32_t m = __ballot_sync(0xffffffffu, s.items > 4); m; m &= m - 1) {
+                const int from = __ffs(m) - 1;
+                RaggedSeq x;
+                x.count = __shfl_sync(0xffffffffu, s.count, from);
+                x.n = __shfl_sync(0xffffffffu, s.n, from);
+                x.items = __shfl_sync(0xffffffffu, s.items, from);
+                long long sum = 0;
+                for (int i = lane; i < x.items; i += 32)
+                    sum += ragged_item(p, x, i).count();
+                for (int o = 16; o; o >>= 1)
+                    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                u = lane == from ? sum : u;
+            }
+            if (b < p.batch)
+                units[b] = (int)u;
+            mine += u;
+        }
+        for (int o = 16; o; o >>= 1)
+            mine += __shfl_xor_sync(0xffffffffu, mine, o);
+        if (lane == 0)
+            sums[warp] = mine;
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
+    if (warp == 0) {
+        long long all = 0;
+        for (int w = 0; w < kRaggedThreads / 32; ++w)
+            all += sums[w];
+        all *= p.pool.kv_heads;
+        if (all > 0x7fffffffll) {   // rows that several sequences claim
+            if (lane == 0)
+                record_page_error();
+            all = 0;
+        }
+        const int total = (int)all;
+        const int ranges = max(1, min(total, (int)gridDim.x));
+        const int c = blockIdx.x;
+        const int start = c < ranges ? range_start(c, total, ranges) : total;
+        const int stop = c < ranges ? range_start(c + 1, total, ranges) : total;
+        if (start < stop) {
+            int at = 0, b = 0, u = 0;
+            for (int b0 = 0;; b0 += 32) {   // the sequence that the range starts in
+                const int x = b0 + lane < p.batch ? units[b0 + lane] * p.pool.kv_heads : 0;
+                int run = x;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, run, o);
+                    run += lane >= o ? y : 0;
+                }
+                const uint32_t m = __ballot_sync(0xffffffffu, start < at + run);
+                if (m) {
+                    const int l = __ffs(m) - 1;
+                    b = b0 + l;
+                    u = __shfl_sync(0xffffffffu, x, l);
+                    at += __shfl_sync(0xffffffffu, run, l) - u;
+                    break;
+                }
+                at += __shfl_sync(0xffffffffu, run, 31);
+            }
+            u /= p.pool.kv_heads;
+            const int head = (start - at) / u;
+            at += head * u;
+            const RaggedSeq s = ragged_seq(p, b, false);
+            int item = 0;
+            for (int i0 = 0;; i0 += 32) {   // the item of that head
+                const int x = i0 + lane < s.items ? ragged_item(p, s, i0 + lane).count() : 0;
+                int run = x;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, run, o);
+                    run += lane >= o ? y : 0;
+                }
+                const uint32_t m = __ballot_sync(0xffffffffu, start < at + run);
+                if (m) {
+                    const int l = __ffs(m) - 1;
+                    item = i0 + l;
+                    at += __shfl_sync(0xffffffffu, run - x, l);
+                    break;
+                }
+                at += __shfl_sync(0xffffffffu, run, 31);
+            }
+            if (lane == 0)
+                *plan = RaggedPlan{b, head, item, start - at, at, start, stop, total, ranges};
+        } else if (lane == 0) {
+            *plan = RaggedPlan{0, 0, 0, 0, 0, 0, 0, 0, 1};
+        }
+    }
+    __syncthreads();
+    const int start = plan->start, stop = plan->stop;
+    auto first_segment = [&]() {
+        RaggedWalk w;
+        w.b = plan->b;
+        w.head = plan->head;
+        w.item = plan->item;
+        w.j = plan->j;
+        w.left = stop - start;
+        w.unit0 = plan->unit0;
+        w.seq = ragged_seq(p, w.b, false);
+        w.describe(p);
+        return w;
+    };
+
+    if (warp >= kProducerWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (start < stop && warp == kProducerWarp) {
+            // ======================================================== the feed
+            // A block is `pieces` pages, a copy each of K and of V; lane l describes page l % pieces of block
+            // l / pieces of a batch of 32 / pieces blocks.
+            const int piece = p.pool.page, pieces = BN / piece, per_batch = 32 / pieces;
+            uint32_t blocks = 0;
+            bool ok = !(p.drop_arrive && blockIdx.x == 0);
+            RaggedWalk w = first_segment();
+            do {
+                for (int j0 = w.j; ok && j0 < w.j1; j0 += per_batch) {
+                    const int j = j0 + lane / pieces;
+                    int64_t id = -1;
+                    float ks = 1.0f, lv = 0.0f;
+                    if (j < w.j1) {
+                        const int token = w.it.key0(j) + (lane % pieces) * piece;
+                        if (token < w.seq.n && ragged_sees(p, w.it, token, piece)) {
+                            id = p.pages[w.b * p.max_pages + (token >> p.pool.page_shift)];
+                            if (id < 0 || id >= p.pool.num_pages) {
+                                record_page_error();
+                                id = -1;
+                            } else {
+                                ks = p.pool.scales[0][id * p.pool.kv_heads + w.head];
+                                lv = log2f(fmaxf(p.pool.scales[1][id * p.pool.kv_heads + w.head], kMinScale));
+                            }
+                        }
+                    }
+                    const uint32_t there = __ballot_sync(0xffffffffu, id >= 0);
+                    const int64_t at = (id * p.pool.kv_heads + w.head) * p.pool.page * HD;
+                    for (int i = 0; i < per_batch && j0 + i < w.j1; ++i, ++blocks) {
+                        const uint32_t s = blocks % G::kRaw, ph = blocks / G::kRaw & 1u;
+                        const bool in = lane / pieces == i;
+                        const uint32_t mine = there >> (i * pieces) & ((1u << pieces) - 1);
+                        const uint32_t bytes = __popc(mine) * piece * HD;
+                        if (!wait_warp(raw_empty(0, s), ph ^ 1u, p.wait_limit_ns, abort_flag, kSiteProducerEmpty)) {
+                            ok = false;
+                            break;
+                        }
+                        RaggedMeta &m = metas[blocks % G::kMetas];
+                        if (in)
+                            for (int g = 0; g < piece / 16; ++g)
+                                m.scale[(lane % pieces) * (piece / 16) + g] = make_float2(ks, lv);
+                        if (lane == 0) {
+                            uint32_t gone = 0;
+                            for (int g = 0; g < kGroups; ++g)
+                                gone |= (mine >> (g * 16 / piece) & 1u) ? 0u : 1u << g;
+                            m.missing = gone;
+                        }
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(meta_full(blocks % G::kMetas));
+                            mbar_arrive_expect_tx(raw_full(0, s), bytes);
+                        }
+                        __syncwarp();
+                        const uint32_t off = s * G::kTile8 + (lane % pieces) * piece * HD;
+                        if (in && id >= 0)
+                            bulk_load(base + G::kOffRawK + off, p.pool.values[0] + at, piece * HD, raw_full(0, s));
+                        if (!wait_warp(raw_empty(1, s), ph ^ 1u, p.wait_limit_ns, abort_flag, kSiteProducerEmpty)) {
+                            ok = false;
+                            ++blocks;   // its K is on its way
+                            break;
+                        }
+                        if (lane == 0)
+                            mbar_arrive_expect_tx(raw_full(1, s), bytes);
+                        __syncwarp();
+                        if (in && id >= 0)
+                            bulk_load(base + G::kOffRawV + off, p.pool.values[1] + at, piece * HD, raw_full(1, s));
+                    }
+                }
+            } while (ok && w.next(p));
+            // Every copy issued has landed before the block may exit.  (After a wait that expired the last
+            // block's V was not asked for; waiting for it only runs into the limit again.)
+            for (uint32_t i = blocks > (uint32_t)G::kRaw ? blocks - G::kRaw : 0u; i < blocks; ++i) {
+                wait_drain(raw_full(0, i % G::kRaw), i / G::kRaw & 1u, p.wait_limit_ns, abort_flag);
+                if (ok || i + 1 < blocks)
+                    wait_drain(raw_full(1, i % G::kRaw), i / G::kRaw & 1u, p.wait_limit_ns, abort_flag);
+            }
+        } else if (start < stop && warp >= kConvWarp) {
+            // ======================================================== e4m3 to fp16
+            const int mine = warp - kConvWarp, row0 = 64 * mine;
+            uint32_t blocks = 0, segments = 0;
+            bool ok = true;
+            RaggedWalk w = first_segment();
+            do {
+                bool bad = false;
+                if (lane == 0)
+                    dirty[mine * 4 + (segments & 3u)] = 0u;
+                for (int j = w.j; ok && j < w.j1; ++j, ++blocks) {
+                    const uint32_t rs = blocks % G::kRaw, rp = blocks / G::kRaw & 1u;
+                    const uint32_t st = blocks & 1u, ph = blocks >> 1 & 1u;
+                    const int key0 = w.it.key0(j);
+                    ok = wait_warp(raw_full(0, rs), rp, p.wait_limit_ns, abort_flag, kSiteMmaFull) &&
+                         wait_warp(empty(0, st), ph ^ 1u, p.wait_limit_ns, abort_flag, kSiteProducerEmpty);
+                    if (!ok)
+                        break;
+                    convert_rows<HD, false>(base + G::kOffRawK + rs * G::kTile8, base + G::kOffK + st * G::kTile16,
+                                            row0, BN, 0u);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(raw_empty(0, rs));
+                        mbar_arrive(full(0, st));
+                    }
+                    ok = wait_warp(meta_full(blocks % G::kMetas), blocks / G::kMetas & 1u, p.wait_limit_ns, abort_flag,
+                                   kSiteMmaFull) &&
+                         wait_warp(raw_full(1, rs), rp, p.wait_limit_ns, abort_flag, kSiteMmaFull) &&
+                         wait_warp(empty(1, st), ph ^ 1u, p.wait_limit_ns, abort_flag, kSiteProducerEmpty);
+                    if (!ok)
+                        break;
+                    const uint32_t src = base + G::kOffRawV + rs * G::kTile8, dst = base + G::kOffV + st * G::kTile16;
+                    const uint32_t missing = metas[blocks % G::kMetas].missing;
+                    if (missing || ragged_masked(p, w.it.first, w.it.last, key0))
+                        bad = convert_rows<HD, true>(src, dst, row0, w.seq.n - key0, missing) || bad;
+                    else
+                        convert_rows<HD, false>(src, dst, row0, BN, 0u);
+                    if (bad)
+                        dirty[mine * 4 + (segments & 3u)] = 1u;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(raw_empty(1, rs));
+                        mbar_arrive(full(1, st));
+                    }
+                }
+                ++segments;
+            } while (ok && w.next(p));
+        } else if (start < stop && warp == kMmaWarp) {
+            // ======================================================== products
+            // (one elected thread issues, the whole warp walks along)
+            const bool leader = elect_one();
+            const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0);
+            const uint64_t q_desc = make_sdesc_sw128(base + G::kOffQ, 16, 1024);
+            const uint64_t k_desc = make_sdesc_sw128(base + G::kOffK, 16, 1024);
+            const uint64_t v_desc = make_sdesc_sw128(base + G::kOffV, kSub, 1024);
+            uint32_t turns0 = 0, turns1 = 0, segs0 = 0, segs1 = 0;
+            // S_t = Q_t K^T of block number i
+            auto score = [&](const uint32_t t, uint32_t i) {
+                const uint64_t qd = q_desc + t * (G::kTile16 >> 4), kd = k_desc + (i & 1u) * (G::kTile16 >> 4);
+#pragma unroll
+                for (int kk = 0; kk < HD / UKA; ++kk) {
+                    const uint32_t o = (kk / 4) * (kSub >> 4) + (kk % 4) * 2;
+                    if (leader)
+                        umma_f16(tmem + G::kTmemS + t * BN, qd + o, kd + o, G::kIdescS, kk > 0 ? 1u : 0u);
+                }
+                if (leader)
+                    umma_commit(s_full(t));
+            };
+            auto wait_q = [&](const uint32_t t, uint32_t &segs) {
+                const bool ok = wait_warp(q_full(t), segs++ & 1u, p.wait_limit_ns, abort_flag, kSiteMmaFull);
+                tc_fence_after_sync();
+                return ok;
+            };
+            auto wait_k = [&](uint32_t i) {
+                const bool ok = wait_warp(full(0, i & 1u), i >> 1 & 1u, p.wait_limit_ns, abort_flag, kSiteMmaFull);
+                tc_fence_after_sync();
+                return ok;
+            };
+            // O_t (+)= P_t V of block number i, P_t from TMEM (over S_t)
+            auto pv = [&](const uint32_t t, uint32_t i, bool fresh, bool complete, uint32_t &turns) {
+                if (!wait_warp(p_full(t), turns++ & 1u, p.wait_limit_ns, abort_flag, kSiteMmaAccEmpty))
+                    return false;
+                tc_fence_after_sync();
+                const uint64_t vd = v_desc + (i & 1u) * (G::kTile16 >> 4);
+                const uint32_t d_o = tmem + G::kTmemO + t * HD, a_p = tmem + G::kTmemS + t * BN;
+#pragma unroll
+                for (int kk = 0; kk < BN / UKA; ++kk)
+                    if (leader)
+                        umma_f16_ts(d_o, a_p + kk * (UKA / 2), vd + kk * ((UKA * 128) >> 4), G::kIdescO,
+                                    kk > 0 || !fresh ? 1u : 0u);
+                if (complete && leader)
+                    umma_commit(o_full(t));
+                return true;
+            };
+            RaggedWalk w = first_segment();
+            bool two = w.rows(p) > BM, more = true, ok = true;
+            int left = w.j1 - w.j;
+            uint32_t i = 0;
+            ok = wait_k(0) && wait_q(0, segs0);
+            if (ok)
+                score(0, 0);
+            if (ok && two) {
+                ok = wait_q(1, segs1);
+                if (ok)
+                    score(1, 0);
+            }
+            if (ok && leader)
+                umma_commit(empty(0, 0));
+            bool fresh = true;
+            while (ok && more) {
+                const bool last = left == 1;
+                bool next_two = two;
+                if (last) {   // the next block is another item's
+                    more = w.next(p);
+                    next_two = more && w.rows(p) > BM;
+                }
+                ok = wait_warp(full(1, i & 1u), i >> 1 & 1u, p.wait_limit_ns, abort_flag, kSiteMmaFull) &&
+                     pv(0, i, fresh, last, turns0);
+                if (ok && !last) {
+                    ok = wait_k(i + 1);
+                    if (ok)
+                        score(0, i + 1);
+                }
+                if (ok && two)
+                    ok = pv(1, i, fresh, last, turns1);
+                if (!ok)
+                    break;
+                if (leader)
+                    umma_commit(empty(1, i & 1u));
+                if (last && more) {
+                    ok = wait_k(i + 1) && wait_q(0, segs0);
+                    if (!ok)
+                        break;
+                    score(0, i + 1);
+                }
+                if (more && next_two) {
+                    if (last)
+                        ok = wait_q(1, segs1);
+                    if (!ok)
+                        break;
+                    score(1, i + 1);
+                }
+                if (more && leader)
+                    umma_commit(empty(0, (i + 1) & 1u));
+                fresh = last;
+                if (last && more) {
+                    left = w.j1 - w.j;
+                    two = next_two;
+                } else {
+                    --left;
+                }
+                ++i;
+            }
+            // all MMAs of this thread complete before TMEM can be released
+            if (leader)
+                umma_commit(drain_bar);
+            wait_drain(drain_bar, 0u, p.wait_limit_ns, abort_flag);
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        if (start < stop) {
+            // ======================================================== softmax / output
+            const int t = warp >> 2;                        // tile
+            const int q = warp & 3;                         // TMEM lanes 32q .. 32q+31
+            const uint32_t lane_base = (uint32_t)(32 * q) << 16;
+            const uint32_t s_addr = tmem_base + lane_base + G::kTmemS + t * BN;
+            const uint32_t o_addr = tmem_base + lane_base + G::kTmemO + t * HD;
+            const int my_row = t * BM + 32 * q + lane;      // row of the item
+            // The warp's 32 rows of Q into shared memory: HD / 8 lanes a row.  bf16 rows are scaled by a power of
+            // two that brings their largest element to [2^14, 2^15), within fp16; returned: what undoes it.
+            auto load_q = [&](const RaggedWalk &w) -> float {
+                constexpr int kLanes = HD / 8, kRows = 32 / kLanes;
+                const int rows = w.rows(p), sub = lane % kLanes;
+                float mine = 1.0f;
+#pragma unroll 4
+                for (int i = 0; i < 32 / kRows; ++i) {
+                    const int r = 32 * q + i * kRows + lane / kLanes, row = t * BM + r;   // of the tile, the item
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    if (row < rows) {
+                        const int token = p.by_group.quotient(w.item * 2 * BM + row);
+                        const int g = w.item * 2 * BM + row - token * p.group;
+                        x = *reinterpret_cast<const uint4 *>(p.q + (w.seq.start + token) * p.q_stride[0] +
+                                                             (w.head * p.group + g) * p.q_stride[1] + sub * 8);
+                    }
+                    if constexpr (kBf16) {
+                        uint32_t v[4] = {x.x, x.y, x.z, x.w};
+                        uint32_t top = 0;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            top = max(top, max(v[e] & 0x7fffu, (v[e] >> 16) & 0x7fffu));
+#pragma unroll
+                        for (int o = 1; o < kLanes; o <<= 1)
+                            top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        int e2 = (int)(top >> 7) - 127;
+                        e2 = e2 < -100 ? -100 : e2 > 127 ? 127 : e2;
+                        const float to = __uint_as_float((uint32_t)(14 - e2 + 127) << 23);
+                        const float back = __uint_as_float((uint32_t)(e2 - 14 + 127) << 23);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 f = pair_to_float2<true>(v[e]);
+                            v[e] = half2_of(f.x * to, f.y * to);
+                        }
+                        x = make_uint4(v[0], v[1], v[2], v[3]);
+                        const float got = __shfl_sync(0xffffffffu, back, (lane % kRows) * kLanes);
+                        mine = lane / kRows == i ? got : mine;
+                    }
+                    st_shared_v4(base + G::kOffQ + t * G::kTile16 + (sub >> 3) * kSub + r * 128 +
+                                     ((uint32_t)((sub & 7) ^ (r & 7)) << 4), x.x, x.y, x.z, x.w);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(q_full((uint32_t)t));
+                return mine;
+            };
+            uint32_t turns = 0, blocks = 0, segments = 0, outputs = 0;
+            bool alive = true;
+            RaggedWalk w = first_segment();
+            float row_scale = t == 0 || w.rows(p) > BM ? load_q(w) : 1.0f;
+            for (bool more = true; alive && more; ++segments) {
+                const RaggedWalk cur = w;
+                const int rows = cur.rows(p);
+                const bool here = t == 0 || rows > BM;
+                const int row = cur.item * 2 * BM + my_row;     // of the sequence and head
+                const int token = p.by_group.quotient(row);
+                const int off = cur.seq.n - cur.seq.count;
+                const int pos = my_row < rows ? off + token : -1;
+                const int first = off + p.by_group.quotient(cur.item * 2 * BM + t * BM);
+                const int last = off + p.by_group.quotient(min(cur.item * 2 * BM + t * BM + BM, cur.seq.count * p.group) - 1);
+                const float c_row = row_scale * p.scale_log2;
+                // of scores of keys with scale ks; not 0, which would make a NaN of a masked score
+                auto factor = [&](float ks) { return fmaxf(c_row * ks, 1.17549435e-38f); };
+                float m = -INFINITY, l = 0.0f;   // reference of the weights, their sum
+                float rr = 0.0f;                 // O's reference above m
+                for (int j = cur.j; here && j < cur.j1; ++j) {
+                    const uint32_t i = blocks + (j - cur.j);
+                    const bool ok = wait_bounded_eager(s_full((uint32_t)t), turns & 1u, p.wait_limit_ns, abort_flag,
+                                                       kSiteEpiAccFull) &&
+                                    wait_bounded_eager(meta_full(i % G::kMetas), i / G::kMetas & 1u, p.wait_limit_ns,
+                                                       abort_flag, kSiteEpiAccFull);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        alive = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    const RaggedMeta &meta = metas[i % G::kMetas];
+                    const int key0 = cur.it.key0(j);
+                    uint32_t v[BN];
+#pragma unroll
+                    for (int c0 = 0; c0 < BN; c0 += 32)
+                        tmem_ld_x32(s_addr + c0, *reinterpret_cast<uint32_t(*)[32]>(&v[c0]));
+#pragma unroll
+                    for (int c0 = 0; c0 < BN; c0 += 32)
+                        tmem_ld_wait_regs(*reinterpret_cast<uint32_t(*)[32]>(&v[c0]));
+                    const uint32_t missing = meta.missing;
+                    if (missing || ragged_masked(p, first, last, key0)) {
+                        // a bit per key, 32 at a time
+                        const int hi = pos - key0;
+                        const int lo = p.window > 0 ? hi - p.window : -1;
+                        const int head = p.sinks - key0;
+#pragma unroll
+                        for (int c0 = 0; c0 < BN; c0 += 32) {
+                            uint32_t seen = keys_below(hi + 1 - c0) & (~keys_below(lo + 1 - c0) | keys_below(head - c0));
+                            seen &= ~((missing >> (c0 / 16) & 1u ? 0x0000ffffu : 0u) |
+                                      (missing >> (c0 / 16 + 1) & 1u ? 0xffff0000u : 0u));
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                v[c0 + e] = seen & (1u << e) ? v[c0 + e] : __float_as_uint(-INFINITY);
+                        }
+                    }
+                    // the largest score of each 16 keys, in base 2
+                    float mx = -INFINITY, x16[kGroups];
+#pragma unroll
+                    for (int g = 0; g < kGroups; ++g) {
+                        float a = __uint_as_float(v[16 * g]), b = __uint_as_float(v[16 * g + 1]);
+#pragma unroll
+                        for (int e = 2; e < 16; e += 2) {
+                            a = fmaxf(a, __uint_as_float(v[16 * g + e]));
+                            b = fmaxf(b, __uint_as_float(v[16 * g + e + 1]));
+                        }
+                        x16[g] = __fmul_rn(fmaxf(a, b), factor(meta.scale[g].x));
+                        mx = fmaxf(mx, x16[g]);
+                    }
+                    const bool move = mx > m + kRescaleLog2;
+                    const float m_new = move ? mx : m;
+                    const float m_ref = m_new == -INFINITY ? 0.0f : m_new;
+                    const float shrink = move ? fast_exp2(m - m_new) : 1.0f;   // 0 at the first scores
+                    // O's reference: rr above m.  The first scores set it, later ones move it.
+                    const float rr_old = m == -INFINITY ? -INFINITY : move ? (m - m_new) + rr : rr;
+                    float over = -INFINITY;
+#pragma unroll
+                    for (int g = 0; g < kGroups; ++g)
+                        over = fmaxf(over, (x16[g] - m_ref) + meta.scale[g].y);
+                    const bool turn = over > rr_old + kRescaleLog2;
+                    const float rr_new = turn ? over : m_new == -INFINITY ? 0.0f : rr_old;
+                    const float alpha = turn ? fast_exp2(rr_old - rr_new) : 1.0f;
+                    float sub = m_ref;
+                    const bool big = __any_sync(0xffffffffu, fabsf(m_ref) >= kBigLog2);
+                    if (big) {
+#pragma unroll
+                        for (int g = 0; g < kGroups; ++g) {
+                            const float c = factor(meta.scale[g].x);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                v[16 * g + e] = __float_as_uint(
+                                    __fsub_rn(__fmul_rn(__uint_as_float(v[16 * g + e]), c), m_ref));
+                        }
+                        sub = 0.0f;
+                    }
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int g = 0; g < kGroups; ++g) {
+                        const float2 sc = meta.scale[g];
+                        const float c = big ? 1.0f : factor(sc.x);
+                        const float a = (sc.y + kPLog2 - rr_new) - sub;
+                        const float2 c2 = make_float2(c, c), a2 = make_float2(a, a);
+                        float2 sa = make_float2(0.0f, 0.0f), sb = make_float2(0.0f, 0.0f);
+                        uint32_t ph[8];
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4) {
+                            const float2 x01 = __ffma2_rn(make_float2(__uint_as_float(v[16 * g + e]),
+                                                                      __uint_as_float(v[16 * g + e + 1])), c2, a2);
+                            const float2 x23 = __ffma2_rn(make_float2(__uint_as_float(v[16 * g + e + 2]),
+                                                                      __uint_as_float(v[16 * g + e + 3])), c2, a2);
+                            const float2 e01 = make_float2(fast_exp2(x01.x), fast_exp2(x01.y));
+                            const float2 e23 = make_float2(fast_exp2(x23.x), fast_exp2(x23.y));
+                            sa = __fadd2_rn(sa, e01);
+                            sb = __fadd2_rn(sb, e23);
+                            ph[e / 2] = half2_of(e01.x, e01.y);
+                            ph[e / 2 + 1] = half2_of(e23.x, e23.y);
+                        }
+                        // (as weights relative to m; bounded, so that no sum of 0 meets an infinity)
+                        const float back = fast_exp2(fminf(rr_new - kPLog2 - sc.y, 126.0f));
+                        sum = fmaf((sa.x + sa.y) + (sb.x + sb.y), back, sum);
+                        tmem_st_x8(s_addr + 8 * g, ph);
+                    }
+                    l = l * shrink + sum;
+                    m = m_new;
+                    rr = rr_new;
+                    if (j > cur.j && __any_sync(0xffffffffu, turn)) {
+#pragma unroll 1
+                        for (int c0 = 0; c0 < HD; c0 += 32) {
+                            uint32_t o[32];
+                            tmem_ld_x32_sync(o_addr + c0, o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                            tmem_st_x32(o_addr + c0, o);
+                        }
+                    }
+                    tmem_st_wait();
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(p_full((uint32_t)t));
+                    ++turns;
+                }
+                if (!alive)
+                    break;
+                blocks += cur.j1 - cur.j;
+                // the next item's rows (the last scores of this one are done with Q)
+                more = w.next(p);
+                if (more && (t == 0 || w.rows(p) > BM))
+                    row_scale = load_q(w);
+                if (!here)
+                    continue;
+                if (!__all_sync(0xffffffffu, wait_bounded_eager(o_full((uint32_t)t), outputs & 1u, p.wait_limit_ns,
+                                                                abort_flag, kSiteEpiAccFull))) {
+                    alive = false;
+                    break;
+                }
+                ++outputs;
+                tc_fence_after_sync();
+                const bool taken = dirty[segments & 3u] | dirty[4 + (segments & 3u)];
+                if (taken)
+                    ragged_add_nan<HD>(p, cur.b, cur.head, cur.item, cur.j, cur.j1, pos, o_addr);
+                const bool valid = my_row < rows;
+                uint16_t *dst = p.out + ((int64_t)(cur.seq.start + token) * p.q_heads + cur.head * p.group +
+                                         (row - token * p.group)) * HD;
+                auto write_out = [&](int c0, const uint32_t (&o)[32], float inv, float f) {
+                    uint4 *d4 = reinterpret_cast<uint4 *>(dst + c0);
+                    if (valid)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t h[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                h[k] = pack_out<kBf16>(__uint_as_float(o[8 * e + 2 * k]) * inv * f * f,
+                                                       __uint_as_float(o[8 * e + 2 * k + 1]) * inv * f * f);
+                            d4[e] = make_uint4(h[0], h[1], h[2], h[3]);
+                        }
+                };
+                const bool whole = cur.j == 0 && cur.j1 == cur.nb;
+                if (whole) {
+                    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;   // 0: the row sees nothing
+                    const float f = exp2f(0.5f * (rr - kPLog2));
+#pragma unroll 1
+                    for (int c0 = 0; c0 < HD; c0 += 32) {
+                        uint32_t o[32];
+                        tmem_ld_x32_sync(o_addr + c0, o);
+                        write_out(c0, o, inv, f);
+                    }
+                } else {
+                    // a part: O, m, l and rr to the workspace; the warp that comes last joins the parts of its rows
+                    const int ranges = plan->ranges, total = plan->total;
+                    const int c_first = range_owner(cur.unit0, total, ranges);
+                    const int c_last = range_owner(cur.unit0 + cur.nb - 1, total, ranges);
+                    auto part_of = [&](int c) {
+                        const bool mid = c == c_first && cur.unit0 != range_start(c, total, ranges);
+                        return p.partial + ((int64_t)(2 * c + (mid ? 1 : 0)) * 8 + warp) * (HD + 4) * 32 + lane;
+                    };
+                    float *part = part_of(blockIdx.x);
+#pragma unroll 1
+                    for (int c0 = 0; c0 < HD; c0 += 32) {
+                        uint32_t o[32];
+                        tmem_ld_x32_sync(o_addr + c0, o);
+                        if (valid)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                __stcg(part + (c0 + e) * 32, __uint_as_float(o[e]));
+                    }
+                    if (valid) {
+                        __stcg(part + HD * 32, m);
+                        __stcg(part + (HD + 1) * 32, l);
+                        __stcg(part + (HD + 2) * 32, rr);
+                    }
+                    __syncwarp();
+                    unsigned before = 0;
+                    if (lane == 0)
+                        before = count_part(p.arrived + c_first * 8 + warp, (unsigned)(c_last - c_first));
+                    before = __shfl_sync(0xffffffffu, before, 0);
+                    __syncwarp();
+                    if (before == (unsigned)(c_last - c_first) && valid) {
+                        float mm = -INFINITY, yy = -INFINITY;   // the largest references
+                        for (int c = c_first; c <= c_last; ++c) {
+                            const float *x = part_of(c);
+                            const float pm = __ldcg(x + HD * 32);
+                            mm = fmaxf(mm, pm);
+                        }
+                        const float ref = mm == -INFINITY ? 0.0f : mm;
+                        for (int c = c_first; c <= c_last; ++c) {
+                            const float *x = part_of(c);
+                            const float pm = __ldcg(x + HD * 32);
+                            if (pm != -INFINITY)
+                                yy = fmaxf(yy, (pm - ref) + __ldcg(x + (HD + 2) * 32));
+                        }
+                        float ll = 0.0f;
+                        for (int c = c_first; c <= c_last; ++c) {
+                            const float *x = part_of(c);
+                            const float pm = __ldcg(x + HD * 32), pl = __ldcg(x + (HD + 1) * 32);
+                            ll += pl != pl ? pl : pm == -INFINITY ? 0.0f : pl * exp2f(pm - ref);
+                        }
+                        const float inv = ll > 0.0f || ll != ll ? 1.0f / ll : 0.0f;
+                        const float f = yy == -INFINITY ? 0.0f : exp2f(0.5f * (yy - kPLog2));
+#pragma unroll 1
+                        for (int c0 = 0; c0 < HD; c0 += 32) {
+                            float s[32];
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                s[e] = 0.0f;
+#pragma unroll 1
+                            for (int c = c_first; c <= c_last; ++c) {
+                                const float *x = part_of(c);
+                                const float pm = __ldcg(x + HD * 32);
+                                const float a = pm == -INFINITY ? 1.0f : exp2f((pm - ref) + __ldcg(x + (HD + 2) * 32) - yy);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    s[e] = fmaf(__ldcg(x + (c0 + e) * 32), a, s[e]);
+                            }
+                            uint32_t o[32];
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                o[e] = __float_as_uint(s[e]);
+                            write_out(c0, o, inv, f);
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+    }
+
+    // ---------------------------------------------------------------- teardown
+    __syncwarp();
+    tc_fence_before_sync();
+    named_bar_sync(1, kRaggedThreads);
+    tc_fence_after_sync();
+    if (warp == kMmaWarp)
+        tmem_dealloc(tmem_base, 512);
+}
+
+}  // namespace kvc
+}  // namespace gemmrelu

@@ -23,6 +23,7 @@
 #include "flash_attention.h"
 #include "gemm_relu.h"
 #include "kv_cache.h"
+#include "rotary.h"
 
 namespace {
 
@@ -33,6 +34,10 @@ decltype(&kv_cache_attention_x16_workspace_bytes) f_workspace_bytes;
 decltype(&kv_cache_evict_e4m3) f_evict;
 decltype(&gemm_relu_stream_capturing) f_capturing;
 decltype(&gemm_relu_stream_id) f_stream_id;
+decltype(&flash_attention_cross_x16) f_cross;
+decltype(&kv_cache_attention_ragged_x16) f_ragged;
+decltype(&kv_cache_attention_ragged_x16_workspace_bytes) f_ragged_bytes;
+decltype(&rotary_x16) f_rotary;
 PyObject *g_error, *g_no_memory;   // GemmReluError, torch.OutOfMemoryError
 
 struct Refusal {
@@ -225,13 +230,13 @@ size_t workspace_bytes(const at::Tensor &q, int64_t kv_heads, int64_t width) {
                             GEMMRELU_KV_COUNTER_BYTES);
 }
 
-at::Tensor new_workspace(const at::Tensor &q, size_t bytes) {
+at::Tensor new_workspace(const at::Tensor &q, size_t bytes, size_t counters) {
     at::Tensor w = at::empty({(int64_t)bytes}, q.options().dtype(at::kByte));
-    w.narrow(0, 0, GEMMRELU_KV_COUNTER_BYTES).zero_();
+    w.narrow(0, 0, (int64_t)counters).zero_();
     return w;
 }
 
-// Workspaces of calls that bring none, one per device and stream, as large as its calls needed so
+// Workspaces of calls that bring none, one per device, stream and operator, as large as its calls needed so
 // far: calls on a stream follow one another, and one that is replaced goes back to torch's
 // allocator for that stream.  A stream is known by its id, since two may share a handle.  Calls being
 // captured get their own, since their graph may run anywhere, and so do those that need more
@@ -241,17 +246,17 @@ at::Tensor new_workspace(const at::Tensor &q, size_t bytes) {
 constexpr size_t kKeep = (size_t)64 << 20;
 constexpr size_t kMostKept = 64;
 
-at::Tensor workspace_for(const at::Tensor &q, int64_t kv_heads, int64_t width, int d, void *stream) {
-    const size_t bytes = workspace_bytes(q, kv_heads, width);
+template <size_t kCounters>
+at::Tensor workspace_for(const at::Tensor &q, size_t bytes, int d, void *stream) {
     uint64_t id;
     if (bytes > kKeep || f_capturing(stream) || f_stream_id(stream, &id) != GEMMRELU_OK)
-        return new_workspace(q, bytes);
+        return new_workspace(q, bytes, kCounters);
     static auto *kept = new std::map<std::pair<int, uint64_t>, at::Tensor>;   // (the GIL is held)
     if (kept->size() >= kMostKept && kept->count({d, id}) == 0)
         kept->clear();
     at::Tensor &w = (*kept)[{d, id}];
     if (!w.defined() || w.nbytes() < bytes)
-        w = new_workspace(q, bytes);
+        w = new_workspace(q, bytes, kCounters);
     return w;
 }
 
@@ -289,7 +294,7 @@ PyObject *attention_impl(PyObject *const *a) {
         void *stream = stream_of(d);
         at::Tensor space;
         if (a[8] == Py_None) {
-            space = workspace_for(q, pool.kv_heads, width, d, stream);
+            space = workspace_for<GEMMRELU_KV_COUNTER_BYTES>(q, workspace_bytes(q, pool.kv_heads, width), d, stream);
         } else {
             space = tensor(a[8], "workspace");
             if (!on(space, d) || !space.is_contiguous())
@@ -309,7 +314,175 @@ PyObject *workspace_impl(PyObject *const *a) {
         refuse(PyExc_ValueError, "q must be [batch, tokens, q_heads, head_dim]");
     const kv_cache_pool pool = pool_of(a[1], d);
     const int64_t width = a[2] == Py_None ? 0 : tensor(a[2], "weights").size(-1);
-    return THPVariable_Wrap(new_workspace(q, workspace_bytes(q, pool.kv_heads, width)));
+    return THPVariable_Wrap(new_workspace(q, workspace_bytes(q, pool.kv_heads, width), GEMMRELU_KV_COUNTER_BYTES));
+}
+
+PyObject *ragged_impl(PyObject *const *a) {
+    const at::Tensor &q = tensor(a[1], "q");
+    const int64_t window = integer(a[5], "window"), sinks = integer(a[6], "sinks");
+    const int d = current_device_of(q), type = dtype_of(q);
+    if (type < 0)
+        refuse(PyExc_TypeError, "q must be float16 or bfloat16");
+    if (q.dim() != 3)
+        refuse(PyExc_ValueError, "q must be [rows, q_heads, head_dim]");
+    const kv_cache_pool pool = pool_of(a[0], d);
+    const int64_t rows = q.size(0), heads = q.size(1);
+    if (q.size(2) != pool.head_dim || pool.kv_heads == 0 || heads == 0 || heads % pool.kv_heads != 0)
+        refuse(PyExc_ValueError, "q has ", heads, " heads of ", q.size(2), ", the cache ", pool.kv_heads, " of ",
+               pool.head_dim);
+    if (window < 0 || sinks < 0)
+        refuse(PyExc_ValueError, "window and sinks must not be negative");
+    const at::Tensor &table = tensor(a[2], "pages");
+    const int64_t batch = table.dim() == 2 ? table.size(0) : -1;
+    int64_t max_pages = 0;
+    const int32_t *pages = ints(table, "pages", batch, d, &max_pages);
+    const int32_t *lengths = ints(tensor(a[3], "lengths"), "lengths", batch, d);
+    const int32_t *starts = ints(tensor(a[4], "starts"), "starts", batch + 1, d);
+    const at::Tensor o = output(q, a[7], d);
+    if (batch > 0 && rows > 0) {
+        const Strides s = strides_of(q.unsqueeze(0), "q");
+        void *stream = stream_of(d);
+        at::Tensor space;
+        if (a[8] == Py_None) {
+            space = workspace_for<GEMMRELU_RAGGED_COUNTER_BYTES>(q, f_ragged_bytes(pool.head_dim), d, stream);
+        } else {
+            space = tensor(a[8], "workspace");
+            if (!on(space, d) || !space.is_contiguous())
+                refuse(PyExc_ValueError, "workspace must be a contiguous tensor on cuda:", d);
+        }
+        done(f_ragged(&pool, q.data_ptr(), type, rows, heads, s.s + 1, o.data_ptr(), batch, starts, pages, max_pages,
+                      lengths, window, sinks, space.data_ptr(), space.nbytes(), stream),
+             "kv_cache_attention_ragged_x16");
+    }
+    return returned(o, a[7]);
+}
+
+PyObject *ragged_workspace_impl(PyObject *const *a) {
+    const at::Tensor &k = tensor(a[0], "cache k");
+    current_device_of(k);
+    const size_t bytes = k.dim() == 4 ? f_ragged_bytes(k.size(3)) : 0;
+    if (bytes == 0)
+        refuse(PyExc_ValueError, "no workspace for a cache of this shape, or on this device");
+    return THPVariable_Wrap(new_workspace(k, bytes, GEMMRELU_RAGGED_COUNTER_BYTES));
+}
+
+PyObject *cross_impl(PyObject *const *a) {
+    const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
+    const int d = current_device_of(q), type = dtype_of(q);
+    if (type < 0 || k.scalar_type() != q.scalar_type() || v.scalar_type() != q.scalar_type())
+        refuse(PyExc_TypeError, "q, k and v must all be float16 or all bfloat16");
+    if (q.dim() != 4 || k.dim() != 4 || v.sizes() != k.sizes() || !on(k, d) || !on(v, d))
+        refuse(PyExc_ValueError, "q must be [batch, q_seq, q_heads, d], k and v [batch, kv_seq, kv_heads, d], "
+                                 "all on one device");
+    const int64_t dim = q.size(3);
+    if (k.size(0) != q.size(0) || k.size(3) != dim || (dim != 64 && dim != 128) || k.size(2) == 0 ||
+        q.size(2) % k.size(2) != 0)
+        refuse(PyExc_ValueError, "shapes ", q.sizes(), " and ", k.sizes(), " do not go together");
+    const int32_t *lengths = a[3] == Py_None ? nullptr : ints(tensor(a[3], "lengths"), "lengths", q.size(0), d);
+    const at::Tensor o = output(q, a[4], d);
+    if (q.numel() > 0) {
+        const Strides qs = strides_of(q, "q"), ks = strides_of(k, "k"), vs = strides_of(v, "v");
+        done(f_cross(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), type, q.size(0), q.size(1), k.size(1),
+                     q.size(2), k.size(2), dim, qs.s, ks.s, vs.s, lengths, stream_of(d)),
+             "flash_attention_cross_x16");
+    }
+    return returned(o, a[4]);
+}
+
+// [batch, tokens, heads, head_dim] of a tensor that may lack its first axis.
+at::Tensor with_batch(const at::Tensor &t) { return t.dim() == 3 ? t.unsqueeze(0) : t; }
+
+// rotary's q or k, and where its result goes.
+struct Rotated {
+    at::Tensor x, y;
+    rotary_tensor t{};
+};
+
+Rotated rotated(PyObject *o, PyObject *out, const char *name, const at::Tensor &q, int d) {
+    Rotated r;
+    if (o == Py_None) {
+        if (out != Py_None)
+            refuse(PyExc_ValueError, "out has a tensor for ", name, ", which is not given");
+        return r;
+    }
+    r.x = tensor(o, name);
+    if (r.x.scalar_type() != q.scalar_type() || r.x.dim() != q.dim() || !on(r.x, d))
+        refuse(PyExc_ValueError, "q and k must have the same type and number of axes, on one device");
+    for (int64_t i = 0; i < q.dim(); ++i)
+        if (i != q.dim() - 2 && r.x.size(i) != q.size(i))
+            refuse(PyExc_ValueError, "shapes ", q.sizes(), " and ", r.x.sizes(), " do not go together");
+    if (out == Py_None) {
+        r.y = at::empty(r.x.sizes(), r.x.options());
+    } else {
+        r.y = tensor(out, "out");
+        if (r.y.sizes() != r.x.sizes() || r.y.scalar_type() != r.x.scalar_type() || !on(r.y, d))
+            refuse(PyExc_ValueError, "out must have the shape and type of ", name);
+    }
+    if (r.x.numel() == 0)
+        return r;
+    const at::Tensor x = with_batch(r.x), y = with_batch(r.y);
+    const Strides xs = strides_of(x, name), ys = strides_of(y, "out");
+    r.t.x = x.data_ptr();
+    r.t.y = y.data_ptr();
+    r.t.heads = x.size(2);
+    for (int i = 0; i < 3; ++i) {
+        if (y.size(i) > 1 && ys.s[i] == 0)
+            refuse(PyExc_ValueError, "out must not be expanded");
+        if (r.t.x == r.t.y && xs.s[i] != ys.s[i])
+            refuse(PyExc_ValueError, "out begins where ", name, " does, with other strides");
+        r.t.x_strides[i] = xs.s[i];
+        r.t.y_strides[i] = ys.s[i];
+    }
+    return r;
+}
+
+PyObject *rotary_impl(PyObject *const *a) {
+    const at::Tensor &q = tensor(a[0], "q"), &positions = tensor(a[2], "positions"), &freq = tensor(a[3], "inv_freq");
+    const int d = current_device_of(q), type = dtype_of(q);
+    if (type < 0)
+        refuse(PyExc_TypeError, "q and k must be float16 or bfloat16");
+    if (q.dim() != 3 && q.dim() != 4)
+        refuse(PyExc_ValueError, "q must be [batch, tokens, heads, head_dim] or [rows, heads, head_dim]");
+    const int64_t dim = q.size(-1);
+    if (dim < 8 || dim > 512 || dim % 8 != 0)
+        refuse(PyExc_ValueError, "head_dim must be a multiple of 8, at most 512: got ", dim);
+    const auto pt = positions.scalar_type(), ft = freq.scalar_type();
+    if ((pt != at::kInt && pt != at::kLong) || !positions.is_contiguous() || !on(positions, d) ||
+        positions.sizes() != q.sizes().slice(0, q.dim() - 2))
+        refuse(PyExc_ValueError, "positions must be a contiguous int32 or int64 tensor ",
+               q.sizes().slice(0, q.dim() - 2), " on cuda:", d);
+    if ((ft != at::kFloat && ft != at::kDouble) || freq.dim() != 1 || !freq.is_contiguous() || !on(freq, d) ||
+        freq.size(0) < 1 || 2 * freq.size(0) > dim)
+        refuse(PyExc_ValueError, "inv_freq must be a contiguous float32 or float64 tensor of 1 to ", dim / 2,
+               " frequencies on cuda:", d);
+    const double amplitude = PyFloat_AsDouble(a[5]);
+    if (amplitude == -1.0 && PyErr_Occurred()) {
+        PyErr_Clear();
+        refuse(PyExc_TypeError, "amplitude must be a number");
+    }
+    PyObject *oq = Py_None, *ok = Py_None;
+    if (a[7] != Py_None) {
+        if (!PyTuple_Check(a[7]) || PyTuple_GET_SIZE(a[7]) != 2)
+            refuse(PyExc_TypeError, "out is a tuple (for q, for k)");
+        oq = PyTuple_GET_ITEM(a[7], 0);
+        ok = PyTuple_GET_ITEM(a[7], 1);
+    }
+    const Rotated rq = rotated(a[0], oq, "q", q, d), rk = rotated(a[1], ok, "k", q, d);
+    const int interleaved = PyObject_IsTrue(a[4]), inverse = PyObject_IsTrue(a[6]);
+    if (interleaved < 0 || inverse < 0)
+        throw Raised{};
+    if (rq.t.heads + rk.t.heads > 0)
+        done(f_rotary(&rq.t, &rk.t, type, q.dim() == 3 ? 1 : q.size(0), q.size(q.dim() - 3), dim, 2 * freq.size(0),
+                      interleaved, positions.data_ptr(), pt == at::kLong ? GEMMRELU_POS_I64 : GEMMRELU_POS_I32,
+                      freq.data_ptr(), ft == at::kDouble ? GEMMRELU_FREQ_F64 : GEMMRELU_FREQ_F32, amplitude, inverse,
+                      stream_of(d)),
+             "rotary_x16");
+    PyObject *y = returned(rq.y, oq);
+    PyObject *z = a[1] == Py_None ? (Py_INCREF(Py_None), Py_None) : returned(rk.y, ok);
+    PyObject *r = y && z ? PyTuple_Pack(2, y, z) : nullptr;
+    Py_XDECREF(y);
+    Py_XDECREF(z);
+    return r;
 }
 
 PyObject *evict_impl(PyObject *const *a) {
@@ -373,11 +546,12 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     return nullptr;
 }
 
-// bind(GemmReluError, torch.OutOfMemoryError, addresses of the seven library functions in the order below)
+// bind(GemmReluError, torch.OutOfMemoryError, addresses of the eleven library functions in the order below)
 PyObject *bind(PyObject *, PyObject *args) {
     PyObject *error, *no_memory;
-    unsigned long long f[7];
-    if (!PyArg_ParseTuple(args, "OOKKKKKKK", &error, &no_memory, &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6]))
+    unsigned long long f[11];
+    if (!PyArg_ParseTuple(args, "OOKKKKKKKKKKK", &error, &no_memory, &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6],
+                          &f[7], &f[8], &f[9], &f[10]))
         return nullptr;
     f_window = reinterpret_cast<decltype(f_window)>((uintptr_t)f[0]);
     f_append = reinterpret_cast<decltype(f_append)>((uintptr_t)f[1]);
@@ -386,6 +560,10 @@ PyObject *bind(PyObject *, PyObject *args) {
     f_evict = reinterpret_cast<decltype(f_evict)>((uintptr_t)f[4]);
     f_capturing = reinterpret_cast<decltype(f_capturing)>((uintptr_t)f[5]);
     f_stream_id = reinterpret_cast<decltype(f_stream_id)>((uintptr_t)f[6]);
+    f_cross = reinterpret_cast<decltype(f_cross)>((uintptr_t)f[7]);
+    f_ragged = reinterpret_cast<decltype(f_ragged)>((uintptr_t)f[8]);
+    f_ragged_bytes = reinterpret_cast<decltype(f_ragged_bytes)>((uintptr_t)f[9]);
+    f_rotary = reinterpret_cast<decltype(f_rotary)>((uintptr_t)f[10]);
     Py_INCREF(error);
     Py_INCREF(no_memory);
     g_error = error;
@@ -402,6 +580,10 @@ PyMethodDef methods[] = {
     ENTRY("attention", attention_impl, 9),
     ENTRY("workspace", workspace_impl, 3),
     ENTRY("evict", evict_impl, 9),
+    ENTRY("cross", cross_impl, 5),
+    ENTRY("ragged", ragged_impl, 9),
+    ENTRY("ragged_workspace", ragged_workspace_impl, 1),
+    ENTRY("rotary", rotary_impl, 8),
     {"bind", bind, METH_VARARGS, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
