@@ -17,18 +17,38 @@ using attn::BM;
 using attn::BN;
 using attn::kSub;
 
-constexpr int kRaggedThreads = attn::kWindowThreads;
-constexpr int kConvWarp = 10, kConvWarps = 2;   // converting warps: 10, 11
+// Four warpgroups: two of softmax, one with the feed's and the issuer's warp, one that converts.  512 threads launch
+// with 128 registers: 2 * 208 + 2 * 48 = 4 * 128.
+constexpr int kRaggedThreads = 512;
+constexpr int kConvWarp = 12, kConvWarps = 4;
+constexpr int kRaggedSoftmaxRegs = 208, kRaggedFeedRegs = 48, kRaggedConvRegs = 48;
+static_assert(2 * kRaggedSoftmaxRegs + kRaggedFeedRegs + kRaggedConvRegs <= 4 * 128, "registers given back cover those taken");
 constexpr int kGroups = BN / 16;                // pieces of 16 tokens of a block: the smallest page
 constexpr int kRaggedMaxCtas = GEMMRELU_RAGGED_COUNTER_BYTES / (8 * (int)sizeof(unsigned));
 constexpr int kRaggedMaxBatch = 16384;          // sequences whose units fit the scratch of the start
 constexpr float kBigLog2 = 2048.0f;             // 2^11: scores from here on are referred before V's scale is added
 
-// Scales of a block, a pair (ks, log2 vs) for each 16 tokens, and a bit for each that is not there.
+// What the feed says of a block.
+//
+// Where its scales are powers of two at most 2^14 apart (kNearScales) the conversion to fp16 brings all keys
+// to the largest of K and the largest of V, exactly: e4m3's least value 2^-9 becomes 2^-23 at least.  Elsewhere
+// the conversion leaves the values alone and every 16 keys have scales of their own.
+enum RaggedFlags : uint32_t {
+    kNearScales = 1,
+    kInPart = 4,                        // some row of the item does not see some key
+    kFirst = 8, kLast = 16,             // of its segment
+    kBothTiles = 32,                    // the item has rows in its second tile
+};
+
 struct RaggedMeta {
-    float2 scale[kGroups];
-    uint32_t missing;
-    uint32_t pad;
+    uint32_t flags;
+    float ks, lv;                  // kNearScales: the block's scale of K, log2 of that of V
+    uint32_t missing;              // a bit for every 16 keys that are not there
+    int valid;                     // keys up to the sequence's end
+    uint32_t segment;              // segments before this one
+    uint32_t pad[2];
+    uint32_t mul[2][kGroups];      // kNearScales: the factors of K and V, twice fp16
+    float2 scale[kGroups];         // (ks, log2 vs)
 };
 
 template <int HD>
@@ -52,7 +72,7 @@ struct RaggedCfg {
     // meta_full[kMetas]; q_full, s_full, p_full, o_full [2]; drain
     static constexpr uint32_t kNumBars = 4 * kRaw + 8 + kMetas + 8 + 1;
     static constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;
-    static constexpr uint32_t kSmem = kOffMisc + 256 + 1024;
+    static constexpr uint32_t kSmem = kOffMisc + 384 + 1024;
     static constexpr uint32_t kTmemS = 0, kTmemO = 2 * BN;
     static constexpr uint32_t kIdescS = make_idesc_f16_f32(BM, BN, 0, 0);
     static constexpr uint32_t kIdescO = make_idesc_f16_f32(BM, HD, 0, 1);
@@ -167,6 +187,16 @@ struct RaggedWalk {
     }
 };
 
+// How many of the launched CTAs get a range.  An item of n blocks cut into x parts takes about n / x blocks and the
+// join of x parts one after the other, which costs about 0.4 blocks each: x = sqrt(2.5 n) is the least.
+__device__ __forceinline__ int ragged_ranges(int total, float items, int grid) {
+    const float most = sqrtf(2.5f * (float)total * items);
+    int n = min(total, grid);
+    if (most < (float)n)
+        n = (int)most;
+    return max(n, 1);
+}
+
 // What the start works out, in shared memory.
 struct RaggedPlan {
     int b, head, item, j, unit0, start, stop, total, ranges;
@@ -227,45 +257,110 @@ __device__ __noinline__ void ragged_add_nan(const RaggedParams &p, int b, int he
     }
 }
 
+// ---------------------------------------------------------------- weights, the rare cases
+
+// What scores of keys with scale ks are multiplied by; not 0, which would make a NaN of a score of -infinity.
+__device__ __forceinline__ float score_factor(float c_row, float ks) { return fmaxf(c_row * ks, 1.17549435e-38f); }
+
+// What brings a sum of P (weights times V's scale, relative to O's reference) back to weights relative to m; bounded, so
+// that no sum of 0 meets an infinity.
+__device__ __forceinline__ float back_of(float rr, float lv) { return attn::fast_exp2(fminf(rr - kPLog2 - lv, 126.0f)); }
+
+// A block whose scales are far apart: its largest score (x), and the largest score plus log2 of V's scale (y) relative to
+// m_ref.
+__device__ __forceinline__ float2 ragged_top(uint32_t s_addr, const RaggedMeta &meta, float c_row, float m_ref) {
+    float mx = -INFINITY, over = -INFINITY;
+#pragma unroll 1
+    for (int g = 0; g < kGroups; ++g) {
+        uint32_t v[16];
+        tmem_ld_x16(s_addr + 16 * g, v);
+        tmem_ld_wait_regs16(v);
+        float a = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            a = fmaxf(a, __uint_as_float(v[e]));
+        const float2 sc = meta.scale[g];
+        const float x = __fmul_rn(a, score_factor(c_row, sc.x));
+        mx = fmaxf(mx, x);
+        over = fmaxf(over, (x - m_ref) + sc.y);
+    }
+    return make_float2(mx, over);
+}
+
+// P and its sum for a block whose scales are far apart, or for scores of 2^11 and more: there the product and the
+// reference are rounded before they are subtracted, and V's scale comes last.
+__device__ __forceinline__ float ragged_weights(uint32_t s_addr, const RaggedMeta &meta, float c_row, float m_ref, float rr) {
+    const bool near = meta.flags & kNearScales;
+    float sum = 0.0f;
+#pragma unroll 1
+    for (int g = 0; g < kGroups; ++g) {
+        const float2 sc = near ? make_float2(meta.ks, meta.lv) : meta.scale[g];
+        const float c = score_factor(c_row, sc.x), a = sc.y + kPLog2 - rr;
+        uint32_t v[16], ph[8];
+        tmem_ld_x16(s_addr + 16 * g, v);
+        tmem_ld_wait_regs16(v);
+        float part = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+            const float x = attn::fast_exp2(__fsub_rn(__fmul_rn(__uint_as_float(v[e]), c), m_ref) + a);
+            const float y = attn::fast_exp2(__fsub_rn(__fmul_rn(__uint_as_float(v[e + 1]), c), m_ref) + a);
+            part += x + y;
+            ph[e / 2] = half2_of(x, y);
+        }
+        tmem_st_x8(s_addr + 8 * g, ph);   // (over scores that have been read)
+        sum = fmaf(part, back_of(rr, sc.y), sum);
+    }
+    return sum;
+}
+
 // ---------------------------------------------------------------- e4m3 to fp16
 
-// Rows [row0, row0 + 64) of a block: bytes at `src` (rows of HD) become fp16 in the sub-tiles of 64
+// Rows [row0, row0 + BN / kConvWarps) of a block: bytes at `src` (rows of HD) become fp16 in the sub-tiles of 64
 // columns at `dst`, 128-byte swizzled, the layout of both products' B operands.  Four lanes take 64 bytes
 // of an even row and four the other half of the next one, so that eight lanes that load or store
-// together touch all banks once.  kCheck: rows past the sequence's end or of pages that are not there become 0
-// and so do NaN; true if the lane met one.
+// together touch all banks once.  Row r is multiplied by mul[r / 16].  kCheck: rows past the sequence's end or of pages
+// that are not there become 0 and so do NaN; true if the lane met one.
 template <int HD, bool kCheck>
-__device__ __forceinline__ bool convert_rows(uint32_t src, uint32_t dst, int row0, int valid, uint32_t missing) {
+__device__ __forceinline__ bool convert_rows(uint32_t src, uint32_t dst, int row0, const uint32_t *mul, int valid,
+                                             uint32_t missing) {
     const int lane = threadIdx.x & 31;
-    const int odd = (lane >> 2) & 1, c4 = lane & 3;
-    uint32_t bad = 0;
+    const int odd = (lane >> 2) & 1, c4 = lane & 3, row1 = row0 + 2 * (lane >> 3) + odd;
     constexpr int kHalves = HD / 64;
-#pragma unroll 4
-    for (int i = 0; i < 64 / 8 * kHalves; ++i) {
-        const int row = row0 + (i / kHalves) * 8 + 2 * (lane >> 3) + odd;
-        const int half = kHalves == 1 ? 0 : (odd ^ (i & 1));
-        const uint4 x = ld_shared_v4(src + row * HD + half * 64 + c4 * 16);
-        uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        if constexpr (kCheck) {
-            const bool there = row < valid && !(missing >> (row >> 4) & 1u);
+    uint32_t bad = 0;
+    src += row1 * HD + c4 * 16;
+    dst += row1 * 128 + ((uint32_t)((2 * c4) ^ (row1 & 7)) << 4);   // (row & 7 does not change below)
+#pragma unroll 2
+    for (int i = 0; i < BN / kConvWarps / 8; ++i) {
+        const int row = row1 + 8 * i;
+        const uint32_t m = mul[row >> 4];
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) {
+            const int half = kHalves == 1 ? 0 : (odd ^ h);
+            const uint4 x = ld_shared_v4(src + 8 * i * HD + half * 64);
+            uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            if constexpr (kCheck) {
+                const bool there = row < valid && !(missing >> (row >> 4) & 1u);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    w[e] = there ? w[e] : 0u;
+                    const uint32_t n = nan_bytes(w[e]);
+                    bad |= n;
+                    w[e] &= ~((n >> 7) * 0xffu);
+                }
+            }
+            uint32_t y[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                w[e] = there ? w[e] : 0u;
-                const uint32_t n = nan_bytes(w[e]);
-                bad |= n;
-                w[e] &= ~((n >> 7) * 0xffu);
+                y[2 * e] = e4m3x2_to_half2(w[e] & 0xffffu);
+                y[2 * e + 1] = e4m3x2_to_half2(w[e] >> 16);
             }
-        }
-        uint32_t h[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            h[2 * e] = e4m3x2_to_half2(w[e] & 0xffffu);
-            h[2 * e + 1] = e4m3x2_to_half2(w[e] >> 16);
+            for (int e = 0; e < 8; ++e)
+                asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(y[e]) : "r"(m));
+            const uint32_t at = dst + 1024 * i + half * kSub;
+            st_shared_v4(at, y[0], y[1], y[2], y[3]);
+            st_shared_v4(at ^ 16u, y[4], y[5], y[6], y[7]);
         }
-        const uint32_t at = dst + half * kSub + row * 128;
-        const uint32_t chunk = (uint32_t)((2 * c4) ^ (row & 7)) << 4;
-        st_shared_v4(at + chunk, h[0], h[1], h[2], h[3]);
-        st_shared_v4(at + (chunk ^ 16u), h[4], h[5], h[6], h[7]);
     }
     return bad != 0;
 }
@@ -298,9 +393,9 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
     RaggedMeta *metas = reinterpret_cast<RaggedMeta *>(gbase + G::kOffMeta);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + G::kOffMisc);
     volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(gbase + G::kOffMisc + 4);
-    volatile uint32_t *dirty = reinterpret_cast<volatile uint32_t *>(gbase + G::kOffMisc + 16);   // [2][4]
-    RaggedPlan *plan = reinterpret_cast<RaggedPlan *>(gbase + G::kOffMisc + 48);
-    long long *sums = reinterpret_cast<long long *>(gbase + G::kOffMisc + 96);                    // [12]
+    volatile uint32_t *dirty = reinterpret_cast<volatile uint32_t *>(gbase + G::kOffMisc + 16);   // [4][4]
+    RaggedPlan *plan = reinterpret_cast<RaggedPlan *>(gbase + G::kOffMisc + 80);
+    long long *sums = reinterpret_cast<long long *>(gbase + G::kOffMisc + 128);   // [2][16]: + 256
 
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);   // uniform
     const int lane = threadIdx.x & 31;
@@ -338,7 +433,7 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
     // sequence, a lane each; those of long chunks are summed by a warp.
     int *units = reinterpret_cast<int *>(gbase + G::kOffK);
     {
-        long long mine = 0;
+        long long mine = 0, items = 0;
         for (int b0 = warp * 32; b0 < p.batch; b0 += kRaggedThreads) {
             const int b = b0 + lane;
             RaggedSeq s{0, 0, 0, 0};
@@ -364,28 +459,36 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
             if (b < p.batch)
                 units[b] = (int)u;
             mine += u;
+            items += s.items;
         }
-        for (int o = 16; o; o >>= 1)
+        for (int o = 16; o; o >>= 1) {
             mine += __shfl_xor_sync(0xffffffffu, mine, o);
-        if (lane == 0)
+            items += __shfl_xor_sync(0xffffffffu, items, o);
+        }
+        if (lane == 0) {
             sums[warp] = mine;
+            sums[16 + warp] = items;
+        }
     }
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
     if (warp == 0) {
-        long long all = 0;
-        for (int w = 0; w < kRaggedThreads / 32; ++w)
+        long long all = 0, items = 0;
+        for (int w = 0; w < kRaggedThreads / 32; ++w) {
             all += sums[w];
+            items += sums[16 + w];
+        }
         all *= p.pool.kv_heads;
+        items *= p.pool.kv_heads;
         if (all > 0x7fffffffll) {   // rows that several sequences claim
             if (lane == 0)
                 record_page_error();
             all = 0;
         }
         const int total = (int)all;
-        const int ranges = max(1, min(total, (int)gridDim.x));
+        const int ranges = ragged_ranges(total, (float)items, gridDim.x);
         const int c = blockIdx.x;
         const int start = c < ranges ? range_start(c, total, ranges) : total;
         const int stop = c < ranges ? range_start(c + 1, total, ranges) : total;
@@ -451,20 +554,23 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
     };
 
     if (warp >= kProducerWarp) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp >= kConvWarp)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRaggedConvRegs));
+        else
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRaggedFeedRegs));
         if (start < stop && warp == kProducerWarp) {
             // ======================================================== the feed
             // A block is `pieces` pages, a copy each of K and of V; lane l describes page l % pieces of block
             // l / pieces of a batch of 32 / pieces blocks.
             const int piece = p.pool.page, pieces = BN / piece, per_batch = 32 / pieces;
-            uint32_t blocks = 0;
+            uint32_t blocks = 0, segment = 0;
             bool ok = !(p.drop_arrive && blockIdx.x == 0);
             RaggedWalk w = first_segment();
             do {
                 for (int j0 = w.j; ok && j0 < w.j1; j0 += per_batch) {
                     const int j = j0 + lane / pieces;
                     int64_t id = -1;
-                    float ks = 1.0f, lv = 0.0f;
+                    float ks = 0.0f, vs = 0.0f;
                     if (j < w.j1) {
                         const int token = w.it.key0(j) + (lane % pieces) * piece;
                         if (token < w.seq.n && ragged_sees(p, w.it, token, piece)) {
@@ -474,30 +580,66 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
                                 id = -1;
                             } else {
                                 ks = p.pool.scales[0][id * p.pool.kv_heads + w.head];
-                                lv = log2f(fmaxf(p.pool.scales[1][id * p.pool.kv_heads + w.head], kMinScale));
+                                vs = p.pool.scales[1][id * p.pool.kv_heads + w.head];
                             }
                         }
                     }
                     const uint32_t there = __ballot_sync(0xffffffffu, id >= 0);
+                    // the block's largest scales, and how far this page's are below
+                    float ks_top = ks, vs_top = vs;
+                    for (int o = 1; o < pieces; o <<= 1) {
+                        ks_top = fmaxf(ks_top, __shfl_xor_sync(0xffffffffu, ks_top, o));
+                        vs_top = fmaxf(vs_top, __shfl_xor_sync(0xffffffffu, vs_top, o));
+                    }
+                    if (id < 0) {
+                        ks = ks_top > 0.0f ? ks_top : 1.0f;
+                        vs = vs_top > 0.0f ? vs_top : 1.0f;
+                    }
+                    const uint32_t k_bits = __float_as_uint(ks), v_bits = __float_as_uint(vs);
+                    const int k_below = (int)(__float_as_uint(fmaxf(ks_top, ks)) - k_bits) >> 23;
+                    const int v_below = (int)(__float_as_uint(fmaxf(vs_top, vs)) - v_bits) >> 23;
+                    const bool fits = ks > 0.0f && vs > 0.0f && ((k_bits | v_bits) & 0x7fffffu) == 0 && k_below <= 14 &&
+                                      v_below <= 14;
+                    const uint32_t near = __ballot_sync(0xffffffffu, fits);
+                    const uint32_t block = (1u << pieces) - 1;
+                    const bool all_fit = (near >> (lane & ~(pieces - 1)) & block) == block;
+                    const uint32_t k_mul = (uint32_t)(all_fit ? 15 - k_below : 15) << 10;   // 2^-k_below, or 1
+                    const uint32_t v_mul = (uint32_t)(all_fit ? 15 - v_below : 15) << 10;
+                    const float lv = log2f(fmaxf(vs, kMinScale)), lv_top = log2f(fmaxf(fmaxf(vs_top, vs), kMinScale));
+                    ks_top = fmaxf(ks_top, ks);
                     const int64_t at = (id * p.pool.kv_heads + w.head) * p.pool.page * HD;
                     for (int i = 0; i < per_batch && j0 + i < w.j1; ++i, ++blocks) {
                         const uint32_t s = blocks % G::kRaw, ph = blocks / G::kRaw & 1u;
                         const bool in = lane / pieces == i;
-                        const uint32_t mine = there >> (i * pieces) & ((1u << pieces) - 1);
+                        const uint32_t mine = there >> (i * pieces) & block;
                         const uint32_t bytes = __popc(mine) * piece * HD;
                         if (!wait_warp(raw_empty(0, s), ph ^ 1u, p.wait_limit_ns, abort_flag, kSiteProducerEmpty)) {
                             ok = false;
                             break;
                         }
                         RaggedMeta &m = metas[blocks % G::kMetas];
-                        if (in)
-                            for (int g = 0; g < piece / 16; ++g)
-                                m.scale[(lane % pieces) * (piece / 16) + g] = make_float2(ks, lv);
-                        if (lane == 0) {
-                            uint32_t gone = 0;
-                            for (int g = 0; g < kGroups; ++g)
-                                gone |= (mine >> (g * 16 / piece) & 1u) ? 0u : 1u << g;
-                            m.missing = gone;
+                        if (in) {
+                            for (int x = 0; x < piece / 16; ++x) {
+                                const int g = (lane % pieces) * (piece / 16) + x;
+                                m.scale[g] = make_float2(ks, lv);
+                                m.mul[0][g] = k_mul * 0x10001u;
+                                m.mul[1][g] = v_mul * 0x10001u;
+                            }
+                            if (lane % pieces == 0) {
+                                const int at = j0 + i, key0 = w.it.key0(at);
+                                uint32_t gone = 0;
+                                for (int g = 0; g < kGroups; ++g)
+                                    gone |= (mine >> (g * 16 / piece) & 1u) ? 0u : 1u << g;
+                                const bool part = gone || ragged_masked(p, w.it.first, w.it.last, key0);
+                                m.flags = (all_fit ? kNearScales : 0) |
+                                          (part ? kInPart : 0) | (at == w.j ? kFirst : 0) |
+                                          (at + 1 == w.j1 ? kLast : 0) | (w.rows(p) > BM ? kBothTiles : 0);
+                                m.ks = ks_top;
+                                m.lv = lv_top;
+                                m.missing = gone;
+                                m.valid = w.seq.n - key0;
+                                m.segment = segment;
+                            }
                         }
                         __syncwarp();
                         if (lane == 0) {
@@ -520,6 +662,7 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
                             bulk_load(base + G::kOffRawV + off, p.pool.values[1] + at, piece * HD, raw_full(1, s));
                     }
                 }
+                ++segment;
             } while (ok && w.next(p));
             // Every copy issued has landed before the block may exit.  (After a wait that expired the last
             // block's V was not asked for; waiting for it only runs into the limit again.)
@@ -530,53 +673,44 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
             }
         } else if (start < stop && warp >= kConvWarp) {
             // ======================================================== e4m3 to fp16
-            const int mine = warp - kConvWarp, row0 = 64 * mine;
-            uint32_t blocks = 0, segments = 0;
-            bool ok = true;
-            RaggedWalk w = first_segment();
-            do {
-                bool bad = false;
-                if (lane == 0)
-                    dirty[mine * 4 + (segments & 3u)] = 0u;
-                for (int j = w.j; ok && j < w.j1; ++j, ++blocks) {
-                    const uint32_t rs = blocks % G::kRaw, rp = blocks / G::kRaw & 1u;
-                    const uint32_t st = blocks & 1u, ph = blocks >> 1 & 1u;
-                    const int key0 = w.it.key0(j);
-                    ok = wait_warp(raw_full(0, rs), rp, p.wait_limit_ns, abort_flag, kSiteMmaFull) &&
-                         wait_warp(empty(0, st), ph ^ 1u, p.wait_limit_ns, abort_flag, kSiteProducerEmpty);
+            const int mine = warp - kConvWarp, row0 = BN / kConvWarps * mine;
+            bool ok = true, bad = false;
+            for (uint32_t i = 0; ok && i < (uint32_t)(stop - start); ++i) {
+                const uint32_t rs = i % G::kRaw, rp = i / G::kRaw & 1u, st = i & 1u, ph = i >> 1 & 1u;
+                ok = wait_warp(meta_full(i % G::kMetas), i / G::kMetas & 1u, p.wait_limit_ns, abort_flag,
+                               kSiteMmaFull);
+                if (!ok)
+                    break;
+                const RaggedMeta &meta = metas[i % G::kMetas];
+                const uint32_t flags = meta.flags;
+#pragma unroll 1
+                for (int kv = 0; ok && kv < 2; ++kv) {
+                    ok = wait_warp(raw_full(kv, rs), rp, p.wait_limit_ns, abort_flag, kSiteMmaFull) &&
+                         wait_warp(empty(kv, st), ph ^ 1u, p.wait_limit_ns, abort_flag, kSiteProducerEmpty);
                     if (!ok)
                         break;
-                    convert_rows<HD, false>(base + G::kOffRawK + rs * G::kTile8, base + G::kOffK + st * G::kTile16,
-                                            row0, BN, 0u);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(raw_empty(0, rs));
-                        mbar_arrive(full(0, st));
+                    const uint32_t src = base + (kv ? G::kOffRawV : G::kOffRawK) + rs * G::kTile8;
+                    const uint32_t dst = base + (kv ? G::kOffV : G::kOffK) + st * G::kTile16;
+                    if (kv && flags & kInPart) {
+                        bad = convert_rows<HD, true>(src, dst, row0, meta.mul[1], meta.valid, meta.missing) ||
+                              (bad && !(flags & kFirst));
+                    } else {
+                        bad = bad && !(kv && flags & kFirst);
+                        convert_rows<HD, false>(src, dst, row0, meta.mul[kv], BN, 0u);
                     }
-                    ok = wait_warp(meta_full(blocks % G::kMetas), blocks / G::kMetas & 1u, p.wait_limit_ns, abort_flag,
-                                   kSiteMmaFull) &&
-                         wait_warp(raw_full(1, rs), rp, p.wait_limit_ns, abort_flag, kSiteMmaFull) &&
-                         wait_warp(empty(1, st), ph ^ 1u, p.wait_limit_ns, abort_flag, kSiteProducerEmpty);
-                    if (!ok)
-                        break;
-                    const uint32_t src = base + G::kOffRawV + rs * G::kTile8, dst = base + G::kOffV + st * G::kTile16;
-                    const uint32_t missing = metas[blocks % G::kMetas].missing;
-                    if (missing || ragged_masked(p, w.it.first, w.it.last, key0))
-                        bad = convert_rows<HD, true>(src, dst, row0, w.seq.n - key0, missing) || bad;
-                    else
-                        convert_rows<HD, false>(src, dst, row0, BN, 0u);
-                    if (bad)
-                        dirty[mine * 4 + (segments & 3u)] = 1u;
+                    if (kv && flags & kLast) {
+                        const bool any = __any_sync(0xffffffffu, bad);
+                        if (lane == 0)
+                            dirty[4 * mine + (meta.segment & 3u)] = any ? 1u : 0u;
+                    }
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        mbar_arrive(raw_empty(1, rs));
-                        mbar_arrive(full(1, st));
+                        mbar_arrive(raw_empty(kv, rs));
+                        mbar_arrive(full(kv, st));
                     }
                 }
-                ++segments;
-            } while (ok && w.next(p));
+            }
         } else if (start < stop && warp == kMmaWarp) {
             // ======================================================== products
             // (one elected thread issues, the whole warp walks along)
@@ -624,64 +758,56 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
                     umma_commit(o_full(t));
                 return true;
             };
-            RaggedWalk w = first_segment();
-            bool two = w.rows(p) > BM, more = true, ok = true;
-            int left = w.j1 - w.j;
-            uint32_t i = 0;
-            ok = wait_k(0) && wait_q(0, segs0);
-            if (ok)
+            // Both tiles' scores of block i; the first ones of a segment wait for its rows
+            auto flags_of = [&](uint32_t i) { return __shfl_sync(0xffffffffu, metas[i % G::kMetas].flags, 0); };
+            const uint32_t blocks = (uint32_t)(stop - start);
+            bool ok = wait_k(0) && wait_q(0, segs0);
+            uint32_t flags = 0;
+            if (ok) {
+                flags = flags_of(0);
                 score(0, 0);
-            if (ok && two) {
-                ok = wait_q(1, segs1);
-                if (ok)
-                    score(1, 0);
-            }
-            if (ok && leader)
-                umma_commit(empty(0, 0));
-            bool fresh = true;
-            while (ok && more) {
-                const bool last = left == 1;
-                bool next_two = two;
-                if (last) {   // the next block is another item's
-                    more = w.next(p);
-                    next_two = more && w.rows(p) > BM;
+                if (flags & kBothTiles) {
+                    ok = wait_q(1, segs1);
+                    if (ok)
+                        score(1, 0);
                 }
+                if (ok && leader)
+                    umma_commit(empty(0, 0));
+            }
+            for (uint32_t i = 0; ok && i < blocks; ++i) {
+                const bool first = i == 0 || flags & kFirst, last = i + 1 == blocks || flags & kLast;
+                const bool more = i + 1 < blocks, two = flags & kBothTiles;
                 ok = wait_warp(full(1, i & 1u), i >> 1 & 1u, p.wait_limit_ns, abort_flag, kSiteMmaFull) &&
-                     pv(0, i, fresh, last, turns0);
+                     pv(0, i, first, last, turns0);
+                // within a segment the first tile's next scores go ahead of the second tile's P V
                 if (ok && !last) {
                     ok = wait_k(i + 1);
                     if (ok)
                         score(0, i + 1);
                 }
                 if (ok && two)
-                    ok = pv(1, i, fresh, last, turns1);
+                    ok = pv(1, i, first, last, turns1);
                 if (!ok)
                     break;
                 if (leader)
                     umma_commit(empty(1, i & 1u));
-                if (last && more) {
+                if (!more)
+                    break;
+                if (last) {
                     ok = wait_k(i + 1) && wait_q(0, segs0);
                     if (!ok)
                         break;
                     score(0, i + 1);
                 }
-                if (more && next_two) {
-                    if (last)
-                        ok = wait_q(1, segs1);
+                flags = flags_of(i + 1);
+                if (flags & kBothTiles) {
+                    ok = !last || wait_q(1, segs1);
                     if (!ok)
                         break;
                     score(1, i + 1);
                 }
-                if (more && leader)
+                if (leader)
                     umma_commit(empty(0, (i + 1) & 1u));
-                fresh = last;
-                if (last && more) {
-                    left = w.j1 - w.j;
-                    two = next_two;
-                } else {
-                    --left;
-                }
-                ++i;
             }
             // all MMAs of this thread complete before TMEM can be released
             if (leader)
@@ -689,7 +815,7 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
             wait_drain(drain_bar, 0u, p.wait_limit_ns, abort_flag);
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRaggedSoftmaxRegs));
         if (start < stop) {
             // ======================================================== softmax / output
             const int t = warp >> 2;                        // tile
@@ -760,10 +886,11 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
                 const int first = off + p.by_group.quotient(cur.item * 2 * BM + t * BM);
                 const int last = off + p.by_group.quotient(min(cur.item * 2 * BM + t * BM + BM, cur.seq.count * p.group) - 1);
                 const float c_row = row_scale * p.scale_log2;
-                // of scores of keys with scale ks; not 0, which would make a NaN of a masked score
-                auto factor = [&](float ks) { return fmaxf(c_row * ks, 1.17549435e-38f); };
+                auto factor = [&](float ks) { return score_factor(c_row, ks); };
                 float m = -INFINITY, l = 0.0f;   // reference of the weights, their sum
-                float rr = 0.0f;                 // O's reference above m
+                float rr = -INFINITY;            // O's reference above m
+                float m_ref = 0.0f, rr_ref = 0.0f;   // both, 0 as long as there are none
+                bool big = false;
                 for (int j = cur.j; here && j < cur.j1; ++j) {
                     const uint32_t i = blocks + (j - cur.j);
                     const bool ok = wait_bounded_eager(s_full((uint32_t)t), turns & 1u, p.wait_limit_ns, abort_flag,
@@ -777,6 +904,26 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
                     tc_fence_after_sync();
                     const RaggedMeta &meta = metas[i % G::kMetas];
                     const int key0 = cur.it.key0(j);
+                    const uint32_t missing = meta.missing, flags = meta.flags;
+                    if (missing || ragged_masked(p, first, last, key0)) {
+                        // -infinity for what is not seen, a bit per key, 32 at a time
+                        const int hi = pos - key0;
+                        const int lo = p.window > 0 ? hi - p.window : -1;
+                        const int head = p.sinks - key0;
+#pragma unroll 1
+                        for (int c0 = 0; c0 < BN; c0 += 32) {
+                            uint32_t x[32];
+                            tmem_ld_x32_sync(s_addr + c0, x);
+                            uint32_t seen = keys_below(hi + 1 - c0) & (~keys_below(lo + 1 - c0) | keys_below(head - c0));
+                            seen &= ~((missing >> (c0 / 16) & 1u ? 0x0000ffffu : 0u) |
+                                      (missing >> (c0 / 16 + 1) & 1u ? 0xffff0000u : 0u));
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                x[e] = seen & (1u << e) ? x[e] : __float_as_uint(-INFINITY);
+                            tmem_st_x32(s_addr + c0, x);
+                        }
+                        tmem_st_wait();
+                    }
                     uint32_t v[BN];
 #pragma unroll
                     for (int c0 = 0; c0 < BN; c0 += 32)
@@ -784,102 +931,82 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
 #pragma unroll
                     for (int c0 = 0; c0 < BN; c0 += 32)
                         tmem_ld_wait_regs(*reinterpret_cast<uint32_t(*)[32]>(&v[c0]));
-                    const uint32_t missing = meta.missing;
-                    if (missing || ragged_masked(p, first, last, key0)) {
-                        // a bit per key, 32 at a time
-                        const int hi = pos - key0;
-                        const int lo = p.window > 0 ? hi - p.window : -1;
-                        const int head = p.sinks - key0;
+                    // the largest score, in base 2
+                    const float c_blk = factor(meta.ks);
+                    float mx;
+                    {
+                        float a = __uint_as_float(v[0]), b = __uint_as_float(v[1]);
 #pragma unroll
-                        for (int c0 = 0; c0 < BN; c0 += 32) {
-                            uint32_t seen = keys_below(hi + 1 - c0) & (~keys_below(lo + 1 - c0) | keys_below(head - c0));
-                            seen &= ~((missing >> (c0 / 16) & 1u ? 0x0000ffffu : 0u) |
-                                      (missing >> (c0 / 16 + 1) & 1u ? 0xffff0000u : 0u));
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                v[c0 + e] = seen & (1u << e) ? v[c0 + e] : __float_as_uint(-INFINITY);
+                        for (int e = 2; e < BN; e += 2) {
+                            a = fmaxf(a, __uint_as_float(v[e]));
+                            b = fmaxf(b, __uint_as_float(v[e + 1]));
                         }
+                        mx = __fmul_rn(fmaxf(a, b), c_blk);
                     }
-                    // the largest score of each 16 keys, in base 2
-                    float mx = -INFINITY, x16[kGroups];
-#pragma unroll
-                    for (int g = 0; g < kGroups; ++g) {
-                        float a = __uint_as_float(v[16 * g]), b = __uint_as_float(v[16 * g + 1]);
-#pragma unroll
-                        for (int e = 2; e < 16; e += 2) {
-                            a = fmaxf(a, __uint_as_float(v[16 * g + e]));
-                            b = fmaxf(b, __uint_as_float(v[16 * g + e + 1]));
-                        }
-                        x16[g] = __fmul_rn(fmaxf(a, b), factor(meta.scale[g].x));
-                        mx = fmaxf(mx, x16[g]);
+                    const float lv = meta.lv;
+                    // the row's largest product with V's scale, above the reference of the weights
+                    float over = (mx - m_ref) + lv;
+                    const bool near = flags & kNearScales;
+                    if (!near) {
+                        const float2 top = ragged_top(s_addr, meta, c_row, m_ref);
+                        mx = top.x;
+                        over = top.y;
                     }
-                    const bool move = mx > m + kRescaleLog2;
-                    const float m_new = move ? mx : m;
-                    const float m_ref = m_new == -INFINITY ? 0.0f : m_new;
-                    const float shrink = move ? fast_exp2(m - m_new) : 1.0f;   // 0 at the first scores
-                    // O's reference: rr above m.  The first scores set it, later ones move it.
-                    const float rr_old = m == -INFINITY ? -INFINITY : move ? (m - m_new) + rr : rr;
-                    float over = -INFINITY;
-#pragma unroll
-                    for (int g = 0; g < kGroups; ++g)
-                        over = fmaxf(over, (x16[g] - m_ref) + meta.scale[g].y);
-                    const bool turn = over > rr_old + kRescaleLog2;
-                    const float rr_new = turn ? over : m_new == -INFINITY ? 0.0f : rr_old;
-                    const float alpha = turn ? fast_exp2(rr_old - rr_new) : 1.0f;
-                    float sub = m_ref;
-                    const bool big = __any_sync(0xffffffffu, fabsf(m_ref) >= kBigLog2);
-                    if (big) {
-#pragma unroll
-                        for (int g = 0; g < kGroups; ++g) {
-                            const float c = factor(meta.scale[g].x);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                v[16 * g + e] = __float_as_uint(
-                                    __fsub_rn(__fmul_rn(__uint_as_float(v[16 * g + e]), c), m_ref));
-                        }
-                        sub = 0.0f;
-                    }
-                    float sum = 0.0f;
-#pragma unroll
-                    for (int g = 0; g < kGroups; ++g) {
-                        const float2 sc = meta.scale[g];
-                        const float c = big ? 1.0f : factor(sc.x);
-                        const float a = (sc.y + kPLog2 - rr_new) - sub;
-                        const float2 c2 = make_float2(c, c), a2 = make_float2(a, a);
-                        float2 sa = make_float2(0.0f, 0.0f), sb = make_float2(0.0f, 0.0f);
-                        uint32_t ph[8];
-#pragma unroll
-                        for (int e = 0; e < 16; e += 4) {
-                            const float2 x01 = __ffma2_rn(make_float2(__uint_as_float(v[16 * g + e]),
-                                                                      __uint_as_float(v[16 * g + e + 1])), c2, a2);
-                            const float2 x23 = __ffma2_rn(make_float2(__uint_as_float(v[16 * g + e + 2]),
-                                                                      __uint_as_float(v[16 * g + e + 3])), c2, a2);
-                            const float2 e01 = make_float2(fast_exp2(x01.x), fast_exp2(x01.y));
-                            const float2 e23 = make_float2(fast_exp2(x23.x), fast_exp2(x23.y));
-                            sa = __fadd2_rn(sa, e01);
-                            sb = __fadd2_rn(sb, e23);
-                            ph[e / 2] = half2_of(e01.x, e01.y);
-                            ph[e / 2 + 1] = half2_of(e23.x, e23.y);
-                        }
-                        // (as weights relative to m; bounded, so that no sum of 0 meets an infinity)
-                        const float back = fast_exp2(fminf(rr_new - kPLog2 - sc.y, 126.0f));
-                        sum = fmaf((sa.x + sa.y) + (sb.x + sb.y), back, sum);
-                        tmem_st_x8(s_addr + 8 * g, ph);
-                    }
-                    l = l * shrink + sum;
-                    m = m_new;
-                    rr = rr_new;
-                    if (j > cur.j && __any_sync(0xffffffffu, turn)) {
+                    // The references of the weights (m) and of O (rr above m) move when a score or a product exceeds them by
+                    // 2^8, and with the first scores.  Mostly none does: one vote and one jump.
+                    if (__any_sync(0xffffffffu, mx > m + kRescaleLog2 || over > rr + kRescaleLog2)) {
+                        const bool move = mx > m + kRescaleLog2;
+                        const float m_new = move ? mx : m;
+                        m_ref = m_new == -INFINITY ? 0.0f : m_new;
+                        over = near ? (mx - m_ref) + lv : ragged_top(s_addr, meta, c_row, m_ref).y;
+                        const float rr_old = move ? (m - m_new) + rr : rr;
+                        const bool turn = over > rr_old + kRescaleLog2;
+                        l *= move ? fast_exp2(m - m_new) : 1.0f;
+                        m = m_new;
+                        rr = turn ? over : rr_old;
+                        rr_ref = rr == -INFINITY ? 0.0f : rr;
+                        big = __any_sync(0xffffffffu, fabsf(m_ref) >= kBigLog2);
+                        if (j > cur.j && __any_sync(0xffffffffu, turn)) {   // (the P V before this block is done)
+                            const float alpha = turn ? fast_exp2(rr_old - rr) : 1.0f;
 #pragma unroll 1
-                        for (int c0 = 0; c0 < HD; c0 += 32) {
-                            uint32_t o[32];
-                            tmem_ld_x32_sync(o_addr + c0, o);
+                            for (int c0 = 0; c0 < HD; c0 += 32) {
+                                uint32_t o[32];
+                                tmem_ld_x32_sync(o_addr + c0, o);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                            tmem_st_x32(o_addr + c0, o);
+                                for (int e = 0; e < 32; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                tmem_st_x32(o_addr + c0, o);
+                            }
                         }
                     }
+                    float sum;
+                    if (near && !big) {
+                        const float a = (lv + kPLog2 - rr_ref) - m_ref;
+                        const float2 c2 = make_float2(c_blk, c_blk), a2 = make_float2(a, a);
+                        float2 sa = make_float2(0.0f, 0.0f), sb = make_float2(0.0f, 0.0f);
+#pragma unroll
+                        for (int e0 = 0; e0 < BN; e0 += 32) {
+                            uint32_t ph[16];
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                const float2 x01 = __ffma2_rn(make_float2(__uint_as_float(v[e0 + e]),
+                                                                          __uint_as_float(v[e0 + e + 1])), c2, a2);
+                                const float2 x23 = __ffma2_rn(make_float2(__uint_as_float(v[e0 + e + 2]),
+                                                                          __uint_as_float(v[e0 + e + 3])), c2, a2);
+                                const float2 e01 = make_float2(fast_exp2(x01.x), fast_exp2(x01.y));
+                                const float2 e23 = make_float2(fast_exp2(x23.x), fast_exp2(x23.y));
+                                sa = __fadd2_rn(sa, e01);
+                                sb = __fadd2_rn(sb, e23);
+                                ph[e / 2] = half2_of(e01.x, e01.y);
+                                ph[e / 2 + 1] = half2_of(e23.x, e23.y);
+                            }
+                            tmem_st_x16(s_addr + e0 / 2, ph);
+                        }
+                        sum = ((sa.x + sa.y) + (sb.x + sb.y)) * back_of(rr_ref, lv);
+                    } else {
+                        sum = ragged_weights(s_addr, meta, c_row, m_ref, rr_ref);
+                    }
+                    l += sum;
                     tmem_st_wait();
                     tc_fence_before_sync();
                     __syncwarp();
@@ -903,7 +1030,9 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
                 }
                 ++outputs;
                 tc_fence_after_sync();
-                const bool taken = dirty[segments & 3u] | dirty[4 + (segments & 3u)];
+                bool taken = false;
+                for (int x = 0; x < kConvWarps; ++x)
+                    taken = taken || dirty[4 * x + (segments & 3u)];
                 if (taken)
                     ragged_add_nan<HD>(p, cur.b, cur.head, cur.item, cur.j, cur.j1, pos, o_addr);
                 const bool valid = my_row < rows;
@@ -963,47 +1092,44 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
                     before = __shfl_sync(0xffffffffu, before, 0);
                     __syncwarp();
                     if (before == (unsigned)(c_last - c_first) && valid) {
-                        float mm = -INFINITY, yy = -INFINITY;   // the largest references
-                        for (int c = c_first; c <= c_last; ++c) {
-                            const float *x = part_of(c);
-                            const float pm = __ldcg(x + HD * 32);
-                            mm = fmaxf(mm, pm);
-                        }
+                        // the largest references, and the sum of weights
+                        float mm = -INFINITY, yy = -INFINITY, ll = 0.0f;
+#pragma unroll 4
+                        for (int c = c_first; c <= c_last; ++c)
+                            mm = fmaxf(mm, __ldcg(part_of(c) + HD * 32));
                         const float ref = mm == -INFINITY ? 0.0f : mm;
+#pragma unroll 4
                         for (int c = c_first; c <= c_last; ++c) {
-                            const float *x = part_of(c);
-                            const float pm = __ldcg(x + HD * 32);
-                            if (pm != -INFINITY)
-                                yy = fmaxf(yy, (pm - ref) + __ldcg(x + (HD + 2) * 32));
-                        }
-                        float ll = 0.0f;
-                        for (int c = c_first; c <= c_last; ++c) {
-                            const float *x = part_of(c);
-                            const float pm = __ldcg(x + HD * 32), pl = __ldcg(x + (HD + 1) * 32);
+                            const float *x = part_of(c) + HD * 32;
+                            const float pm = __ldcg(x), pl = __ldcg(x + 32), pr = __ldcg(x + 64);
+                            yy = fmaxf(yy, pm == -INFINITY ? -INFINITY : (pm - ref) + pr);
                             ll += pl != pl ? pl : pm == -INFINITY ? 0.0f : pl * exp2f(pm - ref);
                         }
                         const float inv = ll > 0.0f || ll != ll ? 1.0f / ll : 0.0f;
                         const float f = yy == -INFINITY ? 0.0f : exp2f(0.5f * (yy - kPLog2));
 #pragma unroll 1
-                        for (int c0 = 0; c0 < HD; c0 += 32) {
-                            float s[32];
+                        for (int c0 = 0; c0 < HD; c0 += 64) {   // (64 loads of a part are under way at once)
+                            float s[64];
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
+                            for (int e = 0; e < 64; ++e)
                                 s[e] = 0.0f;
 #pragma unroll 1
                             for (int c = c_first; c <= c_last; ++c) {
                                 const float *x = part_of(c);
-                                const float pm = __ldcg(x + HD * 32);
-                                const float a = pm == -INFINITY ? 1.0f : exp2f((pm - ref) + __ldcg(x + (HD + 2) * 32) - yy);
+                                const float pm = __ldcg(x + HD * 32), pr = __ldcg(x + (HD + 2) * 32);
+                                const float a = pm == -INFINITY ? 1.0f : exp2f((pm - ref) + pr - yy);
 #pragma unroll
-                                for (int e = 0; e < 32; ++e)
+                                for (int e = 0; e < 64; ++e)
                                     s[e] = fmaf(__ldcg(x + (c0 + e) * 32), a, s[e]);
                             }
-                            uint32_t o[32];
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                o[e] = __float_as_uint(s[e]);
-                            write_out(c0, o, inv, f);
+                            for (int h = 0; h < 64; h += 32) {
+                                uint32_t o[32];
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    o[e] = __float_as_uint(s[h + e]);
+                                write_out(c0 + h, o, inv, f);
+                            }
                         }
                     }
                     __syncwarp();

@@ -69,7 +69,7 @@ __device__ __forceinline__ void turn_one(uint32_t &x, float2 cs) {
 
 // A block: rows_block rows.  Its angles' cosines and sines are computed once, about one a thread, and
 // stay in shared memory; each thread then keeps one item of one row (8 pairs: two vectors of 8 elements,
-// or one pair where the halves are not vectors, or a vector that is copied) over every lanes-th head.
+// one pair where the halves are not vectors, or two vectors that are copied) over every lanes-th head.
 template <bool kBf16, bool kInterleaved, bool kVector>
 __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams p) {
     __shared__ __align__(16) float2 trig[kMostTrig];
@@ -100,60 +100,66 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams 
     if (r >= p.rows_block || row >= p.rows)
         return;
     const int64_t b = row / p.tokens, token = row - b * p.tokens;
-    const int64_t xr[2] = {b * p.xs[0][0] + token * p.xs[0][1], b * p.xs[1][0] + token * p.xs[1][1]};
-    const int64_t yr[2] = {b * p.ys[0][0] + token * p.ys[0][1], b * p.ys[1][0] + token * p.ys[1][1]};
+    const uint16_t *q_src = p.x[0] + b * p.xs[0][0] + token * p.xs[0][1];
+    const uint16_t *k_src = p.x[1] + b * p.xs[1][0] + token * p.xs[1][1];
+    uint16_t *q_dst = p.y[0] + b * p.ys[0][0] + token * p.ys[0][1];
+    uint16_t *k_dst = p.y[1] + b * p.ys[1][0] + token * p.ys[1][1];
     auto src = [&](int h) {
-        const int w = h >= p.heads0;
-        return p.x[w] + xr[w] + (h - (w ? p.heads0 : 0)) * p.xs[w][2];
+        return h < p.heads0 ? q_src + h * p.xs[0][2] : k_src + (h - p.heads0) * p.xs[1][2];
     };
     auto dst = [&](int h) {
-        const int w = h >= p.heads0;
-        return p.y[w] + yr[w] + (h - (w ? p.heads0 : 0)) * p.ys[w][2];
+        return h < p.heads0 ? q_dst + h * p.ys[0][2] : k_dst + (h - p.heads0) * p.ys[1][2];
     };
-    if (item >= p.turned) {   // past the part that turns: a vector as it is
-        const int at = (p.head_dim - 8 * (p.items - p.turned)) + 8 * (item - p.turned);
-        // (where rot is not a multiple of 8 the vectors begin behind it; the few elements between are below)
-        for (int h = lane; h < p.heads; h += p.lanes)
-            *reinterpret_cast<uint4 *>(dst(h) + at) = *reinterpret_cast<const uint4 *>(src(h) + at);
-        return;
-    }
     const float2 *cs = trig + r * p.half;
+    const bool turns = item < p.turned;
+    // what is copied: the vectors from `copied` on, two an item (the last one twice where their number is odd)
+    const int copied = (2 * p.half + 7) / 8 * 8, copy0 = copied + 16 * (item - p.turned), copy1 = min(copy0 + 8, p.head_dim - 8);
     if constexpr (kVector) {
         constexpr int kPairs = 8;
         // pairs of this item: 8 item .. 8 item + 7
-        const int x_at = kInterleaved ? 16 * item : 8 * item, z_at = kInterleaved ? x_at + 8 : p.half + 8 * item;
+        const int x_at = !turns ? copy0 : kInterleaved ? 16 * item : 8 * item;
+        const int z_at = !turns ? copy1 : kInterleaved ? x_at + 8 : p.half + 8 * item;
         float4 c[kPairs / 2];
 #pragma unroll
         for (int i = 0; i < kPairs / 2; ++i)
-            c[i] = *reinterpret_cast<const float4 *>(cs + 8 * item + 2 * i);
-#pragma unroll 2
+            c[i] = turns ? *reinterpret_cast<const float4 *>(cs + 8 * item + 2 * i) : make_float4(1, 0, 1, 0);
+#pragma unroll 4
         for (int h = lane; h < p.heads; h += p.lanes) {
             const uint16_t *s = src(h);
             uint16_t *d = dst(h);
             uint4 x = *reinterpret_cast<const uint4 *>(s + x_at), z = *reinterpret_cast<const uint4 *>(s + z_at);
-            if constexpr (kInterleaved) {
-                turn_one<kBf16>(x.x, make_float2(c[0].x, c[0].y));
-                turn_one<kBf16>(x.y, make_float2(c[0].z, c[0].w));
-                turn_one<kBf16>(x.z, make_float2(c[1].x, c[1].y));
-                turn_one<kBf16>(x.w, make_float2(c[1].z, c[1].w));
-                turn_one<kBf16>(z.x, make_float2(c[2].x, c[2].y));
-                turn_one<kBf16>(z.y, make_float2(c[2].z, c[2].w));
-                turn_one<kBf16>(z.z, make_float2(c[3].x, c[3].y));
-                turn_one<kBf16>(z.w, make_float2(c[3].z, c[3].w));
-            } else {
-                turn_two<kBf16>(x.x, z.x, c[0]);
-                turn_two<kBf16>(x.y, z.y, c[1]);
-                turn_two<kBf16>(x.z, z.z, c[2]);
-                turn_two<kBf16>(x.w, z.w, c[3]);
+            if (turns) {
+                if constexpr (kInterleaved) {
+                    turn_one<kBf16>(x.x, make_float2(c[0].x, c[0].y));
+                    turn_one<kBf16>(x.y, make_float2(c[0].z, c[0].w));
+                    turn_one<kBf16>(x.z, make_float2(c[1].x, c[1].y));
+                    turn_one<kBf16>(x.w, make_float2(c[1].z, c[1].w));
+                    turn_one<kBf16>(z.x, make_float2(c[2].x, c[2].y));
+                    turn_one<kBf16>(z.y, make_float2(c[2].z, c[2].w));
+                    turn_one<kBf16>(z.z, make_float2(c[3].x, c[3].y));
+                    turn_one<kBf16>(z.w, make_float2(c[3].z, c[3].w));
+                } else {
+                    turn_two<kBf16>(x.x, z.x, c[0]);
+                    turn_two<kBf16>(x.y, z.y, c[1]);
+                    turn_two<kBf16>(x.z, z.z, c[2]);
+                    turn_two<kBf16>(x.w, z.w, c[3]);
+                }
             }
             *reinterpret_cast<uint4 *>(d + x_at) = x;
             *reinterpret_cast<uint4 *>(d + z_at) = z;
         }
+    } else if (!turns) {
+        for (int h = lane; h < p.heads; h += p.lanes) {
+            const uint16_t *s = src(h);
+            uint16_t *d = dst(h);
+            const uint4 x = *reinterpret_cast<const uint4 *>(s + copy0), z = *reinterpret_cast<const uint4 *>(s + copy1);
+            *reinterpret_cast<uint4 *>(d + copy0) = x;
+            *reinterpret_cast<uint4 *>(d + copy1) = z;
+        }
     } else {
-        // one pair of elements, and behind the last pair what is left up to a vector's boundary
+        // one pair of elements; the first item also copies what is left up to a vector's boundary
         const int x_at = kInterleaved ? 2 * item : item, z_at = kInterleaved ? x_at + 1 : item + p.half;
         const float2 c = cs[item];
-        const int rest0 = 2 * p.half, rest1 = p.head_dim - 8 * (p.items - p.turned);
         for (int h = lane; h < p.heads; h += p.lanes) {
             const uint16_t *s = src(h);
             uint16_t *d = dst(h);
@@ -162,7 +168,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams 
             d[x_at] = (uint16_t)x;
             d[z_at] = (uint16_t)(x >> 16);
             if (p.copy && item == 0)
-                for (int i = rest0; i < rest1; ++i)
+                for (int i = 2 * p.half; i < copied; ++i)
                     d[i] = s[i];
         }
     }

@@ -70,7 +70,7 @@ extern "C" int rotary_x16(const rotary_tensor *q, const rotary_tensor *k, int dt
     // vectors of 8 pairs where both halves are made of whole vectors
     const bool vector = rot % 16 == 0;
     p.turned = vector ? (int)rot / 16 : p.half;
-    p.items = p.turned + (p.copy ? (int)(head_dim - rot) / 8 : 0);
+    p.items = p.turned + (p.copy ? (int)((head_dim - rot) / 8 + 1) / 2 : 0);   // two vectors an item
     p.amplitude = (float)amplitude;
     p.sine = inverse ? -p.amplitude : p.amplitude;
     // Rows of a block: as many as give its threads an angle each, but two blocks an SM first.  The other
