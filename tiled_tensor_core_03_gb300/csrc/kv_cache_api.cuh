@@ -439,7 +439,7 @@ int kv_cache_attention_ragged_x16(const kv_cache_pool *cache, const void *q, int
     p.sinks = (int)std::min<int64_t>(sinks, kMaxTokens);
     p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)cache->head_dim));
     p.arrived = static_cast<unsigned *>(workspace);
-    p.partial = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + GEMMRELU_RAGGED_COUNTER_BYTES);
+    p.partial = reinterpret_cast<float4 *>(static_cast<unsigned char *>(workspace) + GEMMRELU_RAGGED_COUNTER_BYTES);
     p.drop_arrive = g_drop_arrive.load();
     p.wait_limit_ns = wait_limit_ns();
     cudaStream_t s = static_cast<cudaStream_t>(stream);

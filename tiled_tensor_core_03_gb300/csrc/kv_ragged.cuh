@@ -18,10 +18,10 @@ using attn::BN;
 using attn::kSub;
 
 // Four warpgroups: two of softmax, one with the feed's and the issuer's warp, one that converts.  512 threads launch
-// with 128 registers: 2 * 208 + 2 * 48 = 4 * 128.
+// with 128 registers: 2 * 152 + 2 * 104 = 4 * 128.
 constexpr int kRaggedThreads = 512;
 constexpr int kConvWarp = 12, kConvWarps = 4;
-constexpr int kRaggedSoftmaxRegs = 208, kRaggedFeedRegs = 48, kRaggedConvRegs = 48;
+constexpr int kRaggedSoftmaxRegs = 152, kRaggedFeedRegs = 104, kRaggedConvRegs = 104;
 static_assert(2 * kRaggedSoftmaxRegs + kRaggedFeedRegs + kRaggedConvRegs <= 4 * 128, "registers given back cover those taken");
 constexpr int kGroups = BN / 16;                // pieces of 16 tokens of a block: the smallest page
 constexpr int kRaggedMaxCtas = GEMMRELU_RAGGED_COUNTER_BYTES / (8 * (int)sizeof(unsigned));
@@ -72,7 +72,7 @@ struct RaggedCfg {
     // meta_full[kMetas]; q_full, s_full, p_full, o_full [2]; drain
     static constexpr uint32_t kNumBars = 4 * kRaw + 8 + kMetas + 8 + 1;
     static constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;
-    static constexpr uint32_t kSmem = kOffMisc + 384 + 1024;
+    static constexpr uint32_t kSmem = kOffMisc + 136 + 256 + 1024;
     static constexpr uint32_t kTmemS = 0, kTmemO = 2 * BN;
     static constexpr uint32_t kIdescS = make_idesc_f16_f32(BM, BN, 0, 0);
     static constexpr uint32_t kIdescO = make_idesc_f16_f32(BM, HD, 0, 1);
@@ -90,7 +90,7 @@ struct RaggedParams {
     attn::Divisor by_group;
     int window, sinks;
     float scale_log2;                  // log2(e) / sqrt(D)
-    float *partial;                    // [2 * CTAs][8 warps][D + 4][32 rows]
+    float4 *partial;                   // [2 * CTAs][8 warps][D / 4 of O, then (m, l, rr, unused)][32 rows]
     unsigned *arrived;                 // [CTAs][8 warps]; all 0 between calls
     int drop_arrive;
     uint64_t wait_limit_ns;
@@ -153,9 +153,24 @@ __device__ __forceinline__ bool ragged_sees(const RaggedParams &p, const RaggedI
                                 token + tokens > max(it.first, 0) - p.window + 1);
 }
 
+// How the work is cut.  The blocks of all items in order are dealt to the CTAs in equal ranges (part = 0): each finishes
+// what lies inside its range, and what it has of the items at its two ends are parts that are joined.  With fewer items than
+// CTAs every CTA would have two such ends and little between them: there each item is cut into equal parts of `part` blocks
+// at most, and a CTA has one.  A unit is a block, or such a part.
+__device__ __forceinline__ int ragged_units(int blocks, int part) { return part ? (blocks + part - 1) / part : blocks; }
+
+// `part` for so many blocks and items (0 with no fewer items than CTAs): blocks / part + items parts at most, which fit.
+__device__ __forceinline__ int ragged_part(int blocks, int items, int grid) {
+    return items < grid ? (blocks + grid - items - 1) / (grid - items) : 0;
+}
+
+// Whether to cut that way, given the blocks of the longest part: where it takes no more than an equal range and its two
+// ends, about 8 blocks' time.
+__device__ __forceinline__ bool ragged_cut_pays(int longest, int blocks, int grid) { return longest <= blocks / grid + 8; }
+
 // The segments (runs of blocks of one item) of a CTA's range of units, in order.
 struct RaggedWalk {
-    int b, head, item, j, left;      // where it stands; units left of the range, this segment's too
+    int b, head, item, j, left;      // where it stands; blocks left of the range, this segment's too
     int unit0;                       // first unit of the item
     RaggedSeq seq;
     RaggedItem it;
@@ -187,20 +202,159 @@ struct RaggedWalk {
     }
 };
 
-// How many of the launched CTAs get a range.  An item of n blocks cut into x parts takes about n / x blocks and the
-// join of x parts one after the other, which costs about 0.4 blocks each: x = sqrt(2.5 n) is the least.
-__device__ __forceinline__ int ragged_ranges(int total, float items, int grid) {
-    const float most = sqrtf(2.5f * (float)total * items);
-    int n = min(total, grid);
-    if (most < (float)n)
-        n = (int)most;
-    return max(n, 1);
+// What the start works out, in shared memory: where the CTA's range begins, its blocks, and how units are dealt.
+struct RaggedPlan {
+    int b, head, item, j, unit0, blocks, part, total, ranges;
+    RaggedSeq seq;
+};
+
+// The sum over a warp of values below 2^48.
+__device__ __forceinline__ int64_t warp_sum(int64_t x) {
+    int64_t sum = 0;
+#pragma unroll
+    for (int i = 0; i < 48; i += 16)
+        sum += (int64_t)__reduce_add_sync(0xffffffffu, (unsigned)(x >> i) & 0xffffu) << i;
+    return sum;
 }
 
-// What the start works out, in shared memory.
-struct RaggedPlan {
-    int b, head, item, j, unit0, start, stop, total, ranges;
-};
+// This CTA's range of units: sums over all sequences, a lane each (those of long chunks by a warp), by one warp or, with more
+// than 32 sequences, by all; then one warp looks up where the range begins.  `units`: those of one head of each sequence.
+__device__ __noinline__ void ragged_plan(const RaggedParams &p, RaggedPlan *plan, int *units, int64_t *sums) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, grid = gridDim.x;
+    const bool alone = p.batch <= 32;
+    if (alone && warp > 0)
+        return;
+    int part = 0, total = 0, blocks = 0;
+    for (int pass = 0;; ++pass) {   // in blocks, in parts, and in blocks again where parts do not pay
+        int64_t mine = 0, items = 0;
+        int longest = 0;
+        for (int b0 = warp * 32; b0 < p.batch; b0 += alone ? 32 : kRaggedThreads) {
+            const int b = b0 + lane;
+            RaggedSeq s{0, 0, 0, 0};
+            if (b < p.batch)
+                s = ragged_seq(p, b, pass == 0 && blockIdx.x == 0);
+            int64_t u = 0;
+            auto add = [&](const RaggedSeq &x, int i) {
+                const int n = ragged_item(p, x, i).count(), parts = ragged_units(n, part);
+                if (part)
+                    longest = max(longest, (n + parts - 1) / parts);
+                return parts;
+            };
+            if (s.items <= 4)
+                for (int i = 0; i < s.items; ++i)
+                    u += add(s, i);
+            for (uint32_t m = __ballot_sync(0xffffffffu, s.items > 4); m; m &= m - 1) {
+                const int from = __ffs(m) - 1;
+                RaggedSeq x;
+                x.count = __shfl_sync(0xffffffffu, s.count, from);
+                x.n = __shfl_sync(0xffffffffu, s.n, from);
+                x.items = __shfl_sync(0xffffffffu, s.items, from);
+                int64_t sum = 0;
+                for (int i = lane; i < x.items; i += 32)
+                    sum += add(x, i);
+                sum = warp_sum(sum);
+                u = lane == from ? sum : u;
+            }
+            if (b < p.batch)
+                units[b] = (int)u;
+            mine += u;
+            items += s.items;
+        }
+        mine = warp_sum(mine);
+        items = warp_sum(items);
+        longest = __reduce_max_sync(0xffffffffu, longest);
+        if (!alone) {
+            if (lane == 0) {
+                sums[warp] = mine;
+                sums[16 + warp] = items << 32 | longest;
+            }
+            __syncthreads();
+            mine = items = 0;
+            for (int w = 0; w < kRaggedThreads / 32; ++w) {
+                mine += sums[w];
+                items += sums[16 + w] >> 32;
+                longest = max(longest, (int)sums[16 + w]);
+            }
+            __syncthreads();   // (the sums have been read)
+        }
+        mine *= p.pool.kv_heads;
+        items *= p.pool.kv_heads;
+        if (mine > 0x7fffffff) {   // rows that several sequences claim
+            record_page_error();
+            mine = 0;
+        }
+        total = (int)mine;
+        if (pass == 0) {
+            blocks = total;
+            part = ragged_part(total, (int)(items < grid ? items : grid), grid);
+        } else if (pass == 1 && !ragged_cut_pays(longest, blocks, grid)) {
+            part = 0;
+            continue;
+        }
+        if (part == 0 || pass == 1)
+            break;
+    }
+    if (warp > 0)
+        return;
+    __syncwarp();
+    const int ranges = max(1, min(total, grid)), c = blockIdx.x;
+    const int start = c < ranges ? range_start(c, total, ranges) : total;
+    const int stop = c < ranges ? range_start(c + 1, total, ranges) : total;
+    if (start >= stop) {
+        if (lane == 0)
+            *plan = RaggedPlan{0, 0, 0, 0, 0, 0, 0, 0, 1, RaggedSeq{0, 0, 0, 0}};
+        return;
+    }
+    int at = 0, b = 0, u = 0;
+    for (int b0 = 0;; b0 += 32) {   // the sequence that the range starts in
+        const int x = b0 + lane < p.batch ? units[b0 + lane] * p.pool.kv_heads : 0;
+        int run = x;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, run, o);
+            run += lane >= o ? y : 0;
+        }
+        const uint32_t m = __ballot_sync(0xffffffffu, start < at + run);
+        if (m) {
+            const int l = __ffs(m) - 1;
+            b = b0 + l;
+            u = __shfl_sync(0xffffffffu, x, l);
+            at += __shfl_sync(0xffffffffu, run, l) - u;
+            break;
+        }
+        at += __shfl_sync(0xffffffffu, run, 31);
+    }
+    u /= p.pool.kv_heads;
+    const int head = (start - at) / u;
+    at += head * u;
+    const RaggedSeq s = ragged_seq(p, b, false);
+    int item = 0, nb = 0;
+    for (int i0 = 0;; i0 += 32) {   // the item of that head
+        const int n = i0 + lane < s.items ? ragged_item(p, s, i0 + lane).count() : 0;
+        const int x = ragged_units(n, part);
+        int run = x;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, run, o);
+            run += lane >= o ? y : 0;
+        }
+        const uint32_t m = __ballot_sync(0xffffffffu, start < at + run);
+        if (m) {
+            const int l = __ffs(m) - 1;
+            item = i0 + l;
+            nb = __shfl_sync(0xffffffffu, n, l);
+            at += __shfl_sync(0xffffffffu, run - x, l);
+            break;
+        }
+        at += __shfl_sync(0xffffffffu, run, 31);
+    }
+    int j = start - at, here = stop - start;
+    if (part) {   // part j of the item
+        const int x = ragged_units(nb, part), j0 = range_start(j, nb, x);
+        here = range_start(j + 1, nb, x) - j0;
+        j = j0;
+    }
+    if (lane == 0)
+        *plan = RaggedPlan{b, head, item, j, at, here, part, total, ranges, s};
+}
 
 // ---------------------------------------------------------------- V that is not finite
 
@@ -313,6 +467,92 @@ __device__ __forceinline__ float ragged_weights(uint32_t s_addr, const RaggedMet
     return sum;
 }
 
+// 32 elements of a row of the result: inv f^2 times its sums (f's square spans the range of all scales).
+template <bool kBf16>
+__device__ __forceinline__ void write_row32(uint16_t *dst, const float (&y)[32], float inv, float f) {
+#pragma unroll
+    for (int e = 0; e < 32; e += 8) {
+        uint32_t h[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            h[k] = pack_out<kBf16>(y[e + 2 * k] * inv * f * f, y[e + 2 * k + 1] * inv * f * f);
+        *reinterpret_cast<uint4 *>(dst + e) = make_uint4(h[0], h[1], h[2], h[3]);
+    }
+}
+
+// A (sequence, head, item) that several CTAs have parts of, for one lane's row.
+struct RaggedCut {
+    uint16_t *dst;         // where the row goes; nullptr: there is no such row
+    int first, last;       // CTAs
+    bool mid;              // it begins behind the start of the first one's range: in that one's second part
+};
+
+// What CTA c has of a cut item in the workspace, for one warp's 32 rows: HD / 4 times 4 columns of O, then m, l and rr, a
+// lane's row each.
+template <int HD>
+__device__ __forceinline__ float4 *ragged_part_of(const RaggedParams &p, const RaggedCut &cut, int warp, int lane, int c) {
+    return p.partial + ((int64_t)(2 * c + (c == cut.first && cut.mid ? 1 : 0)) * 8 + warp) * (HD / 4 + 1) * 32 + lane;
+}
+
+// The parts of a lane's row joined, in the order of the CTAs.
+template <int HD, bool kBf16>
+__device__ __noinline__ void ragged_join(const RaggedParams &p, const RaggedCut cut, int warp, int lane) {
+    // the largest references, and the sum of weights
+    float mm = -INFINITY, yy = -INFINITY, ll = 0.0f;
+#pragma unroll 4
+    for (int c = cut.first; c <= cut.last; ++c) {
+        const float4 x = __ldcg(ragged_part_of<HD>(p, cut, warp, lane, c) + HD / 4 * 32);   // m, l, rr
+        const float top = fmaxf(mm, x.x);
+        ll *= mm == top ? 1.0f : exp2f(mm - top);
+        yy = mm == -INFINITY ? -INFINITY : (mm - top) + yy;
+        yy = fmaxf(yy, x.x == -INFINITY ? -INFINITY : (x.x - top) + x.z);
+        ll += x.y != x.y ? x.y : x.x == -INFINITY ? 0.0f : x.y * exp2f(x.x - top);
+        mm = top;
+    }
+    const float ref = mm == -INFINITY ? 0.0f : mm;
+    const float inv = ll > 0.0f || ll != ll ? 1.0f / ll : 0.0f;
+    const float f = yy == -INFINITY ? 0.0f : exp2f(0.5f * (yy - kPLog2));
+#pragma unroll 1
+    for (int c0 = 0; c0 < HD; c0 += 64) {
+        float s[64];
+#pragma unroll
+        for (int e = 0; e < 64; ++e)
+            s[e] = 0.0f;
+#pragma unroll 1
+        for (int c = cut.first; c <= cut.last; c += 2) {   // two parts' loads are under way at once
+            const bool both = c < cut.last;
+            const float4 *x = ragged_part_of<HD>(p, cut, warp, lane, c), *y = ragged_part_of<HD>(p, cut, warp, lane, both ? c + 1 : c);
+            float4 o[2][16];
+            const float4 xs = __ldcg(x + HD / 4 * 32), ys = __ldcg(y + HD / 4 * 32);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                o[0][e] = __ldcg(x + (c0 / 4 + e) * 32);
+                o[1][e] = __ldcg(y + (c0 / 4 + e) * 32);
+            }
+            const float a = xs.x == -INFINITY ? 1.0f : exp2f((xs.x - ref) + xs.z - yy);
+            const float d = ys.x == -INFINITY ? 1.0f : exp2f((ys.x - ref) + ys.z - yy);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                s[4 * e] = fmaf(o[0][e].x, a, s[4 * e]);
+                s[4 * e + 1] = fmaf(o[0][e].y, a, s[4 * e + 1]);
+                s[4 * e + 2] = fmaf(o[0][e].z, a, s[4 * e + 2]);
+                s[4 * e + 3] = fmaf(o[0][e].w, a, s[4 * e + 3]);
+            }
+            if (both)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    s[4 * e] = fmaf(o[1][e].x, d, s[4 * e]);
+                    s[4 * e + 1] = fmaf(o[1][e].y, d, s[4 * e + 1]);
+                    s[4 * e + 2] = fmaf(o[1][e].z, d, s[4 * e + 2]);
+                    s[4 * e + 3] = fmaf(o[1][e].w, d, s[4 * e + 3]);
+                }
+        }
+#pragma unroll
+        for (int e = 0; e < 64; e += 32)
+            write_row32<kBf16>(cut.dst + c0 + e, reinterpret_cast<const float(&)[32]>(s[e]), inv, f);
+    }
+}
+
 // ---------------------------------------------------------------- e4m3 to fp16
 
 // Rows [row0, row0 + BN / kConvWarps) of a block: bytes at `src` (rows of HD) become fp16 in the sub-tiles of 64
@@ -395,7 +635,7 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
     volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(gbase + G::kOffMisc + 4);
     volatile uint32_t *dirty = reinterpret_cast<volatile uint32_t *>(gbase + G::kOffMisc + 16);   // [4][4]
     RaggedPlan *plan = reinterpret_cast<RaggedPlan *>(gbase + G::kOffMisc + 80);
-    long long *sums = reinterpret_cast<long long *>(gbase + G::kOffMisc + 128);   // [2][16]: + 256
+    int64_t *sums = reinterpret_cast<int64_t *>(gbase + G::kOffMisc + 136);   // [2][16]: + 256
 
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);   // uniform
     const int lane = threadIdx.x & 31;
@@ -429,126 +669,21 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
     }
     pdl_wait_primary();
 
-    // ---- this CTA's range of units.  A unit is a block of 128 keys of an item.  Units of one head of every
-    // sequence, a lane each; those of long chunks are summed by a warp.
-    int *units = reinterpret_cast<int *>(gbase + G::kOffK);
-    {
-        long long mine = 0, items = 0;
-        for (int b0 = warp * 32; b0 < p.batch; b0 += kRaggedThreads) {
-            const int b = b0 + lane;
-            RaggedSeq s{0, 0, 0, 0};
-            if (b < p.batch)
-                s = ragged_seq(p, b, blockIdx.x == 0);
-            long long u = 0;
-            if (s.items <= 4)
-                for (int i = 0; i < s.items; ++i)
-                    u += ragged_item(p, s, i).count();
-            for (uint32_t m = __ballot_sync(0xffffffffu, s.items > 4); m; m &= m - 1) {
-                const int from = __ffs(m) - 1;
-                RaggedSeq x;
-                x.count = __shfl_sync(0xffffffffu, s.count, from);
-                x.n = __shfl_sync(0xffffffffu, s.n, from);
-                x.items = __shfl_sync(0xffffffffu, s.items, from);
-                long long sum = 0;
-                for (int i = lane; i < x.items; i += 32)
-                    sum += ragged_item(p, x, i).count();
-                for (int o = 16; o; o >>= 1)
-                    sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                u = lane == from ? sum : u;
-            }
-            if (b < p.batch)
-                units[b] = (int)u;
-            mine += u;
-            items += s.items;
-        }
-        for (int o = 16; o; o >>= 1) {
-            mine += __shfl_xor_sync(0xffffffffu, mine, o);
-            items += __shfl_xor_sync(0xffffffffu, items, o);
-        }
-        if (lane == 0) {
-            sums[warp] = mine;
-            sums[16 + warp] = items;
-        }
-    }
+    ragged_plan(p, plan, reinterpret_cast<int *>(gbase + G::kOffK), sums);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
-    if (warp == 0) {
-        long long all = 0, items = 0;
-        for (int w = 0; w < kRaggedThreads / 32; ++w) {
-            all += sums[w];
-            items += sums[16 + w];
-        }
-        all *= p.pool.kv_heads;
-        items *= p.pool.kv_heads;
-        if (all > 0x7fffffffll) {   // rows that several sequences claim
-            if (lane == 0)
-                record_page_error();
-            all = 0;
-        }
-        const int total = (int)all;
-        const int ranges = ragged_ranges(total, (float)items, gridDim.x);
-        const int c = blockIdx.x;
-        const int start = c < ranges ? range_start(c, total, ranges) : total;
-        const int stop = c < ranges ? range_start(c + 1, total, ranges) : total;
-        if (start < stop) {
-            int at = 0, b = 0, u = 0;
-            for (int b0 = 0;; b0 += 32) {   // the sequence that the range starts in
-                const int x = b0 + lane < p.batch ? units[b0 + lane] * p.pool.kv_heads : 0;
-                int run = x;
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(0xffffffffu, run, o);
-                    run += lane >= o ? y : 0;
-                }
-                const uint32_t m = __ballot_sync(0xffffffffu, start < at + run);
-                if (m) {
-                    const int l = __ffs(m) - 1;
-                    b = b0 + l;
-                    u = __shfl_sync(0xffffffffu, x, l);
-                    at += __shfl_sync(0xffffffffu, run, l) - u;
-                    break;
-                }
-                at += __shfl_sync(0xffffffffu, run, 31);
-            }
-            u /= p.pool.kv_heads;
-            const int head = (start - at) / u;
-            at += head * u;
-            const RaggedSeq s = ragged_seq(p, b, false);
-            int item = 0;
-            for (int i0 = 0;; i0 += 32) {   // the item of that head
-                const int x = i0 + lane < s.items ? ragged_item(p, s, i0 + lane).count() : 0;
-                int run = x;
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(0xffffffffu, run, o);
-                    run += lane >= o ? y : 0;
-                }
-                const uint32_t m = __ballot_sync(0xffffffffu, start < at + run);
-                if (m) {
-                    const int l = __ffs(m) - 1;
-                    item = i0 + l;
-                    at += __shfl_sync(0xffffffffu, run - x, l);
-                    break;
-                }
-                at += __shfl_sync(0xffffffffu, run, 31);
-            }
-            if (lane == 0)
-                *plan = RaggedPlan{b, head, item, start - at, at, start, stop, total, ranges};
-        } else if (lane == 0) {
-            *plan = RaggedPlan{0, 0, 0, 0, 0, 0, 0, 0, 1};
-        }
-    }
-    __syncthreads();
-    const int start = plan->start, stop = plan->stop;
+    const int blocks_here = plan->blocks;
     auto first_segment = [&]() {
         RaggedWalk w;
         w.b = plan->b;
         w.head = plan->head;
         w.item = plan->item;
         w.j = plan->j;
-        w.left = stop - start;
+        w.left = blocks_here;
         w.unit0 = plan->unit0;
-        w.seq = ragged_seq(p, w.b, false);
+        w.seq = plan->seq;
         w.describe(p);
         return w;
     };
@@ -558,7 +693,7 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRaggedConvRegs));
         else
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRaggedFeedRegs));
-        if (start < stop && warp == kProducerWarp) {
+        if (blocks_here > 0 && warp == kProducerWarp) {
             // ======================================================== the feed
             // A block is `pieces` pages, a copy each of K and of V; lane l describes page l % pieces of block
             // l / pieces of a batch of 32 / pieces blocks.
@@ -570,7 +705,9 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
                 for (int j0 = w.j; ok && j0 < w.j1; j0 += per_batch) {
                     const int j = j0 + lane / pieces;
                     int64_t id = -1;
-                    float ks = 0.0f, vs = 0.0f;
+                    float ks = 0.0f, vs = 0.0f, ks_top, lv, lv_top;
+                    uint32_t k_mul, v_mul;
+                    bool all_fit = false;
                     if (j < w.j1) {
                         const int token = w.it.key0(j) + (lane % pieces) * piece;
                         if (token < w.seq.n && ragged_sees(p, w.it, token, piece)) {
@@ -584,38 +721,48 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
                             }
                         }
                     }
-                    const uint32_t there = __ballot_sync(0xffffffffu, id >= 0);
-                    // the block's largest scales, and how far this page's are below
-                    float ks_top = ks, vs_top = vs;
-                    for (int o = 1; o < pieces; o <<= 1) {
-                        ks_top = fmaxf(ks_top, __shfl_xor_sync(0xffffffffu, ks_top, o));
-                        vs_top = fmaxf(vs_top, __shfl_xor_sync(0xffffffffu, vs_top, o));
-                    }
-                    if (id < 0) {
-                        ks = ks_top > 0.0f ? ks_top : 1.0f;
-                        vs = vs_top > 0.0f ? vs_top : 1.0f;
-                    }
-                    const uint32_t k_bits = __float_as_uint(ks), v_bits = __float_as_uint(vs);
-                    const int k_below = (int)(__float_as_uint(fmaxf(ks_top, ks)) - k_bits) >> 23;
-                    const int v_below = (int)(__float_as_uint(fmaxf(vs_top, vs)) - v_bits) >> 23;
-                    const bool fits = ks > 0.0f && vs > 0.0f && ((k_bits | v_bits) & 0x7fffffu) == 0 && k_below <= 14 &&
-                                      v_below <= 14;
-                    const uint32_t near = __ballot_sync(0xffffffffu, fits);
-                    const uint32_t block = (1u << pieces) - 1;
-                    const bool all_fit = (near >> (lane & ~(pieces - 1)) & block) == block;
-                    const uint32_t k_mul = (uint32_t)(all_fit ? 15 - k_below : 15) << 10;   // 2^-k_below, or 1
-                    const uint32_t v_mul = (uint32_t)(all_fit ? 15 - v_below : 15) << 10;
-                    const float lv = log2f(fmaxf(vs, kMinScale)), lv_top = log2f(fmaxf(fmaxf(vs_top, vs), kMinScale));
-                    ks_top = fmaxf(ks_top, ks);
+                    const uint32_t there = __ballot_sync(0xffffffffu, id >= 0), block = (1u << pieces) - 1;
                     const int64_t at = (id * p.pool.kv_heads + w.head) * p.pool.page * HD;
                     for (int i = 0; i < per_batch && j0 + i < w.j1; ++i, ++blocks) {
                         const uint32_t s = blocks % G::kRaw, ph = blocks / G::kRaw & 1u;
                         const bool in = lane / pieces == i;
                         const uint32_t mine = there >> (i * pieces) & block;
                         const uint32_t bytes = __popc(mine) * piece * HD;
+                        const uint32_t off = s * G::kTile8 + (lane % pieces) * piece * HD;
                         if (!wait_warp(raw_empty(0, s), ph ^ 1u, p.wait_limit_ns, abort_flag, kSiteProducerEmpty)) {
                             ok = false;
                             break;
+                        }
+                        if (lane == 0)
+                            mbar_arrive_expect_tx(raw_full(0, s), bytes);
+                        __syncwarp();
+                        if (in && id >= 0)
+                            bulk_load(base + G::kOffRawK + off, p.pool.values[0] + at, piece * HD, raw_full(0, s));
+                        if (i == 0) {
+                            // the blocks' largest scales, and how far the pages' are below (read while the first copies are under way)
+                            ks_top = ks;
+                            float vs_top = vs;
+                            for (int o = 1; o < pieces; o <<= 1) {
+                                ks_top = fmaxf(ks_top, __shfl_xor_sync(0xffffffffu, ks_top, o));
+                                vs_top = fmaxf(vs_top, __shfl_xor_sync(0xffffffffu, vs_top, o));
+                            }
+                            if (id < 0) {
+                                ks = ks_top > 0.0f ? ks_top : 1.0f;
+                                vs = vs_top > 0.0f ? vs_top : 1.0f;
+                            }
+                            ks_top = fmaxf(ks_top, ks);
+                            vs_top = fmaxf(vs_top, vs);
+                            const uint32_t k_bits = __float_as_uint(ks), v_bits = __float_as_uint(vs);
+                            const int k_below = (int)(__float_as_uint(ks_top) - k_bits) >> 23;
+                            const int v_below = (int)(__float_as_uint(vs_top) - v_bits) >> 23;
+                            const bool fits = ks > 0.0f && vs > 0.0f && ((k_bits | v_bits) & 0x7fffffu) == 0 &&
+                                              k_below <= 14 && v_below <= 14;
+                            const uint32_t near = __ballot_sync(0xffffffffu, fits);
+                            all_fit = (near >> (lane & ~(pieces - 1)) & block) == block;
+                            k_mul = (uint32_t)(all_fit ? 15 - k_below : 15) << 10;   // 2^-k_below, or 1
+                            v_mul = (uint32_t)(all_fit ? 15 - v_below : 15) << 10;
+                            lv = log2f(fmaxf(vs, kMinScale));
+                            lv_top = log2f(fmaxf(vs_top, kMinScale));
                         }
                         RaggedMeta &m = metas[blocks % G::kMetas];
                         if (in) {
@@ -631,8 +778,7 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
                                 for (int g = 0; g < kGroups; ++g)
                                     gone |= (mine >> (g * 16 / piece) & 1u) ? 0u : 1u << g;
                                 const bool part = gone || ragged_masked(p, w.it.first, w.it.last, key0);
-                                m.flags = (all_fit ? kNearScales : 0) |
-                                          (part ? kInPart : 0) | (at == w.j ? kFirst : 0) |
+                                m.flags = (all_fit ? kNearScales : 0) | (part ? kInPart : 0) | (at == w.j ? kFirst : 0) |
                                           (at + 1 == w.j1 ? kLast : 0) | (w.rows(p) > BM ? kBothTiles : 0);
                                 m.ks = ks_top;
                                 m.lv = lv_top;
@@ -642,14 +788,8 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
                             }
                         }
                         __syncwarp();
-                        if (lane == 0) {
+                        if (lane == 0)
                             mbar_arrive(meta_full(blocks % G::kMetas));
-                            mbar_arrive_expect_tx(raw_full(0, s), bytes);
-                        }
-                        __syncwarp();
-                        const uint32_t off = s * G::kTile8 + (lane % pieces) * piece * HD;
-                        if (in && id >= 0)
-                            bulk_load(base + G::kOffRawK + off, p.pool.values[0] + at, piece * HD, raw_full(0, s));
                         if (!wait_warp(raw_empty(1, s), ph ^ 1u, p.wait_limit_ns, abort_flag, kSiteProducerEmpty)) {
                             ok = false;
                             ++blocks;   // its K is on its way
@@ -671,11 +811,11 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
                 if (ok || i + 1 < blocks)
                     wait_drain(raw_full(1, i % G::kRaw), i / G::kRaw & 1u, p.wait_limit_ns, abort_flag);
             }
-        } else if (start < stop && warp >= kConvWarp) {
+        } else if (blocks_here > 0 && warp >= kConvWarp) {
             // ======================================================== e4m3 to fp16
             const int mine = warp - kConvWarp, row0 = BN / kConvWarps * mine;
             bool ok = true, bad = false;
-            for (uint32_t i = 0; ok && i < (uint32_t)(stop - start); ++i) {
+            for (uint32_t i = 0; ok && i < (uint32_t)blocks_here; ++i) {
                 const uint32_t rs = i % G::kRaw, rp = i / G::kRaw & 1u, st = i & 1u, ph = i >> 1 & 1u;
                 ok = wait_warp(meta_full(i % G::kMetas), i / G::kMetas & 1u, p.wait_limit_ns, abort_flag,
                                kSiteMmaFull);
@@ -711,7 +851,7 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
                     }
                 }
             }
-        } else if (start < stop && warp == kMmaWarp) {
+        } else if (blocks_here > 0 && warp == kMmaWarp) {
             // ======================================================== products
             // (one elected thread issues, the whole warp walks along)
             const bool leader = elect_one();
@@ -760,7 +900,7 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
             };
             // Both tiles' scores of block i; the first ones of a segment wait for its rows
             auto flags_of = [&](uint32_t i) { return __shfl_sync(0xffffffffu, metas[i % G::kMetas].flags, 0); };
-            const uint32_t blocks = (uint32_t)(stop - start);
+            const uint32_t blocks = (uint32_t)blocks_here;
             bool ok = wait_k(0) && wait_q(0, segs0);
             uint32_t flags = 0;
             if (ok) {
@@ -816,7 +956,7 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRaggedSoftmaxRegs));
-        if (start < stop) {
+        if (blocks_here > 0) {
             // ======================================================== softmax / output
             const int t = warp >> 2;                        // tile
             const int q = warp & 3;                         // TMEM lanes 32q .. 32q+31
@@ -827,21 +967,26 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
             // The warp's 32 rows of Q into shared memory: HD / 8 lanes a row.  bf16 rows are scaled by a power of
             // two that brings their largest element to [2^14, 2^15), within fp16; returned: what undoes it.
             auto load_q = [&](const RaggedWalk &w) -> float {
-                constexpr int kLanes = HD / 8, kRows = 32 / kLanes;
+                constexpr int kLanes = HD / 8, kRows = 32 / kLanes, kLoads = 32 / kRows;
                 const int rows = w.rows(p), sub = lane % kLanes;
                 float mine = 1.0f;
-#pragma unroll 4
-                for (int i = 0; i < 32 / kRows; ++i) {
-                    const int r = 32 * q + i * kRows + lane / kLanes, row = t * BM + r;   // of the tile, the item
-                    uint4 x = make_uint4(0, 0, 0, 0);
+                uint4 x[kLoads];   // (all on their way at once: four at a time took 3 us longer)
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i) {
+                    const int row = t * BM + 32 * q + i * kRows + lane / kLanes;   // of the item
+                    x[i] = make_uint4(0, 0, 0, 0);
                     if (row < rows) {
                         const int token = p.by_group.quotient(w.item * 2 * BM + row);
                         const int g = w.item * 2 * BM + row - token * p.group;
-                        x = *reinterpret_cast<const uint4 *>(p.q + (w.seq.start + token) * p.q_stride[0] +
-                                                             (w.head * p.group + g) * p.q_stride[1] + sub * 8);
+                        x[i] = *reinterpret_cast<const uint4 *>(p.q + (w.seq.start + token) * p.q_stride[0] +
+                                                                (w.head * p.group + g) * p.q_stride[1] + sub * 8);
                     }
+                }
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i) {
+                    const int r = 32 * q + i * kRows + lane / kLanes;   // of the tile
                     if constexpr (kBf16) {
-                        uint32_t v[4] = {x.x, x.y, x.z, x.w};
+                        uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
                         uint32_t top = 0;
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
@@ -858,12 +1003,12 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
                             const float2 f = pair_to_float2<true>(v[e]);
                             v[e] = half2_of(f.x * to, f.y * to);
                         }
-                        x = make_uint4(v[0], v[1], v[2], v[3]);
+                        x[i] = make_uint4(v[0], v[1], v[2], v[3]);
                         const float got = __shfl_sync(0xffffffffu, back, (lane % kRows) * kLanes);
                         mine = lane / kRows == i ? got : mine;
                     }
                     st_shared_v4(base + G::kOffQ + t * G::kTile16 + (sub >> 3) * kSub + r * 128 +
-                                     ((uint32_t)((sub & 7) ^ (r & 7)) << 4), x.x, x.y, x.z, x.w);
+                                     ((uint32_t)((sub & 7) ^ (r & 7)) << 4), x[i].x, x[i].y, x[i].z, x[i].w);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -873,6 +1018,8 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
             };
             uint32_t turns = 0, blocks = 0, segments = 0, outputs = 0;
             bool alive = true;
+            RaggedCut cuts[2];
+            int num_cuts = 0;
             RaggedWalk w = first_segment();
             float row_scale = t == 0 || w.rows(p) > BM ? load_q(w) : 1.0f;
             for (bool more = true; alive && more; ++segments) {
@@ -905,44 +1052,47 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
                     const RaggedMeta &meta = metas[i % G::kMetas];
                     const int key0 = cur.it.key0(j);
                     const uint32_t missing = meta.missing, flags = meta.flags;
-                    if (missing || ragged_masked(p, first, last, key0)) {
-                        // -infinity for what is not seen, a bit per key, 32 at a time
-                        const int hi = pos - key0;
-                        const int lo = p.window > 0 ? hi - p.window : -1;
-                        const int head = p.sinks - key0;
+                    // The scores are read twice, 32 at a time, the next ones while these are worked on: for the largest, where
+                    // those that the row does not see become -infinity, and for the weights.  (All 128 in registers with
+                    // both passes unrolled made the loop 10 KB of code, and fetching it the bound: 890 to 960 us.)
+                    const bool masked = missing || ragged_masked(p, first, last, key0);
+                    const int hi = pos - key0, lo = p.window > 0 ? hi - p.window : -1, head = p.sinks - key0;
+                    auto mask = [&](uint32_t (&x)[32], int c0) {   // a bit per key
+                        uint32_t seen = keys_below(hi + 1 - c0) & (~keys_below(lo + 1 - c0) | keys_below(head - c0));
+                        seen &= ~((missing >> (c0 / 16) & 1u ? 0x0000ffffu : 0u) |
+                                  (missing >> (c0 / 16 + 1) & 1u ? 0xffff0000u : 0u));
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            x[e] = seen & (1u << e) ? x[e] : __float_as_uint(-INFINITY);
+                        tmem_st_x32(s_addr + c0, x);
+                    };
+                    uint32_t xa[32], xb[32];
+                    float ma = -INFINITY, mb = -INFINITY;
+                    auto largest = [&](const uint32_t (&x)[32]) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            ma = fmaxf(ma, __uint_as_float(x[e]));
+                            mb = fmaxf(mb, __uint_as_float(x[e + 1]));
+                        }
+                    };
+                    tmem_ld_x32(s_addr, xa);
 #pragma unroll 1
-                        for (int c0 = 0; c0 < BN; c0 += 32) {
-                            uint32_t x[32];
-                            tmem_ld_x32_sync(s_addr + c0, x);
-                            uint32_t seen = keys_below(hi + 1 - c0) & (~keys_below(lo + 1 - c0) | keys_below(head - c0));
-                            seen &= ~((missing >> (c0 / 16) & 1u ? 0x0000ffffu : 0u) |
-                                      (missing >> (c0 / 16 + 1) & 1u ? 0xffff0000u : 0u));
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                x[e] = seen & (1u << e) ? x[e] : __float_as_uint(-INFINITY);
-                            tmem_st_x32(s_addr + c0, x);
+                    for (int c0 = 0; c0 < BN; c0 += 64) {
+                        tmem_ld_wait_regs(xa);
+                        tmem_ld_x32(s_addr + c0 + 32, xb);
+                        if (masked)
+                            mask(xa, c0);
+                        largest(xa);
+                        tmem_ld_wait_regs(xb);
+                        if (masked) {
+                            mask(xb, c0 + 32);
+                            tmem_st_wait();
                         }
-                        tmem_st_wait();
+                        tmem_ld_x32(s_addr + ((c0 + 64) & (BN - 1)), xa);   // at last the first ones again
+                        largest(xb);
                     }
-                    uint32_t v[BN];
-#pragma unroll
-                    for (int c0 = 0; c0 < BN; c0 += 32)
-                        tmem_ld_x32(s_addr + c0, *reinterpret_cast<uint32_t(*)[32]>(&v[c0]));
-#pragma unroll
-                    for (int c0 = 0; c0 < BN; c0 += 32)
-                        tmem_ld_wait_regs(*reinterpret_cast<uint32_t(*)[32]>(&v[c0]));
-                    // the largest score, in base 2
                     const float c_blk = factor(meta.ks);
-                    float mx;
-                    {
-                        float a = __uint_as_float(v[0]), b = __uint_as_float(v[1]);
-#pragma unroll
-                        for (int e = 2; e < BN; e += 2) {
-                            a = fmaxf(a, __uint_as_float(v[e]));
-                            b = fmaxf(b, __uint_as_float(v[e + 1]));
-                        }
-                        mx = __fmul_rn(fmaxf(a, b), c_blk);
-                    }
+                    float mx = __fmul_rn(fmaxf(ma, mb), c_blk);
                     const float lv = meta.lv;
                     // the row's largest product with V's scale, above the reference of the weights
                     float over = (mx - m_ref) + lv;
@@ -984,15 +1134,14 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
                         const float a = (lv + kPLog2 - rr_ref) - m_ref;
                         const float2 c2 = make_float2(c_blk, c_blk), a2 = make_float2(a, a);
                         float2 sa = make_float2(0.0f, 0.0f), sb = make_float2(0.0f, 0.0f);
-#pragma unroll
-                        for (int e0 = 0; e0 < BN; e0 += 32) {
+                        auto weigh = [&](const uint32_t (&x)[32], int c0) {
                             uint32_t ph[16];
 #pragma unroll
                             for (int e = 0; e < 32; e += 4) {
-                                const float2 x01 = __ffma2_rn(make_float2(__uint_as_float(v[e0 + e]),
-                                                                          __uint_as_float(v[e0 + e + 1])), c2, a2);
-                                const float2 x23 = __ffma2_rn(make_float2(__uint_as_float(v[e0 + e + 2]),
-                                                                          __uint_as_float(v[e0 + e + 3])), c2, a2);
+                                const float2 x01 = __ffma2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])),
+                                                              c2, a2);
+                                const float2 x23 = __ffma2_rn(make_float2(__uint_as_float(x[e + 2]),
+                                                                          __uint_as_float(x[e + 3])), c2, a2);
                                 const float2 e01 = make_float2(fast_exp2(x01.x), fast_exp2(x01.y));
                                 const float2 e23 = make_float2(fast_exp2(x23.x), fast_exp2(x23.y));
                                 sa = __fadd2_rn(sa, e01);
@@ -1000,10 +1149,21 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
                                 ph[e / 2] = half2_of(e01.x, e01.y);
                                 ph[e / 2 + 1] = half2_of(e23.x, e23.y);
                             }
-                            tmem_st_x16(s_addr + e0 / 2, ph);
+                            tmem_st_x16(s_addr + c0 / 2, ph);   // (over scores that have been read)
+                        };
+#pragma unroll 1
+                        for (int c0 = 0; c0 < BN; c0 += 64) {
+                            tmem_ld_wait_regs(xa);
+                            tmem_ld_x32(s_addr + c0 + 32, xb);
+                            weigh(xa, c0);
+                            tmem_ld_wait_regs(xb);
+                            if (c0 + 64 < BN)
+                                tmem_ld_x32(s_addr + c0 + 64, xa);
+                            weigh(xb, c0 + 32);
                         }
                         sum = ((sa.x + sa.y) + (sb.x + sb.y)) * back_of(rr_ref, lv);
                     } else {
+                        tmem_ld_wait_regs(xa);   // (their registers are free now)
                         sum = ragged_weights(s_addr, meta, c_row, m_ref, rr_ref);
                     }
                     l += sum;
@@ -1038,19 +1198,6 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
                 const bool valid = my_row < rows;
                 uint16_t *dst = p.out + ((int64_t)(cur.seq.start + token) * p.q_heads + cur.head * p.group +
                                          (row - token * p.group)) * HD;
-                auto write_out = [&](int c0, const uint32_t (&o)[32], float inv, float f) {
-                    uint4 *d4 = reinterpret_cast<uint4 *>(dst + c0);
-                    if (valid)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            uint32_t h[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                h[k] = pack_out<kBf16>(__uint_as_float(o[8 * e + 2 * k]) * inv * f * f,
-                                                       __uint_as_float(o[8 * e + 2 * k + 1]) * inv * f * f);
-                            d4[e] = make_uint4(h[0], h[1], h[2], h[3]);
-                        }
-                };
                 const bool whole = cur.j == 0 && cur.j1 == cur.nb;
                 if (whole) {
                     const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;   // 0: the row sees nothing
@@ -1059,81 +1206,45 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
                     for (int c0 = 0; c0 < HD; c0 += 32) {
                         uint32_t o[32];
                         tmem_ld_x32_sync(o_addr + c0, o);
-                        write_out(c0, o, inv, f);
+                        if (valid)
+                            write_row32<kBf16>(dst + c0, reinterpret_cast<const float(&)[32]>(o), inv, f);
                     }
                 } else {
-                    // a part: O, m, l and rr to the workspace; the warp that comes last joins the parts of its rows
-                    const int ranges = plan->ranges, total = plan->total;
-                    const int c_first = range_owner(cur.unit0, total, ranges);
-                    const int c_last = range_owner(cur.unit0 + cur.nb - 1, total, ranges);
-                    auto part_of = [&](int c) {
-                        const bool mid = c == c_first && cur.unit0 != range_start(c, total, ranges);
-                        return p.partial + ((int64_t)(2 * c + (mid ? 1 : 0)) * 8 + warp) * (HD + 4) * 32 + lane;
-                    };
-                    float *part = part_of(blockIdx.x);
+                    // a part: O, m, l and rr to the workspace
+                    RaggedCut &cut = cuts[num_cuts++];
+                    cut.dst = valid ? dst : nullptr;
+                    cut.first = range_owner(cur.unit0, plan->total, plan->ranges);
+                    cut.last = range_owner(cur.unit0 + ragged_units(cur.nb, plan->part) - 1, plan->total, plan->ranges);
+                    cut.mid = cur.unit0 != range_start(cut.first, plan->total, plan->ranges);
+                    float4 *part = ragged_part_of<HD>(p, cut, warp, lane, blockIdx.x);
 #pragma unroll 1
                     for (int c0 = 0; c0 < HD; c0 += 32) {
                         uint32_t o[32];
                         tmem_ld_x32_sync(o_addr + c0, o);
                         if (valid)
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                __stcg(part + (c0 + e) * 32, __uint_as_float(o[e]));
+                            for (int e = 0; e < 32; e += 4)
+                                __stcg(part + (c0 + e) / 4 * 32,
+                                       make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
+                                                   __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3])));
                     }
-                    if (valid) {
-                        __stcg(part + HD * 32, m);
-                        __stcg(part + (HD + 1) * 32, l);
-                        __stcg(part + (HD + 2) * 32, rr);
-                    }
-                    __syncwarp();
-                    unsigned before = 0;
-                    if (lane == 0)
-                        before = count_part(p.arrived + c_first * 8 + warp, (unsigned)(c_last - c_first));
-                    before = __shfl_sync(0xffffffffu, before, 0);
-                    __syncwarp();
-                    if (before == (unsigned)(c_last - c_first) && valid) {
-                        // the largest references, and the sum of weights
-                        float mm = -INFINITY, yy = -INFINITY, ll = 0.0f;
-#pragma unroll 4
-                        for (int c = c_first; c <= c_last; ++c)
-                            mm = fmaxf(mm, __ldcg(part_of(c) + HD * 32));
-                        const float ref = mm == -INFINITY ? 0.0f : mm;
-#pragma unroll 4
-                        for (int c = c_first; c <= c_last; ++c) {
-                            const float *x = part_of(c) + HD * 32;
-                            const float pm = __ldcg(x), pl = __ldcg(x + 32), pr = __ldcg(x + 64);
-                            yy = fmaxf(yy, pm == -INFINITY ? -INFINITY : (pm - ref) + pr);
-                            ll += pl != pl ? pl : pm == -INFINITY ? 0.0f : pl * exp2f(pm - ref);
-                        }
-                        const float inv = ll > 0.0f || ll != ll ? 1.0f / ll : 0.0f;
-                        const float f = yy == -INFINITY ? 0.0f : exp2f(0.5f * (yy - kPLog2));
-#pragma unroll 1
-                        for (int c0 = 0; c0 < HD; c0 += 64) {   // (64 loads of a part are under way at once)
-                            float s[64];
-#pragma unroll
-                            for (int e = 0; e < 64; ++e)
-                                s[e] = 0.0f;
-#pragma unroll 1
-                            for (int c = c_first; c <= c_last; ++c) {
-                                const float *x = part_of(c);
-                                const float pm = __ldcg(x + HD * 32), pr = __ldcg(x + (HD + 2) * 32);
-                                const float a = pm == -INFINITY ? 1.0f : exp2f((pm - ref) + pr - yy);
-#pragma unroll
-                                for (int e = 0; e < 64; ++e)
-                                    s[e] = fmaf(__ldcg(x + (c0 + e) * 32), a, s[e]);
-                            }
-#pragma unroll
-                            for (int h = 0; h < 64; h += 32) {
-                                uint32_t o[32];
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    o[e] = __float_as_uint(s[h + e]);
-                                write_out(c0 + h, o, inv, f);
-                            }
-                        }
-                    }
-                    __syncwarp();
+                    if (valid)
+                        __stcg(part + HD / 4 * 32, make_float4(m, l, rr, 0.0f));
                 }
+            }
+            // The parts of cut items (the one that the range starts in and the one that it ends in) are counted now; the warp
+            // that comes last joins those of its rows, in the order of the ranges.
+            for (int k = 0; alive && k < num_cuts; ++k) {
+                const RaggedCut cut = cuts[k];
+                __syncwarp();
+                unsigned before = 0;
+                if (lane == 0)
+                    before = count_part(p.arrived + cut.first * 8 + warp, (unsigned)(cut.last - cut.first));
+                before = __shfl_sync(0xffffffffu, before, 0);
+                __syncwarp();
+                if (before != (unsigned)(cut.last - cut.first) || cut.dst == nullptr)
+                    continue;
+                ragged_join<HD, kBf16>(p, cut, warp, lane);
             }
         }
     }
