@@ -63,7 +63,8 @@ KERNEL_SOURCES = ("gemm_relu_api.cu", "gemm_relu_kernels.cuh", "gemm_relu_splitk
                   "gemm_relu_2sm.cuh", "gemm_relu_gemv.cuh", "flash_attention.cuh", "sm103.cuh",
                   "gemm_relu_stage.cuh", "flash_attention_window.cuh",
                   "flash_attention_window_api.cuh", "kv_cache.cuh", "kv_attention.cuh",
-                  "kv_cache_api.cuh", "kv_ragged.cuh", "rotary.cuh", "rotary_api.cuh")
+                  "kv_cache_api.cuh", "kv_ragged.cuh", "rotary.cuh", "rotary_api.cuh",
+                  "cross_step.cuh")
 
 
 def kernel_source_hash():

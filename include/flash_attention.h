@@ -76,6 +76,16 @@ int flash_attention_window_x16(const void *Q, const void *K, const void *V, void
                                const int64_t *k_strides, const int64_t *v_strides, int64_t window,
                                int64_t sinks, void *stream);
 
+#define GEMMRELU_CROSS_COUNTER_BYTES 4096   /* of flash_attention_cross_x16's workspace */
+
+/*
+ * flash_attention_cross_x16_workspace_bytes -- bytes of device workspace that
+ * flash_attention_cross_x16 needs for these sizes on the current device: 0 unless few query
+ * rows meet fewer heads than fill the GPU (and for invalid arguments, or when no CUDA device is available).
+ */
+size_t flash_attention_cross_x16_workspace_bytes(int64_t batch, int64_t q_seq, int64_t kv_seq,
+                                                 int64_t q_heads, int64_t kv_heads, int64_t head_dim);
+
 /*
  * flash_attention_cross_x16 -- attention to an encoder's states: O = softmax(Q K^T / sqrt(d)) V,
  * where query i of sequence b sees the keys j < lengths[b], whatever i is.
@@ -85,13 +95,18 @@ int flash_attention_window_x16(const void *Q, const void *K, const void *V, void
  *              sequence without keys gets 0; a number out of range counts as 0, and
  *              gemm_relu_status reports GEMMRELU_ERR_PAGE.
  * q_heads    : at most 128 times kv_heads.
+ * workspace  : at least flash_attention_cross_x16_workspace_bytes(...), 16-byte aligned (any
+ *              value where that is 0).  Its first GEMMRELU_CROSS_COUNTER_BYTES must be 0
+ *              before its first call; every call leaves them 0, whatever its sizes.
+ *              Calls that may overlap on the GPU need different workspaces.
  * What stands behind a sequence's keys in K and V, NaN and infinities among it, reaches no query.
  */
 int flash_attention_cross_x16(const void *Q, const void *K, const void *V, void *O, int dtype,
                               int64_t batch, int64_t q_seq, int64_t kv_seq, int64_t q_heads,
                               int64_t kv_heads, int64_t head_dim, const int64_t *q_strides,
                               const int64_t *k_strides, const int64_t *v_strides,
-                              const int32_t *lengths, void *stream);
+                              const int32_t *lengths, void *workspace, size_t workspace_bytes,
+                              void *stream);
 
 /*
  * Host-only test hook: the blocks of 128 keys that flash_attention_window_x16 visits

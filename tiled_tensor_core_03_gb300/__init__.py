@@ -26,6 +26,7 @@ ERR_SCRATCH_LIMIT = 7
 ERR_PAGE = 8
 NOALLOC_SCRATCH_BYTES = 8 << 20
 F16, BF16 = 0, 1   # types of 16-bit tensors
+CROSS_COUNTER_BYTES = 4096   # zeroed once in flash_attention_cross's workspaces
 KV_COUNTER_BYTES = 4096   # zeroed once in kv_cache_attention's workspaces
 RAGGED_COUNTER_BYTES = 8192   # and in kv_cache_attention_ragged's
 
@@ -108,8 +109,11 @@ def lib():
         L.flash_attention_window_x16.argtypes = [vp, vp, vp, vp, i32] + [i64] * 6 + [vp] * 3 + \
             [i64, i64, vp]
         L.flash_attention_window_x16.restype = i32
-        L.flash_attention_cross_x16.argtypes = [vp, vp, vp, vp, i32] + [i64] * 6 + [vp] * 5
+        L.flash_attention_cross_x16.argtypes = [vp, vp, vp, vp, i32] + [i64] * 6 + \
+            [vp] * 5 + [sz, vp]
         L.flash_attention_cross_x16.restype = i32
+        L.flash_attention_cross_x16_workspace_bytes.argtypes = [i64] * 6
+        L.flash_attention_cross_x16_workspace_bytes.restype = sz
         L.flash_attention_window_debug_blocks.argtypes = [i64] * 4 + [vp]
         L.flash_attention_window_debug_blocks.restype = i32
         L.kv_cache_debug_span.argtypes = [i64] * 4 + [vp]
@@ -216,11 +220,17 @@ def kv_cache_attention_x16(cache, q, dtype, batch, tokens, q_heads, q_strides, o
 
 
 def flash_attention_cross_x16(Q, K, V, O, dtype, batch, q_seq, kv_seq, q_heads, kv_heads,
-                              head_dim, q_strides, k_strides, v_strides, lengths, stream=None):
+                              head_dim, q_strides, k_strides, v_strides, lengths, workspace=None,
+                              workspace_bytes=0, stream=None):
     """*_strides: ctypes arrays of three int64 {sequence, token, head}."""
     return lib().flash_attention_cross_x16(Q, K, V, O, dtype, batch, q_seq, kv_seq, q_heads,
                                            kv_heads, head_dim, q_strides, k_strides, v_strides,
-                                           lengths, stream)
+                                           lengths, workspace, workspace_bytes, stream)
+
+
+def flash_attention_cross_x16_workspace_bytes(batch, q_seq, kv_seq, q_heads, kv_heads, head_dim):
+    return lib().flash_attention_cross_x16_workspace_bytes(batch, q_seq, kv_seq, q_heads, kv_heads,
+                                                           head_dim)
 
 
 def kv_cache_attention_ragged_x16_workspace_bytes(head_dim):
@@ -450,6 +460,7 @@ def __getattr__(name):
     # the serving operators' front end needs torch at import; the rest of this module does not
     if name in ("flash_attention_window", "KVCache", "kv_cache_append", "kv_cache_attention",
                 "kv_cache_attention_workspace", "kv_cache_evict", "flash_attention_cross",
+                "flash_attention_cross_workspace",
                 "kv_cache_attention_ragged", "kv_cache_attention_ragged_workspace", "rotary",
                 "rotary_frequencies"):
         from . import serving

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "flash_attention_window.cuh"
+#include "cross_step.cuh"
 
 namespace {
 
@@ -57,6 +58,50 @@ int launch_window(const CUtensorMap &mQ, const CUtensorMap &mK, const CUtensorMa
     return launch_status(cudaLaunchKernelEx(&cfg, kern, mQ, mK, mV, p));
 }
 
+// How a step of cross attention is cut: none (0) for more rows than a step has.
+struct StepSplit {
+    int rows, parts;      // rows of a head; parts of its states
+    size_t bytes;         // of workspace
+};
+
+// Parts of a head's states: as many as there are blocks to an SM for, a unit of 64 keys at least.
+StepSplit step_split(int64_t batch, int64_t q_seq, int64_t kv_seq, int64_t q_heads, int64_t kv_heads,
+                     int64_t head_dim, int sms) {
+    StepSplit s{0, 1, 0};
+    const int64_t group = q_heads / kv_heads;
+    if (q_seq > FA::kStepMostRows || q_seq * group > FA::kStepMostRows)
+        return s;
+    s.rows = (int)(q_seq * group);
+    const int64_t heads = batch * kv_heads, units = (kv_seq + FA::kStepKeys - 1) / FA::kStepKeys;
+    const int64_t slots = (int64_t)sms * (head_dim == 64 ? FA::StepCfg<64, 1>::kBlocksPerSm : FA::StepCfg<128, 1>::kBlocksPerSm);
+    if (heads <= FA::kStepCounters)
+        s.parts = (int)std::max<int64_t>(1, std::min(slots / heads, units));
+    if (s.parts > 1)
+        s.bytes = GEMMRELU_CROSS_COUNTER_BYTES +
+                  (size_t)heads * s.parts * (s.rows <= 8 ? 8 : 16) * (head_dim + 4) * sizeof(float);
+    return s;
+}
+
+template <int D, int kN, bool kBf16>
+int launch_step(const CUtensorMap &mK, const CUtensorMap &mV, const FA::StepParams &p, int64_t blocks, cudaStream_t s,
+                bool &attr_done) {
+    auto kern = FA::cross_step_kernel<D, kN, kBf16>;
+    if (!ensure_smem_attr(attr_done, kern, FA::StepCfg<D, kN>::kSmem))
+        return GEMMRELU_ERR_LAUNCH;
+    return launch_kernel(kern, (unsigned)blocks, (unsigned)FA::kStepThreads, FA::StepCfg<D, kN>::kSmem, s, false, 1u, mK,
+                         mV, p);
+}
+
+template <int D>
+int launch_step_as(int dtype, const CUtensorMap &mK, const CUtensorMap &mV, const FA::StepParams &p, int64_t blocks,
+                   cudaStream_t s, bool *attr) {
+    if (p.rows <= 8)
+        return dtype == GEMMRELU_BF16 ? launch_step<D, 1, true>(mK, mV, p, blocks, s, attr[0])
+                                      : launch_step<D, 1, false>(mK, mV, p, blocks, s, attr[1]);
+    return dtype == GEMMRELU_BF16 ? launch_step<D, 2, true>(mK, mV, p, blocks, s, attr[2])
+                                  : launch_step<D, 2, false>(mK, mV, p, blocks, s, attr[3]);
+}
+
 template <bool kCross>
 int launch_window_as(int dtype, int64_t head_dim, const CUtensorMap &mQ, const CUtensorMap &mK, const CUtensorMap &mV,
                      const FA::WindowParams &p, int sms, cudaStream_t s, bool *attr) {
@@ -84,7 +129,8 @@ template <bool kCross>
 static int attention_strided(const void *Q, const void *K, const void *V, void *O, int dtype, int64_t batch,
                              int64_t q_seq, int64_t kv_seq, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
                              const int64_t *q_strides, const int64_t *k_strides, const int64_t *v_strides,
-                             int64_t window, int64_t sinks, const int32_t *states, void *stream) {
+                             int64_t window, int64_t sinks, const int32_t *states, void *workspace,
+                             size_t workspace_bytes, void *stream) {
     if ((dtype != GEMMRELU_F16 && dtype != GEMMRELU_BF16) || batch < 0 || batch > 65535 ||
         q_seq < 0 || kv_seq < 0 || q_seq > ((int64_t)1 << 30) || kv_seq > ((int64_t)1 << 30) ||
         q_heads < 0 || q_heads > 65535 || kv_heads < 0 || kv_heads > 65535 ||
@@ -111,7 +157,46 @@ static int attention_strided(const void *Q, const void *K, const void *V, void *
     if (kv_seq == 0)   // nobody sees anything
         return launch_status(cudaMemsetAsync(O, 0, (size_t)(batch * q_seq * q_heads * head_dim) * 2, s));
     const int tile_tokens = kCross ? (int)(FA::BM / group) : FA::BM;
+    // Weights stay below 2^8 times a row's largest: 9 + log2(keys that a row can see) keeps their sum
+    // below 1/2.  fp16 values are far from fp32's range, and its weights have none to spare.
+    const int64_t seen = window > 0 ? std::min(kv_seq, std::min(window, kv_seq) + std::min(sinks, kv_seq)) : kv_seq;
+    const float shift = dtype == GEMMRELU_BF16 ? 9.0f + std::ceil(std::log2((float)seen)) : 0.0f;
+    const double scale = 1.4426950408889634 / std::sqrt((double)head_dim);
     CUtensorMap mQ, mK, mV;
+    const StepSplit step = kCross ? step_split(batch, q_seq, kv_seq, q_heads, kv_heads, head_dim, ds->sms) : StepSplit{0, 1, 0};
+    if (step.rows > 0) {
+        const int64_t blocks = batch * kv_heads * step.parts;
+        if (blocks > 0x7fffffff)
+            return GEMMRELU_ERR_INVALID_ARG;
+        if (step.bytes > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < step.bytes))
+            return GEMMRELU_ERR_WORKSPACE;
+        if (!make_strided_map(&mK, K, dtype, batch, kv_seq, kv_heads, head_dim, k_strides, 1, FA::kStepKeys) ||
+            !make_strided_map(&mV, V, dtype, batch, kv_seq, kv_heads, head_dim, v_strides, 1, FA::kStepKeys))
+            return GEMMRELU_ERR_LAUNCH;
+        FA::StepParams p{};
+        p.q = static_cast<const uint16_t *>(Q);
+        const int64_t n[3] = {batch, q_seq, q_heads};
+        for (int i = 0; i < 3; ++i)
+            p.qs[i] = n[i] > 1 ? q_strides[i] : 0;
+        p.o = static_cast<uint16_t *>(O);
+        p.states = states;
+        p.n_q = (int)q_seq;
+        p.n_kv = (int)kv_seq;
+        p.q_heads = (int)q_heads;
+        p.kv_heads = (int)kv_heads;
+        p.group = (int)group;
+        p.rows = step.rows;
+        p.parts = step.parts;
+        p.scale = (float)scale;
+        p.slack = (float)(FA::kRescaleLog2 / scale);
+        p.shift = shift;
+        p.arrived = static_cast<unsigned *>(workspace);
+        p.partial = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + GEMMRELU_CROSS_COUNTER_BYTES);
+        p.drop_arrive = g_drop_arrive.load();
+        p.wait_limit_ns = wait_limit_ns();
+        return head_dim == 64 ? launch_step_as<64>(dtype, mK, mV, p, blocks, s, ds->attr_step)
+                              : launch_step_as<128>(dtype, mK, mV, p, blocks, s, ds->attr_step + 4);
+    }
     if (!make_strided_map(&mQ, Q, dtype, batch, q_seq, q_heads, head_dim, q_strides, kCross ? (int)group : 1,
                           tile_tokens) ||
         !make_strided_map(&mK, K, dtype, batch, kv_seq, kv_heads, head_dim, k_strides) ||
@@ -148,11 +233,8 @@ static int attention_strided(const void *Q, const void *K, const void *V, void *
     p.by_group = FA::Divisor::of(p.group);
     p.window = (int)std::min<int64_t>(window, (int64_t)1 << 30);
     p.sinks = (int)std::min<int64_t>(sinks, (int64_t)1 << 30);
-    p.scale = (float)(1.4426950408889634 / std::sqrt((double)head_dim));
-    // Weights stay below 2^8 times a row's largest: 9 + log2(keys that a row can see) keeps their sum
-    // below 1/2.  fp16 values are far from fp32's range, and its weights have none to spare.
-    const int64_t seen = window > 0 ? std::min(kv_seq, std::min(window, kv_seq) + std::min(sinks, kv_seq)) : kv_seq;
-    p.shift = dtype == GEMMRELU_BF16 ? 9.0f + std::ceil(std::log2((float)seen)) : 0.0f;
+    p.scale = (float)scale;
+    p.shift = shift;
     p.drop_arrive = g_drop_arrive.load();
     p.wait_limit_ns = wait_limit_ns();
     return launch_window_as<kCross>(dtype, head_dim, mQ, mK, mV, p, ds->sms, s,
@@ -166,16 +248,27 @@ extern "C" int flash_attention_window_x16(const void *Q, const void *K, const vo
                                           const int64_t *v_strides, int64_t window, int64_t sinks,
                                           void *stream) {
     return attention_strided<false>(Q, K, V, O, dtype, batch, q_seq, kv_seq, q_heads, kv_heads, head_dim, q_strides,
-                                    k_strides, v_strides, window, sinks, nullptr, stream);
+                                    k_strides, v_strides, window, sinks, nullptr, nullptr, 0, stream);
 }
 
 extern "C" int flash_attention_cross_x16(const void *Q, const void *K, const void *V, void *O, int dtype,
                                          int64_t batch, int64_t q_seq, int64_t kv_seq, int64_t q_heads,
                                          int64_t kv_heads, int64_t head_dim, const int64_t *q_strides,
                                          const int64_t *k_strides, const int64_t *v_strides,
-                                         const int32_t *lengths, void *stream) {
+                                         const int32_t *lengths, void *workspace, size_t workspace_bytes,
+                                         void *stream) {
     return attention_strided<true>(Q, K, V, O, dtype, batch, q_seq, kv_seq, q_heads, kv_heads, head_dim, q_strides,
-                                   k_strides, v_strides, 0, 0, lengths, stream);
+                                   k_strides, v_strides, 0, 0, lengths, workspace, workspace_bytes, stream);
+}
+
+extern "C" size_t flash_attention_cross_x16_workspace_bytes(int64_t batch, int64_t q_seq, int64_t kv_seq,
+                                                            int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
+    DeviceState *ds = nullptr;
+    if (batch < 1 || batch > 65535 || q_seq < 1 || kv_seq < 1 || kv_seq > ((int64_t)1 << 30) || q_heads < 1 ||
+        q_heads > 65535 || kv_heads < 1 || q_heads % kv_heads != 0 || (head_dim != 64 && head_dim != 128) ||
+        current_device_state(&ds) != GEMMRELU_OK)
+        return 0;
+    return step_split(batch, q_seq, kv_seq, q_heads, kv_heads, head_dim, ds->sms).bytes;
 }
 
 extern "C" int flash_attention_window_debug_blocks(int64_t first, int64_t last, int64_t window,

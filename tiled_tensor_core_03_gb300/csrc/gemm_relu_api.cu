@@ -108,6 +108,7 @@ struct DeviceState {
     bool attr_attn[2] = {false, false};
     bool attr_window[4] = {};
     bool attr_cross[4] = {};
+    bool attr_step[8] = {};
     bool attr_ragged[4] = {};
     bool attr_kv[16] = {};   // kv_cache_attention: head_dim x row groups x type x weights or not
 };

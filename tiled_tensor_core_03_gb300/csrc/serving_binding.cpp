@@ -38,6 +38,7 @@ decltype(&flash_attention_cross_x16) f_cross;
 decltype(&kv_cache_attention_ragged_x16) f_ragged;
 decltype(&kv_cache_attention_ragged_x16_workspace_bytes) f_ragged_bytes;
 decltype(&rotary_x16) f_rotary;
+decltype(&flash_attention_cross_x16_workspace_bytes) f_cross_bytes;
 PyObject *g_error, *g_no_memory;   // GemmReluError, torch.OutOfMemoryError
 
 struct Refusal {
@@ -246,7 +247,9 @@ at::Tensor new_workspace(const at::Tensor &q, size_t bytes, size_t counters) {
 constexpr size_t kKeep = (size_t)64 << 20;
 constexpr size_t kMostKept = 64;
 
-template <size_t kCounters>
+enum { kForCache, kForRagged, kForCross };   // whose workspace
+
+template <int kOperator, size_t kCounters>
 at::Tensor workspace_for(const at::Tensor &q, size_t bytes, int d, void *stream) {
     uint64_t id;
     if (bytes > kKeep || f_capturing(stream) || f_stream_id(stream, &id) != GEMMRELU_OK)
@@ -294,7 +297,7 @@ PyObject *attention_impl(PyObject *const *a) {
         void *stream = stream_of(d);
         at::Tensor space;
         if (a[8] == Py_None) {
-            space = workspace_for<GEMMRELU_KV_COUNTER_BYTES>(q, workspace_bytes(q, pool.kv_heads, width), d, stream);
+            space = workspace_for<kForCache, GEMMRELU_KV_COUNTER_BYTES>(q, workspace_bytes(q, pool.kv_heads, width), d, stream);
         } else {
             space = tensor(a[8], "workspace");
             if (!on(space, d) || !space.is_contiguous())
@@ -344,7 +347,7 @@ PyObject *ragged_impl(PyObject *const *a) {
         void *stream = stream_of(d);
         at::Tensor space;
         if (a[8] == Py_None) {
-            space = workspace_for<GEMMRELU_RAGGED_COUNTER_BYTES>(q, f_ragged_bytes(pool.head_dim), d, stream);
+            space = workspace_for<kForRagged, GEMMRELU_RAGGED_COUNTER_BYTES>(q, f_ragged_bytes(pool.head_dim), d, stream);
         } else {
             space = tensor(a[8], "workspace");
             if (!on(space, d) || !space.is_contiguous())
@@ -382,11 +385,31 @@ PyObject *cross_impl(PyObject *const *a) {
     const at::Tensor o = output(q, a[4], d);
     if (q.numel() > 0) {
         const Strides qs = strides_of(q, "q"), ks = strides_of(k, "k"), vs = strides_of(v, "v");
+        void *stream = stream_of(d);
+        at::Tensor space;
+        if (a[5] != Py_None) {
+            space = tensor(a[5], "workspace");
+            if (!on(space, d) || !space.is_contiguous())
+                refuse(PyExc_ValueError, "workspace must be a contiguous tensor on cuda:", d);
+        } else if (const size_t bytes = f_cross_bytes(q.size(0), q.size(1), k.size(1), q.size(2), k.size(2), dim)) {
+            space = workspace_for<kForCross, GEMMRELU_CROSS_COUNTER_BYTES>(q, bytes, d, stream);
+        }
         done(f_cross(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), type, q.size(0), q.size(1), k.size(1),
-                     q.size(2), k.size(2), dim, qs.s, ks.s, vs.s, lengths, stream_of(d)),
+                     q.size(2), k.size(2), dim, qs.s, ks.s, vs.s, lengths, space.defined() ? space.data_ptr() : nullptr,
+                     space.defined() ? space.nbytes() : 0, stream),
              "flash_attention_cross_x16");
     }
     return returned(o, a[4]);
+}
+
+PyObject *cross_workspace_impl(PyObject *const *a) {
+    const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k");
+    current_device_of(q);
+    if (q.dim() != 4 || k.dim() != 4)
+        refuse(PyExc_ValueError, "q must be [batch, q_seq, q_heads, d], k [batch, kv_seq, kv_heads, d]");
+    const size_t bytes = f_cross_bytes(q.size(0), q.size(1), k.size(1), q.size(2), k.size(2), q.size(3));
+    return THPVariable_Wrap(new_workspace(q, std::max<size_t>(bytes, GEMMRELU_CROSS_COUNTER_BYTES),
+                                          GEMMRELU_CROSS_COUNTER_BYTES));
 }
 
 // [batch, tokens, heads, head_dim] of a tensor that may lack its first axis.
@@ -546,12 +569,12 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     return nullptr;
 }
 
-// bind(GemmReluError, torch.OutOfMemoryError, addresses of the eleven library functions in the order below)
+// bind(GemmReluError, torch.OutOfMemoryError, addresses of the twelve library functions in the order below)
 PyObject *bind(PyObject *, PyObject *args) {
     PyObject *error, *no_memory;
-    unsigned long long f[11];
-    if (!PyArg_ParseTuple(args, "OOKKKKKKKKKKK", &error, &no_memory, &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6],
-                          &f[7], &f[8], &f[9], &f[10]))
+    unsigned long long f[12];
+    if (!PyArg_ParseTuple(args, "OOKKKKKKKKKKKK", &error, &no_memory, &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6],
+                          &f[7], &f[8], &f[9], &f[10], &f[11]))
         return nullptr;
     f_window = reinterpret_cast<decltype(f_window)>((uintptr_t)f[0]);
     f_append = reinterpret_cast<decltype(f_append)>((uintptr_t)f[1]);
@@ -564,6 +587,7 @@ PyObject *bind(PyObject *, PyObject *args) {
     f_ragged = reinterpret_cast<decltype(f_ragged)>((uintptr_t)f[8]);
     f_ragged_bytes = reinterpret_cast<decltype(f_ragged_bytes)>((uintptr_t)f[9]);
     f_rotary = reinterpret_cast<decltype(f_rotary)>((uintptr_t)f[10]);
+    f_cross_bytes = reinterpret_cast<decltype(f_cross_bytes)>((uintptr_t)f[11]);
     Py_INCREF(error);
     Py_INCREF(no_memory);
     g_error = error;
@@ -580,7 +604,8 @@ PyMethodDef methods[] = {
     ENTRY("attention", attention_impl, 9),
     ENTRY("workspace", workspace_impl, 3),
     ENTRY("evict", evict_impl, 9),
-    ENTRY("cross", cross_impl, 5),
+    ENTRY("cross", cross_impl, 6),
+    ENTRY("cross_workspace", cross_workspace_impl, 2),
     ENTRY("ragged", ragged_impl, 9),
     ENTRY("ragged_workspace", ragged_workspace_impl, 1),
     ENTRY("rotary", rotary_impl, 8),

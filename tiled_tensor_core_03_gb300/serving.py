@@ -31,7 +31,7 @@ _serving.bind(GemmReluError, torch.OutOfMemoryError, *(
                  "kv_cache_attention_x16_workspace_bytes", "kv_cache_evict_e4m3",
                  "gemm_relu_stream_capturing", "gemm_relu_stream_id", "flash_attention_cross_x16",
                  "kv_cache_attention_ragged_x16", "kv_cache_attention_ragged_x16_workspace_bytes",
-                 "rotary_x16")))
+                 "rotary_x16", "flash_attention_cross_x16_workspace_bytes")))
 
 
 class KVCache(NamedTuple):
@@ -67,17 +67,26 @@ def flash_attention_window(q, k, v, window, sinks=0, out=None, stream=None):
     return _serving.window(q, k, v, window, sinks, out)
 
 
-def flash_attention_cross(q, k, v, lengths=None, out=None, stream=None):
+def flash_attention_cross_workspace(q, k):
+    """A device workspace for flash_attention_cross calls of these sizes (uint8 tensor, its counters
+    zeroed on the current stream); for calls that follow one another."""
+    return _serving.cross_workspace(q, k)
+
+
+def flash_attention_cross(q, k, v, lengths=None, out=None, workspace=None, stream=None):
     """softmax(q k^T / sqrt(d)) v over an encoder's states: q [batch, q_seq, q_heads, d], k and v
     [batch, kv_seq, kv_heads, d], fp16 or bf16, d = 64 or 128; query head h reads K/V head
     h // (q_heads // kv_heads).  Strides as for flash_attention_window.
 
     Every query of sequence b sees the states j < lengths[b] (int32 [batch]; default: all kv_seq).
-    Where there are none it gets 0.  What stands behind them, NaN among it, is not seen."""
+    Where there are none it gets 0.  What stands behind them, NaN among it, is not seen.
+
+    A call of few query rows and heads needs a workspace: without one it uses one that is kept per
+    stream, or its own where it is being captured."""
     if stream is not None:
         with torch.cuda.stream(stream):   # what is allocated belongs to it
-            return _serving.cross(q, k, v, lengths, out)
-    return _serving.cross(q, k, v, lengths, out)
+            return _serving.cross(q, k, v, lengths, out, workspace)
+    return _serving.cross(q, k, v, lengths, out, workspace)
 
 
 def rotary_frequencies(rot, base=10000.0, factor=1.0, context=None, low=1.0, high=32.0, device="cuda"):
