@@ -144,3 +144,17 @@ def test_cross_without_rows_or_states():
     assert gr.flash_attention_cross(z(2, 0, 4, 64, **kw), z(2, 9, 4, 64, **kw), z(2, 9, 4, 64, **kw)).shape == (2, 0, 4, 64)
     out = gr.flash_attention_cross(z(2, 3, 4, 64, **kw) + 1, z(2, 0, 4, 64, **kw), z(2, 0, 4, 64, **kw))
     assert (out == 0).all()
+
+
+@pytest.mark.parametrize("hq,d", [(3, 128), (7, 64), (100, 64)])
+def test_cross_same_bits_whatever_ran_before(hq, d):
+    """Groups that do not divide a tile's 128 rows, after calls that leave other values in shared memory."""
+    import torch
+    rng = np.random.default_rng(8)
+    q, _ = _rand(rng, (1, 129, hq, d), "fp16", 2.0)
+    k, _ = _rand(rng, (1, 513, 1, d), "fp16")
+    want = gr.flash_attention_cross(q, k, k)
+    for scale in (0.0, 1000.0, 30000.0):
+        x = torch.full((4, 300, 8, d), scale, device="cuda", dtype=torch.float16)
+        gr.flash_attention_cross(x, x, x)
+        assert torch.equal(gr.flash_attention_cross(q, k, k).view(torch.int16), want.view(torch.int16))

@@ -159,9 +159,10 @@ __device__ __forceinline__ bool ragged_sees(const RaggedParams &p, const RaggedI
 // at most, and a CTA has one.  A unit is a block, or such a part.
 __device__ __forceinline__ int ragged_units(int blocks, int part) { return part ? (blocks + part - 1) / part : blocks; }
 
-// `part` for so many blocks and items (0 with no fewer items than CTAs): blocks / part + items parts at most, which fit.
+// `part` for so many blocks and items: blocks / part + items parts at most, which fit.  0, ranges, with no fewer items
+// than CTAs, and with so few blocks that a CTA has one or two of them in any case.
 __device__ __forceinline__ int ragged_part(int blocks, int items, int grid) {
-    return items < grid ? (blocks + grid - items - 1) / (grid - items) : 0;
+    return items < grid && blocks >= 4 * grid ? (blocks + grid - items - 1) / (grid - items) : 0;
 }
 
 // Whether to cut that way, given the blocks of the longest part: where it takes no more than an equal range and its two
@@ -202,19 +203,24 @@ struct RaggedWalk {
     }
 };
 
+// How many CTAs get a range: an item of n blocks is cut into about sqrt(2.5 n) parts at most.  (4 sequences of up to 700
+// tokens with up to 5 new ones, 32 heads on 8, 5 blocks an item: 17.8 us so, 20.3 with a CTA a block, 25.7 with sqrt(n)
+// parts.)
+__device__ __forceinline__ int ragged_ranges(int total, int items, int grid) {
+    const float most = sqrtf(2.5f * (float)total * (float)items);
+    return max(1, min(min(total, grid), most < (float)grid ? (int)most : grid));
+}
+
 // What the start works out, in shared memory: where the CTA's range begins, its blocks, and how units are dealt.
 struct RaggedPlan {
     int b, head, item, j, unit0, blocks, part, total, ranges;
     RaggedSeq seq;
 };
 
-// The sum over a warp of values below 2^48.
-__device__ __forceinline__ int64_t warp_sum(int64_t x) {
-    int64_t sum = 0;
-#pragma unroll
-    for (int i = 0; i < 48; i += 16)
-        sum += (int64_t)__reduce_add_sync(0xffffffffu, (unsigned)(x >> i) & 0xffffu) << i;
-    return sum;
+// The sum over a warp of values in [0, 2^31).
+__device__ __forceinline__ int64_t warp_sum(int x) {
+    return ((int64_t)__reduce_add_sync(0xffffffffu, (unsigned)x >> 16) << 16) +
+           __reduce_add_sync(0xffffffffu, (unsigned)x & 0xffffu);
 }
 
 // This CTA's range of units: sums over all sequences, a lane each (those of long chunks by a warp), by one warp or, with more
@@ -224,7 +230,7 @@ __device__ __noinline__ void ragged_plan(const RaggedParams &p, RaggedPlan *plan
     const bool alone = p.batch <= 32;
     if (alone && warp > 0)
         return;
-    int part = 0, total = 0, blocks = 0;
+    int part = 0, total = 0, blocks = 0, all_items = 0;
     for (int pass = 0;; ++pass) {   // in blocks, in parts, and in blocks again where parts do not pay
         int64_t mine = 0, items = 0;
         int longest = 0;
@@ -233,7 +239,7 @@ __device__ __noinline__ void ragged_plan(const RaggedParams &p, RaggedPlan *plan
             RaggedSeq s{0, 0, 0, 0};
             if (b < p.batch)
                 s = ragged_seq(p, b, pass == 0 && blockIdx.x == 0);
-            int64_t u = 0;
+            int u = 0;   // (the host keeps a sequence's units below 2^31)
             auto add = [&](const RaggedSeq &x, int i) {
                 const int n = ragged_item(p, x, i).count(), parts = ragged_units(n, part);
                 if (part)
@@ -249,19 +255,17 @@ __device__ __noinline__ void ragged_plan(const RaggedParams &p, RaggedPlan *plan
                 x.count = __shfl_sync(0xffffffffu, s.count, from);
                 x.n = __shfl_sync(0xffffffffu, s.n, from);
                 x.items = __shfl_sync(0xffffffffu, s.items, from);
-                int64_t sum = 0;
+                int sum = 0;
                 for (int i = lane; i < x.items; i += 32)
                     sum += add(x, i);
-                sum = warp_sum(sum);
+                sum = (int)warp_sum(sum);
                 u = lane == from ? sum : u;
             }
             if (b < p.batch)
-                units[b] = (int)u;
-            mine += u;
-            items += s.items;
+                units[b] = u;
+            mine += warp_sum(u);
+            items += warp_sum(s.items);
         }
-        mine = warp_sum(mine);
-        items = warp_sum(items);
         longest = __reduce_max_sync(0xffffffffu, longest);
         if (!alone) {
             if (lane == 0) {
@@ -286,7 +290,8 @@ __device__ __noinline__ void ragged_plan(const RaggedParams &p, RaggedPlan *plan
         total = (int)mine;
         if (pass == 0) {
             blocks = total;
-            part = ragged_part(total, (int)(items < grid ? items : grid), grid);
+            all_items = (int)(items < grid ? items : grid);   // (more make no difference)
+            part = ragged_part(total, all_items, grid);
         } else if (pass == 1 && !ragged_cut_pays(longest, blocks, grid)) {
             part = 0;
             continue;
@@ -297,7 +302,7 @@ __device__ __noinline__ void ragged_plan(const RaggedParams &p, RaggedPlan *plan
     if (warp > 0)
         return;
     __syncwarp();
-    const int ranges = max(1, min(total, grid)), c = blockIdx.x;
+    const int ranges = part ? max(total, 1) : ragged_ranges(total, all_items, grid), c = blockIdx.x;
     const int start = c < ranges ? range_start(c, total, ranges) : total;
     const int stop = c < ranges ? range_start(c + 1, total, ranges) : total;
     if (start >= stop) {
@@ -667,8 +672,18 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
         tmem_alloc(smem_addr(tmem_slot), 512);
         tmem_relinquish();
     }
+    // Warm L2 with what the start depends on, one load after the other (L2 is where all writes meet, so fetching early
+    // returns nothing stale)
+    {
+        const int64_t i = ((int64_t)blockIdx.x * kRaggedThreads + threadIdx.x) * 32;
+        if (i < p.batch * p.max_pages)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.pages + i));
+        if (i < p.batch) {
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.lengths + i));
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.starts + i));
+        }
+    }
     pdl_wait_primary();
-
     ragged_plan(p, plan, reinterpret_cast<int *>(gbase + G::kOffK), sums);
     tc_fence_before_sync();
     __syncthreads();
