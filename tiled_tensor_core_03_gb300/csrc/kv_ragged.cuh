@@ -18,10 +18,10 @@ using attn::BN;
 using attn::kSub;
 
 // Four warpgroups: two of softmax, one with the feed's and the issuer's warp, one that converts.  512 threads launch
-// with 128 registers: 2 * 152 + 2 * 104 = 4 * 128.
+// with 128 registers: 2 * 168 + 2 * 88 = 4 * 128.
 constexpr int kRaggedThreads = 512;
 constexpr int kConvWarp = 12, kConvWarps = 4;
-constexpr int kRaggedSoftmaxRegs = 152, kRaggedFeedRegs = 104, kRaggedConvRegs = 104;
+constexpr int kRaggedSoftmaxRegs = 168, kRaggedFeedRegs = 88, kRaggedConvRegs = 88;
 static_assert(2 * kRaggedSoftmaxRegs + kRaggedFeedRegs + kRaggedConvRegs <= 4 * 128, "registers given back cover those taken");
 constexpr int kGroups = BN / 16;                // pieces of 16 tokens of a block: the smallest page
 constexpr int kRaggedMaxCtas = GEMMRELU_RAGGED_COUNTER_BYTES / (8 * (int)sizeof(unsigned));
@@ -574,7 +574,7 @@ __device__ __forceinline__ bool convert_rows(uint32_t src, uint32_t dst, int row
     uint32_t bad = 0;
     src += row1 * HD + c4 * 16;
     dst += row1 * 128 + ((uint32_t)((2 * c4) ^ (row1 & 7)) << 4);   // (row & 7 does not change below)
-#pragma unroll 2
+#pragma unroll 1
     for (int i = 0; i < BN / kConvWarps / 8; ++i) {
         const int row = row1 + 8 * i;
         const uint32_t m = mul[row >> 4];
@@ -1067,9 +1067,11 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
                     const RaggedMeta &meta = metas[i % G::kMetas];
                     const int key0 = cur.it.key0(j);
                     const uint32_t missing = meta.missing, flags = meta.flags;
-                    // The scores are read twice, 32 at a time, the next ones while these are worked on: for the largest, where
-                    // those that the row does not see become -infinity, and for the weights.  (All 128 in registers with
-                    // both passes unrolled made the loop 10 KB of code, and fetching it the bound: 890 to 960 us.)
+                    // The scores are read twice: all at once for the largest, then 32 at a time, the next ones while these are
+                    // worked on, for the weights.  (Kept in registers, with the weights' pass unrolled over all 128, the loop
+                    // was 10 KB of code, and fetching it the bound: 2048 tokens in
+                    // 32768 957 us, so 854; the largest 32 at a time, too, 922.)
+                    // First, what the row does not see becomes -infinity.
                     const bool masked = missing || ragged_masked(p, first, last, key0);
                     const int hi = pos - key0, lo = p.window > 0 ? hi - p.window : -1, head = p.sinks - key0;
                     auto mask = [&](uint32_t (&x)[32], int c0) {   // a bit per key
@@ -1081,30 +1083,34 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
                             x[e] = seen & (1u << e) ? x[e] : __float_as_uint(-INFINITY);
                         tmem_st_x32(s_addr + c0, x);
                     };
-                    uint32_t xa[32], xb[32];
-                    float ma = -INFINITY, mb = -INFINITY;
-                    auto largest = [&](const uint32_t (&x)[32]) {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            ma = fmaxf(ma, __uint_as_float(x[e]));
-                            mb = fmaxf(mb, __uint_as_float(x[e + 1]));
-                        }
-                    };
-                    tmem_ld_x32(s_addr, xa);
+                    if (masked) {
 #pragma unroll 1
-                    for (int c0 = 0; c0 < BN; c0 += 64) {
-                        tmem_ld_wait_regs(xa);
-                        tmem_ld_x32(s_addr + c0 + 32, xb);
-                        if (masked)
-                            mask(xa, c0);
-                        largest(xa);
-                        tmem_ld_wait_regs(xb);
-                        if (masked) {
-                            mask(xb, c0 + 32);
-                            tmem_st_wait();
+                        for (int c0 = 0; c0 < BN; c0 += 32) {
+                            uint32_t x[32];
+                            tmem_ld_x32_sync(s_addr + c0, x);
+                            mask(x, c0);
                         }
-                        tmem_ld_x32(s_addr + ((c0 + 64) & (BN - 1)), xa);   // at last the first ones again
-                        largest(xb);
+                        tmem_st_wait();
+                    }
+                    uint32_t xa[32], xb[32];
+                    float ma = -INFINITY, mb = -INFINITY, mc = -INFINITY, md = -INFINITY;
+                    {
+                        uint32_t v[BN];
+#pragma unroll
+                        for (int c0 = 0; c0 < BN; c0 += 32)
+                            tmem_ld_x32(s_addr + c0, *reinterpret_cast<uint32_t(*)[32]>(&v[c0]));
+#pragma unroll
+                        for (int c0 = 0; c0 < BN; c0 += 32)
+                            tmem_ld_wait_regs(*reinterpret_cast<uint32_t(*)[32]>(&v[c0]));
+#pragma unroll
+                        for (int e = 0; e < BN; e += 4) {
+                            ma = fmaxf(ma, __uint_as_float(v[e]));
+                            mb = fmaxf(mb, __uint_as_float(v[e + 1]));
+                            mc = fmaxf(mc, __uint_as_float(v[e + 2]));
+                            md = fmaxf(md, __uint_as_float(v[e + 3]));
+                        }
+                        ma = fmaxf(ma, mc);
+                        mb = fmaxf(mb, md);
                     }
                     const float c_blk = factor(meta.ks);
                     float mx = __fmul_rn(fmaxf(ma, mb), c_blk);
@@ -1146,6 +1152,7 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
                     }
                     float sum;
                     if (near && !big) {
+                        tmem_ld_x32(s_addr, xa);
                         const float a = (lv + kPLog2 - rr_ref) - m_ref;
                         const float2 c2 = make_float2(c_blk, c_blk), a2 = make_float2(a, a);
                         float2 sa = make_float2(0.0f, 0.0f), sb = make_float2(0.0f, 0.0f);
@@ -1178,7 +1185,6 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
                         }
                         sum = ((sa.x + sa.y) + (sb.x + sb.y)) * back_of(rr_ref, lv);
                     } else {
-                        tmem_ld_wait_regs(xa);   // (their registers are free now)
                         sum = ragged_weights(s_addr, meta, c_row, m_ref, rr_ref);
                     }
                     l += sum;
