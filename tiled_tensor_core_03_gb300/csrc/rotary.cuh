@@ -123,11 +123,11 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams 
 #pragma unroll
         for (int i = 0; i < kPairs / 2; ++i)
             c[i] = turns ? *reinterpret_cast<const float4 *>(cs + 8 * item + 2 * i) : make_float4(1, 0, 1, 0);
-#pragma unroll 4
+#pragma unroll 1
         for (int h = lane; h < p.heads; h += p.lanes) {
             const uint16_t *s = src(h);
             uint16_t *d = dst(h);
-            uint4 x = *reinterpret_cast<const uint4 *>(s + x_at), z = *reinterpret_cast<const uint4 *>(s + z_at);
+            uint4 x = __ldcs(reinterpret_cast<const uint4 *>(s + x_at)), z = __ldcs(reinterpret_cast<const uint4 *>(s + z_at));
             if (turns) {
                 if constexpr (kInterleaved) {
                     turn_one<kBf16>(x.x, make_float2(c[0].x, c[0].y));
