@@ -418,8 +418,11 @@ __device__ __noinline__ void ragged_add_nan(const RaggedParams &p, int b, int he
 
 // ---------------------------------------------------------------- weights, the rare cases
 
-// What scores of keys with scale ks are multiplied by; not 0, which would make a NaN of a score of -infinity.
-__device__ __forceinline__ float score_factor(float c_row, float ks) { return fmaxf(c_row * ks, 1.17549435e-38f); }
+// What scores of keys with scale ks are multiplied by: neither 0, which would make a NaN of a score of -infinity, nor an
+// infinity, which would make one of a score of 0.
+__device__ __forceinline__ float score_factor(float c_row, float ks) {
+    return fminf(fmaxf(c_row * ks, 1.17549435e-38f), 3.40282347e+38f);
+}
 
 // What brings a sum of P (weights times V's scale, relative to O's reference) back to weights relative to m; bounded, so
 // that no sum of 0 meets an infinity.
@@ -1037,7 +1040,9 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
             int num_cuts = 0;
             RaggedWalk w = first_segment();
             float row_scale = t == 0 || w.rows(p) > BM ? load_q(w) : 1.0f;
-            for (bool more = true; alive && more; ++segments) {
+            // (after a wait that expired the rest is walked through without it, so that every part is counted and the counters
+            // go back to 0; the status says that the output is not to be used)
+            for (bool more = true; more; ++segments) {
                 const RaggedWalk cur = w;
                 const int rows = cur.rows(p);
                 const bool here = t == 0 || rows > BM;
@@ -1053,7 +1058,7 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
                 float rr = -INFINITY;            // O's reference above m
                 float m_ref = 0.0f, rr_ref = 0.0f;   // both, 0 as long as there are none
                 bool big = false;
-                for (int j = cur.j; here && j < cur.j1; ++j) {
+                for (int j = cur.j; alive && here && j < cur.j1; ++j) {
                     const uint32_t i = blocks + (j - cur.j);
                     const bool ok = wait_bounded_eager(s_full((uint32_t)t), turns & 1u, p.wait_limit_ns, abort_flag,
                                                        kSiteEpiAccFull) &&
@@ -1195,26 +1200,22 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
                         mbar_arrive(p_full((uint32_t)t));
                     ++turns;
                 }
-                if (!alive)
-                    break;
                 blocks += cur.j1 - cur.j;
                 // the next item's rows (the last scores of this one are done with Q)
                 more = w.next(p);
-                if (more && (t == 0 || w.rows(p) > BM))
+                if (alive && more && (t == 0 || w.rows(p) > BM))
                     row_scale = load_q(w);
                 if (!here)
                     continue;
-                if (!__all_sync(0xffffffffu, wait_bounded_eager(o_full((uint32_t)t), outputs & 1u, p.wait_limit_ns,
-                                                                abort_flag, kSiteEpiAccFull))) {
-                    alive = false;
-                    break;
-                }
+                if (alive)
+                    alive = __all_sync(0xffffffffu, wait_bounded_eager(o_full((uint32_t)t), outputs & 1u, p.wait_limit_ns,
+                                                                       abort_flag, kSiteEpiAccFull));
                 ++outputs;
                 tc_fence_after_sync();
                 bool taken = false;
                 for (int x = 0; x < kConvWarps; ++x)
                     taken = taken || dirty[4 * x + (segments & 3u)];
-                if (taken)
+                if (alive && taken)
                     ragged_add_nan<HD>(p, cur.b, cur.head, cur.item, cur.j, cur.j1, pos, o_addr);
                 const bool valid = my_row < rows;
                 uint16_t *dst = p.out + ((int64_t)(cur.seq.start + token) * p.q_heads + cur.head * p.group +
@@ -1224,7 +1225,7 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
                     const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;   // 0: the row sees nothing
                     const float f = exp2f(0.5f * (rr - kPLog2));
 #pragma unroll 1
-                    for (int c0 = 0; c0 < HD; c0 += 32) {
+                    for (int c0 = 0; alive && c0 < HD; c0 += 32) {
                         uint32_t o[32];
                         tmem_ld_x32_sync(o_addr + c0, o);
                         if (valid)
@@ -1239,7 +1240,7 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
                     cut.mid = cur.unit0 != range_start(cut.first, plan->total, plan->ranges);
                     float4 *part = ragged_part_of<HD>(p, cut, warp, lane, blockIdx.x);
 #pragma unroll 1
-                    for (int c0 = 0; c0 < HD; c0 += 32) {
+                    for (int c0 = 0; alive && c0 < HD; c0 += 32) {
                         uint32_t o[32];
                         tmem_ld_x32_sync(o_addr + c0, o);
                         if (valid)
@@ -1249,13 +1250,13 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
                                        make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
                                                    __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3])));
                     }
-                    if (valid)
+                    if (alive && valid)
                         __stcg(part + HD / 4 * 32, make_float4(m, l, rr, 0.0f));
                 }
             }
             // The parts of cut items (the one that the range starts in and the one that it ends in) are counted now; the warp
             // that comes last joins those of its rows, in the order of the ranges.
-            for (int k = 0; alive && k < num_cuts; ++k) {
+            for (int k = 0; k < num_cuts; ++k) {
                 const RaggedCut cut = cuts[k];
                 __syncwarp();
                 unsigned before = 0;
