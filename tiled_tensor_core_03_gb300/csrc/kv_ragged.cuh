@@ -5,6 +5,36 @@
 // over the tokens t that row r sees, rows packed: sequence b has the query tokens starts[b] ..
 // starts[b + 1] - 1, the last of its lengths[b] tokens.  The rows of one K/V head are its group's query
 // heads of every new token, token by token; 128 of them are a tile, two neighbouring tiles an item.
+//
+// The work: items go over the 128-key blocks that some row of theirs sees, a CTA to an SM has a run of consecutive blocks of
+// the whole call (ragged_plan, from starts and lengths on the device: no host knows them), and items that several CTAs have
+// parts of are joined by the one that comes last, in the CTAs' order: no CTA waits for another, and the same call
+// gives the same bits.
+//
+// A block: the feed's warp looks the pages up and copies K's and V's bytes (a bulk copy per page and head), a warpgroup turns
+// them to fp16 in the products' layout, one warp issues S = Q K^T and O += P V (tcgen05, Q from shared memory, P from TMEM),
+// and a warpgroup per tile makes P of S, a row a thread.  e4m3 is exact in fp16, and so is a power of two beside it: K's
+// scales within a block go into the keys and V's into the values as long as they lie near each other (RaggedMeta), so
+// that a row has one factor a block.
+//
+// Two references a row: m, the largest score, for the sum of weights, and rr, the largest score plus log2 of V's scale above
+// it, for P and O: P = 2^(score + log2 vs - m - rr + 7) is at most 2^7 whatever the scales are, so that fp16 holds it to half a
+// step down to 2^-21 of the largest and the fp32 sums of a block do not overflow.  Sums, references and O are fp32; P in fp16 is
+// the only rounding besides the result's.
+//
+// V's bytes may be NaN where no row looks (0 * NaN is NaN): the conversion takes NaN out of blocks that are masked in part, and
+// ragged_add_nan gives them back to the rows that see them.
+//
+// Bound, 2048 new tokens that end 32768, 32 heads on 8 of 128 (1.07 TFLOP, 555 us of products at the measured rate): 862 us,
+// 1.24 PFLOP/s.  A block of two tiles takes about 4000 cycles for 2048 of products: S, softmax and P V of a tile
+// follow each other, the other tile's fill the gaps, and a tile's softmax (2250 cycles: 128 reads from TMEM, 128 exponentials
+// at 16 a cycle of an SM for both tiles, packing) is longer than the other's products; S reads both
+// operands from shared memory, all 128 bytes a cycle, which the conversion's reads and writes interrupt.  Measured beside it, same
+// case: no exponentials and no conversion 680 us.  Not kept: two threads a row 1004; S in steps of 64 keys, twice buffered
+// 1095 (Q is read twice); P handed over in halves 1258 (the issuer goes in order); the rare paths unrolled or inlined 1016
+// (instruction fetch: the loops of the four roles have to stay in the cache together); two converting warps 1018.
+// 16 sequences of up to 8000 tokens, 1000 of them new: 808 us; 6 of 12000, 2000 new, 16 heads of 64 with a window of 1024: 117; 4 of
+// 700 with up to 5 new: 17, most of it loads that wait for one another: counts, pages, keys, the other CTAs' parts.
 #pragma once
 
 #include "flash_attention_window.cuh"
@@ -504,7 +534,7 @@ __device__ __forceinline__ float4 *ragged_part_of(const RaggedParams &p, const R
 
 // The parts of a lane's row joined, in the order of the CTAs.
 template <int HD, bool kBf16>
-__device__ __noinline__ void ragged_join(const RaggedParams &p, const RaggedCut cut, int warp, int lane) {
+__device__ __forceinline__ void ragged_join(const RaggedParams &p, const RaggedCut cut, int warp, int lane) {
     // the largest references, and the sum of weights
     float mm = -INFINITY, yy = -INFINITY, ll = 0.0f;
 #pragma unroll 4
@@ -559,6 +589,49 @@ __device__ __noinline__ void ragged_join(const RaggedParams &p, const RaggedCut 
         for (int e = 0; e < 64; e += 32)
             write_row32<kBf16>(cut.dst + c0 + e, reinterpret_cast<const float(&)[32]>(s[e]), inv, f);
     }
+}
+
+// The same for a warp with no more than 8 rows: four lanes a row, HD / 4 columns each (every fourth of the float4), so that
+// the parts' loads are few and many parts' are under way at once.  `row_dst` is the row's.  (One token after 1000, 32 heads on
+// 8: 17.0 us so, 21.0 with a lane a row; after 30000: 45.7 and 55.2.)
+template <int HD, bool kBf16>
+__device__ __noinline__ void ragged_join_few(const RaggedParams &p, const RaggedCut cut, uint16_t *row_dst, int warp, int lane) {
+    const int row = lane & 7, nth = lane >> 3;
+    float mm = -INFINITY, yy = -INFINITY, ll = 0.0f;
+    float4 s[HD / 16];
+#pragma unroll
+    for (int e = 0; e < HD / 16; ++e)
+        s[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
+    for (int c = cut.first; c <= cut.last; ++c) {
+        const float4 *at = ragged_part_of<HD>(p, cut, warp, row, c);
+        const float4 x = __ldcg(at + HD / 4 * 32);   // m, l, rr
+        float4 o[HD / 16];
+#pragma unroll
+        for (int e = 0; e < HD / 16; ++e)
+            o[e] = __ldcg(at + (4 * e + nth) * 32);
+        const float top = fmaxf(mm, x.x), ref = top == -INFINITY ? 0.0f : top;
+        const float shrink = mm == top ? 1.0f : exp2f(mm - top);
+        ll = ll * shrink + (x.y != x.y ? x.y : x.x == -INFINITY ? 0.0f : x.y * exp2f(x.x - ref));
+        const float mine = x.x == -INFINITY ? -INFINITY : (x.x - ref) + x.z;
+        const float old = mm == -INFINITY ? -INFINITY : (mm - top) + yy;
+        const float now = fmaxf(old, mine), base = now == -INFINITY ? 0.0f : now;
+        const float a = x.x == -INFINITY ? 1.0f : exp2f(mine - base), d = old == -INFINITY ? 1.0f : exp2f(old - base);
+#pragma unroll
+        for (int e = 0; e < HD / 16; ++e)
+            s[e] = make_float4(fmaf(o[e].x, a, s[e].x * d), fmaf(o[e].y, a, s[e].y * d), fmaf(o[e].z, a, s[e].z * d),
+                               fmaf(o[e].w, a, s[e].w * d));
+        mm = top;
+        yy = now;
+    }
+    const float inv = ll > 0.0f || ll != ll ? 1.0f / ll : 0.0f;
+    const float f = yy == -INFINITY ? 0.0f : exp2f(0.5f * (yy - kPLog2));
+    if (row_dst != nullptr)
+#pragma unroll
+        for (int e = 0; e < HD / 16; ++e)
+            *reinterpret_cast<uint2 *>(row_dst + 4 * (4 * e + nth)) =
+                make_uint2(pack_out<kBf16>(s[e].x * inv * f * f, s[e].y * inv * f * f),
+                           pack_out<kBf16>(s[e].z * inv * f * f, s[e].w * inv * f * f));
 }
 
 // ---------------------------------------------------------------- e4m3 to fp16
@@ -1264,9 +1337,16 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
                     before = count_part(p.arrived + cut.first * 8 + warp, (unsigned)(cut.last - cut.first));
                 before = __shfl_sync(0xffffffffu, before, 0);
                 __syncwarp();
-                if (before != (unsigned)(cut.last - cut.first) || cut.dst == nullptr)
+                if (before != (unsigned)(cut.last - cut.first))
                     continue;
-                ragged_join<HD, kBf16>(p, cut, warp, lane);
+                const uint32_t rows = __ballot_sync(0xffffffffu, cut.dst != nullptr);
+                if (rows >> 8) {
+                    if (cut.dst != nullptr)
+                        ragged_join<HD, kBf16>(p, cut, warp, lane);
+                } else if (rows) {
+                    const uint64_t at = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(cut.dst), lane & 7);
+                    ragged_join_few<HD, kBf16>(p, cut, reinterpret_cast<uint16_t *>(at), warp, lane);
+                }
             }
         }
     }

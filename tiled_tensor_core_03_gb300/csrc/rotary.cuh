@@ -5,6 +5,12 @@
 // The angle is kept in turns, as a 64-bit fraction: a frequency f radians a token is the integer
 // f / (2 pi) * 2^64 mod 2^64, and its product with a position, wrapped at 64 bits, is the angle's
 // fraction of a turn for any position (an fp32 product of the two loses all of it from 2^24 on).
+//
+// Bound: every element is read and written once.  So a block takes a few rows and works their cosines and sines out into shared
+// memory once for all heads (sincospi of the fraction's top 32 bits as fp32: the angle is off by 2^-23 at most), and its
+// threads go over the heads 16 bytes at a time.  A thread has one head under way: four took registers and with them
+// occupancy (60 us against 57).  4 x 4096 tokens, 32 + 8 heads of 128, bf16: 57 us, 5.9 TB/s; 3 x 5001 tokens, half of 16 + 16
+// heads of 64 turned in pairs side by side: 22 us, 5.6 TB/s; 64 single tokens: 2.8 us on the GPU.
 #pragma once
 
 #include "kv_attention.cuh"
