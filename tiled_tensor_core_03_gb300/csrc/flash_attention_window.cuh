@@ -278,14 +278,18 @@ struct WindowItem {
 };
 
 // The items of this CTA, one a round.  Within a chunk of heads their cost falls, so that with
-// rounds dealt out forwards and backwards in turn every CTA gets about the same sum.
+// rounds dealt out forwards and backwards in turn every CTA gets about the same sum.  (kCross: their cost falls over all
+// of them, and the CTAs that a last, short round leaves out are those with the most before it.)
+template <bool kCross>
 struct WindowWalk {
     int base, total;
     bool back;
     __device__ __forceinline__ WindowWalk(const WindowParams &p)
         : base(0), total(p.pairs * p.kv_heads * p.batch), back(false) {}
-    __device__ __forceinline__ bool more() const { return base + (int)blockIdx.x < total; }
+    __device__ __forceinline__ bool more() const { return (kCross ? index() : base + (int)blockIdx.x) < total; }
     __device__ __forceinline__ int index() const {
+        if (kCross)
+            return base + (back ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
         return back ? min(base + (int)gridDim.x, total) - 1 - (int)blockIdx.x : base + (int)blockIdx.x;
     }
     __device__ __forceinline__ void next() {
@@ -371,8 +375,9 @@ __device__ __forceinline__ WindowItem window_item(const WindowParams &p, int ind
 
 // kCross: cross attention.  Queries see all keys of their sequence (states_of), and a tile's rows are
 // tile_tokens queries with all heads of one K/V head's group.  Up to kMostOrdered sequences go by their number of keys,
-// the longest first, so that a CTA whose first item is long gets a short one in the next round (8 sequences of up to 1500
-// keys, 448 queries, 16 heads of 64, two rounds of items: 35.1 us, 36.6 in the batch's order).
+// the longest first, so that a CTA whose first item is long gets a short one in the next round (448 queries, 16 heads of 64:
+// 8 sequences of up to 1500 keys 33.4 us, 36.6 in the batch's order; 6 of up to 3000 38.2, and 52.0 where the heads' last
+// queries all went first, and the CTAs with the least before it got nothing of the last round).
 constexpr int kMostOrdered = 128;
 
 template <int HD, bool kBf16, bool kCross = false>
@@ -491,7 +496,7 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
             uint32_t queries = 0, blocks = 0;   // Q loads and K/V blocks issued
             bool ok = !(p.drop_arrive && blockIdx.x == 0);
             for (int pass = 0;; ++pass) {
-                for (WindowWalk walk(p); lane == 0 && ok && walk.more(); walk.next()) {
+                for (WindowWalk<kCross> walk(p); lane == 0 && ok && walk.more(); walk.next()) {
                     const WindowItem w = window_item<HD, kCross>(p, walk.index(), order);
                     if (w.nb == 0)
                         continue;
@@ -609,7 +614,7 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
                 return true;
             };
             for (int pass = 0;; ++pass) {
-                WindowWalk walk(p);
+                WindowWalk<kCross> walk(p);
                 WindowItem w{};
                 if (walk.more())
                     w = window_item<HD, kCross>(p, walk.index(), order);
@@ -684,7 +689,7 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
         // (compiled once for each walk: the second one's code between the turns cost the first 2.7%)
         auto walk_items = [&](auto again) __attribute__((always_inline)) {
             constexpr bool kAgain = decltype(again)::value;
-            for (WindowWalk walk(p); alive && walk.more(); walk.next()) {
+            for (WindowWalk<kCross> walk(p); alive && walk.more(); walk.next()) {
                 const WindowItem w = window_item<HD, kCross>(p, walk.index(), order);
                 const uint32_t block0 = blocks;
                 blocks += w.nb;

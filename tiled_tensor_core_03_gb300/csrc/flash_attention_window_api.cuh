@@ -222,7 +222,9 @@ static int attention_strided(const void *Q, const void *K, const void *V, void *
     p.items = (int)items;
     p.pairs = (int)((items + 1) / 2);
     const int64_t heads = batch * kv_heads;
-    const int64_t fit = std::max<int64_t>(1, kWindowChunkBytes / (kv_seq * head_dim * 4));
+    // (cross attention: a head's items see the same keys, so one head after the other falls in cost over all of them, as
+    // the order by length has it)
+    const int64_t fit = kCross ? 1 : std::max<int64_t>(1, kWindowChunkBytes / (kv_seq * head_dim * 4));
     const int64_t chunks = (heads + fit - 1) / fit;
     p.chunk = (int)((heads + chunks - 1) / chunks);
     p.chunk_items = p.chunk * p.pairs;
