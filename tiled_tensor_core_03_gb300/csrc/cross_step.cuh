@@ -12,7 +12,7 @@
 // head's states are cut into equal parts as long as there are fewer heads than fill the GPU; the block that
 // comes last joins the parts, in order: no block waits for another, and the same call gives the same bits.
 //
-// Measured: 48 sequences of up to 1500 states, 16 heads of 64 (217 MB): 36 us, 6.0 TB/s; 2 of up to 700: 6.4 us, where a launch
+// Measured: 48 sequences of up to 1500 states, 16 heads of 64 (217 MB): 36 us, 6.0 TB/s; 2 of up to 700: 6.6 us, where a launch
 // that does nothing takes 2.  At more than 16 rows the tiles of the long form are faster: each 8 rows more
 // are another read of the fragments from shared memory.
 #pragma once
