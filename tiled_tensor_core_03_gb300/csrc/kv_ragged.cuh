@@ -25,7 +25,7 @@
 // V's bytes may be NaN where no row looks (0 * NaN is NaN): the conversion takes NaN out of blocks that are masked in part, and
 // ragged_add_nan gives them back to the rows that see them.
 //
-// Bound, 2048 new tokens that end 32768, 32 heads on 8 of 128 (1.07 TFLOP, 555 us of products at the measured rate): 862 us,
+// Bound, 2048 new tokens that end 32768, 32 heads on 8 of 128 (1.07 TFLOP, 555 us of products at the measured rate): 858 us,
 // 1.24 PFLOP/s.  A block of two tiles takes about 4000 cycles for 2048 of products: S, softmax and P V of a tile
 // follow each other, the other tile's fill the gaps, and a tile's softmax (2250 cycles: 128 reads from TMEM, 128 exponentials
 // at 16 a cycle of an SM for both tiles, packing) is longer than the other's products; S reads both
@@ -33,7 +33,7 @@
 // case: no exponentials and no conversion 680 us.  Not kept: two threads a row 1004; S in steps of 64 keys, twice buffered
 // 1095 (Q is read twice); P handed over in halves 1258 (the issuer goes in order); the rare paths unrolled or inlined 1016
 // (instruction fetch: the loops of the four roles have to stay in the cache together); two converting warps 1018.
-// 16 sequences of up to 8000 tokens, 1000 of them new: 808 us; 6 of 12000, 2000 new, 16 heads of 64 with a window of 1024: 117; 4 of
+// 16 sequences of up to 8000 tokens, 1000 of them new: 808 us; 6 of 12000, 2000 new, 16 heads of 64 with a window of 1024: 119; 4 of
 // 700 with up to 5 new: 17, most of it loads that wait for one another: counts, pages, keys, the other CTAs' parts.
 #pragma once
 
@@ -793,6 +793,19 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
             bool ok = !(p.drop_arrive && blockIdx.x == 0);
             RaggedWalk w = first_segment();
             do {
+                // The item's rows into L2, the softmax warps load them some blocks later (816 -> 808 us, and 120.3 -> 118.9 under the
+                // window; a segment's change costs 7000 to 9000 cycles, 3200 of them for its rows).
+                if (segment > 0) {
+                    const int rows = min(w.rows(p), 2 * BM);
+#pragma unroll 1
+                    for (int r = lane; r < rows; r += 32) {
+                        const int token = p.by_group.quotient(w.item * 2 * BM + r), g = w.item * 2 * BM + r - token * p.group;
+                        const uint16_t *at = p.q + (w.seq.start + token) * p.q_stride[0] + (w.head * p.group + g) * p.q_stride[1];
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+                        if (HD == 128)
+                            asm volatile("prefetch.global.L2 [%0];" ::"l"(at + 64));
+                    }
+                }
                 for (int j0 = w.j; ok && j0 < w.j1; j0 += per_batch) {
                     const int j = j0 + lane / pieces;
                     int64_t id = -1;
