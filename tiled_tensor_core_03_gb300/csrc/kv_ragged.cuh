@@ -25,15 +25,15 @@
 // V's bytes may be NaN where no row looks (0 * NaN is NaN): the conversion takes NaN out of blocks that are masked in part, and
 // ragged_add_nan gives them back to the rows that see them.
 //
-// Bound, 2048 new tokens that end 32768, 32 heads on 8 of 128 (1.07 TFLOP, 555 us of products at the measured rate): 858 us,
-// 1.24 PFLOP/s.  A block of two tiles takes about 4000 cycles for 2048 of products: S, softmax and P V of a tile
+// Bound, 2048 new tokens that end 32768, 32 heads on 8 of 128 (1.07 TFLOP, 555 us of products at the measured rate): 851 us,
+// 1.25 PFLOP/s.  A block of two tiles takes about 4000 cycles for 2048 of products: S, softmax and P V of a tile
 // follow each other, the other tile's fill the gaps, and a tile's softmax (2250 cycles: 128 reads from TMEM, 128 exponentials
 // at 16 a cycle of an SM for both tiles, packing) is longer than the other's products; S reads both
 // operands from shared memory, all 128 bytes a cycle, which the conversion's reads and writes interrupt.  Measured beside it, same
 // case: no exponentials and no conversion 680 us.  Not kept: two threads a row 1004; S in steps of 64 keys, twice buffered
 // 1095 (Q is read twice); P handed over in halves 1258 (the issuer goes in order); the rare paths unrolled or inlined 1016
 // (instruction fetch: the loops of the four roles have to stay in the cache together); two converting warps 1018.
-// 16 sequences of up to 8000 tokens, 1000 of them new: 808 us; 6 of 12000, 2000 new, 16 heads of 64 with a window of 1024: 119; 4 of
+// 16 sequences of up to 8000 tokens, 1000 of them new: 808 us; 6 of 12000, 2000 new, 16 heads of 64 with a window of 1024: 116; 4 of
 // 700 with up to 5 new: 17, most of it loads that wait for one another: counts, pages, keys, the other CTAs' parts.
 #pragma once
 
@@ -1071,48 +1071,55 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
             // The warp's 32 rows of Q into shared memory: HD / 8 lanes a row.  bf16 rows are scaled by a power of
             // two that brings their largest element to [2^14, 2^15), within fp16; returned: what undoes it.
             auto load_q = [&](const RaggedWalk &w) -> float {
-                constexpr int kLanes = HD / 8, kRows = 32 / kLanes, kLoads = 32 / kRows;
+                constexpr int kLanes = HD / 8, kRows = 32 / kLanes;
+                // Loads on their way at once: all; of bf16, whose conversion is long, a quarter, so that the loop is rolled (the
+                // feed has brought the rows into L2).  Measured: bf16 858 -> 851 us, under the window 118.7 -> 116.3; fp16 a quarter
+                // at a time 808 -> 825.
+                constexpr int kLoads = 32 / kRows / (kBf16 ? 4 : 1);
                 const int rows = w.rows(p), sub = lane % kLanes;
                 float mine = 1.0f;
-                uint4 x[kLoads];   // (all on their way at once: four at a time took 3 us longer)
+#pragma unroll 1
+                for (int i0 = 0; i0 < 32 / kRows; i0 += kLoads) {
+                    uint4 x[kLoads];
 #pragma unroll
-                for (int i = 0; i < kLoads; ++i) {
-                    const int row = t * BM + 32 * q + i * kRows + lane / kLanes;   // of the item
-                    x[i] = make_uint4(0, 0, 0, 0);
-                    if (row < rows) {
-                        const int token = p.by_group.quotient(w.item * 2 * BM + row);
-                        const int g = w.item * 2 * BM + row - token * p.group;
-                        x[i] = *reinterpret_cast<const uint4 *>(p.q + (w.seq.start + token) * p.q_stride[0] +
-                                                                (w.head * p.group + g) * p.q_stride[1] + sub * 8);
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < kLoads; ++i) {
-                    const int r = 32 * q + i * kRows + lane / kLanes;   // of the tile
-                    if constexpr (kBf16) {
-                        uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-                        uint32_t top = 0;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            top = max(top, max(v[e] & 0x7fffu, (v[e] >> 16) & 0x7fffu));
-#pragma unroll
-                        for (int o = 1; o < kLanes; o <<= 1)
-                            top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                        int e2 = (int)(top >> 7) - 127;
-                        e2 = e2 < -100 ? -100 : e2 > 127 ? 127 : e2;
-                        const float to = __uint_as_float((uint32_t)(14 - e2 + 127) << 23);
-                        const float back = __uint_as_float((uint32_t)(e2 - 14 + 127) << 23);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 f = pair_to_float2<true>(v[e]);
-                            v[e] = half2_of(f.x * to, f.y * to);
+                    for (int i = 0; i < kLoads; ++i) {
+                        const int row = t * BM + 32 * q + (i0 + i) * kRows + lane / kLanes;   // of the item
+                        x[i] = make_uint4(0, 0, 0, 0);
+                        if (row < rows) {
+                            const int token = p.by_group.quotient(w.item * 2 * BM + row);
+                            const int g = w.item * 2 * BM + row - token * p.group;
+                            x[i] = *reinterpret_cast<const uint4 *>(p.q + (w.seq.start + token) * p.q_stride[0] +
+                                                                    (w.head * p.group + g) * p.q_stride[1] + sub * 8);
                         }
-                        x[i] = make_uint4(v[0], v[1], v[2], v[3]);
-                        const float got = __shfl_sync(0xffffffffu, back, (lane % kRows) * kLanes);
-                        mine = lane / kRows == i ? got : mine;
                     }
-                    st_shared_v4(base + G::kOffQ + t * G::kTile16 + (sub >> 3) * kSub + r * 128 +
-                                     ((uint32_t)((sub & 7) ^ (r & 7)) << 4), x[i].x, x[i].y, x[i].z, x[i].w);
+#pragma unroll
+                    for (int i = 0; i < kLoads; ++i) {
+                        const int r = 32 * q + (i0 + i) * kRows + lane / kLanes;   // of the tile
+                        if constexpr (kBf16) {
+                            uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                            uint32_t top = 0;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                top = max(top, max(v[e] & 0x7fffu, (v[e] >> 16) & 0x7fffu));
+#pragma unroll
+                            for (int o = 1; o < kLanes; o <<= 1)
+                                top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                            int e2 = (int)(top >> 7) - 127;
+                            e2 = e2 < -100 ? -100 : e2 > 127 ? 127 : e2;
+                            const float to = __uint_as_float((uint32_t)(14 - e2 + 127) << 23);
+                            const float back = __uint_as_float((uint32_t)(e2 - 14 + 127) << 23);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float2 f = pair_to_float2<true>(v[e]);
+                                v[e] = half2_of(f.x * to, f.y * to);
+                            }
+                            x[i] = make_uint4(v[0], v[1], v[2], v[3]);
+                            const float got = __shfl_sync(0xffffffffu, back, (lane % kRows) * kLanes);
+                            mine = lane / kRows == i0 + i ? got : mine;
+                        }
+                        st_shared_v4(base + G::kOffQ + t * G::kTile16 + (sub >> 3) * kSub + r * 128 +
+                                         ((uint32_t)((sub & 7) ^ (r & 7)) << 4), x[i].x, x[i].y, x[i].z, x[i].w);
+                    }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
