@@ -53,6 +53,12 @@ constexpr int kRaggedThreads = 512;
 constexpr int kConvWarp = 12, kConvWarps = 4;
 constexpr int kRaggedSoftmaxRegs = 168, kRaggedFeedRegs = 88, kRaggedConvRegs = 88;
 static_assert(2 * kRaggedSoftmaxRegs + kRaggedFeedRegs + kRaggedConvRegs <= 4 * 128, "registers given back cover those taken");
+// Segments of a tile whose flags (NaN of V were taken out) are kept.  A tile's flags are numbered by the segments that it has
+// rows in.  When those of its segment n are written, the P V two blocks before are done, with them one at least of
+// its segment n - 2, whose P each of its warps brought after it had read the flags of segment n - 3: three would do, a
+// power of two is quicker to index.
+constexpr int kDirty = 4;
+static_assert(kDirty >= 3, "flags stay until they have been read");
 constexpr int kGroups = BN / 16;                // pieces of 16 tokens of a block: the smallest page
 constexpr int kRaggedMaxCtas = GEMMRELU_RAGGED_COUNTER_BYTES / (8 * (int)sizeof(unsigned));
 constexpr int kRaggedMaxBatch = 16384;          // sequences whose units fit the scratch of the start
@@ -75,8 +81,7 @@ struct RaggedMeta {
     float ks, lv;                  // kNearScales: the block's scale of K, log2 of that of V
     uint32_t missing;              // a bit for every 16 keys that are not there
     int valid;                     // keys up to the sequence's end
-    uint32_t segment;              // segments before this one
-    uint32_t pad[2];
+    uint32_t pad[3];
     uint32_t mul[2][kGroups];      // kNearScales: the factors of K and V, twice fp16
     float2 scale[kGroups];         // (ks, log2 vs)
 };
@@ -102,7 +107,10 @@ struct RaggedCfg {
     // meta_full[kMetas]; q_full, s_full, p_full, o_full [2]; drain
     static constexpr uint32_t kNumBars = 4 * kRaw + 8 + kMetas + 8 + 1;
     static constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;
-    static constexpr uint32_t kSmem = kOffMisc + 136 + 256 + 1024;
+    static constexpr uint32_t kOffDirty = kOffMisc + 16;         // [tiles][converting warps][kDirty]
+    static constexpr uint32_t kOffPlan = (kOffDirty + 2 * kConvWarps * kDirty * 4 + 7) / 8 * 8;
+    static constexpr uint32_t kOffSums = kOffPlan + 56;          // [2][warps], 64 bits each
+    static constexpr uint32_t kSmem = kOffSums + 256 + 1024;
     static constexpr uint32_t kTmemS = 0, kTmemO = 2 * BN;
     static constexpr uint32_t kIdescS = make_idesc_f16_f32(BM, BN, 0, 0);
     static constexpr uint32_t kIdescO = make_idesc_f16_f32(BM, HD, 0, 1);
@@ -714,9 +722,10 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
     RaggedMeta *metas = reinterpret_cast<RaggedMeta *>(gbase + G::kOffMeta);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + G::kOffMisc);
     volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(gbase + G::kOffMisc + 4);
-    volatile uint32_t *dirty = reinterpret_cast<volatile uint32_t *>(gbase + G::kOffMisc + 16);   // [4][4]
-    RaggedPlan *plan = reinterpret_cast<RaggedPlan *>(gbase + G::kOffMisc + 80);
-    int64_t *sums = reinterpret_cast<int64_t *>(gbase + G::kOffMisc + 136);   // [2][16]: + 256
+    volatile uint32_t *dirty = reinterpret_cast<volatile uint32_t *>(gbase + G::kOffDirty);
+    RaggedPlan *plan = reinterpret_cast<RaggedPlan *>(gbase + G::kOffPlan);
+    static_assert(sizeof(RaggedPlan) <= 56 && G::kOffPlan % 8 == 0, "the plan and the sums behind it");
+    int64_t *sums = reinterpret_cast<int64_t *>(gbase + G::kOffSums);
 
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);   // uniform
     const int lane = threadIdx.x & 31;
@@ -888,7 +897,6 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
                                 m.lv = lv_top;
                                 m.missing = gone;
                                 m.valid = w.seq.n - key0;
-                                m.segment = segment;
                             }
                         }
                         __syncwarp();
@@ -919,6 +927,7 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
             // ======================================================== e4m3 to fp16
             const int mine = warp - kConvWarp, row0 = BN / kConvWarps * mine;
             bool ok = true, bad = false;
+            uint32_t segments0 = 0, segments1 = 0;   // of the tiles
             for (uint32_t i = 0; ok && i < (uint32_t)blocks_here; ++i) {
                 const uint32_t rs = i % G::kRaw, rp = i / G::kRaw & 1u, st = i & 1u, ph = i >> 1 & 1u;
                 ok = wait_warp(meta_full(i % G::kMetas), i / G::kMetas & 1u, p.wait_limit_ns, abort_flag,
@@ -943,9 +952,14 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
                         convert_rows<HD, false>(src, dst, row0, meta.mul[kv], BN, 0u);
                     }
                     if (kv && flags & kLast) {
-                        const bool any = __any_sync(0xffffffffu, bad);
-                        if (lane == 0)
-                            dirty[4 * mine + (meta.segment & 3u)] = any ? 1u : 0u;
+                        const bool any = __any_sync(0xffffffffu, bad), both = flags & kBothTiles;
+                        if (lane == 0) {
+                            dirty[kDirty * mine + segments0 % kDirty] = any ? 1u : 0u;
+                            if (both)
+                                dirty[kDirty * (kConvWarps + mine) + segments1 % kDirty] = any ? 1u : 0u;
+                        }
+                        ++segments0;
+                        segments1 += both;
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -1127,7 +1141,7 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
                     mbar_arrive(q_full((uint32_t)t));
                 return mine;
             };
-            uint32_t turns = 0, blocks = 0, segments = 0, outputs = 0;
+            uint32_t turns = 0, blocks = 0, outputs = 0;
             bool alive = true;
             RaggedCut cuts[2];
             int num_cuts = 0;
@@ -1135,7 +1149,7 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
             float row_scale = t == 0 || w.rows(p) > BM ? load_q(w) : 1.0f;
             // (after a wait that expired the rest is walked through without it, so that every part is counted and the counters
             // go back to 0; the status says that the output is not to be used)
-            for (bool more = true; more; ++segments) {
+            for (bool more = true; more;) {
                 const RaggedWalk cur = w;
                 const int rows = cur.rows(p);
                 const bool here = t == 0 || rows > BM;
@@ -1303,11 +1317,11 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
                 if (alive)
                     alive = __all_sync(0xffffffffu, wait_bounded_eager(o_full((uint32_t)t), outputs & 1u, p.wait_limit_ns,
                                                                        abort_flag, kSiteEpiAccFull));
-                ++outputs;
                 tc_fence_after_sync();
                 bool taken = false;
                 for (int x = 0; x < kConvWarps; ++x)
-                    taken = taken || dirty[4 * x + (segments & 3u)];
+                    taken = taken || dirty[kDirty * (kConvWarps * t + x) + outputs % kDirty];
+                ++outputs;
                 if (alive && taken)
                     ragged_add_nan<HD>(p, cur.b, cur.head, cur.item, cur.j, cur.j1, pos, o_addr);
                 const bool valid = my_row < rows;
