@@ -18,9 +18,9 @@
 // that a row has one factor a block.
 //
 // Two references a row: m, the largest score, for the sum of weights, and rr, the largest score plus log2 of V's scale above
-// it, for P and O: P = 2^(score + log2 vs - m - rr + 7) is at most 2^7 whatever the scales are, so that fp16 holds it to half a
-// step down to 2^-21 of the largest and the fp32 sums of a block do not overflow.  Sums, references and O are fp32; P in fp16 is
-// the only rounding besides the result's.
+// it, for P and O.  A reference moves when it is exceeded by 2^8, so P = 2^(score + log2 vs - m - rr + 7) is at most 2^15 whatever
+// the scales are: fp16 holds it, to half a step down to 2^-21 of the largest, and the fp32 sums of a block do not overflow.  Sums,
+// references and O are fp32; P in fp16 is the only rounding besides the result's.
 //
 // V's bytes may be NaN where no row looks (0 * NaN is NaN): the conversion takes NaN out of blocks that are masked in part, and
 // ragged_add_nan gives them back to the rows that see them.
@@ -62,6 +62,7 @@ static_assert(kDirty >= 3, "flags stay until they have been read");
 constexpr int kGroups = BN / 16;                // pieces of 16 tokens of a block: the smallest page
 constexpr int kRaggedMaxCtas = GEMMRELU_RAGGED_COUNTER_BYTES / (8 * (int)sizeof(unsigned));
 constexpr int kRaggedMaxBatch = 16384;          // sequences whose units fit the scratch of the start
+static_assert(kPLog2 + attn::kRescaleLog2 <= 15.0f, "P stays below fp16's largest, 2^16 (1 - 2^-11), its exponent's rounding included");
 constexpr float kBigLog2 = 2048.0f;             // 2^11: scores from here on are referred before V's scale is added
 
 // What the feed says of a block.
