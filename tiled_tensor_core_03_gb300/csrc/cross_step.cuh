@@ -32,7 +32,6 @@ template <int D, int kN>
 struct StepCfg {
     static constexpr int kRows = 8 * kN;
     static constexpr int kStages = D == 64 ? 4 : 3;
-    static constexpr int kBlocksPerSm = D == 64 ? 3 : 2;
     static constexpr uint32_t kSub8 = kStepKeys * 128;           // [64 keys][64] 16-bit, 128-byte swizzle
     static constexpr uint32_t kTile = D / 64 * kSub8;            // K (or V) of a stage
     static constexpr uint32_t kOffV = kStages * kTile;
@@ -42,6 +41,11 @@ struct StepCfg {
     static constexpr int kPitch = D + 4;
     static constexpr uint32_t kOffJoin = kOffStat + 2 * kStepWarps * kRows * 4;   // [4 warps][kRows][kPitch]
     static constexpr uint32_t kSmem = kOffJoin + kStepWarps * kRows * kPitch * 4 + 1024;
+    // Blocks that an SM's 228 KB of shared memory hold, 1 KB of it reserved for each: heads of 64 three with 8 rows and two
+    // with 16, heads of 128 one.
+    static constexpr int kBlocksPerSm = 228 * 1024 / ((int)kSmem + 1024);
+    // What the compiler is told: with one block an SM it took more registers, and heads of 128 with 16 rows were 1 to 3% slower.
+    static constexpr int kBlocksToCompileFor = kBlocksPerSm < 2 ? 2 : kBlocksPerSm;
 };
 
 struct StepParams {
@@ -83,7 +87,7 @@ __device__ __forceinline__ void load_matrices(uint32_t (&r)[4], uint32_t addr) {
 }
 
 template <int D, int kN, bool kBf16>
-__global__ void __launch_bounds__(kStepThreads, StepCfg<D, kN>::kBlocksPerSm)
+__global__ void __launch_bounds__(kStepThreads, StepCfg<D, kN>::kBlocksToCompileFor)
     cross_step_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const StepParams p) {
     using G = StepCfg<D, kN>;

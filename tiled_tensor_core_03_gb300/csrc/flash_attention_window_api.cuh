@@ -73,7 +73,9 @@ StepSplit step_split(int64_t batch, int64_t q_seq, int64_t kv_seq, int64_t q_hea
         return s;
     s.rows = (int)(q_seq * group);
     const int64_t heads = batch * kv_heads, units = (kv_seq + FA::kStepKeys - 1) / FA::kStepKeys;
-    const int64_t slots = (int64_t)sms * (head_dim == 64 ? FA::StepCfg<64, 1>::kBlocksPerSm : FA::StepCfg<128, 1>::kBlocksPerSm);
+    const bool few = s.rows <= 8;
+    const int64_t slots = (int64_t)sms * (head_dim == 64 ? few ? FA::StepCfg<64, 1>::kBlocksPerSm : FA::StepCfg<64, 2>::kBlocksPerSm
+                                                         : few ? FA::StepCfg<128, 1>::kBlocksPerSm : FA::StepCfg<128, 2>::kBlocksPerSm);
     // One block joins all parts of a head, about as long a part as a stage of states takes: no more parts than stages of one.
     // (One row on 30000 states, one head of 64: 13.7 us, 57 with a block on every SM slot; 16 rows on 1774, 10 heads of 128: 12.7 and
     // 24; one on 700, 16 heads of 64: 6.6 and 7.6; twice the square root: 13.1, 12.0 and 7.0.)
@@ -82,7 +84,7 @@ StepSplit step_split(int64_t batch, int64_t q_seq, int64_t kv_seq, int64_t q_hea
         s.parts = (int)std::max<int64_t>(1, std::min({slots / heads, units, most}));
     if (s.parts > 1)
         s.bytes = GEMMRELU_CROSS_COUNTER_BYTES +
-                  (size_t)heads * s.parts * (s.rows <= 8 ? 8 : 16) * (head_dim + 4) * sizeof(float);
+                  (size_t)heads * s.parts * (few ? 8 : 16) * (head_dim + 4) * sizeof(float);
     return s;
 }
 
