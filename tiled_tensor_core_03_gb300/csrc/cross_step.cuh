@@ -86,6 +86,15 @@ __device__ __forceinline__ void load_matrices(uint32_t (&r)[4], uint32_t addr) {
                      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 
+// The numbers of states where no sequence has any: another number than 0 is out of range.
+__global__ void cross_no_states_kernel(const int32_t *states, int batch) {
+    pdl_launch_dependents();
+    pdl_wait_primary();
+    const int b = blockIdx.x * blockDim.x + threadIdx.x;
+    if (b < batch && states[b] != 0)
+        atomicCAS(&g_status, 0u, kStatusLength);
+}
+
 template <int D, int kN, bool kBf16>
 __global__ void __launch_bounds__(kStepThreads, StepCfg<D, kN>::kBlocksToCompileFor)
     cross_step_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,

@@ -160,8 +160,13 @@ static int attention_strided(const void *Q, const void *K, const void *V, void *
     if (rc != GEMMRELU_OK)
         return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (kv_seq == 0)   // nobody sees anything
-        return launch_status(cudaMemsetAsync(O, 0, (size_t)(batch * q_seq * q_heads * head_dim) * 2, s));
+    if (kv_seq == 0) {   // nobody sees anything
+        const int set = launch_status(cudaMemsetAsync(O, 0, (size_t)(batch * q_seq * q_heads * head_dim) * 2, s));
+        if (set != GEMMRELU_OK || states == nullptr)
+            return set;
+        return launch_kernel(FA::cross_no_states_kernel, (unsigned)((batch + 255) / 256), 256u, 0u, s, false, 1u, states,
+                             (int)batch);
+    }
     const int tile_tokens = kCross ? (int)(FA::BM / group) : FA::BM;
     // Weights stay below 2^8 times a row's largest: 9 + log2(keys that a row can see) keeps their sum
     // below 1/2.  fp16 values are far from fp32's range, and its weights have none to spare.
