@@ -12,9 +12,17 @@
 // head's states are cut into equal parts as long as there are fewer heads than fill the GPU; the block that
 // comes last joins the parts, in order: no block waits for another, and the same call gives the same bits.
 //
-// Measured: 48 sequences of up to 1500 states, 16 heads of 64 (217 MB): 36 us, 6.0 TB/s; 2 of up to 700: 6.6 us, where a launch
-// that does nothing takes 2.  At more than 16 rows the tiles of the long form are faster: each 8 rows more
-// are another read of the fragments from shared memory.
+// Scores, softmax statistics and sums are fp32; the weights are rounded to the inputs' type for the second product, which
+// takes both operands in one type (against 64 bits: fp16 0.00025 of the result, 0.00020 with weights in 32 bits; bf16 0.0023,
+// 0.0017).
+//
+// Measured, up to 1500 states (times and the bytes' floor): 48 sequences, 16 heads of 64: 36 us (31.9), 6.1 TB/s, 41 with 16
+// rows a head; of 128: 71 (63.8), 80; 32 sequences, 8 heads of 128: 26.9 (20.7), 30.1; 4 sequences, 8 heads of 64: 7.6, 9.4; of 128:
+// 8.0, 11.0.  2 of up to 700, 8 heads of 64: 6.5, where a launch that does nothing takes 2.
+//
+// More than 16 rows go to the tiles of the long form, which does not cut a head's states and takes about the same time
+// from 17 rows to 256: 70 us for the first of these, 93 at heads of 128, 35 for the second; where there are few heads its few
+// CTAs walk over all states alone (one sequence of 8192 states, 1 to 8 heads of 64: 12 us with 16 rows, 73 with 17; of 128: 17 and 88).
 #pragma once
 
 #include "kv_attention.cuh"

@@ -378,6 +378,8 @@ __device__ __forceinline__ WindowItem window_item(const WindowParams &p, int ind
 // the longest first, so that a CTA whose first item is long gets a short one in the next round (448 queries, 16 heads of 64:
 // 8 sequences of up to 1500 keys 33.4 us, 36.6 in the batch's order; 6 of up to 3000 38.2, and 52.0 where the heads' last
 // queries all went first, and the CTAs with the least before it got nothing of the last round).
+// Weights are rounded to the inputs' type, as in the windowed form: the second product takes both operands in one type (against
+// 64 bits, bf16 0.0023 of the result, 0.0017 with weights in 32 bits; fp16 0.00029 and 0.00021).
 constexpr int kMostOrdered = 128;
 
 template <int HD, bool kBf16, bool kCross = false>

@@ -64,7 +64,8 @@ struct StepSplit {
     size_t bytes;         // of workspace
 };
 
-// Parts of a head's states: as many as there are blocks to an SM for, a unit of 64 keys at least.
+// Parts of a head's states: as many as run at once, a unit of 64 keys at least.  (13 sequences of up to 1500 states, 8 heads of
+// 128: 14.9 us, and 19.5 cut for twice as many blocks; 16 rows a head 16.5 and 24.1.)
 StepSplit step_split(int64_t batch, int64_t q_seq, int64_t kv_seq, int64_t q_heads, int64_t kv_heads,
                      int64_t head_dim, int sms) {
     StepSplit s{0, 1, 0};

@@ -25,7 +25,7 @@
 // V's bytes may be NaN where no row looks (0 * NaN is NaN): the conversion takes NaN out of blocks that are masked in part, and
 // ragged_add_nan gives them back to the rows that see them.
 //
-// Bound, 2048 new tokens that end 32768, 32 heads on 8 of 128 (1.07 TFLOP, 555 us of products at the measured rate): 851 us,
+// Bound, 2048 new tokens that end 32768, 32 heads on 8 of 128 (1.07 TFLOP, 555 us of products at the measured rate): 854 us,
 // 1.25 PFLOP/s.  A block of two tiles takes about 4000 cycles for 2048 of products: S, softmax and P V of a tile
 // follow each other, the other tile's fill the gaps, and a tile's softmax (2250 cycles: 128 reads from TMEM, 128 exponentials
 // at 16 a cycle of an SM for both tiles, packing) is longer than the other's products; S reads both
@@ -33,8 +33,10 @@
 // case: no exponentials and no conversion 680 us.  Not kept: two threads a row 1004; S in steps of 64 keys, twice buffered
 // 1095 (Q is read twice); P handed over in halves 1258 (the issuer goes in order); the rare paths unrolled or inlined 1016
 // (instruction fetch: the loops of the four roles have to stay in the cache together); two converting warps 1018.
-// 16 sequences of up to 8000 tokens, 1000 of them new: 808 us; 6 of 12000, 2000 new, 16 heads of 64 with a window of 1024: 116; 4 of
-// 700 with up to 5 new: 17, most of it loads that wait for one another: counts, pages, keys, the other CTAs' parts.
+// 16 sequences of up to 8000 tokens, 1000 of them new: 809 us; 6 of 12000, 2000 new, 16 heads of 64 with a window of 1024: 117; 4 of
+// 700 with up to 5 new: 18, most of it loads that wait for one another: counts, pages, keys, the other CTAs' parts.  Over fourteen
+// sizes of this kind (fp16, 32 heads on 8 of 128) a call took 14 us, 2.09 us a block of a CTA and 14.7 us an item (pages of 32; 13,
+// 2.00 and 14.9 at pages of 128), within 6% but for one (11%).
 #pragma once
 
 #include "flash_attention_window.cuh"

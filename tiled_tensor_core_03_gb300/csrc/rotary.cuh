@@ -10,7 +10,9 @@
 // memory once for all heads (sincospi of the fraction's top 32 bits as fp32: the angle is off by 2^-23 at most), and its
 // threads go over the heads 16 bytes at a time.  A thread has one head under way: four took registers and with them
 // occupancy (60 us against 57).  4 x 4096 tokens, 32 + 8 heads of 128, bf16: 57 us, 5.9 TB/s; 3 x 5001 tokens, half of 16 + 16
-// heads of 64 turned in pairs side by side: 22 us, 5.6 TB/s; 64 single tokens: 2.8 us on the GPU.
+// heads of 64 turned in pairs side by side: 26 us, 4.7 TB/s (22 where one call after the other writes the same 61 MB, which then
+// stay in L2); 64 single tokens: 2.8 us on the GPU.  Where rot is no multiple of 16, pairs go one at a time in accesses of 2
+// bytes: the same tokens with rot 24 58 us and 20 72 (32: 22); 4 x 4096, heads of 128, 24 127, 20 146, 120 173 (96: 57).
 #pragma once
 
 #include "kv_attention.cuh"
