@@ -79,7 +79,8 @@ def flash_attention_cross(q, k, v, lengths=None, out=None, workspace=None, strea
     h // (q_heads // kv_heads).  Strides as for flash_attention_window.
 
     Every query of sequence b sees the states j < lengths[b] (int32 [batch]; default: all kv_seq).
-    Where there are none it gets 0.  What stands behind them, NaN among it, is not seen.
+    Where there are none it gets 0.  What stands behind them, NaN among it, is not seen; with more than 16
+    query rows a K/V head, padding that is not finite takes two to three times as long as finite.
 
     A call of few query rows and heads needs a workspace: without one it uses one that is kept per
     stream, or its own where it is being captured."""
@@ -117,7 +118,8 @@ def rotary(q, k, positions, inv_freq, interleaved=False, amplitude=1.0, inverse=
     positions int32 or int64 [batch, tokens] (or [rows]); inv_freq float32 or float64 [rot / 2], as
     rotary_frequencies makes them.  The first rot elements of a head turn in pairs (p, p + rot / 2), or
     `interleaved` (2p, 2p + 1), and are multiplied by `amplitude`; the others are copied.  With `inverse`
-    they turn back: rotary(dq, dk, ..., inverse=True) is the gradient with respect to the inputs.
+    they turn back: rotary(dq, dk, ..., inverse=True) is the gradient with respect to the inputs.  A rot that is
+    no multiple of 16 takes about three times as long.
 
     Heads are contiguous and start on 16-byte boundaries; other strides are free.  `out`: a tuple of
     tensors for the results, which may be q and k themselves; other overlaps are not checked."""
